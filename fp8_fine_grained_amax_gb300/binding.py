@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -35,6 +36,11 @@ FP8Q_BSCALE_ROW = 2
 
 # name -> (restype, argtypes) for every entry point declared in include/fp8q.h
 _P, _I64, _INT, _U64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64
+_F32 = ctypes.c_float
+_GLU = [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _INT, _I64,
+        _I64, _I64, _P]
+_GLU_GROUPED = [_P, _I64, _P, _I64, _P, _I64, _P, _P, _INT, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
+                _INT, _I64, _I64, _I64, _P]
 SIGNATURES = {
     "fp8q_quant_act": (_INT, [_P, _I64, _I64, _I64, _P, _I64, _P, _I64, _INT, _P]),
     "fp8q_quant_act_T": (_INT, [_P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
@@ -56,6 +62,15 @@ SIGNATURES = {
                                  _I64, _I64, _I64, _P]),
     "fp8q_grouped_gemm_pow2": (_INT, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _INT, _P, _I64, _INT,
                                       _I64, _I64, _I64, _P]),
+    "fp8q_gemm_swiglu": (_INT, _GLU),
+    "fp8q_gemm_swiglu_pow2": (_INT, _GLU),
+    "fp8q_grouped_gemm_swiglu": (_INT, _GLU_GROUPED),
+    "fp8q_grouped_gemm_swiglu_pow2": (_INT, _GLU_GROUPED),
+    "fp8q_swiglu_bwd": (_INT, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
+                               _P, _I64, _P, _I64, _I64, _I64, _INT, _P]),
+    "fp8q_newton_schulz_workspace_bytes": (_I64, [_I64, _I64, _I64]),
+    "fp8q_newton_schulz": (_INT, [_P, _I64, _I64, _INT, _P, _I64, _I64, _INT, _I64, _I64, _I64, _INT,
+                                  _F32, _F32, _F32, _F32, _P, _I64, _P]),
     "fp8q_cast_e4m3": (_INT, [_P, _I64, _P, _P]),
     "fp8q_sync_status": (_INT, [_P]),
     "fp8q_set_wait_timeout_ns": (None, [_U64]),
@@ -308,6 +323,182 @@ def fp8q_grouped_gemm_pow2(a, sa, b, sb, offs, *, out_dtype=FP8Q_OUT_BF16, c=Non
     """fp8q_grouped_gemm for power-of-two scales on the block-scaled MMA."""
     return fp8q_grouped_gemm(a, sa, b, sb, offs, out_dtype=out_dtype, c=c, stream=stream,
                              _entry="fp8q_grouped_gemm_pow2")
+
+
+class SwigluOut(NamedTuple):
+    """Results of the gated feed-forward calls; None where not asked for."""
+    h: Optional[torch.Tensor]   # BF16 [M][F]
+    gu: Optional[torch.Tensor]  # BF16 [M][2F]: g, then u
+    q: Optional[torch.Tensor]   # uint8 [M][F]: 1x128 codes of h
+    s: Optional[torch.Tensor]   # f32 [F/128][M]
+
+
+class SwigluGrads(NamedTuple):
+    """Results of fp8q_swiglu_bwd; None where not asked for."""
+    d: Optional[torch.Tensor]    # BF16 [T][2F]: dg, then du
+    q: Optional[torch.Tensor]    # uint8 [T][2F]: 1x128 codes of d
+    s: Optional[torch.Tensor]    # f32 [2F/128][T]
+    qT: Optional[torch.Tensor]   # uint8 [2F][T]: 128x1 codes of d
+    sT: Optional[torch.Tensor]   # f32 [T/128][2F]
+    hT: Optional[torch.Tensor]   # uint8 [F][T]: 128x1 codes of h
+    shT: Optional[torch.Tensor]  # f32 [T/128][F]
+
+
+def _out(t, wanted, shape, dtype, device, name):
+    """The caller's output tensor (checked), a new one where wanted, or None."""
+    if t is not None:
+        if tuple(t.shape) != shape or t.dtype != dtype:
+            raise ValueError(f"{name} must be a {dtype} tensor of shape {shape}")
+        return t
+    return torch.empty(shape, dtype=dtype, device=device) if wanted else None
+
+
+def _ld(t, name, empty=0):
+    """Row pitch of an optional matrix; the strides of one-long axes do not count."""
+    if t is None:
+        return 0
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with a contiguous last dimension")
+    if not t.numel():
+        return max(empty, t.shape[1])
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _need(t, dtype, name):
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor")
+
+
+def _glu_call(entry, a, sa, b, sb, offs, F, with_h, with_gu, with_codes, scale_mode, h, gu, q, s,
+              stream):
+    M, K = a.shape
+    _need(a, torch.uint8, "a")
+    _need(b, torch.uint8, "b")
+    _need(sa, torch.float32, "sa")
+    _need(sb, torch.float32, "sb")
+    if b.shape[-1] != K or b.shape[-2] != 2 * F:
+        raise ValueError("b must hold both projections: [2F][K] rows, with a's K")
+    dev = a.device
+    h = _out(h, with_h, (M, F), torch.bfloat16, dev, "h")
+    gu = _out(gu, with_gu, (M, 2 * F), torch.bfloat16, dev, "gu")
+    q = _out(q, with_codes, (M, F), torch.uint8, dev, "q")
+    s = _out(s, q is not None, (F // 128, M), torch.float32, dev, "s")
+    lib = load_library()
+    head = [_ptr(a), _ld(a, "a", K), _ptr(sa), _ld(sa, "sa", M), _ptr(b), b.stride(-2), _ptr(sb)]
+    if offs is None:
+        head.append(_ld(sb, "sb", K // 128))
+    else:
+        _need(offs, torch.int32, "offs")
+        if offs.numel() != b.shape[0] + 1 or not offs.is_contiguous():
+            raise ValueError("offs must be a contiguous int32 [G+1] tensor")
+        if not sb.is_contiguous():
+            raise ValueError("sb must be contiguous [G][2F/128][K/128]")
+        head += [_ptr(offs), b.shape[0]]
+    _check(getattr(lib, entry)(
+        *head, _ptr(h), _ld(h, "h", F), _ptr(gu), _ld(gu, "gu", 2 * F), _ptr(q), _ld(q, "q", F),
+        _ptr(s), _ld(s, "s", M), scale_mode, M, F, K, _stream(stream)), entry)
+    return SwigluOut(h, gu, q, s)
+
+
+def fp8q_gemm_swiglu(a, sa, b, sb, *, with_h=True, with_gu=False, with_codes=False,
+                     scale_mode=FP8Q_SCALE_FP32, h=None, gu=None, q=None, s=None, stream=None,
+                     _entry="fp8q_gemm_swiglu"):
+    """h = silu(X Wg^T) * (X Wu^T) from codes a uint8 [M][K] (sa f32 [K/128][M]) and the stacked
+    projections b uint8 [2F][K] (sb f32 [2F/128][K/128]) -> SwigluOut(h, gu, q, s)."""
+    if b.dim() != 2 or b.stride(1) != 1 or b.shape[0] % 2:
+        raise ValueError("b must be [2F][K] with a contiguous last dimension")
+    if tuple(sa.shape) != (a.shape[1] // 128, a.shape[0]) or \
+            tuple(sb.shape) != (b.shape[0] // 128, a.shape[1] // 128):
+        raise ValueError("sa must be [K/128][M] and sb [2F/128][K/128]")
+    return _glu_call(_entry, a, sa, b, sb, None, b.shape[0] // 2, with_h, with_gu, with_codes,
+                     scale_mode, h, gu, q, s, stream)
+
+
+def fp8q_gemm_swiglu_pow2(a, sa, b, sb, **kw):
+    """fp8q_gemm_swiglu for power-of-two input scales on the block-scaled MMA."""
+    return fp8q_gemm_swiglu(a, sa, b, sb, _entry="fp8q_gemm_swiglu_pow2", **kw)
+
+
+def fp8q_grouped_gemm_swiglu(a, sa, b, sb, offs, *, with_h=True, with_gu=False, with_codes=False,
+                             scale_mode=FP8Q_SCALE_FP32, h=None, gu=None, q=None, s=None,
+                             stream=None, _entry="fp8q_grouped_gemm_swiglu"):
+    """fp8q_gemm_swiglu per expert: b uint8 [G][2F][K], sb f32 [G][2F/128][K/128], offs int32
+    [G+1] on the device.  Rows outside [offs[0], offs[G]) are left as is."""
+    if b.dim() != 3 or b.stride(2) != 1 or b.stride(0) != b.shape[1] * b.stride(1) or \
+            b.shape[1] % 2:
+        raise ValueError("b must be [G][2F][ldb] with experts packed back to back")
+    if tuple(sa.shape) != (a.shape[1] // 128, a.shape[0]) or \
+            tuple(sb.shape) != (b.shape[0], b.shape[1] // 128, a.shape[1] // 128):
+        raise ValueError("sa must be [K/128][M] and sb [G][2F/128][K/128]")
+    return _glu_call(_entry, a, sa, b, sb, offs, b.shape[1] // 2, with_h, with_gu, with_codes,
+                     scale_mode, h, gu, q, s, stream)
+
+
+def fp8q_grouped_gemm_swiglu_pow2(a, sa, b, sb, offs, **kw):
+    """fp8q_grouped_gemm_swiglu for power-of-two input scales on the block-scaled MMA."""
+    return fp8q_grouped_gemm_swiglu(a, sa, b, sb, offs, _entry="fp8q_grouped_gemm_swiglu_pow2",
+                                    **kw)
+
+
+def fp8q_swiglu_bwd(dh, gu, *, with_d=False, with_rows=True, with_cols=True, with_h=True,
+                    scale_mode=FP8Q_SCALE_FP32, d=None, q=None, s=None, qT=None, sT=None, hT=None,
+                    shT=None, stream=None):
+    """Backward of h = silu(g) * u: dh BF16 [T][F], gu BF16 [T][2F] -> SwigluGrads, any of the
+    BF16 gradient d (with_d), its 1x128 codes (with_rows), its transposed 128x1 codes (with_cols)
+    and the transposed 128x1 codes of h (with_h; both need T % 128 == 0)."""
+    T, F = dh.shape
+    _need(dh, torch.bfloat16, "dh")
+    _need(gu, torch.bfloat16, "gu")
+    if tuple(gu.shape) != (T, 2 * F):
+        raise ValueError("gu must be [T][2F]")
+    dev = dh.device
+    d = _out(d, with_d, (T, 2 * F), torch.bfloat16, dev, "d")
+    q = _out(q, with_rows, (T, 2 * F), torch.uint8, dev, "q")
+    s = _out(s, q is not None, (2 * F // 128, T), torch.float32, dev, "s")
+    qT = _out(qT, with_cols, (2 * F, T), torch.uint8, dev, "qT")
+    sT = _out(sT, qT is not None, (T // 128, 2 * F), torch.float32, dev, "sT")
+    hT = _out(hT, with_h, (F, T), torch.uint8, dev, "hT")
+    shT = _out(shT, hT is not None, (T // 128, F), torch.float32, dev, "shT")
+    _check(load_library().fp8q_swiglu_bwd(
+        _ptr(dh), _ld(dh, "dh", F), _ptr(gu), _ld(gu, "gu", 2 * F), _ptr(d), _ld(d, "d", 2 * F),
+        _ptr(q), _ld(q, "q", 2 * F), _ptr(s), _ld(s, "s", T), _ptr(qT), _ld(qT, "qT", T),
+        _ptr(sT), _ld(sT, "sT", 2 * F), _ptr(hT), _ld(hT, "hT", T), _ptr(shT),
+        _ld(shT, "shT", F), T, F, scale_mode, _stream(stream)), "fp8q_swiglu_bwd")
+    return SwigluGrads(d, q, s, qT, sT, hT, shT)
+
+
+def fp8q_newton_schulz_workspace_bytes(batch: int, m: int, n: int) -> int:
+    return int(load_library().fp8q_newton_schulz_workspace_bytes(batch, m, n))
+
+
+def fp8q_newton_schulz(g, *, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7,
+                       out_dtype=FP8Q_OUT_BF16, out=None, workspace=None, stream=None):
+    """Orthogonalised update of g ([m][n] or a batch [B][m][n], FP32 or BF16): `steps` steps
+    X <- aX + (bA + cA^2)X, A = X X^T, from X = g / (|g|_F + eps) -> BF16 or FP32, g's shape.
+    A workspace tensor is allocated with torch when not given."""
+    if g.dim() not in (2, 3) or g.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("g must be an FP32 or BF16 matrix or batch of matrices")
+    dt = torch.bfloat16 if out_dtype == FP8Q_OUT_BF16 else torch.float32
+    if out is None:
+        out = torch.empty(g.shape, dtype=dt, device=g.device)
+    elif out.shape != g.shape or out.dtype != dt:
+        raise ValueError("out must have g's shape and the type out_dtype names")
+    for t, name in ((g, "g"), (out, "out")):
+        if t.numel() and t.stride(-1) != 1:
+            raise ValueError(f"{name} must have a contiguous last dimension")
+    B = g.shape[0] if g.dim() == 3 else 1
+    m, n = g.shape[-2:]
+    nbytes = fp8q_newton_schulz_workspace_bytes(B, m, n)
+    if workspace is None:
+        workspace = torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=g.device)
+    a, b, c = coeffs
+    _check(load_library().fp8q_newton_schulz(
+        _ptr(g), g.stride(-2) if g.numel() else n, g.stride(0) if g.dim() == 3 else 0,
+        FP8Q_OUT_FP32 if g.dtype == torch.float32 else FP8Q_OUT_BF16, _ptr(out),
+        out.stride(-2) if g.numel() else n, out.stride(0) if g.dim() == 3 else 0, out_dtype, B, m, n,
+        steps, a, b, c, eps, _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream(stream)), "fp8q_newton_schulz")
+    return out
 
 
 def fp8q_cast_e4m3(x, *, q=None, stream=None):

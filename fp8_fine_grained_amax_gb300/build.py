@@ -25,7 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfp8q.so")
-SOURCES = ["gemm.cu", "gemm_mx.cu", "quant.cu", "api.cu"]
+SOURCES = ["gemm.cu", "gemm_mx.cu", "quant.cu", "swiglu.cu", "newton_schulz.cu", "api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

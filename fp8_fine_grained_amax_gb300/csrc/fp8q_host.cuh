@@ -114,5 +114,9 @@ inline bool make_tmap_2d(CUtensorMap *m, CUtensorMapDataType type, const void *b
 fp8q_status quant_status_take(cudaStream_t s);
 // The same for the power-of-two (block-scaled MMA) GEMM; defined in gemm_mx.cu.
 fp8q_status mx_status_take(cudaStream_t s);
+// The same for the few-token gated feed-forward kernel; defined in swiglu.cu.
+fp8q_status glu_status_take(cudaStream_t s);
+// The same for the Newton-Schulz kernels; defined in newton_schulz.cu.
+fp8q_status ns_status_take(cudaStream_t s);
 
 }  // namespace fp8q

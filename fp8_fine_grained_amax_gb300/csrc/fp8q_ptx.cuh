@@ -192,8 +192,9 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
 // segments instead of 32 scattered pieces, with an L2 evict-first hint.  The
 // block starts at (row0, col0); rows >= row_end and columns >= n are left
 // alone.  kEsz: element size (2 or 4); kAccum (FP32 only): C += values, one
-// FP32 addition per element.
-template <int kEsz, bool kAccum>
+// FP32 addition per element; kOnce: nothing reads the block back soon (the
+// evict-first hint).
+template <int kEsz, bool kAccum, bool kOnce = true>
 __device__ __forceinline__ void warp_store_block64(uint32_t buf, const uint4 (&u)[4], void *c,
                                                    int64_t ldc, int row0, int row_end, int col0,
                                                    int n, int lane) {
@@ -220,7 +221,8 @@ __device__ __forceinline__ void warp_store_block64(uint32_t buf, const uint4 (&u
         v.z = __float_as_uint(__fadd_rn(old.z, __uint_as_float(v.z)));
         v.w = __float_as_uint(__fadd_rn(old.w, __uint_as_float(v.w)));
       }
-      st_global_v4_hint(dst, v, l2_evict_first_policy());
+      if (kOnce) st_global_v4_hint(dst, v, l2_evict_first_policy());
+      else *reinterpret_cast<uint4 *>(dst) = v;
     } else {
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
       for (int e = 0; e < kUnitCols && col + e < n; ++e) {
@@ -486,6 +488,16 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The two halves of a cluster barrier that only tells that every CTA of the
+// cluster has started (its shared memory may be written from outside): arrive
+// early, wait before the first remote store.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Arrive on an mbarrier given by its shared::cluster address (may be the peer's).

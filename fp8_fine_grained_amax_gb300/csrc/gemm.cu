@@ -49,6 +49,7 @@
 #include <mutex>
 
 #include "fp8q.h"
+#include "fp8q_glu.cuh"
 #include "fp8q_host.cuh"
 #include "fp8q_ptx.cuh"
 
@@ -135,6 +136,7 @@ struct GemmArgs {
   const int32_t *offs;  // grouped only
   int G;
   uint64_t timeout_ns;
+  GluOut glu;  // gated GEMM only: N = F, tiles of 128 columns of h
 };
 
 // Shared-memory control block, after the operand ring and the output staging.
@@ -149,6 +151,7 @@ struct alignas(8) SmemCtl {
   // per-column B scales (Wgrad): each epilogue warp stages the scales of its
   // own columns for the current K-group, double-buffered
   alignas(16) float sb_warp[kEpiWarps][2][kEpiCols];
+  GluExchange glu;  // gated GEMM only
 };
 
 // Output staging: 8 KB per epilogue warp: its 32 rows x 128 BF16 columns as
@@ -174,10 +177,12 @@ struct Tile {
 
 // Grouped tables in shared memory: s_lo[g] .. s_lo[g + 1] = clamped row range of
 // expert g, s_pre[g] = number of m-tiles of experts before g (s_pre[G] = all).
-template <bool kGrouped, int kTileM>
+// kGlu: a tile is 128 columns of h wide; expert g's rows of B start at 2 N g.
+template <bool kGrouped, int kTileM, bool kGlu>
 __device__ __forceinline__ Tile tile_of(int t, const GemmArgs &p, const int *s_lo,
                                         const int *s_pre) {
   Tile r;
+  constexpr int kTileN = kGlu ? BN / 2 : BN;
   if (!kGrouped) {
     const int band_tiles = kGroupM * p.tiles_n;
     const int band = t / band_tiles, within = t - band * band_tiles;
@@ -186,7 +191,7 @@ __device__ __forceinline__ Tile tile_of(int t, const GemmArgs &p, const int *s_l
     const int mt = mt0 + within % rows, nt = within / rows;
     r.a_row = mt * kTileM;
     r.row_end = p.M;
-    r.n0 = nt * BN;
+    r.n0 = nt * kTileN;
     r.b_row = r.n0;
     r.g = 0;
   } else {
@@ -203,8 +208,8 @@ __device__ __forceinline__ Tile tile_of(int t, const GemmArgs &p, const int *s_l
     const int mt = local % mtiles, nt = local / mtiles;
     r.a_row = s_lo[g] + mt * kTileM;
     r.row_end = s_lo[g + 1];
-    r.n0 = nt * BN;
-    r.b_row = g * p.N + r.n0;
+    r.n0 = nt * kTileN;
+    r.b_row = g * (kGlu ? 2 * p.N : p.N) + r.n0;
     r.g = g;
   }
   return r;
@@ -213,12 +218,17 @@ __device__ __forceinline__ Tile tile_of(int t, const GemmArgs &p, const int *s_l
 // kTmaOut (dense BF16, N a multiple of 8): C leaves only as whole-block TMA
 // tensor stores; without the coalesced-store path in the same kernel the fold
 // keeps its registers.
+// kGlu: B holds two stacked projections; a tile's 256 accumulator columns are
+// 64 gate, 64 up, 64 gate, 64 up columns, the fold takes each half's own block
+// scale, and the epilogue stores the gated results (fp8q_glu.cuh).
 template <int kBScale, bool kOutF32, bool kGrouped, bool kPair, bool kAccum = false,
-          bool kTmaOut = false>
+          bool kTmaOut = false, bool kGlu = false>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8q_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmC, const GemmArgs p) {
   using C = Cfg<kPair>;
+  static_assert(!kGlu || (kPair && kBScale == FP8Q_BSCALE_BLOCK && !kAccum && !kTmaOut),
+                "the gated form runs on CTA pairs with block scales");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -246,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->tempty[i]), C::kTemptyCount);
     }
     mbar_init(smem_u32(&ctl->drain), 1);
+    if (kGlu) glu_exchange_init(ctl->glu);
     ctl->abort_flag = 0;
     fence_barrier_init();
   }
@@ -321,14 +332,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     int tb = 0;
     uint32_t tphase = 0;
     uint32_t sb_iter = 0;
+    uint32_t glu_uses = 0;
     bool ok = true;
     for (int t = tile_first; ok && t < total_tiles; t += tile_step) {
-      const Tile tl = tile_of<kGrouped, C::kTileM>(t, p, s_lo, s_prefix);
+      const Tile tl = tile_of<kGrouped, C::kTileM, kGlu>(t, p, s_lo, s_prefix);
       const int m = tl.a_row + row_in_tile;
-      const int ncol0 = tl.n0 + col_base;
+      const int ncol0 = tl.n0 + (kGlu ? col_base / 2 : col_base);
       const int nb = ncol0 / 128;
       const float *sb_g = p.sb;
-      if (kGrouped) sb_g += static_cast<int64_t>(tl.g) * NB * p.num_kb;
+      if (kGrouped) sb_g += static_cast<int64_t>(tl.g) * (kGlu ? 2 * NB : NB) * p.num_kb;
       // Scales of K-group kb: sa of this lane's row (per-column kind: each
       // thread takes its four rows' scales from their lanes by shuffles); sb
       // of this warp's columns (block kinds: one value; per-column kind: lane
@@ -346,12 +358,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           : kBScale == FP8Q_BSCALE_BLOCK_T ? p.sb + (sb_in ? nb : 0)
                                            : p.sb + ncol0 + 16 * (lane & 7) + 2 * (lane >> 3);
       const int64_t sb_step = kBScale == FP8Q_BSCALE_BLOCK ? 1 : p.ld_sb;
+      // gated form: the up projection's block, NB rows of blocks further down
+      const int64_t sb_up = static_cast<int64_t>(NB) * (kGrouped ? p.num_kb : p.ld_sb);
       // per-column kind: this lane's first column
       const int ncol = ncol0 + 16 * (lane & 7) + 2 * (lane >> 3);
       auto load_sa = [&]() { return sa_in ? __ldg(sa_ptr) : 0.0f; };
       auto load_sb = [&]() {
         return kBScale != FP8Q_BSCALE_ROW && sb_in ? __ldg(sb_ptr) : 0.0f;
       };
+      auto load_sbu = [&]() { return kGlu ? __ldg(sb_ptr + sb_up) : 0.0f; };
       auto load_sb4 = [&]() {
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (kBScale == FP8Q_BSCALE_ROW) {
@@ -368,17 +383,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < kEpiCols / 2; ++j) acc[j] = 0ull;
       float sa_nx = p.num_kb > 0 ? load_sa() : 0.0f;
       float sb_nx = p.num_kb > 0 ? load_sb() : 0.0f;
+      float sbu_nx = p.num_kb > 0 ? load_sbu() : 0.0f;
       float4 sb4_nx = p.num_kb > 0 ? load_sb4() : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 
       for (int kb = 0; kb < p.num_kb; ++kb) {
         // the scales of group kb were loaded one iteration ago; fetch kb+1 now
-        const float sa_v = sa_nx, sb_v = sb_nx;
+        const float sa_v = sa_nx, sb_v = sb_nx, sbu_v = sbu_nx;
         const float4 sb4 = sb4_nx;
         if (kb + 1 < p.num_kb) {
           sa_ptr += p.ld_sa;
           sb_ptr += sb_step;
           sa_nx = load_sa();
           sb_nx = load_sb();
+          sbu_nx = load_sbu();
           sb4_nx = load_sb4();
         }
         if (kBScale == FP8Q_BSCALE_ROW) {
@@ -388,6 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         const uint64_t scale2 = pack_f32x2(sa_v * sb_v, sa_v * sb_v);
+        const uint64_t scale2u = kGlu ? pack_f32x2(sa_v * sbu_v, sa_v * sbu_v) : scale2;
         uint64_t sa2f[4];  // per-column kind: this thread's four row scales, packed twice
         if (kFrag) {
 #pragma unroll
@@ -434,7 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              ffma2(acc[ch * 8 + j], pack_u32x2(r[2 * j], r[2 * j + 1]), scale2);
+              ffma2(acc[ch * 8 + j], pack_u32x2(r[2 * j], r[2 * j + 1]),
+                    kGlu && ch >= kEpiCols / 32 ? scale2u : scale2);
           }
         }
         tc_fence_before();
@@ -449,6 +468,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
 
+      if constexpr (kGlu) {
+        const int wrow0 = tl.a_row + row_in_tile - lane;
+        if (wrow0 < tl.row_end)
+          ok = glu_store(acc, p.glu, smem_u32(sC) + static_cast<uint32_t>(ew) * kStageWarpBytes,
+                         wrow0, tl.row_end, ncol0, ew, lane, ctl->glu, glu_uses, abort_flag,
+                         &g_status, p.timeout_ns);
+        continue;
+      }
       if (kFrag && kOutF32 && !kGrouped) {
         // FP32 straight from the fragments: for each (i, r) the four lanes of a
         // quad write 32 contiguous bytes of one row (8 rows per instruction)
@@ -600,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t armed = 0, armed_phase = 0;  // per-stage bit masks
       bool ok = true;
       for (int t = tile_first; ok && t < total_tiles; t += tile_step) {
-        const Tile tl = tile_of<kGrouped, C::kTileM>(t, p, s_lo, s_prefix);
+        const Tile tl = tile_of<kGrouped, C::kTileM, kGlu>(t, p, s_lo, s_prefix);
         for (int kb = 0; kb < p.num_kb; ++kb) {
           if (!mbar_wait_bounded(smem_u32(&ctl->empty[stage]), phase ^ 1, abort_flag, &g_status,
                                  p.timeout_ns, FP8Q_ERR_TIMEOUT)) {
@@ -615,8 +642,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t fb0 = mapa_shared(fb, 0);
             tma_load_2d_pair(smem_u32(sA + stage * C::kABytes), &tmA, fb0, kb * BK,
                              tl.a_row + static_cast<int>(rank) * BM);
-            tma_load_2d_pair(smem_u32(sB + stage * C::kBBytes), &tmB, fb0, kb * BK,
-                             tl.b_row + static_cast<int>(rank) * (BN / 2));
+            if (kGlu) {
+              // 64 gate rows, then the up rows of the same 64 columns of h
+              const int brow = tl.b_row + static_cast<int>(rank) * (BN / 4);
+              tma_load_2d_pair(smem_u32(sB + stage * C::kBBytes), &tmB, fb0, kb * BK, brow);
+              tma_load_2d_pair(smem_u32(sB + stage * C::kBBytes + C::kBBytes / 2), &tmB, fb0,
+                               kb * BK, brow + p.N);
+            } else {
+              tma_load_2d_pair(smem_u32(sB + stage * C::kBBytes), &tmB, fb0, kb * BK,
+                               tl.b_row + static_cast<int>(rank) * (BN / 2));
+            }
           } else {
             mbar_arrive_expect_tx(fb, C::kTxBytes);
             tma_load_2d(smem_u32(sA + stage * C::kABytes), &tmA, fb, kb * BK, tl.a_row);
@@ -744,10 +779,10 @@ bool make_tmap_c(CUtensorMap *m, void *base, uint64_t rows, uint64_t cols, uint6
 // upper bound for the grouped GEMM); the grid is persistent: one CTA (or one
 // CTA pair) per SM that can hold one, never more than there are tiles.
 template <int kBScale, bool kOutF32, bool kGrouped, bool kPair, bool kAccum = false,
-          bool kTmaOut = false>
+          bool kTmaOut = false, bool kGlu = false>
 fp8q_status launch(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc,
                    const GemmArgs &args, int64_t work_tiles, cudaStream_t s) {
-  auto kern = fp8q_gemm_kernel<kBScale, kOutF32, kGrouped, kPair, kAccum, kTmaOut>;
+  auto kern = fp8q_gemm_kernel<kBScale, kOutF32, kGrouped, kPair, kAccum, kTmaOut, kGlu>;
   const size_t smem = smem_bytes(kGrouped, kPair);
   static int max_units[kMaxDevices] = {};  // co-resident CTAs (or CTA pairs) per device
   static std::mutex mu;
@@ -853,6 +888,49 @@ fp8q_status check_common(const void *a, int64_t lda, const void *b, int64_t ldb,
 }
 
 }  // namespace
+
+// Gated feed-forward block, FP32 scales (arguments checked by the caller).
+fp8q_status gemm_glu(const GluIn &in, const GluOut &out, cudaStream_t s) {
+  const bool grouped = in.offs != nullptr;
+  DeviceInfo dev;
+  if (fp8q_status st = device_info(dev)) return st;
+  if (dev.max_smem_optin < static_cast<int>(smem_bytes(grouped, true)))
+    return FP8Q_ERR_UNSUPPORTED;
+  // K == 0: no loads happen; describe a dummy 1 x 128 tensor so the maps are valid
+  const bool k0 = in.K == 0;
+  const void *any = out.h ? out.h : out.gu ? out.gu : out.q;
+  const uint64_t brows = static_cast<uint64_t>(in.G) * 2 * in.F;
+  CUtensorMap ta, tb;
+  if (!make_tmap_u8(&ta, k0 ? any : in.a, k0 ? 1 : in.M, k0 ? 128 : in.K, k0 ? 128 : in.lda, BM) ||
+      !make_tmap_u8(&tb, k0 ? any : in.b, k0 ? 1 : brows, k0 ? 128 : in.K, k0 ? 128 : in.ldb,
+                    BN / 4))
+    return FP8Q_ERR_CUDA;
+  GemmArgs args{};
+  args.sa = in.sa;
+  args.ld_sa = in.ld_sa;
+  args.sb = in.sb;
+  args.ld_sb = in.ld_sb;
+  args.M = static_cast<int>(in.M);
+  args.N = static_cast<int>(in.F);
+  args.num_kb = static_cast<int>(in.K / 128);
+  args.tiles_m = static_cast<int>((in.M + Cfg<true>::kTileM - 1) / Cfg<true>::kTileM);
+  args.tiles_n = static_cast<int>(in.F / 128);
+  args.offs = in.offs;
+  args.G = in.G;
+  args.timeout_ns = wait_timeout_ns().load();
+  args.glu = out;
+  // grouped: each expert adds at most one partial m-tile
+  const int64_t tiles =
+      (static_cast<int64_t>(args.tiles_m) + (grouped ? in.G : 0)) * args.tiles_n;
+  if (tiles >= (1ll << 31)) return FP8Q_ERR_SHAPE;
+  // no C tensor: its map slot repeats A's
+  if (grouped)
+    return launch<FP8Q_BSCALE_BLOCK, false, true, true, false, false, true>(ta, tb, ta, args,
+                                                                            tiles, s);
+  return launch<FP8Q_BSCALE_BLOCK, false, false, true, false, false, true>(ta, tb, ta, args, tiles,
+                                                                           s);
+}
+
 }  // namespace fp8q
 
 using namespace fp8q;
@@ -990,8 +1068,10 @@ extern "C" fp8q_status fp8q_sync_status(void *stream) {
   }
   const fp8q_status q = quant_status_take(s);
   const fp8q_status x = mx_status_take(s);
+  const fp8q_status g = glu_status_take(s);
+  const fp8q_status n = ns_status_take(s);
   if (v != 0) return static_cast<fp8q_status>(v);
-  return q != FP8Q_OK ? q : x;
+  return q != FP8Q_OK ? q : x != FP8Q_OK ? x : g != FP8Q_OK ? g : n;
 }
 
 extern "C" void fp8q_set_wait_timeout_ns(uint64_t ns) {

@@ -52,6 +52,7 @@
 #include <mutex>
 
 #include "fp8q.h"
+#include "fp8q_glu.cuh"
 #include "fp8q_host.cuh"
 #include "fp8q_ptx.cuh"
 
@@ -118,6 +119,7 @@ struct MxArgs {
   const int32_t *offs;  // grouped only: expert row offsets [G + 1] (device)
   int G;
   uint64_t timeout_ns;
+  GluOut glu;           // gated GEMM only: N = F, tiles of 128 columns of h
 };
 
 // Per-column B scale preparation (dense GEMMs with FP8Q_BSCALE_ROW): every
@@ -145,6 +147,7 @@ struct alignas(8) MxCtl {
   uint64_t pfree[kPrepSlots];   // every CTA: the four B producer warps read them
   uint32_t tmem_base;
   int abort_flag;
+  GluExchange glu;  // gated GEMM only
 };
 
 constexpr int kMaxGroups = 1024;
@@ -186,11 +189,13 @@ struct MxTile {
 
 // Dense: bands of kGroupM m-tiles for L2 reuse.  Grouped: expert-major, m-tiles
 // fastest; s_lo / s_hi = clamped row range of expert g, s_pre[g] = m-tiles of
-// the experts before g.
-template <bool kGrouped>
+// the experts before g.  kGlu: a tile is 128 columns of h wide; expert g's
+// rows of B start at 2 N g.
+template <bool kGrouped, bool kGlu>
 __device__ __forceinline__ MxTile mx_tile_of(int t, const MxArgs &p, const int *s_lo,
                                              const int *s_hi, const int *s_pre) {
   MxTile r;
+  constexpr int kTileN = kGlu ? BN / 2 : BN;
   if (!kGrouped) {
     const int band_tiles = kGroupM * p.tiles_n;
     const int band = t / band_tiles, within = t - band * band_tiles;
@@ -198,7 +203,7 @@ __device__ __forceinline__ MxTile mx_tile_of(int t, const MxArgs &p, const int *
     const int rows = min(kGroupM, p.tiles_m - mt0);
     r.m0 = (mt0 + within % rows) * kTileM;
     r.row_end = p.M;
-    r.n0 = (within / rows) * BN;
+    r.n0 = (within / rows) * kTileN;
     r.b_row = r.n0;
     r.g = 0;
   } else {
@@ -212,19 +217,24 @@ __device__ __forceinline__ MxTile mx_tile_of(int t, const MxArgs &p, const int *
     const int local = t - s_pre[g] * p.tiles_n;
     r.m0 = s_lo[g] + (local % mtiles) * kTileM;
     r.row_end = s_hi[g];
-    r.n0 = (local / mtiles) * BN;
-    r.b_row = g * p.N + r.n0;
+    r.n0 = (local / mtiles) * kTileN;
+    r.b_row = g * (kGlu ? 2 * p.N : p.N) + r.n0;
     r.g = g;
   }
   return r;
 }
 
-template <int kBScale, bool kOutF32, bool kAccum, bool kGrouped = false>
+// kGlu: B holds two stacked projections; a tile's 256 accumulator columns are
+// 64 gate, 64 up, 64 gate, 64 up columns, and the drain stores the gated
+// results (fp8q_glu.cuh).
+template <int kBScale, bool kOutF32, bool kAccum, bool kGrouped = false, bool kGlu = false>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8q_gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB, const MxArgs p) {
   // per-column B scales of a dense GEMM are prepared in warps 2-3
   constexpr bool kPrep = kBScale == FP8Q_BSCALE_ROW && !kGrouped;
+  static_assert(!kGlu || (kBScale == FP8Q_BSCALE_BLOCK && !kOutF32 && !kAccum && BN == 256),
+                "the gated form takes block scales and 256-column tiles");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -262,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->pready[i]), 2);
       mbar_init(smem_u32(&ctl->pfree[i]), 4);
     }
+    if (kGlu) glu_exchange_init(ctl->glu);
     ctl->abort_flag = 0;
     fence_barrier_init();
   }
@@ -319,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ss = 0;           // next scale stage slot to write
     uint32_t sphase = 0;  // its phase
     uint32_t tphase = 0;  // bit b: phase of tfull[b]
+    uint32_t glu_uses = 0;
     bool ok = true;
 
     // Scale production walks a cursor over (tile, stage) in the order the MMA
@@ -341,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int NB = (p.N + 127) / 128;
     auto load_raw = [&](int t, int js, float (&r)[kRaw]) {
       if (kPrep && !do_a) return;  // the B words come from warps 2-3
-      const MxTile tl = mx_tile_of<kGrouped>(t, p, s_lo, s_hi, s_pre);
+      const MxTile tl = mx_tile_of<kGrouped, kGlu>(t, p, s_lo, s_hi, s_pre);
       const int kb0 = js * kGroupsPerStage;
 #pragma unroll
       for (int i = 0; i < kRaw; ++i) r[i] = 1.0f;
@@ -367,13 +379,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // columns past N in a partial block read zero-filled B rows, so the
         // block's own scale is as good as any for them
-        const float *sbg = kGrouped ? p.sb + static_cast<int64_t>(tl.g) * NB * p.num_kb : p.sb;
+        const float *sbg =
+            kGrouped ? p.sb + static_cast<int64_t>(tl.g) * (kGlu ? 2 * NB : NB) * p.num_kb : p.sb;
 #pragma unroll
         for (int h = 0; h < BN / 128; ++h) {
-          const int nb = tl.n0 / 128 + h;
+          // gated form: the gate block and the up block of the same columns
+          const int nb = tl.n0 / 128 + (kGlu ? h * NB : h);
 #pragma unroll
           for (int j = 0; j < kGroupsPerStage; ++j)
-            if (kb0 + j < p.num_kb && nb < NB)
+            if (kb0 + j < p.num_kb && nb < (kGlu ? 2 * NB : NB))
               rb[4 * h + j] = kBScale == FP8Q_BSCALE_BLOCK
                                   ? __ldg(sbg + static_cast<int64_t>(nb) * p.ld_sb + kb0 + j)
                                   : __ldg(p.sb + static_cast<int64_t>(kb0 + j) * p.ld_sb + nb);
@@ -454,7 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             wb[h] = word;
           }
 #pragma unroll
-          for (int c = 0; c < 8; ++c) w[c] = c < kBCols32 ? wb[c / 4] : 0x7F7F7F7Fu;
+          for (int c = 0; c < 8; ++c)
+            w[c] = c < kBCols32 ? wb[kGlu ? (c / 2) & 1 : c / 4] : 0x7F7F7F7Fu;
         }
         tmem_st_32x32b_x8(tmem_base + lane_addr + col + kSfbOffset, w);
       }
@@ -486,12 +501,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kChunks = kEpiCols / 16;
       const uint32_t taddr = tmem_base + lane_addr +
                              static_cast<uint32_t>(buf_acc * BN + col_half * kEpiCols);
-      const MxTile tl = mx_tile_of<kGrouped>(t, p, s_lo, s_hi, s_pre);
-      const int ncol0 = tl.n0 + col_half * kEpiCols;
+      const MxTile tl = mx_tile_of<kGrouped, kGlu>(t, p, s_lo, s_hi, s_pre);
+      const int ncol0 = tl.n0 + col_half * (kGlu ? kEpiCols / 2 : kEpiCols);
       const int wrow0 = tl.m0 + row_in_tile - lane;
       const bool warp_ok = wrow0 < tl.row_end && ncol0 < p.N;  // warp-uniform
       const uint32_t buf = smem_u32(sC) + static_cast<uint32_t>(ew) * 2048u;
-      if (kOutF32 && kPrep) {
+      if constexpr (kGlu) {
+        // the whole row is read first and the accumulator released before any
+        // store: the next tile's MMAs run while this one is gated and stored
+        uint32_t v[kChunks][16];
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) tmem_ld_32x32b_x16(taddr + i * 16, v[i]);
+        tmem_wait_ld_tied(v[0]);
+#pragma unroll
+        for (int i = 1; i < kChunks; ++i) reg_tie(v[i]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty0 + static_cast<uint32_t>(buf_acc) * 8u);
+        uint64_t acc[64];
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          acc[i] = pack_u32x2(v[i / 8][2 * (i % 8)], v[i / 8][2 * (i % 8) + 1]);
+        return !warp_ok || glu_store(acc, p.glu, buf, wrow0, tl.row_end, ncol0, ew, lane, ctl->glu,
+                                     glu_uses, abort_flag, &g_mx_status, p.timeout_ns);
+      } else if (kOutF32 && kPrep) {
         // FP32 out, per-column scales: these warps hold no raw scales, so the
         // whole row of kEpiCols values is read first and the accumulator is
         // released before any store; stores go 64 bytes (16 columns) of each
@@ -613,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t armed = 0, armed_phase = 0;
       bool ok = true;
       for (int t = tile_first; ok && t < total_tiles; t += tile_step) {
-        const MxTile tl = mx_tile_of<kGrouped>(t, p, s_lo, s_hi, s_pre);
+        const MxTile tl = mx_tile_of<kGrouped, kGlu>(t, p, s_lo, s_hi, s_pre);
         for (int kb = 0; kb < p.num_kb; ++kb) {
           if (!mbar_wait_bounded(smem_u32(&ctl->empty[stage]), phase ^ 1, abort_flag,
                                  &g_mx_status, p.timeout_ns, FP8Q_ERR_TIMEOUT)) {
@@ -625,8 +658,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t fb0 = mapa_shared(fb, 0);
           tma_load_2d_pair(smem_u32(sA + stage * kABytes), &tmA, fb0, kb * BK,
                            tl.m0 + static_cast<int>(rank) * BM);
-          tma_load_2d_pair(smem_u32(sB + stage * kBBytes), &tmB, fb0, kb * BK,
-                           tl.b_row + static_cast<int>(rank) * (BN / 2));
+          if (kGlu) {
+            // 64 gate rows, then the up rows of the same 64 columns of h
+            const int brow = tl.b_row + static_cast<int>(rank) * (BN / 4);
+            tma_load_2d_pair(smem_u32(sB + stage * kBBytes), &tmB, fb0, kb * BK, brow);
+            tma_load_2d_pair(smem_u32(sB + stage * kBBytes + kBBytes / 2), &tmB, fb0, kb * BK,
+                             brow + p.N);
+          } else {
+            tma_load_2d_pair(smem_u32(sB + stage * kBBytes), &tmB, fb0, kb * BK,
+                             tl.b_row + static_cast<int>(rank) * (BN / 2));
+          }
           armed |= 1u << stage;
           armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
           if (++stage == kStages) {
@@ -651,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g = 0;
     bool ok = true;
     for (int t = tile_first; ok && t < total_tiles; t += tile_step) {
-      const MxTile tl = mx_tile_of<kGrouped>(t, p, s_lo, s_hi, s_pre);
+      const MxTile tl = mx_tile_of<kGrouped, kGlu>(t, p, s_lo, s_hi, s_pre);
       for (int js = 0; js < nst; ++js, ++g) {
         const int kb0 = js * kGroupsPerStage;
         const int slot = g % kPrepSlots;
@@ -763,10 +804,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ host
-template <int kBScale, bool kOutF32, bool kAccum, bool kGrouped = false>
+template <int kBScale, bool kOutF32, bool kAccum, bool kGrouped = false, bool kGlu = false>
 fp8q_status launch_mx(const CUtensorMap &ta, const CUtensorMap &tb, const MxArgs &args,
                       int64_t tiles, cudaStream_t s) {
-  auto kern = fp8q_gemm_mx_kernel<kBScale, kOutF32, kAccum, kGrouped>;
+  auto kern = fp8q_gemm_mx_kernel<kBScale, kOutF32, kAccum, kGrouped, kGlu>;
   constexpr size_t smem = kSmemBytes + (kGrouped ? kGroupTables : 0) +
                           (kBScale == FP8Q_BSCALE_ROW && !kGrouped ? kPrepBytes : 0);
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
@@ -885,6 +926,43 @@ fp8q_status mx_entry(const void *a, int64_t lda, const float *sa, int64_t ld_sa,
 }
 
 }  // namespace
+
+// Gated feed-forward block, power-of-two scales (arguments checked by the
+// caller; K > 0).
+fp8q_status gemm_mx_glu(const GluIn &in, const GluOut &out, cudaStream_t s) {
+  const bool grouped = in.offs != nullptr;
+  DeviceInfo dev;
+  if (fp8q_status st = device_info(dev)) return st;
+  if (dev.max_smem_optin < static_cast<int>(kSmemBytes + (grouped ? kGroupTables : 0)))
+    return FP8Q_ERR_UNSUPPORTED;
+  CUtensorMap ta, tb;
+  if (!make_tmap_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, in.a, in.M, in.K, in.lda, 128, BM,
+                    CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, in.b,
+                    static_cast<uint64_t>(in.G) * 2 * in.F, in.K, in.ldb, 128, BN / 4,
+                    CU_TENSOR_MAP_SWIZZLE_128B))
+    return FP8Q_ERR_CUDA;
+  MxArgs args{};
+  args.sa = in.sa;
+  args.ld_sa = in.ld_sa;
+  args.sb = in.sb;
+  args.ld_sb = in.ld_sb;
+  args.M = static_cast<int>(in.M);
+  args.N = static_cast<int>(in.F);
+  args.num_kb = static_cast<int>(in.K / 128);
+  args.tiles_m = static_cast<int>((in.M + kTileM - 1) / kTileM);
+  args.tiles_n = static_cast<int>(in.F / 128);
+  args.offs = in.offs;
+  args.G = in.G;
+  args.timeout_ns = wait_timeout_ns().load();
+  args.glu = out;
+  const int64_t tiles =
+      (static_cast<int64_t>(args.tiles_m) + (grouped ? in.G : 0)) * args.tiles_n;
+  if (tiles >= (1ll << 31)) return FP8Q_ERR_SHAPE;
+  return grouped
+             ? launch_mx<FP8Q_BSCALE_BLOCK, false, false, true, true>(ta, tb, args, tiles, s)
+             : launch_mx<FP8Q_BSCALE_BLOCK, false, false, false, true>(ta, tb, args, tiles, s);
+}
 
 fp8q_status mx_status_take(cudaStream_t s) {
   if (cudaStreamSynchronize(s) != cudaSuccess) return FP8Q_ERR_CUDA;

@@ -288,6 +288,118 @@ fp8q_status fp8q_grouped_gemm_pow2(const void *a, int64_t lda, const float *sa,
                                    int64_t N, int64_t K, void *stream);
 
 /*
+ * Gated feed-forward block (SwiGLU), both projections, the activation and the
+ * product in one kernel, from FP8 operands as fp8q_gemm takes them:
+ *   g = X Wg^T, u = X Wu^T (per-128-K-group scales, FP32 sums),
+ *   h = silu(g) * u,  silu(g) = g / (1 + exp(-g)), in FP32.
+ *   a   E4M3 [M][lda] codes of X, sa FP32 at sa[kb * ld_sa + m].
+ *   b   E4M3 [2F][ldb]: Wg in rows [0, F), Wu in rows [F, 2F), one matrix as
+ *       fp8q_quant_weight quantises it; sb FP32 [2F/128][ld_sb] (BLOCK layout).
+ * Results, each optional (NULL to skip), at least one required:
+ *   h   BF16 [M][ldh], rounded to nearest-even.
+ *   gu  BF16 [M][ld_gu]: g in columns [0, F), u in [F, 2F) -- what the
+ *       backward pass (fp8q_swiglu_bwd) reads.
+ *   q   E4M3 [M][ldq] with s FP32 at s[(f/128) * ld_s + m]: the 1x128
+ *       quantisation, by scale_mode, of the unrounded FP32 h -- the A operand
+ *       of the down projection's fp8q_gemm.
+ * M >= 0; F % 128 == 0, K % 128 == 0; K == 0 gives g = u = h = 0.
+ * Alignment: a, b, h, gu, q 16-byte aligned; lda, ldb, ldq % 16, ldh, ld_gu
+ * % 8 == 0.  The inputs' scales may come from either scale mode.
+ */
+fp8q_status fp8q_gemm_swiglu(const void *a, int64_t lda, const float *sa, int64_t ld_sa,
+                             const void *b, int64_t ldb, const float *sb, int64_t ld_sb,
+                             void *h, int64_t ldh, void *gu, int64_t ld_gu, void *q,
+                             int64_t ldq, float *s, int64_t ld_s, int scale_mode, int64_t M,
+                             int64_t F, int64_t K, void *stream);
+
+/*
+ * fp8q_gemm_swiglu for power-of-two input scales, on the block-scaled MMA: the
+ * same arguments and results, with fp8q_gemm_pow2's precondition on sa and sb.
+ */
+fp8q_status fp8q_gemm_swiglu_pow2(const void *a, int64_t lda, const float *sa, int64_t ld_sa,
+                                  const void *b, int64_t ldb, const float *sb, int64_t ld_sb,
+                                  void *h, int64_t ldh, void *gu, int64_t ld_gu, void *q,
+                                  int64_t ldq, float *s, int64_t ld_s, int scale_mode,
+                                  int64_t M, int64_t F, int64_t K, void *stream);
+
+/*
+ * fp8q_gemm_swiglu for MoE experts: rows [offs[g], offs[g+1]) of A meet expert
+ * g's two projections.
+ *   b     E4M3 [G][2F][ldb], sb FP32 [G][2F/128][K/128].
+ *   offs  int32 DEVICE array [G+1], as for fp8q_grouped_gemm: rows outside
+ *         [offs[0], offs[G]) are not written, in any of the results.
+ *   1 <= G <= 1024; other rules as fp8q_gemm_swiglu.
+ */
+fp8q_status fp8q_grouped_gemm_swiglu(const void *a, int64_t lda, const float *sa, int64_t ld_sa,
+                                     const void *b, int64_t ldb, const float *sb,
+                                     const int32_t *offs, int G, void *h, int64_t ldh, void *gu,
+                                     int64_t ld_gu, void *q, int64_t ldq, float *s, int64_t ld_s,
+                                     int scale_mode, int64_t M, int64_t F, int64_t K,
+                                     void *stream);
+
+/* fp8q_grouped_gemm_swiglu for power-of-two input scales (block-scaled MMA). */
+fp8q_status fp8q_grouped_gemm_swiglu_pow2(const void *a, int64_t lda, const float *sa,
+                                          int64_t ld_sa, const void *b, int64_t ldb,
+                                          const float *sb, const int32_t *offs, int G, void *h,
+                                          int64_t ldh, void *gu, int64_t ld_gu, void *q,
+                                          int64_t ldq, float *s, int64_t ld_s, int scale_mode,
+                                          int64_t M, int64_t F, int64_t K, void *stream);
+
+/*
+ * Backward pass of the gated product, down to the gradients d = [dg | du] of
+ * the two projections' outputs, in one pass over dh and the forward's gu:
+ *   du = dh * silu(g),  dg = dh * u * s * (1 + g * (1 - s)),  s = 1/(1+exp(-g)).
+ *   dh  BF16 [T][ld_dh], columns [0, F);  gu BF16 [T][ld_gu], columns [0, 2F).
+ * Results, each optional (NULL to skip), at least one required:
+ *   d   BF16 [T][ld_d], dg in columns [0, F), du in [F, 2F).
+ *   q   E4M3 [T][ldq], columns [0, 2F), s FP32 at s[(c/128) * ld_s + t]: the
+ *       1x128 quantisation of the unrounded FP32 d -- the A operand of
+ *       dX = d [Wg; Wu] (fp8q_gemm over K = 2F with the weight's qT, BLOCK_T).
+ *   qT  E4M3 [2F][ldqT], sT FP32 at sT[(t/128) * ld_sT + c]: the 128x1
+ *       quantisation of d, transposed -- the A operand of the two projections'
+ *       Wgrad.  T % 128 == 0.
+ *   hT  E4M3 [F][ld_hT], shT FP32 at shT[(t/128) * ld_shT + c]: the 128x1
+ *       quantisation of h = silu(g) * u (recomputed from gu, unrounded),
+ *       transposed -- the B operand of the down projection's Wgrad.
+ *       T % 128 == 0.
+ * F % 128 == 0, T <= 65535 * 128.  Alignment: all tensors 16-byte aligned;
+ * ld_dh, ld_gu, ld_d % 8, ldq, ldqT, ld_hT % 16 == 0.
+ */
+fp8q_status fp8q_swiglu_bwd(const void *dh, int64_t ld_dh, const void *gu, int64_t ld_gu,
+                            void *d, int64_t ld_d, void *q, int64_t ldq, float *s, int64_t ld_s,
+                            void *qT, int64_t ldqT, float *sT, int64_t ld_sT, void *hT,
+                            int64_t ld_hT, float *shT, int64_t ld_shT, int64_t T, int64_t F,
+                            int scale_mode, void *stream);
+
+/*
+ * Orthogonalised update of a weight gradient by Newton-Schulz steps, for a
+ * batch of matrices (gradients leave fp8q_gemm_accumulate as FP32 [m][n]):
+ *   X = G / (|G|_F + eps), oriented with the shorter side as its rows;
+ *   steps times:  A = X X^T,  B = b A + c A^2,  X = a X + B X;
+ *   out = X in G's orientation.
+ * Products take FP16 operands (X, A, B scaled by 2^8) with FP32 sums.
+ *   g    FP32 or BF16 (in_dtype: FP8Q_OUT_FP32 / FP8Q_OUT_BF16) [m][ldg],
+ *        matrix i at g + i * g_stride elements.
+ *   out  FP32 or BF16 (out_dtype) [m][ldo], matrix i at out + i * o_stride;
+ *        may not overlap g or the workspace.
+ *   steps >= 1, eps >= 0 (a zero matrix with eps > 0 gives zeros).
+ *   Limits: 0 <= m, n <= 2^20, batch <= 65535; the sum of G's squares must be
+ *   an FP32 value, and |a|, |b|, |c| such that the entries of X, A and B stay
+ *   below 255 (FP16 after scaling; the usual coefficients keep them below 12).
+ *   workspace  device scratch of at least
+ *              fp8q_newton_schulz_workspace_bytes(batch, m, n) bytes, 256-byte
+ *              aligned, owned by the caller; contents on entry do not matter.
+ * g and out need only their element's alignment, at any pitch >= n.
+ * workspace_bytes returns 0 for sizes outside the limits.
+ */
+int64_t fp8q_newton_schulz_workspace_bytes(int64_t batch, int64_t m, int64_t n);
+fp8q_status fp8q_newton_schulz(const void *g, int64_t ldg, int64_t g_stride, int in_dtype,
+                               void *out, int64_t ldo, int64_t o_stride, int out_dtype,
+                               int64_t batch, int64_t m, int64_t n, int steps, float a, float b,
+                               float c, float eps, void *workspace, int64_t workspace_bytes,
+                               void *stream);
+
+/*
  * Plain FP32 -> E4M3 conversion of n values (round to nearest-even, saturate
  * to +-448, NaN -> 0x7F), with no scaling.  The quantisers use the same
  * conversion; this entry exposes it so it can be checked on every FP32 bit
