@@ -95,6 +95,8 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     check_gemm_registers(results["gemm.cu"][1], launch_regs_of(os.path.join(CSRC, "gemm.cu")))
     check_gemm_registers(results["gemm_mx.cu"][1], launch_regs_of(os.path.join(CSRC, "gemm_mx.cu")),
                          "fp8q_gemm_mx_kernel")
+    check_gemm_registers(results["newton_schulz.cu"][1],
+                         launch_regs_of(os.path.join(CSRC, "newton_schulz.cu")), "ns_steps_kernel")
     if verbose:
         for src, (_, log) in results.items():
             print(f"== {src}\n{log}")

@@ -54,13 +54,33 @@ fp8q_status ns_status_take(cudaStream_t s) {
 namespace {
 
 constexpr float kS = 256.0f;        // scale of the stored FP16 matrices
-constexpr int kMaxParts = 256;      // partial sums of squares per matrix
+constexpr int kMaxParts = 304;      // partial sums of squares per matrix
 
 // ------------------------------------------------------------------ set-up
 __device__ __forceinline__ float load_in(const float *p) { return __ldg(p); }
 __device__ __forceinline__ float load_in(const uint16_t *p) {
   return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
 }
+// 16 bytes of input (4 FP32 or 8 BF16 values), kept in the cache: the matrix is
+// read a second time by the next kernel.
+__device__ __forceinline__ void load_vec(const float *p, float (&v)[4]) {
+  const float4 f = __ldg(reinterpret_cast<const float4 *>(p));
+  v[0] = f.x;
+  v[1] = f.y;
+  v[2] = f.z;
+  v[3] = f.w;
+}
+__device__ __forceinline__ void load_vec(const uint16_t *p, float (&v)[8]) {
+  const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_lo(w[i]);
+    v[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+template <typename In>
+constexpr int kVecOf = 16 / static_cast<int>(sizeof(In));
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -68,140 +88,270 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum of squares of matrix blockIdx.y, part blockIdx.x of gridDim.x: rows
-// blockIdx.x, blockIdx.x + gridDim.x, ...  Fixed order, so repeated calls agree.
-template <typename In>
+// Sum of squares of matrix blockIdx.y, part blockIdx.x of gridDim.x; a warp
+// takes whole rows.  kVec: rows begin on 16-byte boundaries.  The order is
+// fixed, so repeated calls agree.  Also zeroes the counters that the steps
+// kernel of this call uses.
+template <typename In, bool kVec>
 __global__ void __launch_bounds__(256) ns_sumsq_kernel(const In *__restrict__ g, int64_t ldg,
                                                        int64_t batch_stride, int64_t m, int64_t n,
-                                                       float *__restrict__ part) {
+                                                       float *__restrict__ part,
+                                                       uint32_t *__restrict__ counters,
+                                                       int n_counters) {
+  constexpr int V = kVec ? kVecOf<In> : 1;
   __shared__ float sums[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < n_counters; i += 256) counters[i] = 0u;
   const In *base = g + blockIdx.y * batch_stride;
-  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t r = blockIdx.x; r < m; r += gridDim.x) {
+  float acc = 0.0f;
+  for (int64_t r = blockIdx.x * 8 + warp; r < m; r += 8 * gridDim.x) {
     const In *row = base + r * ldg;
-    int64_t c = threadIdx.x;
-    for (; c + 768 < n; c += 1024)
+    const int64_t whole = n / V * V;
+    int64_t c = lane * V;
+    if constexpr (kVec) {
+      for (; c + 7 * 32 * V < whole; c += 8 * 32 * V) {  // eight loads in flight
+        float v[8][V];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float v = load_in(row + c + 256 * i);
-        acc[i] = fmaf(v, v, acc[i]);
+        for (int i = 0; i < 8; ++i) load_vec(row + c + i * 32 * V, v[i]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int j = 0; j < V; ++j) acc = fmaf(v[i][j], v[i][j], acc);
       }
-    for (; c < n; c += 256) {
+      for (; c < whole; c += 32 * V) {
+        float v[V];
+        load_vec(row + c, v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc = fmaf(v[j], v[j], acc);
+      }
+      c = whole + lane;
+    }
+    for (; c < n; c += 32) {
       const float v = load_in(row + c);
-      acc[0] = fmaf(v, v, acc[0]);
+      acc = fmaf(v, v, acc);
     }
   }
-  const float s = warp_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
+  acc = warp_sum(acc);
+  if (lane == 0) sums[warp] = acc;
   __syncthreads();
   if (threadIdx.x < 32) {
-    const float t = warp_sum(threadIdx.x < 8 ? sums[threadIdx.x] : 0.0f);
-    if (threadIdx.x == 0) part[blockIdx.y * kMaxParts + blockIdx.x] = t;
+    const float t = warp_sum(lane < 8 ? sums[lane] : 0.0f);
+    if (lane == 0) part[blockIdx.y * kMaxParts + blockIdx.x] = t;
   }
 }
 
-// X^ = FP16(S g / (|g|_F + eps)), transposed when kTall.  One 64 x 64 tile of g
-// per block (256 threads).
-template <typename In, bool kTall>
+// S / (|g|_F + eps) of matrix blockIdx.z from its partial sums, to every thread.
+__device__ __forceinline__ float ns_scale(const float *part, int parts, float eps, float *shared) {
+  if (threadIdx.x < 32) {
+    float v = 0.0f;
+    for (int i = threadIdx.x; i < parts; i += 32) v += part[blockIdx.z * kMaxParts + i];
+    v = warp_sum(v);
+    if (threadIdx.x == 0) *shared = kS / (sqrtf(v) + eps);
+  }
+  __syncthreads();
+  return *shared;
+}
+
+__device__ __forceinline__ uint4 pack_half8(const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// X^ = FP16(S g / (|g|_F + eps)), g no taller than wide: blocks of 32 rows x
+// 256 columns, eight columns of four rows per thread.  The pitch ldx is a
+// multiple of 8, so every 16-byte unit that begins inside the row is whole.
+template <typename In, bool kVec>
 __global__ void __launch_bounds__(256) ns_load_kernel(const In *__restrict__ g, int64_t ldg,
                                                       int64_t batch_stride, int64_t m, int64_t n,
                                                       const float *__restrict__ part, int parts,
                                                       float eps, __half *__restrict__ x,
                                                       int64_t ldx) {
+  constexpr int V = kVecOf<In>;
   __shared__ float s_scale;
-  __shared__ float tile[kTall ? 64 : 1][65];
-  const int tid = threadIdx.x;
-  if (tid < 32) {
-    float v = 0.0f;
-    for (int i = tid; i < parts; i += 32) v += part[blockIdx.z * kMaxParts + i];
-    v = warp_sum(v);
-    if (tid == 0) s_scale = kS / (sqrtf(v) + eps);
+  const In *base = g + blockIdx.z * batch_stride;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + 8 * (threadIdx.x & 31);
+  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 32 + (threadIdx.x >> 5);
+  float v[4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = r0 + 8 * i;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    if (r >= m || c >= n) continue;
+    const In *src = base + r * ldg + c;
+    if (kVec && c + 8 <= n) {
+#pragma unroll
+      for (int j = 0; j < 8; j += V) {
+        float t[V];
+        load_vec(src + j, t);
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[i][j + k] = t[k];
+      }
+    } else {
+      for (int j = 0; j < 8; ++j)
+        if (c + j < n) v[i][j] = load_in(src + j);
+    }
   }
-  __syncthreads();
-  const float scale = s_scale;
+  const float scale = ns_scale(part, parts, eps, &s_scale);
+  __half *dst = x + blockIdx.z * (m * ldx);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = r0 + 8 * i;
+    if (r >= m || c >= n) continue;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] *= scale;
+    *reinterpret_cast<uint4 *>(dst + r * ldx + c) = pack_half8(v[i]);
+  }
+}
+
+// The same, transposed (g taller than wide): 64 x 64 blocks through shared memory.
+template <typename In, bool kVec>
+__global__ void __launch_bounds__(256) ns_load_tall_kernel(const In *__restrict__ g, int64_t ldg,
+                                                           int64_t batch_stride, int64_t m,
+                                                           int64_t n,
+                                                           const float *__restrict__ part,
+                                                           int parts, float eps,
+                                                           __half *__restrict__ x, int64_t ldx) {
+  constexpr int V = kVecOf<In>;
+  constexpr int kLanes = 64 / V;         // threads across a block row
+  constexpr int kRows = 256 / kLanes;    // rows per pass
+  __shared__ float s_scale;
+  __shared__ float tile[64][65];
   const In *base = g + blockIdx.z * batch_stride;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 64, c0 = static_cast<int64_t>(blockIdx.x) * 64;
-  if (!kTall) {
-    __half *dst = x + blockIdx.z * (m * ldx);
-    const int64_t c = c0 + 2 * (tid & 31);
-    for (int i = tid >> 5; i < 64; i += 8) {
-      const int64_t r = r0 + i;
-      if (r >= m || c >= n) continue;
-      const float v0 = load_in(base + r * ldg + c);
-      const float v1 = c + 1 < n ? load_in(base + r * ldg + c + 1) : 0.0f;
-      // ldx is a multiple of 8 and c is even: the pair stays inside the row's pitch
-      *reinterpret_cast<__half2 *>(dst + r * ldx + c) = __floats2half2_rn(v0 * scale, v1 * scale);
+  const int tid = threadIdx.x, j0 = V * (tid % kLanes);
+#pragma unroll
+  for (int i = 0; i < 64 / kRows; ++i) {
+    const int rr = i * kRows + tid / kLanes;
+    const int64_t r = r0 + rr, c = c0 + j0;
+    float v[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = 0.0f;
+    if (r < m && c < n) {
+      const In *src = base + r * ldg + c;
+      if (kVec && c + V <= n) {
+        load_vec(src, v);
+      } else {
+        for (int k = 0; k < V; ++k)
+          if (c + k < n) v[k] = load_in(src + k);
+      }
     }
-  } else {
-    for (int i = tid; i < 64 * 64; i += 256) {
-      const int64_t r = r0 + (i >> 6), c = c0 + (i & 63);
-      tile[i >> 6][i & 63] = r < m && c < n ? load_in(base + r * ldg + c) * scale : 0.0f;
-    }
-    __syncthreads();
-    __half *dst = x + blockIdx.z * (n * ldx);
-    const int j = 2 * (tid & 31);
-    const int64_t r = r0 + j;
-    for (int i = tid >> 5; i < 64; i += 8) {
-      const int64_t c = c0 + i;
-      if (c >= n || r >= m) continue;
-      *reinterpret_cast<__half2 *>(dst + c * ldx + r) = __floats2half2_rn(tile[j][i], tile[j + 1][i]);
-    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) tile[rr][j0 + k] = v[k];
+  }
+  const float scale = ns_scale(part, parts, eps, &s_scale);  // also: the block is complete
+  __half *dst = x + blockIdx.z * (n * ldx);
+  const int j = 8 * (tid & 7);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int cc = 32 * i + (tid >> 3);
+    if (c0 + cc >= n || r0 + j >= m) continue;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = tile[j + k][cc] * scale;
+    *reinterpret_cast<uint4 *>(dst + (c0 + cc) * ldx + r0 + j) = pack_half8(v);
   }
 }
 
 // ------------------------------------------------------------------ products
-// D = L R^T (A, A^2) or L R (the update) on CTA pairs: a 256 x BN tile per pair
-// (tcgen05.mma.cta_group::2, M = 256, K = 16), each CTA staging its 128 rows of
-// L and half of R's columns per 64-wide K block (128-byte rows, 128-byte
-// swizzle).  R is K-major where it is a row block of X or A, and N-major (64
-// columns x 64 K rows per box, as X is stored) in the update, so no transposed
-// copy of X exists.  Two TMEM accumulators: the epilogue of one tile runs under
-// the MMAs of the next.
-//   warp 0 TMA producer, warp 1 MMA issuer (leading CTA), warps 4-11 epilogue
-//   (each thread one row, BN / 2 columns).
-enum class Op { kGram, kPoly, kUpdate };  // A = X X^T | B = bA + cA^2 | X' = aX + BX
+// One persistent kernel runs every step: 3 * steps phases on CTA pairs
+// (tcgen05.mma.cta_group::2, tiles of 256 rows x 256, 128 or 64 columns, K = 16
+// per instruction), one pair per two SMs.  Against one launch per product this saves the launch, the
+// set-up and the pipeline's first fill, which took longer than the products
+// themselves for all but the largest matrices (a 301 x 999 update: 9 us per
+// launch).
+//  - A matrix moves on to its next phase when its own tiles of the last one are
+//    done (a counter per matrix), so the matrices of a batch do not wait for
+//    one another.
+//  - Tiles are dealt out to the pairs in turn, so that a pair's tiles of a phase
+//    belong to different matrices of a batch and the first of them are ready
+//    when it comes to the next phase.  Where whole tiles would leave pairs idle
+//    for long, pair i takes units [i per, (i + 1) per) of (tile, 64-wide K block)
+//    instead, an even share that splits tiles.  A pair whose range begins inside a tile
+//    writes its FP32 partial sums to its slot of the workspace; the pair that
+//    began the tile, which reaches it last in its own range, adds the partials
+//    of the pairs after it in order.  The order is fixed, so results repeat bit
+//    by bit.
+//  - D = L R^T: both operands are row blocks of X or A, K-major.  The update
+//    D = L R reads X as an N-major operand (64 columns x 64 K rows per box), so
+//    no transposed copy of X exists.
+//  - Two TMEM accumulators: the epilogue of one tile runs under the MMAs of the
+//    next.  A warp's old values of X or A are fetched and put into shared
+//    memory before it waits for the accumulator, the results replace them
+//    there, and global accesses are whole 64-byte pieces of rows.
+//  - Data written by other SMs in an earlier phase is read past L1 (ld.cg), and
+//    by TMA after a proxy fence on both sides of the counter.
+//  - The tile width is chosen per phase kind (see Plan): 256 columns feed the
+//    tensor cores best (62 bytes of operands per clock and SM), narrower tiles
+//    cover the matrix with less waste and finish sooner where there are few.
+//   warp 0 TMA producer, warp 1 MMA issuer (leading CTA), warp 2 counts done
+//   tiles, warps 4-11 epilogue (each thread one row, half of the tile's columns).
+constexpr int kGram = 0, kPoly = 1, kUpdate = 2;  // A = X X^T | B = bA + cA^2 | X' = aX + BX
 
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
+constexpr int kTile = 256;               // rows of a pair's tile, and its largest width
+constexpr int kStages = 5;
+constexpr uint32_t kOpBytes = 128 * 128;  // one operand's share of a CTA: 128 x 64 FP16
+constexpr int kMaxPairs = 76;            // slots for partial sums
+// Register split as in the GEMMs: built for kLaunchRegs (checked by the build),
+// the control warpgroup hands registers to the two epilogue warpgroups.
+constexpr int kLaunchRegs = 168;
+constexpr int kCtlRegs = 56, kEpiRegs = 224;
+static_assert(kCtlRegs + 2 * kEpiRegs <= 3 * kLaunchRegs, "register split must fit the launch");
 constexpr uint64_t kDrainNs = 1000000000ull;
-constexpr uint32_t kLBytes = 128 * 128;  // L: 128 rows x 64 FP16
-
-template <int BN>
-struct Cfg {
-  static constexpr int kStages = BN == 256 ? 5 : 7;
-  static constexpr uint32_t kRBytes = (BN / 2) * 128;  // R: half of the columns
-  static constexpr uint32_t kTx = 2 * (kLBytes + kRBytes);
-  static constexpr size_t kRing = static_cast<size_t>(kStages) * (kLBytes + kRBytes);
-};
+// Staging of one epilogue warp: its 32 rows x 128 columns as FP16, in blocks of
+// 32 columns (2 KB each; also a padded FP32 block of the final result).
+constexpr uint32_t kStageBlock = 2048, kStageWarp = 4 * kStageBlock;
+static_assert(4 * kStageBlock >= 32 * 33 * 4, "a padded FP32 block fits");
+constexpr int64_t kSlotFloats = 2 * 128 * 256;
 
 struct alignas(8) Ctl {
-  uint64_t full[8], empty[8], tfull[2], tempty[2], drain;
+  uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+  uint64_t stored[4];  // a tile's results are written, by tile number mod 4
   uint32_t tmem_base;
   int abort_flag;
 };
-constexpr uint32_t kStageWarp = 32 * 33 * 4;  // staging of one epilogue warp
+constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * 2 * kOpBytes +
+                         kEpiWarps * kStageWarp + sizeof(Ctl);
+static_assert(kSmem <= 227 * 1024, "shared memory");
 
-template <int BN>
-constexpr size_t smem_of() {
-  return 1024 + Cfg<BN>::kRing + kEpiWarps * kStageWarp + sizeof(Ctl);
-}
-static_assert(smem_of<256>() <= 227 * 1024 && smem_of<128>() <= 227 * 1024, "shared memory");
+// Counters in the workspace, zeroed by the set-up kernel of each call; after
+// them, per matrix, the number of its tiles done in all phases (two CTAs each).
+struct Sync {
+  uint32_t part[kMaxPairs][2][kEpiWarps];  // phase + 1 of the partial sums in the slot
+  uint32_t used[kMaxPairs][2][kEpiWarps];  // phase + 1 of the partial sums that were added
+};
 
 struct NsArgs {
-  int batch, rows, cols, kblocks;  // D is [rows][cols] per matrix
-  int tiles_m, tiles_n, tiles;     // tiles: per matrix
-  float c_old, c_acc;              // D = c_old * old + c_acc * (sum + diagonal terms)
-  float c_diag;                    // update: weight of d_B
-  const __half *old;               // A^ or X^ (not read for the Gram matrix)
-  const float *diag;               // S d_A or S d_B of the matrix read, pitch ldd
-  float *diag_out;                 // symmetric results: their diagonal
-  int64_t ldd;
-  __half *dst;                     // FP16 result, or null
-  int64_t ld;                      // pitch of old and dst
-  void *out;                       // final result (update only), or null
+  int batch, p, q, steps;
+  int kb_q, kb_p;          // 64-wide K blocks along q and p
+  int row_tiles;           // 256-row tiles along p
+  int bn[3], tiles[3];     // by phase kind: tile width, tiles per matrix,
+  int per[3];              // units per pair of an even split, or 0: whole tiles
+  float a, b, c;
+  __half *x[2], *am, *bm;
+  int64_t ldx, lda;
+  float *da, *db;        // S d_A, S d_B, pitch lda
+  float *partial;        // [pair][CTA][warp][float4 column][lane]
+  Sync *sync;
+  uint32_t *done;
+  void *out;
   int64_t ldo, out_stride;
-  int out_f32, tall;
+  int out_f32, tall, out_vec;  // out_vec: 16-byte units of BF16 rows may be stored
   uint64_t timeout_ns;
+};
+
+struct Maps {
+  CUtensorMap x[2], a, b;  // left operands: 128 rows x 64
+  CUtensorMap xr[2], ar;   // right operands of A and A^2: half a tile's columns x 64
+  CUtensorMap xn[2];       // right operand of the update: 64 K rows x 64 columns
 };
 
 __device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
@@ -240,54 +390,227 @@ __device__ __forceinline__ void mbar_wait_drain(uint32_t bar, uint32_t parity) {
   while (!mbar_try_wait(bar, parity))
     if (global_timer_ns() - t0 > kDrainNs) return;
 }
-
-struct NsTile {
-  int b, row0, col0;  // matrix, first row (of the pair), first column
-};
-// Symmetric products: row block i (256 rows) has column blocks from its own
-// diagonal on (col >= 256 i).
-template <int BN, bool kSym>
-__device__ __forceinline__ NsTile tile_of(int t, const NsArgs &p) {
-  NsTile r;
-  r.b = t / p.tiles;
-  int w = t - r.b * p.tiles;
-  if (kSym) {
-    constexpr int kPer = 256 / BN;  // column blocks per row block
-    int i = 0;
-    while (w >= p.tiles_n - kPer * i) {
-      w -= p.tiles_n - kPer * i;
-      ++i;
-    }
-    r.row0 = i * 256;
-    r.col0 = (kPer * i + w) * BN;
-  } else {
-    r.row0 = (w % p.tiles_m) * 256;
-    r.col0 = (w / p.tiles_m) * BN;
-  }
-  return r;
+// Order generic-proxy and async-proxy (TMA) accesses of global memory.
+__device__ __forceinline__ void fence_proxy_async_all() {
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t *p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_release(uint32_t *p, uint32_t v) {
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ void red_release(uint32_t *p) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p) : "memory");
 }
 
-template <int BN, Op kOp>
+// Bounded wait until *p has reached `want` (counters only grow within a call).
+__device__ __forceinline__ bool wait_count(const uint32_t *p, uint32_t want,
+                                           volatile int *abort_flag, uint64_t limit_ns) {
+  if (ld_acquire(p) >= want) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (ld_acquire(p) >= want) return true;
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > limit_ns) {
+      *abort_flag = 1;
+      atomicExch(&g_ns_status, FP8Q_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
+// One pair's walk over its units of a phase, as segments of tiles.
+struct Segment {
+  int b, row0, col0;  // matrix, first row and column of the tile
+  int kb0, kb1;       // its K blocks
+};
+struct Walk {
+  int kind, kblocks, u, end, stride;  // units; stride: to the pair's next whole tile
+  uint32_t ready;  // a matrix's count of done tiles that lets it into this phase
+  __device__ Walk(const NsArgs &p, int phase, int pair) {
+    kind = phase % 3;
+    kblocks = kind == kGram ? p.kb_q : p.kb_p;
+    const int units = p.tiles[kind] * p.batch * kblocks;
+    int before = phase / 3 * (p.tiles[0] + p.tiles[1] + p.tiles[2]);
+    if (kind > 0) before += p.tiles[0];
+    if (kind > 1) before += p.tiles[1];
+    ready = 2u * static_cast<uint32_t>(before);
+    if (p.per[kind] > 0) {
+      u = min(pair * p.per[kind], units);
+      end = min(u + p.per[kind], units);
+      stride = 0;
+    } else {
+      u = pair < p.tiles[kind] * p.batch ? pair * kblocks : units;
+      end = units;
+      stride = static_cast<int>(gridDim.x >> 1) * kblocks;
+    }
+  }
+  __device__ bool next(const NsArgs &p, Segment &s) {
+    if (u >= end) return false;
+    const int t = u / kblocks;
+    s.kb0 = u - t * kblocks;
+    s.kb1 = min(kblocks, s.kb0 + (end - u));
+    u = stride == 0 ? u + (s.kb1 - s.kb0) : end - u > stride ? u + stride : end;
+    s.b = t / p.tiles[kind];
+    int w = t - s.b * p.tiles[kind];
+    const int bn = p.bn[kind];
+    if (kind == kUpdate) {
+      s.row0 = (w % p.row_tiles) * kTile;
+      s.col0 = (w / p.row_tiles) * bn;
+    } else {  // row tile i has the columns from its own first row on
+      const int per_row = kTile / bn, n = (p.p + bn - 1) / bn;
+      int i = 0;
+      while (w >= n - per_row * i) w -= n - per_row * i++;
+      s.row0 = i * kTile;
+      s.col0 = (per_row * i + w) * bn;
+    }
+    return true;
+  }
+};
+
+// What an epilogue warp knows of its own place.
+struct Epi {
+  uint32_t stage;   // its staging: four blocks of 32 x 32
+  int row0, lane;   // its first row
+};
+// 16-byte unit k of row r in a staged block (conflict-free by row and by piece).
+__device__ __forceinline__ uint32_t unit_at(uint32_t block, uint32_t r, uint32_t k) {
+  return block + r * 64 + 16 * (k ^ ((r >> 1) & 3));
+}
+
+// A warp's old values, 32 rows x 128 columns: lane l fetches 16-byte unit l % 4
+// of rows l / 4 + 8 i of each 32-column block.  Pitches are multiples of 8, so a
+// unit that begins inside the matrix may be read to its end.
+__device__ __forceinline__ void stage_old(const Epi &e, const __half *m, int64_t ld, int rows,
+                                          int cols, int cbase, int blocks) {
+  uint4 v[4][4];
+  const int r0 = e.row0 + (e.lane >> 2);
+  const __half *src = m + static_cast<int64_t>(r0) * ld + cbase + 8 * (e.lane & 3);
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[c][i] = make_uint4(0, 0, 0, 0);
+      if (c < blocks && r0 + 8 * i < rows && cbase + 32 * c + 8 * (e.lane & 3) < cols)
+        v[c][i] = __ldcg(reinterpret_cast<const uint4 *>(src + 8 * i * ld + 32 * c));
+    }
+  __syncwarp();  // the blocks' previous contents have been read
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c < blocks) st_shared_v4(unit_at(e.stage + c * kStageBlock, (e.lane >> 2) + 8 * i, e.lane & 3), v[c][i]);
+  __syncwarp();
+}
+// This lane's row of a staged block, FP16 pairs.
+__device__ __forceinline__ void read_row(const Epi &e, int c, uint32_t (&w)[16]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint4 u = ld_shared_v4(unit_at(e.stage + c * kStageBlock, e.lane, k));
+    w[4 * k] = u.x;
+    w[4 * k + 1] = u.y;
+    w[4 * k + 2] = u.z;
+    w[4 * k + 3] = u.w;
+  }
+}
+__device__ __forceinline__ void write_row(const Epi &e, int c, const uint32_t (&w)[16]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    st_shared_v4(unit_at(e.stage + c * kStageBlock, e.lane, k),
+                 make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
+}
+// The staged 16-bit results to rows of m, 64-byte pieces; the last partial unit
+// of a row element by element.
+__device__ __forceinline__ void store_staged(const Epi &e, uint16_t *m, int64_t ld, int rows,
+                                             int cols, int cbase, int blocks) {
+  __syncwarp();
+  const int r0 = e.row0 + (e.lane >> 2);
+  uint16_t *dst = m + static_cast<int64_t>(r0) * ld + cbase + 8 * (e.lane & 3);
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int left = cols - (cbase + 32 * c + 8 * (e.lane & 3));
+      if (c >= blocks || r0 + 8 * i >= rows || left <= 0) continue;
+      const uint4 u =
+          ld_shared_v4(unit_at(e.stage + c * kStageBlock, (e.lane >> 2) + 8 * i, e.lane & 3));
+      uint16_t *at = dst + 8 * i * ld + 32 * c;
+      if (left >= 8) {
+        *reinterpret_cast<uint4 *>(at) = u;
+      } else {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int k = 0; k < 7; ++k)
+          if (k < left) at[k] = static_cast<uint16_t>(k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xFFFFu);
+      }
+    }
+}
+// A lane's row of a block, transposed: column runs are contiguous over the lanes.
+__device__ __forceinline__ void store_mirror(const Epi &e, const uint32_t (&w)[16], __half *m,
+                                             int64_t ld, int n, int col0) {
+  const int row = e.row0 + e.lane;
+  if (row >= n) return;
+  uint16_t *dst = reinterpret_cast<uint16_t *>(m) + static_cast<int64_t>(col0) * ld + row;
+  const int left = n - col0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    if (i < left) *dst = static_cast<uint16_t>(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
+    dst += ld;
+  }
+}
+
+// A 32 x 32 block of the final result into the caller's matrix, any pitch: column
+// runs (tall) are contiguous over the lanes; row runs go through shared memory.
+__device__ __forceinline__ void store_out(const Epi &e, const float (&v)[32], const NsArgs &p, int b,
+                                          int col0, float *st) {
+  const int64_t base = static_cast<int64_t>(b) * p.out_stride;
+  const int row = e.row0 + e.lane;
+  if (p.tall) {
+    if (row < p.p) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (col0 + i < p.q) {
+          const int64_t at = base + static_cast<int64_t>(col0 + i) * p.ldo + row;
+          if (p.out_f32) static_cast<float *>(p.out)[at] = v[i];
+          else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(v[i]);
+        }
+    }
+    return;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) st[e.lane * 33 + i] = v[i];
+  __syncwarp();
+  if (col0 + e.lane < p.q) {
+    const int n = min(32, p.p - e.row0);
+    for (int i = 0; i < n; ++i) {
+      const int64_t at = base + static_cast<int64_t>(e.row0 + i) * p.ldo + col0 + e.lane;
+      const float f = st[i * 33 + e.lane];
+      if (p.out_f32) static_cast<float *>(p.out)[at] = f;
+      else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(f);
+    }
+  }
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    ns_gemm_kernel(const __grid_constant__ CUtensorMap tmL, const __grid_constant__ CUtensorMap tmR,
-                   const NsArgs p) {
-  using C = Cfg<BN>;
-  constexpr bool kSym = kOp != Op::kUpdate;
-  constexpr uint32_t kTmem = 2 * BN;
+    ns_steps_kernel(const __grid_constant__ Maps maps, const NsArgs p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const uint32_t sL = smem_u32(smem), sR = sL + C::kStages * kLBytes;
-  float *stage = reinterpret_cast<float *>(smem + C::kRing);
-  Ctl *ctl = reinterpret_cast<Ctl *>(smem + C::kRing + kEpiWarps * kStageWarp);
+  const uint32_t sL = smem_u32(smem), sR = sL + kStages * kOpBytes;
+  uint8_t *staging = smem + static_cast<size_t>(kStages) * 2 * kOpBytes;
+  Ctl *ctl = reinterpret_cast<Ctl *>(staging + kEpiWarps * kStageWarp);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int *abort_flag = &ctl->abort_flag;
   const uint32_t rank = cluster_ctarank();
-  const int first = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
-  const int total = p.tiles * p.batch;
+  const int pair = static_cast<int>(blockIdx.x >> 1);
+  const int phases = 3 * p.steps;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&ctl->full[i]), 1);
       mbar_init(smem_u32(&ctl->empty[i]), 1);
     }
@@ -297,14 +620,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&ctl->drain), 1);
     ctl->abort_flag = 0;
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&ctl->stored[i]), kEpiWarps);
     fence_barrier_init();
   }
-  if (warp == 0 && lane == 0) {
-    prefetch_tmap(&tmL);
-    prefetch_tmap(&tmR);
-  }
+  if (warp == 0 && lane < static_cast<int>(sizeof(Maps) / sizeof(CUtensorMap)))
+    prefetch_tmap(&maps.x[0] + lane);
   if (warp == 1) {
-    tmem_alloc_pair(smem_u32(&ctl->tmem_base), kTmem);
+    tmem_alloc_pair(smem_u32(&ctl->tmem_base), 512);
     tc_fence_before();
   }
   __syncwarp();
@@ -313,187 +635,287 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = ctl->tmem_base;
 
   if (warp >= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     // ================================================== epilogue
     const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
     const uint32_t tempty0 = mapa_shared(smem_u32(&ctl->tempty[0]), 0);
-    float *st = stage + ew * (kStageWarp / 4);
-    int buf = 0;
-    uint32_t phase = 0;
-    for (int t = first; t < total; t += step) {
-      const NsTile tl = tile_of<BN, kSym>(t, p);
-      const bool got = mbar_wait_bounded(smem_u32(&ctl->tfull[buf]), phase, abort_flag,
-                                         &g_ns_status, p.timeout_ns, FP8Q_ERR_TIMEOUT);
-      if (!__all_sync(0xffffffffu, got)) break;
-      tc_fence_after();
-      const int row0 = tl.row0 + static_cast<int>(rank) * 128 + quarter * 32;  // the warp's rows
-      const int row = row0 + lane;
-      const int cbase = tl.col0 + half * (BN / 2);
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                             static_cast<uint32_t>(buf * BN + half * (BN / 2));
-      const int64_t mat = static_cast<int64_t>(tl.b) * p.rows * p.ld;
-      // tiles of the diagonal block hold both triangles themselves
-      const bool mirror = kSym && tl.col0 >= tl.row0 + 256;
-      const float *diag = p.diag + static_cast<int64_t>(tl.b) * p.ldd;
-      const float d_row = kOp != Op::kGram && row < p.rows ? diag[row] : 0.0f;
-      const float c_old = kOp == Op::kUpdate ? fmaf(p.c_diag, d_row, p.c_old) : p.c_old;
-#pragma unroll 1
-      for (int c = 0; c < BN / 2; c += 32) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(taddr + c, r);
-        const int col0 = cbase + c;
-        const bool live = row0 < p.rows && col0 < p.cols;  // warp-uniform
-        float old[32];
-        const bool whole = col0 + 32 <= p.cols;
-        if (kOp != Op::kGram && live) {
-          const __half *src = p.old + mat + static_cast<int64_t>(row) * p.ld + col0;
-          // the pitch is a multiple of 8, so an 8-column unit that begins
-          // inside the matrix is readable to its end
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (row < p.rows && col0 + 8 * k < p.cols) v = *reinterpret_cast<const uint4 *>(src + 8 * k);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              old[8 * k + 2 * e] = f16_lo(w[e]);
-              old[8 * k + 2 * e + 1] = f16_hi(w[e]);
-            }
+    Epi e;
+    float *st = reinterpret_cast<float *>(staging + ew * kStageWarp);
+    e.stage = smem_u32(st);
+    e.lane = lane;
+    // this warp's part of a pair's slot of partial sums, as float4
+    auto slot_of = [&](int pr) {
+      return reinterpret_cast<float4 *>(p.partial + pr * kSlotFloats) +
+             (static_cast<int>(rank) * kEpiWarps + ew) * 32 * 32 + lane;
+    };
+    // lane 0 waits for a counter; the answer goes to the whole warp
+    auto warp_wait = [&](const uint32_t *count, uint32_t want) {
+      const bool got = lane != 0 || wait_count(count, want, abort_flag, p.timeout_ns);
+      return __all_sync(0xffffffffu, got) != 0;
+    };
+    int buf = 0, tile_no = 0;
+    uint32_t tphase = 0, given = 0;  // given: phase + 1 of this warp's last partial sums
+    bool ok = true;
+    for (int phase = 0; ok && phase < phases; ++phase) {
+      const int kind = phase % 3, cur = (phase / 3) & 1;
+      const bool last = phase + 1 == phases;
+      Walk walk(p, phase, pair);
+      Segment s;
+      while (walk.next(p, s)) {
+        e.row0 = s.row0 + static_cast<int>(rank) * 128 + quarter * 32;
+        const int bn = p.bn[kind], blocks = bn / 64;  // 32-column blocks of this warp
+        const int row = e.row0 + lane, cbase = s.col0 + half * (bn / 2);
+        const int cols = kind == kUpdate ? p.q : p.p;
+        const bool live = e.row0 < p.p && cbase < cols;  // warp-uniform
+        const bool owner = s.kb0 == 0;
+        const int64_t xmat = static_cast<int64_t>(s.b) * p.p * p.ldx,
+                      amat = static_cast<int64_t>(s.b) * p.p * p.lda;
+        const float *diag = (kind == kUpdate ? p.db : p.da) + static_cast<int64_t>(s.b) * p.lda;
+        float d_row = 0.0f;
+        float4 d_col = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // c/S d_A of columns 4 lane .. + 3
+        if (owner && live && kind != kGram) {
+          // old values are on their way, or in place, before the accumulator is
+          // waited for: under the MMAs' own traffic a load takes over a microsecond
+          if (!(ok = warp_wait(&p.done[s.b], walk.ready))) break;
+          if (row < p.p) d_row = __ldcg(diag + row);
+          if (kind == kPoly) {  // the pitch is whole
+            const int dc = cbase + 4 * lane;
+            if (dc < cols && lane < 8 * blocks)
+              d_col = __ldcg(reinterpret_cast<const float4 *>(diag + dc));
+            const float cs = p.c / kS;
+            d_col = make_float4(cs * d_col.x, cs * d_col.y, cs * d_col.z, cs * d_col.w);
           }
+          if (kind == kUpdate) stage_old(e, p.x[cur] + xmat, p.ldx, p.p, cols, cbase, blocks);
+          else stage_old(e, p.am + amat, p.lda, p.p, cols, cbase, blocks);
         }
+
+        const bool got = mbar_wait_bounded(smem_u32(&ctl->tfull[buf]), tphase, abort_flag,
+                                           &g_ns_status, p.timeout_ns, FP8Q_ERR_TIMEOUT);
+        if (!(ok = __all_sync(0xffffffffu, got))) break;
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                               static_cast<uint32_t>(buf * kTile + half * (bn / 2));
+        uint32_t r[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c < blocks) tmem_ld_32x32b_x32(taddr + 32 * c, r[c]);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
-        if (c + 32 == BN / 2) {  // the accumulator has been read
-          tc_fence_before();
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[c][i]));
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty0 + static_cast<uint32_t>(buf) * 8u);
+        buf ^= 1;
+        if (buf == 0) tphase ^= 1;
+
+        if (!owner) {  // partial sums for the pair that began the tile
+          // ... once it has added this warp's last ones
+          if (given && !(ok = warp_wait(&p.sync->used[pair][rank][ew], given))) break;
+          float4 *slot = slot_of(pair);
+          if (live) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if (c < blocks) __stcg(slot + (8 * c + k) * 32,
+                       make_float4(__uint_as_float(r[c][4 * k]), __uint_as_float(r[c][4 * k + 1]),
+                                   __uint_as_float(r[c][4 * k + 2]),
+                                   __uint_as_float(r[c][4 * k + 3])));
+          }
+          given = static_cast<uint32_t>(phase) + 1;
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(tempty0 + static_cast<uint32_t>(buf) * 8u);
-        }
-        if (!live) continue;
-        float v[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float s = __uint_as_float(r[i]);
-          if (kOp == Op::kGram) v[i] = p.c_acc * s;
-          if (kOp == Op::kUpdate) v[i] = fmaf(c_old, old[i], p.c_acc * s);
-        }
-        // the diagonal crosses this warp's 32 x 32 block (both begin at
-        // multiples of 32)
-        const bool on_diag = kSym && row0 == col0;
-        if (kOp == Op::kPoly) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            // the pitch is a multiple of 8; what lies past the matrix is not stored
-            const float4 d = col0 + 4 * k < p.cols
-                                 ? *reinterpret_cast<const float4 *>(diag + col0 + 4 * k)
-                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            const float dc[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = 4 * k + e;
-              const float s = __uint_as_float(r[i]);
-              v[i] = fmaf(p.c_old, old[i], p.c_acc * fmaf(d_row + dc[e], old[i], s));
-              if (on_diag && i == lane) v[i] = fmaf(p.c_old, d_row, p.c_acc * fmaf(d_row, d_row, s));
-            }
-          }
-        }
-        if (on_diag && row < p.rows) {
-          float d = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i == lane) {
-              d = v[i];
-              v[i] = 0.0f;
-            }
-          p.diag_out[static_cast<int64_t>(tl.b) * p.ldd + row] = d;
-        }
-        if (kOp == Op::kUpdate && p.out) {
-          // final result, any pitch: column runs (tall) are contiguous over
-          // the lanes; row runs go through the staging buffer
-          const int64_t obase = static_cast<int64_t>(tl.b) * p.out_stride;
-          if (p.tall) {
-            if (row < p.rows)
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (whole || col0 + i < p.cols) {
-                  const int64_t at = obase + static_cast<int64_t>(col0 + i) * p.ldo + row;
-                  if (p.out_f32) static_cast<float *>(p.out)[at] = v[i];
-                  else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(v[i]);
-                }
-          } else {
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) st[lane * 33 + i] = v[i];
-            __syncwarp();
-            if (col0 + lane < p.cols) {
-              const int n = min(32, p.rows - row0);
-              for (int i = 0; i < n; ++i) {
-                const int64_t at = obase + static_cast<int64_t>(row0 + i) * p.ldo + col0 + lane;
-                const float f = st[i * 33 + lane];
-                if (p.out_f32) static_cast<float *>(p.out)[at] = f;
-                else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(f);
-              }
-            }
-          }
+          if (lane == 0) st_release(&p.sync->part[pair][rank][ew], given);
           continue;
         }
-        uint4 u[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __half2 h = __floats2half2_rn(v[8 * k + 2 * e], v[8 * k + 2 * e + 1]);
-            w[e] = *reinterpret_cast<const uint32_t *>(&h);
-          }
-          u[k] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        warp_store_block64<2, false, false>(smem_u32(st), u, p.dst + mat, p.ld, row0, p.rows, col0,
-                                            p.cols, lane);
-        if (mirror && row < p.rows) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const uint32_t w = reinterpret_cast<const uint32_t *>(u)[i / 2];
-            if (whole || col0 + i < p.cols)
-              reinterpret_cast<uint16_t *>(p.dst + mat)[static_cast<int64_t>(col0 + i) * p.ld + row] =
-                  static_cast<uint16_t>(i & 1 ? w >> 16 : w & 0xFFFFu);
-          }
-        }
-      }
-      buf ^= 1;
-      if (buf == 0) phase ^= 1;
-    }
-  } else if (warp == 0) {
-    // ================================================== TMA producer
-    if (lane == 0) {
-      int s = 0;
-      uint32_t phase = 0, armed = 0, armed_phase = 0;
-      bool ok = true;
-      for (int t = first; ok && t < total; t += step) {
-        const NsTile tl = tile_of<BN, kSym>(t, p);
-        for (int kb = 0; kb < p.kblocks; ++kb) {
-          if (!mbar_wait_bounded(smem_u32(&ctl->empty[s]), phase ^ 1, abort_flag, &g_ns_status,
-                                 p.timeout_ns, FP8Q_ERR_TIMEOUT)) {
-            ok = false;
+        // pairs after this one that hold the rest of the tile
+        const int helpers =
+            s.kb1 == walk.kblocks ? 0 : (walk.kblocks - s.kb1 + p.per[kind] - 1) / p.per[kind];
+        for (int h = 1; ok && h <= helpers; ++h) {
+          if (!(ok = warp_wait(&p.sync->part[pair + h][rank][ew], static_cast<uint32_t>(phase) + 1)))
             break;
+          if (live) {
+            const float4 *src = slot_of(pair + h);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                if (c >= blocks) continue;
+                const float4 f = __ldcg(src + (8 * c + k) * 32);
+                r[c][4 * k] = __float_as_uint(__uint_as_float(r[c][4 * k]) + f.x);
+                r[c][4 * k + 1] = __float_as_uint(__uint_as_float(r[c][4 * k + 1]) + f.y);
+                r[c][4 * k + 2] = __float_as_uint(__uint_as_float(r[c][4 * k + 2]) + f.z);
+                r[c][4 * k + 3] = __float_as_uint(__uint_as_float(r[c][4 * k + 3]) + f.w);
+              }
           }
-          const uint32_t fb = smem_u32(&ctl->full[s]);
-          if (rank == 0) mbar_arrive_expect_tx(fb, C::kTx);
-          const uint32_t fb0 = mapa_shared(fb, 0);
-          tma_load_3d_pair(sL + s * kLBytes, &tmL, fb0, kb * 64,
-                           tl.row0 + static_cast<int>(rank) * 128, tl.b);
-          const int rc = tl.col0 + static_cast<int>(rank) * (BN / 2);
-          if (kSym) {
-            tma_load_3d_pair(sR + s * C::kRBytes, &tmR, fb0, kb * 64, rc, tl.b);
+          __syncwarp();
+          if (lane == 0)
+            st_release(&p.sync->used[pair + h][rank][ew], static_cast<uint32_t>(phase) + 1);
+        }
+        if (!ok) break;
+        if (live) {
+          const bool bf16_rows = last && p.out_vec;
+          // tiles on the diagonal hold both triangles themselves
+          const bool mirror = kind != kUpdate && s.col0 >= s.row0 + kTile;
+          if (kind == kGram) __syncwarp();  // the blocks' previous contents have been read
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c >= blocks) continue;
+            const int col0 = cbase + 32 * c;
+            uint32_t w[16];
+            if (kind == kUpdate) {
+              const float scale = last ? 1.0f / (kS * kS) : 1.0f / kS;
+              float co = fmaf(1.0f / kS, d_row, p.a);
+              if (last) co *= 1.0f / kS;
+              read_row(e, c, w);
+              if (!last || bf16_rows) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  const float x = fmaf(co, f16_lo(w[k]), scale * __uint_as_float(r[c][2 * k]));
+                  const float y = fmaf(co, f16_hi(w[k]), scale * __uint_as_float(r[c][2 * k + 1]));
+                  if (last) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+                    w[k] = *reinterpret_cast<const uint32_t *>(&h);
+                  } else {
+                    const __half2 h = __floats2half2_rn(x, y);
+                    w[k] = *reinterpret_cast<const uint32_t *>(&h);
+                  }
+                }
+                write_row(e, c, w);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  r[c][i] = __float_as_uint(
+                      fmaf(co, i & 1 ? f16_hi(w[i / 2]) : f16_lo(w[i / 2]),
+                           scale * __uint_as_float(r[c][i])));
+              }
+              continue;
+            }
+            float d_new = 0.0f;
+            if (kind == kGram) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                r[c][i] = __float_as_uint((1.0f / kS) * __uint_as_float(r[c][i]));
+            } else {
+              const float cs = p.c / kS, co = fmaf(cs, d_row, p.b);
+              read_row(e, c, w);
+              if (e.row0 == col0) {  // b d_A + c/S (sum + d_A^2) on the diagonal
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (i == lane)
+                    d_new = fmaf(p.b, d_row, cs * fmaf(d_row, d_row, __uint_as_float(r[c][i])));
+              }
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float dc[4] = {__shfl_sync(0xffffffffu, d_col.x, 8 * c + k),
+                                     __shfl_sync(0xffffffffu, d_col.y, 8 * c + k),
+                                     __shfl_sync(0xffffffffu, d_col.z, 8 * c + k),
+                                     __shfl_sync(0xffffffffu, d_col.w, 8 * c + k)};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int i = 4 * k + j;
+                  const float o = i & 1 ? f16_hi(w[i / 2]) : f16_lo(w[i / 2]);
+                  r[c][i] = __float_as_uint(fmaf(co + dc[j], o, cs * __uint_as_float(r[c][i])));
+                }
+              }
+            }
+            if (e.row0 == col0) {
+              // the diagonal crosses this block (both begin at multiples of 32): its
+              // values leave as FP32, the FP16 matrix holds zeros there
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i == lane) {
+                  if (kind == kGram) d_new = __uint_as_float(r[c][i]);
+                  r[c][i] = 0u;
+                }
+              if (row < p.p)
+                __stcg((kind == kGram ? p.da : p.db) + static_cast<int64_t>(s.b) * p.lda + row, d_new);
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const __half2 h = __floats2half2_rn(__uint_as_float(r[c][2 * k]),
+                                                  __uint_as_float(r[c][2 * k + 1]));
+              w[k] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            write_row(e, c, w);
+            if (mirror) store_mirror(e, w, (kind == kGram ? p.am : p.bm) + amat, p.lda, p.p, col0);
+          }
+          if (!last) {
+            __half *dst = kind == kUpdate ? p.x[cur ^ 1] + xmat : (kind == kGram ? p.am : p.bm) + amat;
+            store_staged(e, reinterpret_cast<uint16_t *>(dst), kind == kUpdate ? p.ldx : p.lda, p.p,
+                         cols, cbase, blocks);
+          } else if (bf16_rows) {
+            store_staged(e, static_cast<uint16_t *>(p.out) + static_cast<int64_t>(s.b) * p.out_stride,
+                         p.ldo, p.p, cols, cbase, blocks);
           } else {
 #pragma unroll
-            for (int j = 0; j < BN / 128; ++j)
-              tma_load_3d_pair(sR + s * C::kRBytes + j * 8192, &tmR, fb0, rc + 64 * j, kb * 64, tl.b);
+            for (int c = 0; c < 4; ++c)
+              if (c < blocks && cbase + 32 * c < cols) {
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[c][i]);
+                store_out(e, v, p, s.b, cbase + 32 * c, st);
+              }
           }
-          armed |= 1u << s;
-          armed_phase = (armed_phase & ~(1u << s)) | (phase << s);
-          if (++s == C::kStages) {
-            s = 0;
-            phase ^= 1;
+        }
+        // warp 2 counts the tile as done.  A warp is at most two tiles ahead of
+        // another (two accumulators), so four barriers are enough.
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->stored[tile_no & 3]));
+        ++tile_no;
+      }
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync_all();
+    return;
+  }
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
+  if (warp == 0) {
+    // ================================================== TMA producer
+    if (lane == 0) {
+      int st = 0;
+      uint32_t ring = 0, armed = 0, armed_phase = 0;
+      bool ok = true;
+      for (int phase = 0; ok && phase < phases; ++phase) {
+        const int kind = phase % 3, cur = (phase / 3) & 1;
+        const CUtensorMap *ml = kind == kGram ? &maps.x[cur] : kind == kPoly ? &maps.a : &maps.b;
+        const CUtensorMap *mr = kind == kGram   ? &maps.xr[cur]
+                                : kind == kPoly ? &maps.ar
+                                                : &maps.xn[cur];
+        const int half_cols = p.bn[kind] / 2;
+        const uint32_t tx = 2 * (kOpBytes + static_cast<uint32_t>(half_cols) * 128);
+        Walk walk(p, phase, pair);
+        Segment s;
+        while (ok && walk.next(p, s)) {
+          if (!(ok = wait_count(&p.done[s.b], walk.ready, abort_flag, p.timeout_ns))) break;
+          fence_proxy_async_all();
+          for (int kb = s.kb0; kb < s.kb1; ++kb) {
+            if (!mbar_wait_bounded(smem_u32(&ctl->empty[st]), ring ^ 1, abort_flag, &g_ns_status,
+                                   p.timeout_ns, FP8Q_ERR_TIMEOUT)) {
+              ok = false;
+              break;
+            }
+            const uint32_t fb = smem_u32(&ctl->full[st]);
+            if (rank == 0) mbar_arrive_expect_tx(fb, tx);
+            const uint32_t fb0 = mapa_shared(fb, 0);
+            tma_load_3d_pair(sL + st * kOpBytes, ml, fb0, kb * 64,
+                             s.row0 + static_cast<int>(rank) * 128, s.b);
+            const int rc = s.col0 + static_cast<int>(rank) * half_cols;
+            if (kind != kUpdate) {
+              tma_load_3d_pair(sR + st * kOpBytes, mr, fb0, kb * 64, rc, s.b);
+            } else {
+              tma_load_3d_pair(sR + st * kOpBytes, mr, fb0, rc, kb * 64, s.b);
+              if (half_cols > 64)
+                tma_load_3d_pair(sR + st * kOpBytes + 8192, mr, fb0, rc + 64, kb * 64, s.b);
+            }
+            armed |= 1u << st;
+            armed_phase = (armed_phase & ~(1u << st)) | (ring << st);
+            if (++st == kStages) {
+              st = 0;
+              ring ^= 1;
+            }
           }
         }
       }
@@ -501,52 +923,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // this CTA's copies land before it exits (the leading CTA's barriers
         // see both CTAs' copies; the other waits long enough for any copy)
         if (rank == 0)
-          for (int i = 0; i < C::kStages; ++i)
+          for (int i = 0; i < kStages; ++i)
             if (armed & (1u << i)) mbar_wait_drain(smem_u32(&ctl->full[i]), (armed_phase >> i) & 1);
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < 1000000ull) {
         }
       }
     }
+  } else if (warp == 2) {
+    // ================================================== counts of done tiles
+    // One device-wide fence per tile covers all epilogue warps' writes, seen
+    // through the barrier; the epilogue does not wait for it (1.5 us).
+    if (lane == 0) {
+      int tile_no = 0;
+      bool ok = true;
+      for (int phase = 0; ok && phase + 1 < phases; ++phase) {
+        Walk walk(p, phase, pair);
+        Segment s;
+        while (ok && walk.next(p, s)) {
+          if (s.kb0 != 0) continue;  // the pair that began the tile counts it
+          ok = mbar_wait_bounded(smem_u32(&ctl->stored[tile_no & 3]),
+                                 static_cast<uint32_t>(tile_no >> 2) & 1u, abort_flag, &g_ns_status,
+                                 p.timeout_ns, FP8Q_ERR_TIMEOUT);
+          if (!ok) break;
+          fence_proxy_async_all();
+          __threadfence();
+          red_release(&p.done[s.b]);
+          ++tile_no;
+        }
+      }
+    }
   } else if (warp == 1) {
     // ================================================== MMA issuer
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t kIdesc = idesc_f16(256, BN, !kSym);
-      int s = 0, buf = 0;
-      uint32_t phase = 0, tphase = 0;
+      int st = 0, buf = 0;
+      uint32_t ring = 0, tphase = 0;
       bool ok = true, issued = false;
-      for (int t = first; ok && t < total; t += step) {
-        if (!mbar_wait_bounded(smem_u32(&ctl->tempty[buf]), tphase ^ 1, abort_flag, &g_ns_status,
-                               p.timeout_ns, FP8Q_ERR_TIMEOUT)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
-        for (int kb = 0; kb < p.kblocks; ++kb) {
-          if (!mbar_wait_bounded(smem_u32(&ctl->full[s]), phase, abort_flag, &g_ns_status,
+      for (int phase = 0; ok && phase < phases; ++phase) {
+        Walk walk(p, phase, pair);
+        const bool n_major = walk.kind == kUpdate;
+        const uint32_t idesc = idesc_f16(256, p.bn[walk.kind], n_major);
+        Segment s;
+        while (ok && walk.next(p, s)) {
+          if (!mbar_wait_bounded(smem_u32(&ctl->tempty[buf]), tphase ^ 1, abort_flag, &g_ns_status,
                                  p.timeout_ns, FP8Q_ERR_TIMEOUT)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t ad = smem_desc_sw128(sL + s * kLBytes);
-          const uint64_t bd = kSym ? smem_desc_sw128(sR + s * C::kRBytes)
-                                   : smem_desc_sw128_mn(sR + s * C::kRBytes, 8192);
+          const uint32_t d = tmem_base + static_cast<uint32_t>(buf * kTile);
+          for (int kb = s.kb0; kb < s.kb1; ++kb) {
+            if (!mbar_wait_bounded(smem_u32(&ctl->full[st]), ring, abort_flag, &g_ns_status,
+                                   p.timeout_ns, FP8Q_ERR_TIMEOUT)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t ad = smem_desc_sw128(sL + st * kOpBytes);
+            const uint64_t bd = n_major ? smem_desc_sw128_mn(sR + st * kOpBytes, 8192)
+                                        : smem_desc_sw128(sR + st * kOpBytes);
+            const uint64_t bstep = n_major ? 128 : 2;  // 16 K: 16 rows of 128 bytes, or 32 bytes
 #pragma unroll
-          for (int k = 0; k < 4; ++k)  // 16 K: 32 bytes of a row, or 16 rows of 128 bytes
-            mma_f16_pair(d, ad + 2 * k, bd + (kSym ? 2 : 128) * k, kIdesc, (kb | k) != 0 ? 1u : 0u);
-          mma_commit_pair_multicast(smem_u32(&ctl->empty[s]), 0x3);
-          issued = true;
-          if (++s == C::kStages) {
-            s = 0;
-            phase ^= 1;
+            for (int k = 0; k < 4; ++k)
+              mma_f16_pair(d, ad + 2 * k, bd + bstep * k, idesc,
+                           kb != s.kb0 || k != 0 ? 1u : 0u);
+            mma_commit_pair_multicast(smem_u32(&ctl->empty[st]), 0x3);
+            issued = true;
+            if (++st == kStages) {
+              st = 0;
+              ring ^= 1;
+            }
           }
+          if (!ok) break;
+          mma_commit_pair_multicast(smem_u32(&ctl->tfull[buf]), 0x3);
+          buf ^= 1;
+          if (buf == 0) tphase ^= 1;
         }
-        if (!ok) break;
-        mma_commit_pair_multicast(smem_u32(&ctl->tfull[buf]), 0x3);
-        buf ^= 1;
-        if (buf == 0) tphase ^= 1;
       }
       if (!ok && issued) {  // MMAs in flight finish before TMEM is freed
         mma_commit_pair_multicast(smem_u32(&ctl->drain), 0x1);
@@ -559,7 +1011,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, kTmem);
+    tmem_dealloc_pair(tmem_base, 512);
   }
 }
 
@@ -578,44 +1030,87 @@ bool make_tmap_f16(CUtensorMap *m, const void *base, uint64_t batch, uint64_t ro
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, Op kOp>
-fp8q_status launch_ns(const CUtensorMap &l, const CUtensorMap &r, const NsArgs &a, cudaStream_t s) {
-  auto kern = ns_gemm_kernel<BN, kOp>;
-  constexpr size_t smem = smem_of<BN>();
-  static int max_pairs[kMaxDevices] = {};
+// Pairs that can run at once on the current device (at most kMaxPairs).
+fp8q_status max_pairs(int &pairs) {
+  static int known[kMaxDevices] = {};
   static std::mutex mu;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FP8Q_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (max_pairs[dev] == 0) {
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(smem)) != cudaSuccess)
-        return FP8Q_ERR_CUDA;
-      int n = 0;
-      cfg.gridDim = dim3(2, 1, 1);
-      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1)
-        return FP8Q_ERR_UNSUPPORTED;
-      max_pairs[dev] = n;
-    }
+  std::lock_guard<std::mutex> lock(mu);
+  if (known[dev] == 0) {
+    if (cudaFuncSetAttribute(ns_steps_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmem)) != cudaSuccess)
+      return FP8Q_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.gridDim = dim3(2, 1, 1);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, ns_steps_kernel, &cfg) != cudaSuccess || n < 1)
+      return FP8Q_ERR_UNSUPPORTED;
+    known[dev] = n < kMaxPairs ? n : kMaxPairs;
   }
-  const int64_t tiles = static_cast<int64_t>(a.tiles) * a.batch;
-  const int64_t pairs = tiles < max_pairs[dev] ? tiles : max_pairs[dev];
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
-  return cudaLaunchKernelEx(&cfg, kern, l, r, a) == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
+  pairs = known[dev];
+  return FP8Q_OK;
 }
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
+// Tile width and share of each phase kind, by an estimate of its time: rounds of
+// tiles, each the longer of its MMAs and its epilogue, and the last epilogue.  A
+// K block of a 256-row tile measured 0.34 us at 256 columns (tensor cores), 0.25
+// at 128 and 0.2 at 64 (operand traffic); an epilogue about 0.8 us and 0.55 per 64
+// columns; handing split tiles over 9 us (every pair's 256 KB of partial sums go
+// through L2 at once).
+struct Plan {
+  int bn[3];
+  int64_t tiles[3], per[3], pairs;
+};
+// A split saves at most one tile's MMAs, so it never pays for short sums (which
+// then need no room for partial sums either).
+bool may_split(int64_t kblocks) { return kblocks > 26; }
+Plan plan_of(int64_t batch, int64_t p, int64_t q, int64_t pairs) {
+  Plan r{};
+  const int64_t row_tiles = (p + kTile - 1) / kTile;
+  for (int k = 0; k < 3; ++k) {
+    const int64_t kblocks = ((k == kGram ? q : p) + 63) / 64, cols = k == kUpdate ? q : p;
+    double best = 0;
+    for (int bn = kTile; bn >= (k == kUpdate ? 128 : 64); bn /= 2) {
+      const int64_t n = (cols + bn - 1) / bn;
+      int64_t tiles = row_tiles * n;
+      if (k != kUpdate) tiles -= kTile / bn * (row_tiles * (row_tiles - 1) / 2);
+      const int64_t all = tiles * batch, rounds = (all + pairs - 1) / pairs;
+      const double block = bn == 256 ? 0.34 : bn == 128 ? 0.25 : 0.2;
+      const double epi = 0.8 + 0.55 * (bn / 64);
+      const double mma = block * static_cast<double>(kblocks);
+      double t = static_cast<double>(rounds) * (mma > epi ? mma : epi) + epi;
+      int64_t per = 0;
+      const int64_t even = (all * kblocks + pairs - 1) / pairs;
+      const double split = block * static_cast<double>(even) + epi + 9.0;
+      if (bn == kTile && may_split(kblocks) && split < t) {
+        t = split;
+        per = even;
+      }
+      if (bn == kTile || t < best) {
+        best = t;
+        r.bn[k] = bn;
+        r.tiles[k] = tiles;
+        r.per[k] = per;
+      }
+    }
+    int64_t busy = r.tiles[k] * batch;
+    if (r.per[k] > 0) busy = (busy * kblocks + r.per[k] - 1) / r.per[k];
+    if (busy > pairs) busy = pairs;
+    if (busy > r.pairs) r.pairs = busy;
+  }
+  return r;
+}
+
 // Workspace: X (two copies), O_A, O_B as FP16 with pitches of a multiple of 8,
-// d_A, d_B and the partial sums of squares; every part starts at a multiple of
-// 256 bytes.
+// d_A, d_B, the partial sums of squares and of split tiles, and the counters;
+// every part starts at a multiple of 256 bytes.
 struct Layout {
-  int64_t p, q, ldx, lda, x0, x1, a, b, da, db, part, bytes;
+  int64_t p, q, ldx, lda, x0, x1, a, b, da, db, part, sync, split, bytes;
 };
 Layout layout_of(int64_t batch, int64_t m, int64_t n) {
   Layout l{};
@@ -632,27 +1127,51 @@ Layout layout_of(int64_t batch, int64_t m, int64_t n) {
   l.da = l.b + ab;
   l.db = l.da + db;
   l.part = l.db + db;
-  l.bytes = l.part + batch * kMaxParts * 4;
+  l.sync = up(l.part + batch * kMaxParts * 4, 256);
+  l.split = up(l.sync + static_cast<int64_t>(sizeof(Sync)) + 4 * batch, 256);
+  l.bytes = l.split + (may_split((l.q + 63) / 64) ? kMaxPairs * kSlotFloats * 4 : 0);
   return l;
 }
 
+// Sizes are bounded so that every count of units (of the narrowest tiles) is an int.
 bool shape_ok(int64_t batch, int64_t m, int64_t n) {
-  return batch >= 0 && m >= 0 && n >= 0 && batch <= 65535 && m <= (1 << 20) && n <= (1 << 20);
+  if (batch < 0 || m < 0 || n < 0 || batch > 65535 || m > (1 << 20) || n > (1 << 20)) return false;
+  const int64_t p = m < n ? m : n, q = m < n ? n : m;
+  const int64_t units = batch * ((p + 255) / 256) * ((q + 63) / 64) * ((p + 63) / 64);
+  return units < (1ll << 30);
 }
 
-template <typename In>
+template <typename In, bool kVec>
 fp8q_status load_x(const In *g, int64_t ldg, int64_t bs, int64_t batch, int64_t m, int64_t n,
                    float eps, const Layout &l, uint8_t *ws, cudaStream_t s) {
   float *part = reinterpret_cast<float *>(ws + l.part);
   __half *x = reinterpret_cast<__half *>(ws + l.x0);
-  const int parts = static_cast<int>(m < kMaxParts ? m : kMaxParts);
-  fp8q_status st = launch_on(ns_sumsq_kernel<In>, dim3(parts, static_cast<unsigned>(batch)),
-                             dim3(256), 0, s, g, ldg, bs, m, n, part);
-  if (st) return st;
-  const dim3 grid(static_cast<unsigned>((n + 63) / 64), static_cast<unsigned>((m + 63) / 64),
-                  static_cast<unsigned>(batch));
-  return launch_on(m > n ? ns_load_kernel<In, true> : ns_load_kernel<In, false>, grid, dim3(256), 0,
-                   s, g, ldg, bs, m, n, static_cast<const float *>(part), parts, eps, x, l.ldx);
+  const int64_t row_blocks = (m + 7) / 8;
+  const int parts = static_cast<int>(row_blocks < kMaxParts ? row_blocks : kMaxParts);
+  const unsigned b = static_cast<unsigned>(batch);
+  if (fp8q_status st = launch_on(ns_sumsq_kernel<In, kVec>, dim3(parts, b), dim3(256), 0, s, g, ldg,
+                                 bs, m, n, part, reinterpret_cast<uint32_t *>(ws + l.sync),
+                                 static_cast<int>(sizeof(Sync) / 4 + batch)))
+    return st;
+  if (m > n)
+    return launch_on(ns_load_tall_kernel<In, kVec>,
+                     dim3(static_cast<unsigned>((n + 63) / 64), static_cast<unsigned>((m + 63) / 64), b),
+                     dim3(256), 0, s, g, ldg, bs, m, n, static_cast<const float *>(part), parts, eps,
+                     x, l.ldx);
+  return launch_on(ns_load_kernel<In, kVec>,
+                   dim3(static_cast<unsigned>((n + 255) / 256), static_cast<unsigned>((m + 31) / 32), b),
+                   dim3(256), 0, s, g, ldg, bs, m, n, static_cast<const float *>(part), parts, eps, x,
+                   l.ldx);
+}
+
+template <typename In>
+fp8q_status load_any(const void *g, int64_t ldg, int64_t bs, int64_t batch, int64_t m, int64_t n,
+                     float eps, const Layout &l, uint8_t *ws, cudaStream_t s) {
+  const In *in = static_cast<const In *>(g);
+  constexpr int64_t V = kVecOf<In>;
+  return aligned16(g) && ldg % V == 0 && bs % V == 0
+             ? load_x<In, true>(in, ldg, bs, batch, m, n, eps, l, ws, s)
+             : load_x<In, false>(in, ldg, bs, batch, m, n, eps, l, ws, s);
 }
 
 }  // namespace
@@ -673,7 +1192,7 @@ extern "C" fp8q_status fp8q_newton_schulz(const void *g, int64_t ldg, int64_t g_
   const bool in_f32 = in_dtype == FP8Q_OUT_FP32, out_f32 = out_dtype == FP8Q_OUT_FP32;
   if ((!in_f32 && in_dtype != FP8Q_OUT_BF16) || (!out_f32 && out_dtype != FP8Q_OUT_BF16))
     return FP8Q_ERR_INVALID;
-  if (!(eps >= 0.0f) || steps < 1) return FP8Q_ERR_INVALID;
+  if (!(eps >= 0.0f) || steps < 1 || steps > 1000) return FP8Q_ERR_INVALID;
   if (!shape_ok(batch, m, n) || ldg < n || ldo < n) return FP8Q_ERR_SHAPE;
   if (batch == 0 || m == 0 || n == 0) return FP8Q_OK;
   if (batch > 1 && (g_stride < 0 || o_stride < (m - 1) * ldo + n)) return FP8Q_ERR_SHAPE;
@@ -686,83 +1205,71 @@ extern "C" fp8q_status fp8q_newton_schulz(const void *g, int64_t ldg, int64_t g_
     return FP8Q_ERR_ALIGN;
   DeviceInfo dev;
   if (fp8q_status st = device_info(dev)) return st;
-  if (dev.max_smem_optin < static_cast<int>(smem_of<256>() > smem_of<128>() ? smem_of<256>()
-                                                                            : smem_of<128>()))
-    return FP8Q_ERR_UNSUPPORTED;
+  if (dev.max_smem_optin < static_cast<int>(kSmem)) return FP8Q_ERR_UNSUPPORTED;
+  int pairs = 0;
+  if (fp8q_status st = max_pairs(pairs)) return st;
   auto s = static_cast<cudaStream_t>(stream);
   auto *ws = static_cast<uint8_t *>(workspace);
-  const uint64_t B = static_cast<uint64_t>(batch), P = static_cast<uint64_t>(l.p),
-                 Q = static_cast<uint64_t>(l.q);
-  __half *x[2] = {reinterpret_cast<__half *>(ws + l.x0), reinterpret_cast<__half *>(ws + l.x1)};
-  float *da = reinterpret_cast<float *>(ws + l.da), *db = reinterpret_cast<float *>(ws + l.db);
-  __half *am = reinterpret_cast<__half *>(ws + l.a), *bm = reinterpret_cast<__half *>(ws + l.b);
-  CUtensorMap xl[2], xr[2], xn[2], al, ar, bl;
+  NsArgs v{};
+  v.batch = static_cast<int>(batch);
+  v.p = static_cast<int>(l.p);
+  v.q = static_cast<int>(l.q);
+  v.steps = steps;
+  v.row_tiles = (v.p + kTile - 1) / kTile;
+  v.kb_p = (v.p + 63) / 64;
+  v.kb_q = (v.q + 63) / 64;
+  const Plan plan = plan_of(batch, l.p, l.q, pairs);
+  for (int k = 0; k < 3; ++k) {
+    v.bn[k] = plan.bn[k];
+    v.tiles[k] = static_cast<int>(plan.tiles[k]);
+    v.per[k] = static_cast<int>(plan.per[k]);
+  }
+  v.a = a;
+  v.b = b;
+  v.c = c;
+  v.x[0] = reinterpret_cast<__half *>(ws + l.x0);
+  v.x[1] = reinterpret_cast<__half *>(ws + l.x1);
+  v.am = reinterpret_cast<__half *>(ws + l.a);
+  v.bm = reinterpret_cast<__half *>(ws + l.b);
+  v.ldx = l.ldx;
+  v.lda = l.lda;
+  v.da = reinterpret_cast<float *>(ws + l.da);
+  v.db = reinterpret_cast<float *>(ws + l.db);
+  v.partial = reinterpret_cast<float *>(ws + l.split);
+  v.sync = reinterpret_cast<Sync *>(ws + l.sync);
+  v.done = reinterpret_cast<uint32_t *>(v.sync + 1);
+  v.out = out;
+  v.ldo = ldo;
+  v.out_stride = batch > 1 ? o_stride : 0;
+  v.out_f32 = out_f32;
+  v.tall = m > n;
+  v.out_vec = !v.tall && !out_f32 && aligned16(out) && ldo % 8 == 0 && v.out_stride % 8 == 0;
+  v.timeout_ns = wait_timeout_ns().load();
+  Maps maps;
   for (int i = 0; i < 2; ++i)
-    if (!make_tmap_f16(&xl[i], x[i], B, P, Q, l.ldx, 128) ||
-        !make_tmap_f16(&xr[i], x[i], B, P, Q, l.ldx, 64))
+    if (!make_tmap_f16(&maps.x[i], v.x[i], batch, l.p, l.q, l.ldx, 128) ||
+        !make_tmap_f16(&maps.xr[i], v.x[i], batch, l.p, l.q, l.ldx, plan.bn[kGram] / 2) ||
+        !make_tmap_f16(&maps.xn[i], v.x[i], batch, l.p, l.q, l.ldx, 64))
       return FP8Q_ERR_CUDA;
-  xn[0] = xr[0];  // the update's N-major boxes: 64 columns x 64 rows as well
-  xn[1] = xr[1];
-  if (!make_tmap_f16(&al, am, B, P, P, l.lda, 128) || !make_tmap_f16(&ar, am, B, P, P, l.lda, 64) ||
-      !make_tmap_f16(&bl, bm, B, P, P, l.lda, 128))
+  if (!make_tmap_f16(&maps.a, v.am, batch, l.p, l.p, l.lda, 128) ||
+      !make_tmap_f16(&maps.ar, v.am, batch, l.p, l.p, l.lda, plan.bn[kPoly] / 2) ||
+      !make_tmap_f16(&maps.b, v.bm, batch, l.p, l.p, l.lda, 128))
     return FP8Q_ERR_CUDA;
   const int64_t bs = batch > 1 ? g_stride : 0;
-  fp8q_status st = in_f32 ? load_x(static_cast<const float *>(g), ldg, bs, batch, m, n, eps, l, ws, s)
-                          : load_x(static_cast<const uint16_t *>(g), ldg, bs, batch, m, n, eps, l,
-                                   ws, s);
-  if (st) return st;
-
-  NsArgs sym{};
-  sym.batch = static_cast<int>(batch);
-  sym.rows = sym.cols = static_cast<int>(l.p);
-  sym.tiles_m = static_cast<int>((l.p + 255) / 256);
-  sym.tiles_n = static_cast<int>((l.p + 127) / 128);
-  for (int i = 0; i < sym.tiles_m; ++i) sym.tiles += sym.tiles_n - 2 * i;
-  sym.ld = sym.ldd = l.lda;
-  sym.timeout_ns = wait_timeout_ns().load();
-  NsArgs upd = sym;
-  upd.cols = static_cast<int>(l.q);
-  upd.tiles_n = static_cast<int>((l.q + 255) / 256);
-  upd.tiles = upd.tiles_m * upd.tiles_n;
-  upd.ld = l.ldx;
-  if (static_cast<int64_t>(upd.tiles) * batch >= (1ll << 31)) return FP8Q_ERR_SHAPE;
-  const int kx = static_cast<int>((l.q + 63) / 64), kp = static_cast<int>((l.p + 63) / 64);
-  for (int i = 0; i < steps; ++i) {
-    const int cur = i & 1;
-    NsArgs ga = sym;
-    ga.kblocks = kx;
-    ga.c_acc = 1.0f / kS;
-    ga.dst = am;
-    ga.diag = ga.diag_out = da;
-    if ((st = launch_ns<128, Op::kGram>(xl[cur], xr[cur], ga, s))) return st;
-    NsArgs pa = sym;
-    pa.kblocks = kp;
-    pa.c_old = b;
-    pa.c_acc = c / kS;
-    pa.old = am;
-    pa.dst = bm;
-    pa.diag = da;
-    pa.diag_out = db;
-    if ((st = launch_ns<128, Op::kPoly>(al, ar, pa, s))) return st;
-    NsArgs ua = upd;
-    ua.kblocks = kp;
-    ua.c_old = a;
-    ua.c_acc = 1.0f / kS;
-    ua.c_diag = 1.0f / kS;
-    ua.diag = db;
-    ua.old = x[cur];
-    ua.dst = x[cur ^ 1];
-    if (i + 1 == steps) {  // the last step leaves as the caller's matrix, unscaled
-      ua.c_old = a / kS;
-      ua.c_diag = 1.0f / (kS * kS);
-      ua.c_acc = 1.0f / (kS * kS);
-      ua.out = out;
-      ua.ldo = ldo;
-      ua.out_stride = batch > 1 ? o_stride : 0;
-      ua.out_f32 = out_f32;
-      ua.tall = m > n;
-    }
-    if ((st = launch_ns<256, Op::kUpdate>(bl, xn[cur], ua, s))) return st;
-  }
-  return FP8Q_OK;
+  if (fp8q_status st = in_f32 ? load_any<float>(g, ldg, bs, batch, m, n, eps, l, ws, s)
+                              : load_any<uint16_t>(g, ldg, bs, batch, m, n, eps, l, ws, s))
+    return st;
+  // the pairs wait for one another: a cooperative launch runs all of them at once
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * plan.pairs), 1, 1);
+  return cudaLaunchKernelEx(&cfg, ns_steps_kernel, maps, v) == cudaSuccess ? FP8Q_OK
+                                                                           : FP8Q_ERR_CUDA;
 }

@@ -382,9 +382,11 @@ fp8q_status fp8q_swiglu_bwd(const void *dh, int64_t ld_dh, const void *gu, int64
  *        matrix i at g + i * g_stride elements.
  *   out  FP32 or BF16 (out_dtype) [m][ldo], matrix i at out + i * o_stride;
  *        may not overlap g or the workspace.
- *   steps >= 1, eps >= 0 (a zero matrix with eps > 0 gives zeros).
- *   Limits: 0 <= m, n <= 2^20, batch <= 65535; the sum of G's squares must be
- *   an FP32 value, and |a|, |b|, |c| such that the entries of X, A and B stay
+ *   1 <= steps <= 1000, eps >= 0 (a zero matrix with eps > 0 gives zeros).
+ *   Limits: 0 <= m, n <= 2^20, batch <= 65535, and fewer than 2^30 units of
+ *   work (256 x 64 tiles of the update's product times 64-wide blocks of its
+ *   inner dimension: a 65536 x 65536 matrix passes); the sum of G's squares
+ *   must be an FP32 value, and |a|, |b|, |c| such that the entries of X, A and B stay
  *   below 255 (FP16 after scaling; the usual coefficients keep them below 12).
  *   workspace  device scratch of at least
  *              fp8q_newton_schulz_workspace_bytes(batch, m, n) bytes, 256-byte

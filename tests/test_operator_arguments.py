@@ -108,9 +108,11 @@ def test_empty_work_succeeds(lib, B):
 
 
 def test_workspace_size(lib):
-    # two copies of X, A and B in FP16, their diagonals and the partial sums
+    # two copies of X, A and B in FP16, their diagonals, counters and partial
+    # sums; at most 76 pairs' FP32 partial tiles of 256 x 256
     f = lib.fp8q_newton_schulz_workspace_bytes
     assert f(1, 2048, 7168) == f(1, 7168, 2048)
-    need = 2 * 2048 * 7168 * 2 + 2 * 2048 * 2048 * 2 + 2 * 2048 * 4 + 1024
-    assert need <= f(1, 2048, 7168) <= need + 4096
-    assert f(-1, 8, 8) == 0 and f(1, 1 << 21, 8) == 0
+    need = 2 * 2048 * 7168 * 2 + 2 * 2048 * 2048 * 2 + 2 * 2048 * 4
+    assert need <= f(1, 2048, 7168) <= need + 76 * 256 * 256 * 4 + 32768
+    assert f(1, 8, 8) <= 256 * 256 * 4 + 32768
+    assert f(-1, 8, 8) == 0 and f(1, 1 << 21, 8) == 0 and f(4096, 1 << 16, 1 << 16) == 0
