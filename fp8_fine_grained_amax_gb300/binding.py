@@ -344,59 +344,61 @@ class SwigluGrads(NamedTuple):
     shT: Optional[torch.Tensor]  # f32 [T/128][F]
 
 
-def _out(t, wanted, shape, dtype, device, name):
-    """The caller's output tensor (checked), a new one where wanted, or None."""
-    if t is not None:
-        if tuple(t.shape) != shape or t.dtype != dtype:
-            raise ValueError(f"{name} must be a {dtype} tensor of shape {shape}")
-        return t
-    return torch.empty(shape, dtype=dtype, device=device) if wanted else None
+# The calls below marshal up to 18 tensors each; a small call costs more time
+# here than on the device, so each tensor is looked at once.
+_U8, _BF16, _F32T = torch.uint8, torch.bfloat16, torch.float32
+_empty = torch.empty
 
 
-def _ld(t, name, empty=0):
-    """Row pitch of an optional matrix; the strides of one-long axes do not count."""
-    if t is None:
-        return 0
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be 2-D with a contiguous last dimension")
-    if not t.numel():
-        return max(empty, t.shape[1])
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _mat(t, rows, cols, dtype, name):
+    """(address, row pitch) of a caller's matrix, whose shape and type must be as
+    given; the strides of one-long axes do not count."""
+    if t.dtype is not dtype or t.shape != (rows, cols):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {(rows, cols)}")
+    st = t.stride()
+    if cols > 1 and rows and st[1] != 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    return t.data_ptr() or None, st[0] if rows > 1 else cols
 
 
-def _need(t, dtype, name):
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be a {dtype} tensor")
+def _raw_current_stream(stream):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
 
 
-def _glu_call(entry, a, sa, b, sb, offs, F, with_h, with_gu, with_codes, scale_mode, h, gu, q, s,
-              stream):
-    M, K = a.shape
-    _need(a, torch.uint8, "a")
-    _need(b, torch.uint8, "b")
-    _need(sa, torch.float32, "sa")
-    _need(sb, torch.float32, "sb")
-    if b.shape[-1] != K or b.shape[-2] != 2 * F:
-        raise ValueError("b must hold both projections: [2F][K] rows, with a's K")
-    dev = a.device
-    h = _out(h, with_h, (M, F), torch.bfloat16, dev, "h")
-    gu = _out(gu, with_gu, (M, 2 * F), torch.bfloat16, dev, "gu")
-    q = _out(q, with_codes, (M, F), torch.uint8, dev, "q")
-    s = _out(s, q is not None, (F // 128, M), torch.float32, dev, "s")
-    lib = load_library()
-    head = [_ptr(a), _ld(a, "a", K), _ptr(sa), _ld(sa, "sa", M), _ptr(b), b.stride(-2), _ptr(sb)]
-    if offs is None:
-        head.append(_ld(sb, "sb", K // 128))
-    else:
-        _need(offs, torch.int32, "offs")
-        if offs.numel() != b.shape[0] + 1 or not offs.is_contiguous():
-            raise ValueError("offs must be a contiguous int32 [G+1] tensor")
-        if not sb.is_contiguous():
-            raise ValueError("sb must be contiguous [G][2F/128][K/128]")
-        head += [_ptr(offs), b.shape[0]]
-    _check(getattr(lib, entry)(
-        *head, _ptr(h), _ld(h, "h", F), _ptr(gu), _ld(gu, "gu", 2 * F), _ptr(q), _ld(q, "q", F),
-        _ptr(s), _ld(s, "s", M), scale_mode, M, F, K, _stream(stream)), entry)
+def _glu_call(entry, a, sa, b_args, M, F, K, dev, with_h, with_gu, with_codes, scale_mode, h, gu, q,
+              s, stream):
+    # results: the caller's, checked, or new ones
+    p_h = p_gu = p_q = p_s = None
+    ld_h, ld_gu, ld_q, ld_s = F, 2 * F, F, M
+    if h is not None:
+        p_h, ld_h = _mat(h, M, F, _BF16, "h")
+    elif with_h:
+        h = _empty((M, F), dtype=_BF16, device=dev)
+        p_h = h.data_ptr()
+    if gu is not None:
+        p_gu, ld_gu = _mat(gu, M, 2 * F, _BF16, "gu")
+    elif with_gu:
+        gu = _empty((M, 2 * F), dtype=_BF16, device=dev)
+        p_gu = gu.data_ptr()
+    if q is not None:
+        p_q, ld_q = _mat(q, M, F, _U8, "q")
+    elif with_codes:
+        q = _empty((M, F), dtype=_U8, device=dev)
+        p_q = q.data_ptr()
+    if s is not None:
+        p_s, ld_s = _mat(s, F // 128, M, _F32T, "s")
+    elif q is not None:
+        s = _empty((F // 128, M), dtype=_F32T, device=dev)
+        p_s = s.data_ptr()
+    p_a, ld_a = _mat(a, M, K, _U8, "a")
+    p_sa, ld_sa = _mat(sa, K // 128, M, _F32T, "sa")
+    st = getattr(_lib or load_library(), entry)(
+        p_a, ld_a, p_sa, ld_sa, *b_args, p_h, ld_h, p_gu, ld_gu, p_q, ld_q, p_s, ld_s, scale_mode, M,
+        F, K, _raw_current_stream(stream))
+    if st:
+        raise FP8QError(st, entry)
     return SwigluOut(h, gu, q, s)
 
 
@@ -405,13 +407,14 @@ def fp8q_gemm_swiglu(a, sa, b, sb, *, with_h=True, with_gu=False, with_codes=Fal
                      _entry="fp8q_gemm_swiglu"):
     """h = silu(X Wg^T) * (X Wu^T) from codes a uint8 [M][K] (sa f32 [K/128][M]) and the stacked
     projections b uint8 [2F][K] (sb f32 [2F/128][K/128]) -> SwigluOut(h, gu, q, s)."""
-    if b.dim() != 2 or b.stride(1) != 1 or b.shape[0] % 2:
-        raise ValueError("b must be [2F][K] with a contiguous last dimension")
-    if tuple(sa.shape) != (a.shape[1] // 128, a.shape[0]) or \
-            tuple(sb.shape) != (b.shape[0] // 128, a.shape[1] // 128):
-        raise ValueError("sa must be [K/128][M] and sb [2F/128][K/128]")
-    return _glu_call(_entry, a, sa, b, sb, None, b.shape[0] // 2, with_h, with_gu, with_codes,
-                     scale_mode, h, gu, q, s, stream)
+    M, K = a.shape
+    N = b.shape[0]
+    if N % 2:
+        raise ValueError("b must hold both projections: [2F][K]")
+    p_b, ld_b = _mat(b, N, K, _U8, "b")
+    p_sb, ld_sb = _mat(sb, N // 128, K // 128, _F32T, "sb")
+    return _glu_call(_entry, a, sa, (p_b, ld_b, p_sb, ld_sb), M, N // 2, K, a.device, with_h, with_gu,
+                     with_codes, scale_mode, h, gu, q, s, stream)
 
 
 def fp8q_gemm_swiglu_pow2(a, sa, b, sb, **kw):
@@ -424,14 +427,19 @@ def fp8q_grouped_gemm_swiglu(a, sa, b, sb, offs, *, with_h=True, with_gu=False, 
                              stream=None, _entry="fp8q_grouped_gemm_swiglu"):
     """fp8q_gemm_swiglu per expert: b uint8 [G][2F][K], sb f32 [G][2F/128][K/128], offs int32
     [G+1] on the device.  Rows outside [offs[0], offs[G]) are left as is."""
-    if b.dim() != 3 or b.stride(2) != 1 or b.stride(0) != b.shape[1] * b.stride(1) or \
-            b.shape[1] % 2:
-        raise ValueError("b must be [G][2F][ldb] with experts packed back to back")
-    if tuple(sa.shape) != (a.shape[1] // 128, a.shape[0]) or \
-            tuple(sb.shape) != (b.shape[0], b.shape[1] // 128, a.shape[1] // 128):
-        raise ValueError("sa must be [K/128][M] and sb [G][2F/128][K/128]")
-    return _glu_call(_entry, a, sa, b, sb, offs, b.shape[1] // 2, with_h, with_gu, with_codes,
-                     scale_mode, h, gu, q, s, stream)
+    M, K = a.shape
+    G, N, Kb = b.shape
+    st = b.stride()
+    if b.dtype is not _U8 or Kb != K or N % 2 or (b.numel() and (st[2] != 1 or st[0] != N * st[1])):
+        raise ValueError("b must be uint8 [G][2F][K], its last dimension contiguous and its experts "
+                         "back to back")
+    if sb.dtype is not _F32T or sb.shape != (G, N // 128, K // 128) or not sb.is_contiguous():
+        raise ValueError("sb must be a contiguous float32 [G][2F/128][K/128] tensor")
+    if offs.dtype is not torch.int32 or offs.shape != (G + 1,) or not offs.is_contiguous():
+        raise ValueError("offs must be a contiguous int32 [G+1] tensor")
+    return _glu_call(_entry, a, sa,
+                     (b.data_ptr() or None, st[1], sb.data_ptr() or None, offs.data_ptr(), G), M,
+                     N // 2, K, a.device, with_h, with_gu, with_codes, scale_mode, h, gu, q, s, stream)
 
 
 def fp8q_grouped_gemm_swiglu_pow2(a, sa, b, sb, offs, **kw):
@@ -447,28 +455,65 @@ def fp8q_swiglu_bwd(dh, gu, *, with_d=False, with_rows=True, with_cols=True, wit
     BF16 gradient d (with_d), its 1x128 codes (with_rows), its transposed 128x1 codes (with_cols)
     and the transposed 128x1 codes of h (with_h; both need T % 128 == 0)."""
     T, F = dh.shape
-    _need(dh, torch.bfloat16, "dh")
-    _need(gu, torch.bfloat16, "gu")
-    if tuple(gu.shape) != (T, 2 * F):
-        raise ValueError("gu must be [T][2F]")
+    N = 2 * F
+    p_dh, ld_dh = _mat(dh, T, F, _BF16, "dh")
+    p_gu, ld_gu = _mat(gu, T, N, _BF16, "gu")
     dev = dh.device
-    d = _out(d, with_d, (T, 2 * F), torch.bfloat16, dev, "d")
-    q = _out(q, with_rows, (T, 2 * F), torch.uint8, dev, "q")
-    s = _out(s, q is not None, (2 * F // 128, T), torch.float32, dev, "s")
-    qT = _out(qT, with_cols, (2 * F, T), torch.uint8, dev, "qT")
-    sT = _out(sT, qT is not None, (T // 128, 2 * F), torch.float32, dev, "sT")
-    hT = _out(hT, with_h, (F, T), torch.uint8, dev, "hT")
-    shT = _out(shT, hT is not None, (T // 128, F), torch.float32, dev, "shT")
-    _check(load_library().fp8q_swiglu_bwd(
-        _ptr(dh), _ld(dh, "dh", F), _ptr(gu), _ld(gu, "gu", 2 * F), _ptr(d), _ld(d, "d", 2 * F),
-        _ptr(q), _ld(q, "q", 2 * F), _ptr(s), _ld(s, "s", T), _ptr(qT), _ld(qT, "qT", T),
-        _ptr(sT), _ld(sT, "sT", 2 * F), _ptr(hT), _ld(hT, "hT", T), _ptr(shT),
-        _ld(shT, "shT", F), T, F, scale_mode, _stream(stream)), "fp8q_swiglu_bwd")
+    p_d = p_q = p_s = p_qT = p_sT = p_hT = p_shT = None
+    ld_d, ld_q, ld_s, ld_qT, ld_sT, ld_hT, ld_shT = N, N, T, T, N, T, F
+    if d is not None:
+        p_d, ld_d = _mat(d, T, N, _BF16, "d")
+    elif with_d:
+        d = _empty((T, N), dtype=_BF16, device=dev)
+        p_d = d.data_ptr()
+    if q is not None:
+        p_q, ld_q = _mat(q, T, N, _U8, "q")
+    elif with_rows:
+        q = _empty((T, N), dtype=_U8, device=dev)
+        p_q = q.data_ptr()
+    if s is not None:
+        p_s, ld_s = _mat(s, N // 128, T, _F32T, "s")
+    elif q is not None:
+        s = _empty((N // 128, T), dtype=_F32T, device=dev)
+        p_s = s.data_ptr()
+    if qT is not None:
+        p_qT, ld_qT = _mat(qT, N, T, _U8, "qT")
+    elif with_cols:
+        qT = _empty((N, T), dtype=_U8, device=dev)
+        p_qT = qT.data_ptr()
+    if sT is not None:
+        p_sT, ld_sT = _mat(sT, T // 128, N, _F32T, "sT")
+    elif qT is not None:
+        sT = _empty((T // 128, N), dtype=_F32T, device=dev)
+        p_sT = sT.data_ptr()
+    if hT is not None:
+        p_hT, ld_hT = _mat(hT, F, T, _U8, "hT")
+    elif with_h:
+        hT = _empty((F, T), dtype=_U8, device=dev)
+        p_hT = hT.data_ptr()
+    if shT is not None:
+        p_shT, ld_shT = _mat(shT, T // 128, F, _F32T, "shT")
+    elif hT is not None:
+        shT = _empty((T // 128, F), dtype=_F32T, device=dev)
+        p_shT = shT.data_ptr()
+    st = (_lib or load_library()).fp8q_swiglu_bwd(
+        p_dh, ld_dh, p_gu, ld_gu, p_d, ld_d, p_q, ld_q, p_s, ld_s, p_qT, ld_qT, p_sT, ld_sT, p_hT,
+        ld_hT, p_shT, ld_shT, T, F, scale_mode, _raw_current_stream(stream))
+    if st:
+        raise FP8QError(st, "fp8q_swiglu_bwd")
     return SwigluGrads(d, q, s, qT, sT, hT, shT)
 
 
 def fp8q_newton_schulz_workspace_bytes(batch: int, m: int, n: int) -> int:
     return int(load_library().fp8q_newton_schulz_workspace_bytes(batch, m, n))
+
+
+def _pitches(t, m, n, name):
+    """Row and matrix pitch of a matrix or a batch of matrices."""
+    st = t.stride()
+    if n > 1 and m and st[-1] != 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    return st[-2] if m > 1 else n, st[0] if len(st) == 3 else 0
 
 
 def fp8q_newton_schulz(g, *, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7,
@@ -483,21 +528,21 @@ def fp8q_newton_schulz(g, *, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7
         out = torch.empty(g.shape, dtype=dt, device=g.device)
     elif out.shape != g.shape or out.dtype != dt:
         raise ValueError("out must have g's shape and the type out_dtype names")
-    for t, name in ((g, "g"), (out, "out")):
-        if t.numel() and t.stride(-1) != 1:
-            raise ValueError(f"{name} must have a contiguous last dimension")
     B = g.shape[0] if g.dim() == 3 else 1
     m, n = g.shape[-2:]
-    nbytes = fp8q_newton_schulz_workspace_bytes(B, m, n)
+    ld_g, stride_g = _pitches(g, m, n, "g")
+    ld_o, stride_o = _pitches(out, m, n, "out")
+    lib = _lib or load_library()
     if workspace is None:
-        workspace = torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=g.device)
+        nbytes = lib.fp8q_newton_schulz_workspace_bytes(B, m, n)
+        workspace = _empty((max(nbytes, 1),), dtype=_U8, device=g.device)
     a, b, c = coeffs
-    _check(load_library().fp8q_newton_schulz(
-        _ptr(g), g.stride(-2) if g.numel() else n, g.stride(0) if g.dim() == 3 else 0,
-        FP8Q_OUT_FP32 if g.dtype == torch.float32 else FP8Q_OUT_BF16, _ptr(out),
-        out.stride(-2) if g.numel() else n, out.stride(0) if g.dim() == 3 else 0, out_dtype, B, m, n,
-        steps, a, b, c, eps, _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _stream(stream)), "fp8q_newton_schulz")
+    _check(lib.fp8q_newton_schulz(
+        g.data_ptr() or None, ld_g, stride_g,
+        FP8Q_OUT_FP32 if g.dtype is _F32T else FP8Q_OUT_BF16, out.data_ptr() or None, ld_o, stride_o,
+        out_dtype, B, m, n, steps, a, b, c, eps, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _raw_current_stream(stream)),
+        "fp8q_newton_schulz")
     return out
 
 
