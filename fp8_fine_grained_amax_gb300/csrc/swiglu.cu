@@ -56,6 +56,13 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&p);
 }
 
+// Wait for a phase for at most 1 s regardless of any abort (own copies only).
+__device__ __forceinline__ void mbar_wait_drain(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (global_timer_ns() - t0 > 1000000000ull) return;
+}
+
 // One FP32 value into the shared memory of CTA `rank` of the cluster.
 __device__ __forceinline__ void st_cluster_f32(uint32_t local_addr, uint32_t rank, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(local_addr, rank)), "f"(v)
@@ -63,46 +70,51 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t local_addr, uint32_t ran
 }
 
 // ------------------------------------------------------------------ few tokens
-// With few tokens the block only streams its weights (2 F K bytes), and a
-// 256-row tensor-core tile would leave most SMs idle: a CTA here takes 16
-// columns of h (16 gate rows and 16 up rows of the weights) and every token,
-// its warps split K by 128-wide groups, and a cluster of eight CTAs covers a
-// 1x128 group of h, exchanging one max-abs per token through distributed
-// shared memory.
-//  - mma.sync m16n8k32 (E4M3, FP32 sums): rows 0-7 are eight gate rows, rows
-//    8-15 the up rows of the same eight columns, so g and u of one (token,
-//    column) land in the same thread; columns are eight tokens.  The tensor
-//    cores are far from busy; the form only saves the decode and FMAs.
-//  - Within a group the K order is free (the same for both operands): lane
-//    4r + t loads bytes 16t and 64 + 16t of row r's 128, whole 64-byte pieces
-//    of eight rows per instruction, and feeds the words to the MMAs in pairs.
-//  - Each group's FP32 sums are scaled by sa * sb and added to FP32
-//    accumulators; the warps' accumulators are summed in warp order.
-constexpr int kFewWarps = 8;
-constexpr int kFewTokens = 32;
+// With few tokens the block only streams its weights (2 F K bytes), and the
+// 256-row tiles of the GEMMs would leave most SMs idle.  Here the weights are
+// the MMA's M side and the tokens its N side: a CTA takes 64 columns of h (64
+// gate rows and the 64 up rows of the same columns: one 128-row operand), N
+// tokens, and a quarter of the K-groups; a cluster of eight CTAs covers the
+// 1x128 group of h (two column halves) times the four K quarters.
+//   warp 0     TMA producer: weights and tokens per K-group into a ring that
+//              keeps 64 to 160 KB per SM on their way, which is what streaming
+//              at the memory's rate needs
+//   warp 1     MMA issuer: per K-group 4 x tcgen05.mma (M = 128, N tokens,
+//              K = 32) into one of four TMEM buffers
+//   warps 2-5  fold: each thread one weight row, acc += P * sa * sb in FP32,
+//              the tokens' scales broadcast through shared memory
+// Then the K quarters are summed: each CTA sends its sums of a quarter of the
+// tokens to the CTA that finishes them (distributed shared memory, every sum
+// has its own place, added in K order), which gates them; for the codes the two
+// column halves of a group exchange one max-abs per token.
+constexpr int kFewSplit = 4;       // CTAs along K
+constexpr int kFewThreads = 192;
+constexpr int kFewBufs = 4;        // TMEM buffers
+
+template <int N>
+struct Few {
+  static constexpr uint32_t kWBytes = 128 * 128, kXBytes = N * 128;
+  // ring depth: what two CTAs per SM leave room for (three shallower ones
+  // measured slower: 24 tokens of 7168 x 7168 28.6 us, against 24.5)
+  static constexpr int kStages = N == 16 ? 5 : N == 32 ? 4 : 3;
+  static constexpr int kPerSm = 2;
+  static constexpr int kQuarter = N / kFewSplit;  // tokens finished by a CTA
+  static constexpr uint32_t kRecv = kFewSplit * kQuarter * 128 * 4;
+  static constexpr uint32_t kCols = kFewBufs * N;
+  static constexpr size_t kSmem = 1024 + kStages * (kWBytes + kXBytes) + kRecv;
+  static_assert(kPerSm * (kSmem + 4096) <= 227 * 1024, "shared memory");
+  static_assert(kPerSm * kCols <= 512, "tensor memory");
+};
 
 struct FewArgs {
-  const uint8_t *a;
-  int64_t lda;
   const float *sa;
   int64_t ld_sa;
-  const uint8_t *b;
-  int64_t ldb;
   const float *sb;
   int64_t ld_sb;
   int M, num_kb;
   GluOut out;
+  uint64_t timeout_ns;
 };
-
-__device__ __forceinline__ void mma_e4m3_16x8x32(float (&d)[4], uint32_t a0, uint32_t a1,
-                                                 uint32_t a2, uint32_t a3, uint32_t b0,
-                                                 uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // A power-of-two scale, or, for any other value, the power of two of its
 // exponent field with `bad` set (as the block-scaled MMA path treats it).
@@ -116,180 +128,309 @@ __device__ __forceinline__ float pow2_of(float s, bool &bad) {
   return __uint_as_float((e < 0xFFu ? e : 0xFEu) << 23);
 }
 
-// NT: token blocks of eight (M <= 8 NT).
-template <int NT, bool kPow2>
-__global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kFewWarps * 32)
-    glu_few_tokens_kernel(const FewArgs p) {
-  constexpr int R = 2;  // blocks of eight columns of h per CTA
-  __shared__ float red[kFewWarps][R * NT * 4][32];
-  __shared__ float cl_amax[8][8 * NT];  // [CTA of the cluster][token]
-  __shared__ int tok_amax[8 * NT];      // bits of this CTA's max-abs
+template <int N, bool kPow2>
+__global__ void __cluster_dims__(2 * kFewSplit, 1, 1)
+    __launch_bounds__(kFewThreads, Few<N>::kPerSm)
+        glu_few_tokens_kernel(const __grid_constant__ CUtensorMap tmW,
+                              const __grid_constant__ CUtensorMap tmX, const FewArgs p) {
+  using C = Few<N>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[C::kStages], empty[C::kStages], tfull[kFewBufs], tempty[kFewBufs], drain;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ __align__(16) float s_sa[4][2][N];          // per fold warp, double-buffered
+  __shared__ float s_amax[2][C::kQuarter];               // [column half][token]
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sW = smem_u32(smem), sX = sW + C::kStages * C::kWBytes;
+  float *recv = reinterpret_cast<float *>(smem + C::kStages * (C::kWBytes + C::kXBytes));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r8 = lane >> 2, t4 = lane & 3;
-  const int F = p.out.F;
-  const int c0 = static_cast<int>(blockIdx.x) * (8 * R);
-  const int nb = c0 / 128, NB = F / 128;
-  const float *sbg = p.sb + static_cast<int64_t>(nb) * p.ld_sb;
-  const float *sbu = p.sb + static_cast<int64_t>(NB + nb) * p.ld_sb;
-  if (threadIdx.x < 8 * NT) tok_amax[threadIdx.x] = 0;
-  if (p.out.q) cluster_arrive_relaxed();
+  volatile int *abort_flag = &s_abort;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int half = rank >> 2, quarter = rank & 3;        // column half, K quarter
+  const int group = static_cast<int>(blockIdx.x) / (2 * kFewSplit);
+  const int F = p.out.F, c0 = group * 128 + half * 64;   // first column of h
+  const int m0 = static_cast<int>(blockIdx.y) * N;       // first token
+  const int per = (p.num_kb + kFewSplit - 1) / kFewSplit;
+  const int kb0 = min(quarter * per, p.num_kb), kb1 = min(kb0 + per, p.num_kb);
 
-  const uint8_t *wg[R], *wu[R], *xp[NT];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    wg[r] = p.b + static_cast<int64_t>(c0 + 8 * r + r8) * p.ldb + 16 * t4;
-    wu[r] = wg[r] + static_cast<int64_t>(F) * p.ldb;
-  }
-  bool tok_in[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    tok_in[n] = 8 * n + r8 < p.M;
-    xp[n] = p.a + static_cast<int64_t>(tok_in[n] ? 8 * n + r8 : 0) * p.lda + 16 * t4;
-  }
-  float acc[R][NT][4];
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[r][n][i] = 0.0f;
-  bool bad = false;
-
-#pragma unroll 2
-  for (int kb = warp; kb < p.num_kb; kb += kFewWarps) {
-    const int64_t off = static_cast<int64_t>(kb) * 128;
-    uint4 g[R][2], u[R][2], x[NT][2];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        g[r][i] = ld_stream_v4(wg[r] + off + 64 * i);
-        u[r][i] = ld_stream_v4(wu[r] + off + 64 * i);
-      }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        x[n][i] = tok_in[n] ? __ldg(reinterpret_cast<const uint4 *>(xp[n] + off + 64 * i))
-                            : make_uint4(0, 0, 0, 0);
-    float s_g = __ldg(sbg + kb), s_u = __ldg(sbu + kb);
-    if (kPow2) {
-      s_g = pow2_of(s_g, bad);
-      s_u = pow2_of(s_u, bad);
+  cluster_arrive_relaxed();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), 1);
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      // scales of this thread's two tokens, 8n + 2t and + 1
-      float s_x[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int m = 8 * n + 2 * t4 + i;
-        s_x[i] = m < p.M ? __ldg(p.sa + static_cast<int64_t>(kb) * p.ld_sa + m) : 0.0f;
-        if (kPow2 && m < p.M) s_x[i] = pow2_of(s_x[i], bad);
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          mma_e4m3_16x8x32(d, g[r][i].x, u[r][i].x, g[r][i].y, u[r][i].y, x[n][i].x, x[n][i].y);
-          mma_e4m3_16x8x32(d, g[r][i].z, u[r][i].z, g[r][i].w, u[r][i].w, x[n][i].z, x[n][i].w);
-        }
-        acc[r][n][0] = fmaf(d[0], s_x[0] * s_g, acc[r][n][0]);
-        acc[r][n][1] = fmaf(d[1], s_x[1] * s_g, acc[r][n][1]);
-        acc[r][n][2] = fmaf(d[2], s_x[0] * s_u, acc[r][n][2]);
-        acc[r][n][3] = fmaf(d[3], s_x[1] * s_u, acc[r][n][3]);
-      }
+    for (int i = 0; i < kFewBufs; ++i) {
+      mbar_init(smem_u32(&tfull[i]), 1);
+      mbar_init(smem_u32(&tempty[i]), 4);
     }
+    mbar_init(smem_u32(&drain), 1);
+    s_abort = 0;
+    fence_barrier_init();
   }
-  if (kPow2 && bad) atomicCAS(&g_glu_status, 0, FP8Q_ERR_INVALID);
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) red[warp][(r * NT + n) * 4 + i][lane] = acc[r][n][i];
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmW);
+    prefetch_tmap(&tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&s_tmem), C::kCols);
+    tc_fence_before();
+  }
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
 
-  // (token, column) values: 128 NT of them, item = ((r NT + n) 2 + i) 32 + lane
-  constexpr int kItems = R * NT * 2 * 32;
-  constexpr int kPer = (kItems + kFewWarps * 32 - 1) / (kFewWarps * 32);
-  float h[kPer];
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t armed = 0, armed_phase = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const int st = (kb - kb0) % C::kStages;
+        const uint32_t phase = static_cast<uint32_t>((kb - kb0) / C::kStages) & 1u;
+        ok = mbar_wait_bounded(smem_u32(&empty[st]), phase ^ 1, abort_flag, &g_glu_status,
+                               p.timeout_ns, FP8Q_ERR_TIMEOUT);
+        if (!ok) break;
+        const uint32_t fb = smem_u32(&full[st]);
+        mbar_arrive_expect_tx(fb, C::kWBytes + C::kXBytes);
+        tma_load_2d(sW + st * C::kWBytes, &tmW, fb, kb * 128, c0);
+        tma_load_2d(sW + st * C::kWBytes + C::kWBytes / 2, &tmW, fb, kb * 128, F + c0);
+        tma_load_2d(sX + st * C::kXBytes, &tmX, fb, kb * 128, m0);
+        armed |= 1u << st;
+        armed_phase = (armed_phase & ~(1u << st)) | (phase << st);
+      }
+      if (!ok)  // copies in flight land before the CTA's shared memory goes
+        for (int i = 0; i < C::kStages; ++i)
+          if (armed & (1u << i)) mbar_wait_drain(smem_u32(&full[i]), (armed_phase >> i) & 1);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      bool ok = true, issued = false;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const int i = kb - kb0, st = i % C::kStages, buf = i % kFewBufs;
+        ok = mbar_wait_bounded(smem_u32(&tempty[buf]),
+                               (static_cast<uint32_t>(i / kFewBufs) & 1u) ^ 1u, abort_flag,
+                               &g_glu_status, p.timeout_ns, FP8Q_ERR_TIMEOUT) &&
+             mbar_wait_bounded(smem_u32(&full[st]), static_cast<uint32_t>(i / C::kStages) & 1u,
+                               abort_flag, &g_glu_status, p.timeout_ns, FP8Q_ERR_TIMEOUT);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t wd = smem_desc_sw128(sW + st * C::kWBytes);
+        const uint64_t xd = smem_desc_sw128(sX + st * C::kXBytes);
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int item = static_cast<int>(threadIdx.x) + k * kFewWarps * 32;
-    h[k] = 0.0f;
-    if (item < kItems) {
-      const int l = item & 31, i = (item >> 5) & 1, rn = item >> 6;
-      const int m = 8 * (rn % NT) + 2 * (l & 3) + i, c = c0 + 8 * (rn / NT) + (l >> 2);
+        for (int k = 0; k < 4; ++k)
+          mma_f8f6f4(tmem + buf * N, wd + 2 * k, xd + 2 * k, idesc_e4m3_f32(128, N),
+                     k > 0 ? 1u : 0u);
+        mma_commit(smem_u32(&empty[st]));
+        mma_commit(smem_u32(&tfull[buf]));
+        issued = true;
+      }
+      if (!ok && issued) {  // MMAs in flight finish before TMEM is freed
+        mma_commit(smem_u32(&drain));
+        mbar_wait_drain(smem_u32(&drain), 0);
+      }
+    }
+  } else {
+    const int fw = warp & 3;  // TMEM lane quarter: weight rows 32 fw .. + 31: gate for fw < 2, then up
+    const float *sb = p.sb + static_cast<int64_t>(group + (fw < 2 ? 0 : F / 128)) * p.ld_sb;
+    constexpr int kPer = (N + 31) / 32;  // token scales per lane
+    uint64_t acc[N / 2];  // tokens 2i, 2i + 1
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) acc[i] = 0ull;
+    bool bad = false;
+    float x_nx[kPer], w_nx = 0.0f;
+    auto load = [&](int kb) {
+      w_nx = __ldg(sb + kb);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int m = m0 + lane + 32 * i;
+        x_nx[i] = lane + 32 * i < N && m < p.M
+                      ? __ldg(p.sa + static_cast<int64_t>(kb) * p.ld_sa + m)
+                      : 1.0f;
+      }
+    };
+    if (kb0 < kb1) load(kb0);
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const int i = kb - kb0, buf = i % kFewBufs;
+      float w = w_nx, x[kPer];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) x[j] = x_nx[j];
+      if (kb + 1 < kb1) load(kb + 1);
+      if (kPow2) {
+        w = pow2_of(w, bad);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) x[j] = pow2_of(x[j], bad);
+      }
+      // last read two groups ago, before the previous __syncwarp
+      float *sx = s_sa[fw][i & 1];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (lane + 32 * j < N) sx[lane + 32 * j] = w * x[j];
+      __syncwarp();
+      const bool got = mbar_wait_bounded(smem_u32(&tfull[buf]),
+                                         static_cast<uint32_t>(i / kFewBufs) & 1u, abort_flag,
+                                         &g_glu_status, p.timeout_ns, FP8Q_ERR_TIMEOUT);
+      ok = __all_sync(0xffffffffu, got);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(fw * 32) << 16) + buf * N;
+#pragma unroll
+      for (int c = 0; c < N / 16; ++c) {
+        uint32_t r[16];
+        tmem_ld_32x32b_x16(taddr + 16 * c, r);
+        tmem_wait_ld_tied(r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 sc = ld_shared_v4(smem_u32(sx + 16 * c + 4 * j));
+          ffma2(acc[8 * c + 2 * j], pack_u32x2(r[4 * j], r[4 * j + 1]), pack_u32x2(sc.x, sc.y));
+          ffma2(acc[8 * c + 2 * j + 1], pack_u32x2(r[4 * j + 2], r[4 * j + 3]),
+                pack_u32x2(sc.z, sc.w));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&tempty[buf]));
+    }
+    if (kPow2 && __any_sync(0xffffffffu, bad) && lane == 0)
+      atomicCAS(&g_glu_status, 0, FP8Q_ERR_INVALID);
+    tc_fence_before();
+    __syncwarp();
+    cluster_wait();  // every CTA of the cluster has started
+    // token n's sums go to the CTA that finishes it, at [K quarter][token][row]
+    const uint32_t mine = smem_u32(recv) + static_cast<uint32_t>(
+        (quarter * C::kQuarter * 128 + fw * 32 + lane) * 4);
+#pragma unroll
+    for (int d = 0; d < kFewSplit; ++d) {
+      const uint32_t dst = mapa_shared(mine, static_cast<uint32_t>(half * kFewSplit + d));
+#pragma unroll
+      for (int j = 0; j < C::kQuarter; ++j) {
+        const int n = d * C::kQuarter + j;
+        if (m0 + n < p.M) {
+          const float2 v = unpack_f32x2(acc[n / 2]);
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + j * 512), "f"(n & 1 ? v.y : v.x)
+                       : "memory");
+        }
+      }
+    }
+  }
+  if (warp < 2) {
+    __syncwarp();
+    cluster_wait();
+  }
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  }
+
+  // ---- this CTA's quarter of the tokens: 64 columns of h, two per lane
+  constexpr int kWarps = kFewThreads / 32;
+  constexpr int kTok = (C::kQuarter + kWarps - 1) / kWarps;  // tokens per warp
+  float h[kTok][2];
+#pragma unroll
+  for (int k = 0; k < kTok; ++k) {
+    const int j = warp + kWarps * k, m = m0 + quarter * C::kQuarter + j;
+    h[k][0] = h[k][1] = 0.0f;
+    if (j >= C::kQuarter || m >= p.M) continue;  // warp-uniform
+    float amax = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int col = lane + 32 * e;
       float g = 0.0f, u = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) {
-        g += red[w][rn * 4 + i][l];
-        u += red[w][rn * 4 + 2 + i][l];
+      for (int s = 0; s < kFewSplit; ++s) {
+        const float *src = recv + (s * C::kQuarter + j) * 128 + col;
+        g += src[0];
+        u += src[64];
       }
-      if (m < p.M) {
-        h[k] = silu(g) * u;
-        if (p.out.gu) {
-          uint16_t *row = static_cast<uint16_t *>(p.out.gu) + static_cast<int64_t>(m) * p.out.ld_gu;
-          row[c] = bf16_bits(g);
-          row[F + c] = bf16_bits(u);
-        }
-        if (p.out.h)
-          static_cast<uint16_t *>(p.out.h)[static_cast<int64_t>(m) * p.out.ldh + c] =
-              bf16_bits(h[k]);
-        // magnitudes order as their bits do
-        if (p.out.q) atomicMax(&tok_amax[m], __float_as_int(fabsf(h[k])));
+      h[k][e] = silu(g) * u;
+      amax = fmaxf(amax, fabsf(h[k][e]));
+      if (p.out.gu) {
+        uint16_t *row = static_cast<uint16_t *>(p.out.gu) + static_cast<int64_t>(m) * p.out.ld_gu;
+        row[c0 + col] = bf16_bits(g);
+        row[F + c0 + col] = bf16_bits(u);
       }
+      if (p.out.h)
+        static_cast<uint16_t *>(p.out.h)[static_cast<int64_t>(m) * p.out.ldh + c0 + col] =
+            bf16_bits(h[k][e]);
+    }
+    if (p.out.q) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      if (lane < 2)  // to both column halves of the group
+        st_cluster_f32(smem_u32(&s_amax[half][j]), static_cast<uint32_t>(lane * kFewSplit + quarter),
+                       amax);
     }
   }
   if (!p.out.q) return;  // the same in every CTA of the cluster
-  __syncthreads();
-  cluster_wait();  // every CTA of the cluster has started
-  const uint32_t rank = cluster_ctarank();
-  for (int i = threadIdx.x; i < 8 * 8 * NT; i += kFewWarps * 32)
-    st_cluster_f32(smem_u32(&cl_amax[rank][i >> 3]), static_cast<uint32_t>(i & 7),
-                   __int_as_float(tok_amax[i >> 3]));
   cluster_sync_all();
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int item = static_cast<int>(threadIdx.x) + k * kFewWarps * 32;
-    if (item >= kItems) continue;
-    const int l = item & 31, i = (item >> 5) & 1, rn = item >> 6;
-    const int mt = 8 * (rn % NT) + 2 * (l & 3) + i, c = 8 * (rn / NT) + (l >> 2);
-    if (mt >= p.M) continue;
-    float amax = cl_amax[0][mt];
-#pragma unroll
-    for (int j = 1; j < 8; ++j) amax = fmaxf(amax, cl_amax[j][mt]);
+  for (int k = 0; k < kTok; ++k) {
+    const int j = warp + kWarps * k, m = m0 + quarter * C::kQuarter + j;
+    if (j >= C::kQuarter || m >= p.M) continue;
     float sc, inv;
-    group_scale(amax, p.out.pow2 != 0, sc, inv);
-    p.out.q[static_cast<int64_t>(mt) * p.out.ldq + c0 + c] =
-        static_cast<uint8_t>(pack_e4m3x2(__fmul_rn(h[k], inv), 0.0f) & 0xFFu);
-    if (rank == 0 && c == 0) p.out.s[static_cast<int64_t>(nb) * p.out.ld_s + mt] = sc;
+    group_scale(fmaxf(s_amax[0][j], s_amax[1][j]), p.out.pow2 != 0, sc, inv);
+    uint8_t *row = p.out.q + static_cast<int64_t>(m) * p.out.ldq + c0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      row[lane + 32 * e] =
+          static_cast<uint8_t>(pack_e4m3x2(__fmul_rn(h[k][e], inv), 0.0f) & 0xFFu);
+    if (half == 0 && lane == 0) p.out.s[static_cast<int64_t>(group) * p.out.ld_s + m] = sc;
   }
 }
 
-template <bool kPow2>
+template <int N, bool kPow2>
 fp8q_status launch_few(const GluIn &in, const GluOut &out, cudaStream_t s) {
+  using C = Few<N>;
+  auto kern = glu_few_tokens_kernel<N, kPow2>;
+  static bool attr_set[kMaxDevices] = {};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FP8Q_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!attr_set[dev]) {
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(C::kSmem)) != cudaSuccess)
+        return FP8Q_ERR_CUDA;
+      attr_set[dev] = true;
+    }
+  }
+  // K == 0: no loads happen; describe a dummy 1 x 128 tensor so the maps are valid
+  const bool k0 = in.K == 0;
+  const void *any = out.h ? out.h : out.gu ? out.gu : out.q;
+  CUtensorMap tw, tx;
+  if (!make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, k0 ? any : in.b, k0 ? 1 : 2 * in.F,
+                    k0 ? 128 : in.K, k0 ? 128 : in.ldb, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, k0 ? any : in.a, k0 ? 1 : in.M,
+                    k0 ? 128 : in.K, k0 ? 128 : in.lda, 128, N, CU_TENSOR_MAP_SWIZZLE_128B))
+    return FP8Q_ERR_CUDA;
   FewArgs a{};
-  a.a = static_cast<const uint8_t *>(in.a);
-  a.lda = in.lda;
   a.sa = in.sa;
   a.ld_sa = in.ld_sa;
-  a.b = static_cast<const uint8_t *>(in.b);
-  a.ldb = in.ldb;
   a.sb = in.sb;
   a.ld_sb = in.ld_sb;
   a.M = static_cast<int>(in.M);
   a.num_kb = static_cast<int>(in.K / 128);
   a.out = out;
-  const dim3 grid(static_cast<unsigned>(in.F / 16)), block(kFewWarps * 32);
-  switch ((in.M + 7) / 8) {
-    case 1: return launch_on(glu_few_tokens_kernel<1, kPow2>, grid, block, 0, s, a);
-    case 2: return launch_on(glu_few_tokens_kernel<2, kPow2>, grid, block, 0, s, a);
-    case 3: return launch_on(glu_few_tokens_kernel<3, kPow2>, grid, block, 0, s, a);
-    default: return launch_on(glu_few_tokens_kernel<4, kPow2>, grid, block, 0, s, a);
-  }
+  a.timeout_ns = wait_timeout_ns().load();
+  const dim3 grid(static_cast<unsigned>(in.F / 128 * 2 * kFewSplit),
+                  static_cast<unsigned>((in.M + N - 1) / N));
+  return launch_on(kern, grid, dim3(kFewThreads), C::kSmem, s, tw, tx, a);
+}
+
+template <bool kPow2>
+fp8q_status launch_few(const GluIn &in, const GluOut &out, cudaStream_t s) {
+  return in.M <= 16   ? launch_few<16, kPow2>(in, out, s)
+         : in.M <= 32 ? launch_few<32, kPow2>(in, out, s)
+                      : launch_few<64, kPow2>(in, out, s);
+}
+
+// Blocks of 64 tokens share the weights through L2, so a little more than one
+// wave of the few-token kernel's CTAs (two per SM) still beats the GEMMs' tiles,
+// which take the time of a whole K loop however few they are.
+bool few_tokens(const GluIn &in) {
+  return in.M <= 64 || in.F / 16 * ((in.M + 63) / 64) <= 512;
 }
 
 bool valid_mode(int m) { return m == FP8Q_SCALE_FP32 || m == FP8Q_SCALE_POW2; }
@@ -325,7 +466,7 @@ fp8q_status glu_entry(const GluIn &in, const GluOut &o, int scale_mode, bool pow
   DeviceInfo dev;
   if (fp8q_status st = device_info(dev)) return st;
   auto s = static_cast<cudaStream_t>(stream);
-  if (!grouped && in.M <= kFewTokens)
+  if (!grouped && few_tokens(in))
     return pow2 ? launch_few<true>(in, o, s) : launch_few<false>(in, o, s);
   return pow2 && in.K > 0 ? gemm_mx_glu(in, o, s) : gemm_glu(in, o, s);
 }
