@@ -509,34 +509,33 @@ GluOut glu_out(void *h, int64_t ldh, void *gu, int64_t ld_gu, void *q, int64_t l
 
 // ------------------------------------------------------------------ backward
 // Memory bound: dh, g and u are read once (6 bytes per element of h) and every
-// requested result is written from the same registers.
-//  - A cluster of kCl CTAs covers a tile of 128 tokens x 128 columns of h, each
-//    CTA 128 / kCl columns; a thread holds 4 tokens x 8 columns of dg, du and h
-//    (16-byte loads, whole token rows of a CTA's columns per instruction).
+// requested result is written from the same registers.  The kernel is
+// persistent, two CTAs of 256 threads per SM, and TMA brings in the next tile
+// while this one is turned into codes.
+//  - A cluster of two CTAs covers a tile of 128 tokens x 128 columns of h, each
+//    CTA 64 columns; a thread holds 4 tokens x 8 columns of dg, du and h as
+//    packed FP32 pairs (96 registers; two-lane multiplies, three-input maxima).
 //  - 1x128 max-abs (dg and du, per token): shuffles over a token's threads,
-//    then one value per token and CTA to every CTA of the cluster through
-//    distributed shared memory.  128x1 max-abs (dg, du, h, per column):
-//    shuffles over a warp's tokens, then an atomic max on the values' bits in
-//    shared memory (magnitudes order as their bits do; the result does not
-//    depend on the order).
+//    then one value per token and CTA to both CTAs through distributed shared
+//    memory.  128x1 max-abs (dg, du, h, per column): shuffles over a warp's
+//    tokens, then an atomic max on the values' bits in shared memory
+//    (magnitudes order as their bits do; the result does not depend on the
+//    order).
 //  - One thread per group turns a max-abs into its scale, so that the two IEEE
 //    divisions are done once per group.
 //  - The transposed codes pass through shared memory: a thread's 4 tokens of a
 //    column are one 32-bit word; word w of column row r sits at w ^ f(r), which
 //    spreads a warp's words over all banks on the way in and keeps 16-byte
 //    units whole on the way out, where eight lanes write a column's 128 bytes.
-constexpr int kCl = 2;
-constexpr int kChan = 128 / kCl;               // columns of h per CTA
-constexpr int kBwdThreads = 4 * kChan;         // 32 token quads x kChan / 8 column octets
-constexpr int kLW = kChan / 8;                 // lanes across a token row
-constexpr int kRowsPerWarp = 32 / kLW;         // token quads per warp
-static_assert(kCl == 2, "the swizzle below keeps 16-byte units whole for two CTAs per tile");
+// An abandoned wait leaves the loop's barriers in place (the cluster's CTAs
+// make the same number of steps) and only stops the copies and the stores.
+constexpr int kChan = 64;                      // columns of h per CTA
+constexpr int kBwdThreads = 256;               // 32 token quads x 8 column octets
+constexpr int kBwdCtasPerSm = 2;
+constexpr uint32_t kRawBytes = 128 * kChan * 2;  // one input's tile of a CTA
+constexpr uint32_t kXposeBytes = kChan * 128;    // one transposed tile of codes
 
 struct BwdArgs {
-  const uint16_t *dh;
-  int64_t ld_dh;
-  const uint16_t *gu;
-  int64_t ld_gu;
   uint16_t *d;
   int64_t ld_d;
   uint8_t *q;
@@ -552,208 +551,339 @@ struct BwdArgs {
   float *shT;
   int64_t ld_shT;
   int64_t T, F;
+  int ncb, ntb;  // 128-wide column blocks, token blocks
   int pow2;
+  uint64_t timeout_ns;
 };
 
 __device__ __forceinline__ uint32_t xpose_word(uint32_t r, uint32_t w) {
-  return r * 32u + (w ^ (static_cast<uint32_t>(kRowsPerWarp) * ((r >> 3) % kLW)));
+  return r * 32u + (w ^ (4u * ((r >> 3) & 7u)));
+}
+// max(|a|, |b|, |c|)
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Four FP32 values -> four E4M3 codes, a in the low byte.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+__device__ __forceinline__ uint32_t codes4(uint64_t ab, uint64_t cd) {
+  const float2 x = unpack_f32x2(ab), y = unpack_f32x2(cd);
+  return codes4(x.x, x.y, y.x, y.y);
+}
+__device__ __forceinline__ uint64_t bf16_pair(uint32_t w) {
+  return pack_f32x2(bf16_lo(w), bf16_hi(w));
 }
 
 template <bool kRows, bool kCols, bool kH>
-__global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kBwdThreads, 512 / kBwdThreads)
-    swiglu_bwd_kernel(const BwdArgs p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, kBwdCtasPerSm)
+    swiglu_bwd_kernel(const __grid_constant__ CUtensorMap tmD,
+                      const __grid_constant__ CUtensorMap tmG, const BwdArgs p) {
   constexpr int kColArrays = (kCols ? 2 : 0) + (kH ? 1 : 0);  // dg, du | h
   constexpr int kH0 = kCols ? 2 : 0;                          // h's place among them
-  __shared__ float row_amax[kRows ? kCl : 1][2][128];         // [CTA of the cluster][dg, du][token]
+  extern __shared__ uint8_t dsm_raw[];
+  uint8_t *raw = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(dsm_raw) + 127) & ~static_cast<uintptr_t>(127));
+  uint32_t *xpose = reinterpret_cast<uint32_t *>(raw + 3 * kRawBytes);
+  __shared__ float row_amax[2][2][2][128];  // [step parity][CTA of the cluster][dg, du][token]
   __shared__ float row_inv[2][128];
   __shared__ __align__(16) uint32_t col_bits[3][kChan];
   __shared__ __align__(16) float col_inv[3][kChan];
-  __shared__ __align__(16) uint32_t xpose[kColArrays > 0 ? kColArrays : 1][kColArrays > 0 ? kChan * 32 : 4];
+  __shared__ uint64_t full;
+  __shared__ int abort_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int l8 = lane % kLW;                               // column octet
-  const int quad = warp * kRowsPerWarp + lane / kLW;       // token quad
-  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 128;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kChan;
-  const int64_t c = c0 + 8 * l8;
+  const int l8 = lane & 7;                     // column octet
+  const int quad = 4 * warp + (lane >> 3);     // token quad
   const uint32_t rank = cluster_ctarank();
   if (kRows) cluster_arrive_relaxed();
-  if (kColArrays > 0) {
-    for (int i = tid; i < kColArrays * kChan; i += kBwdThreads) (&col_bits[0][0])[i] = 0u;
-    __syncthreads();
-  }
 
-  uint4 rd[4], rg[4], ru[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t t = t0 + 4 * quad + i;
-    rd[i] = rg[i] = ru[i] = make_uint4(0, 0, 0, 0);
-    if (t < p.T) {
-      rd[i] = ld_stream_v4(p.dh + t * p.ld_dh + c);
-      rg[i] = ld_stream_v4(p.gu + t * p.ld_gu + c);
-      ru[i] = ld_stream_v4(p.gu + t * p.ld_gu + p.F + c);
+  // tile t = (token block t / ncb, column block t % ncb), column blocks fastest;
+  // this cluster takes every (gridDim.x / 2)-th, walked incrementally
+  const uint32_t ncb = static_cast<uint32_t>(p.ncb), ntb = static_cast<uint32_t>(p.ntb);
+  const uint32_t clusters = gridDim.x >> 1, id = blockIdx.x >> 1;
+  const uint32_t dcb = clusters % ncb, dtb = clusters / ncb;
+  uint32_t cb = id % ncb, tb = id / ncb;
+  auto step = [&]() {
+    cb += dcb;
+    tb += dtb;
+    if (cb >= ncb) {
+      cb -= ncb;
+      ++tb;
+    }
+  };
+  auto issue = [&](uint32_t cbn, uint32_t tbn) {
+    const uint32_t bar = smem_u32(&full), dst = smem_u32(raw);
+    const int32_t c = static_cast<int32_t>(cbn * 128u + rank * kChan);
+    const int32_t t = static_cast<int32_t>(tbn * 128u);
+    mbar_arrive_expect_tx(bar, 3 * kRawBytes);
+    tma_load_2d(dst, &tmD, bar, c, t);
+    tma_load_2d(dst + kRawBytes, &tmG, bar, c, t);
+    tma_load_2d(dst + 2 * kRawBytes, &tmG, bar, static_cast<int32_t>(p.F) + c, t);
+  };
+  bool pending = false;  // thread 0: a copy is on its way
+  if (tid == 0) {
+    abort_flag = 0;
+    mbar_init(smem_u32(&full), 1);
+    fence_barrier_init();
+    if (tb < ntb) {
+      issue(cb, tb);
+      pending = true;
     }
   }
-  float dg[4][8], du[4][8], h[4][8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t wd[4] = {rd[i].x, rd[i].y, rd[i].z, rd[i].w};
-    const uint32_t wg[4] = {rg[i].x, rg[i].y, rg[i].z, rg[i].w};
-    const uint32_t wu[4] = {ru[i].x, ru[i].y, ru[i].z, ru[i].w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float y = j & 1 ? bf16_hi(wd[j / 2]) : bf16_lo(wd[j / 2]);
-      const float g = j & 1 ? bf16_hi(wg[j / 2]) : bf16_lo(wg[j / 2]);
-      const float u = j & 1 ? bf16_hi(wu[j / 2]) : bf16_lo(wu[j / 2]);
-      const float sg = __fdividef(1.0f, 1.0f + __expf(-g));
-      const float sl = g * sg;
-      du[i][j] = y * sl;
-      dg[i][j] = y * u * fmaf(sl, 1.0f - sg, sg);
-      if (kH) h[i][j] = sl * u;
-    }
-    if (p.d) {
-      const int64_t t = t0 + 4 * quad + i;
-      if (t < p.T) {
-        uint16_t *dst = p.d + t * p.ld_d + c;
-        *reinterpret_cast<uint4 *>(dst) =
-            make_uint4(bf16x2_bits(dg[i][0], dg[i][1]), bf16x2_bits(dg[i][2], dg[i][3]),
-                       bf16x2_bits(dg[i][4], dg[i][5]), bf16x2_bits(dg[i][6], dg[i][7]));
-        *reinterpret_cast<uint4 *>(dst + p.F) =
-            make_uint4(bf16x2_bits(du[i][0], du[i][1]), bf16x2_bits(du[i][2], du[i][3]),
-                       bf16x2_bits(du[i][4], du[i][5]), bf16x2_bits(du[i][6], du[i][7]));
-      }
-    }
-  }
-  if (!kRows && kColArrays == 0) return;
-
-  // ---- max-abs of the groups
-  if (kRows) {
-    cluster_wait();  // every CTA of the cluster has started
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float a = 0.0f, b = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        a = fmaxf(a, fabsf(dg[i][j]));
-        b = fmaxf(b, fabsf(du[i][j]));
-      }
-#pragma unroll
-      for (int o = kLW / 2; o > 0; o >>= 1) {
-        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
-      }
-      if (l8 < kCl) {  // lane l8 of a token serves CTA l8
-        st_cluster_f32(smem_u32(&row_amax[rank][0][4 * quad + i]), static_cast<uint32_t>(l8), a);
-        st_cluster_f32(smem_u32(&row_amax[rank][1][4 * quad + i]), static_cast<uint32_t>(l8), b);
-      }
-    }
-  }
-  if (kColArrays > 0) {
-#pragma unroll
-    for (int k = 0; k < kColArrays; ++k) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float a = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          a = fmaxf(a, fabsf(kH && k == kH0 ? h[i][j] : k == 0 ? dg[i][j] : du[i][j]));
-#pragma unroll
-        for (int o = kLW; o < 32; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        // the warp's token quads share the atomics: quad (j mod kRowsPerWarp)
-        if (lane / kLW == j % kRowsPerWarp)
-          atomicMax(&col_bits[k][8 * l8 + j], __float_as_uint(a));
-      }
-    }
-  }
-  if (kRows) cluster_sync_all();
-  else __syncthreads();
-
-  // ---- scales, one group per thread
-  if (kRows) {
-    for (int i = tid; i < 256; i += kBwdThreads) {
-      const int k = i >> 7, t = i & 127;
-      float a = row_amax[0][k][t];
-#pragma unroll
-      for (int j = 1; j < kCl; ++j) a = fmaxf(a, row_amax[j][k][t]);
-      float sc, inv;
-      group_scale(a, p.pow2 != 0, sc, inv);
-      row_inv[k][t] = inv;
-      if (rank == 0 && t0 + t < p.T)
-        p.s[(k * (p.F / 128) + c0 / 128) * p.ld_s + t0 + t] = sc;
-    }
-  }
-  if (kColArrays > 0) {
-    for (int i = tid; i < kColArrays * kChan; i += kBwdThreads) {
-      const int k = i / kChan, cc = i % kChan;
-      float sc, inv;
-      group_scale(__uint_as_float(col_bits[k][cc]), p.pow2 != 0, sc, inv);
-      col_inv[k][cc] = inv;
-      if (kH && k == kH0) p.shT[(t0 / 128) * p.ld_shT + c0 + cc] = sc;
-      else p.sT[(t0 / 128) * p.ld_sT + k * p.F + c0 + cc] = sc;
-    }
-  }
+  for (int i = tid; i < 3 * kChan; i += kBwdThreads) (&col_bits[0][0])[i] = 0u;
   __syncthreads();
+  if (kRows) cluster_wait();  // every CTA of the cluster has started
 
-  // ---- codes
-  if (kRows) {
+  const uint64_t log2e2 = pack_f32x2(-1.4426950408889634f, -1.4426950408889634f);
+  const uint64_t one2 = pack_f32x2(1.0f, 1.0f), neg2 = pack_f32x2(-1.0f, -1.0f);
+  bool ok = true;
+  for (uint32_t it = 0; tb < ntb; ++it) {
+    const int64_t t0 = static_cast<int64_t>(tb) * 128;
+    const int64_t c0 = static_cast<int64_t>(cb) * 128 + rank * kChan;
+    const int64_t c = c0 + 8 * l8;
+    const bool got = mbar_wait_bounded(smem_u32(&full), it & 1u, &abort_flag, &g_glu_status,
+                                       p.timeout_ns, FP8Q_ERR_TIMEOUT);
+    ok = ok && __all_sync(0xffffffffu, got);
+    if (tid == 0 && ok) pending = false;
+
+    // ---- dg, du, h of 4 tokens x 8 columns, as pairs of neighbouring columns
+    uint64_t dg[4][4], du[4][4], h[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int tl = 4 * quad + i;
-      if (t0 + tl < p.T) {
-        uint8_t *dst = p.q + (t0 + tl) * p.ldq + c;
-        const float a = row_inv[0][tl], b = row_inv[1][tl];
-        const uint64_t a2 = pack_f32x2(a, a), b2 = pack_f32x2(b, b);
-        uint32_t w[4];
+      const uint32_t src = smem_u32(raw) + static_cast<uint32_t>(4 * quad + i) * 128u + 16u * l8;
+      const uint4 vd = ld_shared_v4(src), vg = ld_shared_v4(src + kRawBytes),
+                  vu = ld_shared_v4(src + 2 * kRawBytes);
+      const uint32_t wd[4] = {vd.x, vd.y, vd.z, vd.w}, wg[4] = {vg.x, vg.y, vg.z, vg.w},
+                     wu[4] = {vu.x, vu.y, vu.z, vu.w};
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float2 x = unpack_f32x2(fmul2(pack_f32x2(dg[i][4 * e], dg[i][4 * e + 1]), a2));
-          const float2 y = unpack_f32x2(fmul2(pack_f32x2(dg[i][4 * e + 2], dg[i][4 * e + 3]), a2));
-          w[e] = pack_e4m3x4(x.x, x.y, y.x, y.y);
-          const float2 v = unpack_f32x2(fmul2(pack_f32x2(du[i][4 * e], du[i][4 * e + 1]), b2));
-          const float2 z = unpack_f32x2(fmul2(pack_f32x2(du[i][4 * e + 2], du[i][4 * e + 3]), b2));
-          w[2 + e] = pack_e4m3x4(v.x, v.y, z.x, z.y);
-        }
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-        *reinterpret_cast<uint2 *>(dst + p.F) = make_uint2(w[2], w[3]);
+      for (int k = 0; k < 4; ++k) {
+        const uint64_t y = bf16_pair(wd[k]), g = bf16_pair(wg[k]), u = bf16_pair(wu[k]);
+        const float2 x = unpack_f32x2(fmul2(g, log2e2));
+        const float2 e = unpack_f32x2(fadd2(pack_f32x2(ex2_ftz(x.x), ex2_ftz(x.y)), one2));
+        const uint64_t s = pack_f32x2(rcp_ftz(e.x), rcp_ftz(e.y));
+        const uint64_t sl = fmul2(g, s);  // silu(g)
+        du[i][k] = fmul2(y, sl);
+        dg[i][k] = fmul2(fmul2(y, u), fma2(sl, fma2(s, neg2, one2), s));
+        if (kH) h[i][k] = fmul2(sl, u);
       }
     }
-  }
-  if (kColArrays > 0) {
+    if (p.d && ok) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t t = t0 + 4 * quad + i;
+        if (t < p.T) {
+          uint16_t *dst = p.d + t * p.ld_d + c;
+          uint32_t w[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 a = unpack_f32x2(dg[i][k]), b = unpack_f32x2(du[i][k]);
+            w[k] = bf16x2_bits(a.x, a.y);
+            w[4 + k] = bf16x2_bits(b.x, b.y);
+          }
+          *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4 *>(dst + p.F) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      }
+    }
+
+    // ---- max-abs of the groups
+    if (kRows) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float a = 0.0f, b = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 x = unpack_f32x2(dg[i][k]), y = unpack_f32x2(du[i][k]);
+          a = max3_abs(a, x.x, x.y);
+          b = max3_abs(b, y.x, y.y);
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) {
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+          b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+        }
+        // lanes 0-1 of a token take dg to the two CTAs, lanes 2-3 du
+        if (l8 < 4)
+          st_cluster_f32(smem_u32(&row_amax[it & 1][rank][l8 >> 1][4 * quad + i]),
+                         static_cast<uint32_t>(l8 & 1), l8 < 2 ? a : b);
+      }
+    }
 #pragma unroll
     for (int k = 0; k < kColArrays; ++k) {
-      float inv[8];
-      *reinterpret_cast<float4 *>(&inv[0]) = *reinterpret_cast<const float4 *>(&col_inv[k][8 * l8]);
-      *reinterpret_cast<float4 *>(&inv[4]) =
-          *reinterpret_cast<const float4 *>(&col_inv[k][8 * l8 + 4]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         float v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[i] = kH && k == kH0 ? h[i][j] : k == 0 ? dg[i][j] : du[i][j];
-        const uint64_t i2 = pack_f32x2(inv[j], inv[j]);
-        const float2 x = unpack_f32x2(fmul2(pack_f32x2(v[0], v[1]), i2));
-        const float2 y = unpack_f32x2(fmul2(pack_f32x2(v[2], v[3]), i2));
-        xpose[k][xpose_word(8 * l8 + j, quad)] = pack_e4m3x4(x.x, x.y, y.x, y.y);
+        for (int i = 0; i < 4; ++i) {
+          const float2 x =
+              unpack_f32x2(kH && k == kH0 ? h[i][j / 2] : k == 0 ? dg[i][j / 2] : du[i][j / 2]);
+          v[i] = j & 1 ? x.y : x.x;
+        }
+        float a = max3_abs(max3_abs(v[0], v[1], v[2]), v[3], 0.0f);
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 8));
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16));
+        // the warp's four token quads share the atomics
+        if ((lane >> 3) == (j & 3)) atomicMax(&col_bits[k][8 * l8 + j], __float_as_uint(a));
+      }
+    }
+    if (kRows) cluster_sync_all();
+    else __syncthreads();
+    // every thread has read the raw tile: the next one may come
+    const uint32_t cbc = cb;
+    step();
+    if (tid == 0 && ok && tb < ntb) {
+      fence_proxy_async_shared();
+      issue(cb, tb);
+      pending = true;
+    }
+    if (!kRows && kColArrays == 0) continue;
+
+    // ---- scales, one group per thread at a time
+    if (kRows) {
+      const int k = tid >> 7, t = tid & 127;
+      const float a = fmaxf(row_amax[it & 1][0][k][t], row_amax[it & 1][1][k][t]);
+      float sc, inv;
+      group_scale(a, p.pow2 != 0, sc, inv);
+      row_inv[k][t] = inv;
+      if (rank == 0 && ok && t0 + t < p.T)
+        p.s[(static_cast<int64_t>(k) * p.ncb + cbc) * p.ld_s + t0 + t] = sc;
+    }
+    if (kColArrays > 0 && tid < kColArrays * kChan) {
+      const int k = tid / kChan, cc = tid % kChan;
+      float sc, inv;
+      group_scale(__uint_as_float(col_bits[k][cc]), p.pow2 != 0, sc, inv);
+      col_bits[k][cc] = 0u;
+      col_inv[k][cc] = inv;
+      if (ok) {
+        if (kH && k == kH0) p.shT[(t0 / 128) * p.ld_shT + c0 + cc] = sc;
+        else p.sT[(t0 / 128) * p.ld_sT + k * p.F + c0 + cc] = sc;
       }
     }
     __syncthreads();
-    // eight lanes write the 128 tokens of a column
-    for (int i = tid; i < kColArrays * kChan * 8; i += kBwdThreads) {
-      const int k = i / (kChan * 8), r = (i >> 3) % kChan, ch = i & 7;
-      const uint4 v = *reinterpret_cast<const uint4 *>(&xpose[k][xpose_word(r, 4 * ch)]);
-      uint8_t *dst = kH && k == kH0
-                         ? p.hT + (c0 + r) * p.ld_hT + t0 + 16 * ch
-                         : p.qT + (k * p.F + c0 + r) * p.ldqT + t0 + 16 * ch;
-      *reinterpret_cast<uint4 *>(dst) = v;
+
+    // ---- codes
+    if (kRows && ok) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tl = 4 * quad + i;
+        if (t0 + tl < p.T) {
+          uint8_t *dst = p.q + (t0 + tl) * p.ldq + c;
+          const float a = row_inv[0][tl], b = row_inv[1][tl];
+          const uint64_t a2 = pack_f32x2(a, a), b2 = pack_f32x2(b, b);
+          *reinterpret_cast<uint2 *>(dst) =
+              make_uint2(codes4(fmul2(dg[i][0], a2), fmul2(dg[i][1], a2)),
+                         codes4(fmul2(dg[i][2], a2), fmul2(dg[i][3], a2)));
+          *reinterpret_cast<uint2 *>(dst + p.F) =
+              make_uint2(codes4(fmul2(du[i][0], b2), fmul2(du[i][1], b2)),
+                         codes4(fmul2(du[i][2], b2), fmul2(du[i][3], b2)));
+        }
+      }
+    }
+    if (kColArrays > 0) {
+#pragma unroll
+      for (int k = 0; k < kColArrays; ++k) {
+        const ulonglong2 i01 = *reinterpret_cast<const ulonglong2 *>(&col_inv[k][8 * l8]);
+        const ulonglong2 i23 = *reinterpret_cast<const ulonglong2 *>(&col_inv[k][8 * l8 + 4]);
+        const uint64_t inv[4] = {i01.x, i01.y, i23.x, i23.y};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[i] = unpack_f32x2(
+                fmul2(kH && k == kH0 ? h[i][j] : k == 0 ? dg[i][j] : du[i][j], inv[j]));
+          uint32_t *row = xpose + k * (kXposeBytes / 4);
+          row[xpose_word(8 * l8 + 2 * j, quad)] = codes4(v[0].x, v[1].x, v[2].x, v[3].x);
+          row[xpose_word(8 * l8 + 2 * j + 1, quad)] = codes4(v[0].y, v[1].y, v[2].y, v[3].y);
+        }
+      }
+      __syncthreads();
+      // eight lanes write the 128 tokens of a column
+      if (ok) {
+#pragma unroll
+        for (int k = 0; k < kColArrays; ++k)
+#pragma unroll
+          for (int i = 0; i < kChan * 8 / kBwdThreads; ++i) {
+            const int r = (tid >> 3) + 32 * i, ch = tid & 7;
+            const uint4 v = *reinterpret_cast<const uint4 *>(
+                &xpose[k * (kXposeBytes / 4) + xpose_word(r, 4 * ch)]);
+            uint8_t *dst = kH && k == kH0 ? p.hT + (c0 + r) * p.ld_hT + t0 + 16 * ch
+                                          : p.qT + (k * p.F + c0 + r) * p.ldqT + t0 + 16 * ch;
+            *reinterpret_cast<uint4 *>(dst) = v;
+          }
+      }
+    }
+  }
+  // a copy still in flight after an abandoned wait lands before the CTA's shared
+  // memory goes
+  if (tid == 0 && pending) {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 1000000ull) {
     }
   }
 }
 
+template <bool kRows, bool kCols, bool kH>
+fp8q_status launch_bwd(const CUtensorMap &tmD, const CUtensorMap &tmG, const BwdArgs &a,
+                       cudaStream_t s) {
+  auto kern = swiglu_bwd_kernel<kRows, kCols, kH>;
+  constexpr size_t smem = 128 + 3 * kRawBytes + ((kCols ? 2 : 0) + (kH ? 1 : 0)) * kXposeBytes;
+  static bool attr_set[kMaxDevices] = {};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FP8Q_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!attr_set[dev]) {
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(smem)) != cudaSuccess)
+        return FP8Q_ERR_CUDA;
+      attr_set[dev] = true;
+    }
+  }
+  DeviceInfo info;
+  if (fp8q_status st = device_info(info)) return st;
+  const int64_t tiles = static_cast<int64_t>(a.ncb) * a.ntb;
+  const int64_t room = static_cast<int64_t>(info.sm_count) * kBwdCtasPerSm / 2;
+  return launch_on(kern, dim3(static_cast<unsigned>(2 * (tiles < room ? tiles : room))),
+                   dim3(kBwdThreads), smem, s, tmD, tmG, a);
+}
+
 template <bool kRows, bool kCols>
-fp8q_status launch_bwd(const BwdArgs &a, dim3 grid, cudaStream_t s) {
-  return a.hT ? launch_on(swiglu_bwd_kernel<kRows, kCols, true>, grid, dim3(kBwdThreads), 0, s, a)
-              : launch_on(swiglu_bwd_kernel<kRows, kCols, false>, grid, dim3(kBwdThreads), 0, s, a);
+fp8q_status launch_bwd(const CUtensorMap &tmD, const CUtensorMap &tmG, const BwdArgs &a,
+                       cudaStream_t s) {
+  return a.hT ? launch_bwd<kRows, kCols, true>(tmD, tmG, a, s)
+              : launch_bwd<kRows, kCols, false>(tmD, tmG, a, s);
 }
 
 }  // namespace
@@ -827,10 +957,6 @@ extern "C" fp8q_status fp8q_swiglu_bwd(const void *dh, int64_t ld_dh, const void
   DeviceInfo dev;
   if (fp8q_status st = device_info(dev)) return st;
   BwdArgs a{};
-  a.dh = static_cast<const uint16_t *>(dh);
-  a.ld_dh = ld_dh;
-  a.gu = static_cast<const uint16_t *>(gu);
-  a.ld_gu = ld_gu;
   a.d = static_cast<uint16_t *>(d);
   a.ld_d = ld_d;
   a.q = static_cast<uint8_t *>(q);
@@ -848,8 +974,17 @@ extern "C" fp8q_status fp8q_swiglu_bwd(const void *dh, int64_t ld_dh, const void
   a.T = T;
   a.F = F;
   a.pow2 = scale_mode == FP8Q_SCALE_POW2;
-  const dim3 grid(static_cast<unsigned>(F / kChan), static_cast<unsigned>((T + 127) / 128));
+  a.ncb = static_cast<int>(F / 128);
+  a.ntb = static_cast<int>((T + 127) / 128);
+  a.timeout_ns = wait_timeout_ns().load();
+  CUtensorMap tmD, tmG;
+  if (!make_tmap_2d(&tmD, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dh, T, F, ld_dh * 2, kChan, 128,
+                    CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !make_tmap_2d(&tmG, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, gu, T, 2 * F, ld_gu * 2, kChan, 128,
+                    CU_TENSOR_MAP_SWIZZLE_NONE))
+    return FP8Q_ERR_CUDA;
   auto st = static_cast<cudaStream_t>(stream);
-  if (q) return qT ? launch_bwd<true, true>(a, grid, st) : launch_bwd<true, false>(a, grid, st);
-  return qT ? launch_bwd<false, true>(a, grid, st) : launch_bwd<false, false>(a, grid, st);
+  if (q)
+    return qT ? launch_bwd<true, true>(tmD, tmG, a, st) : launch_bwd<true, false>(tmD, tmG, a, st);
+  return qT ? launch_bwd<false, true>(tmD, tmG, a, st) : launch_bwd<false, false>(tmD, tmG, a, st);
 }
