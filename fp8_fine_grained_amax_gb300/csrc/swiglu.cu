@@ -515,25 +515,27 @@ GluOut glu_out(void *h, int64_t ldh, void *gu, int64_t ld_gu, void *q, int64_t l
 //  - A cluster of two CTAs covers a tile of 128 tokens x 128 columns of h, each
 //    CTA 64 columns; a thread holds 4 tokens x 8 columns of dg, du and h as
 //    packed FP32 pairs (96 registers; two-lane multiplies, three-input maxima).
-//  - 1x128 max-abs (dg and du, per token): shuffles over a token's threads,
-//    then one value per token and CTA to both CTAs through distributed shared
-//    memory.  128x1 max-abs (dg, du, h, per column): shuffles over a warp's
-//    tokens, then an atomic max on the values' bits in shared memory
-//    (magnitudes order as their bits do; the result does not depend on the
-//    order).
+//  - 1x128 max-abs (dg and du, per token): a halving exchange over a token's
+//    eight threads (each ends with one of the eight maxima), then one value per
+//    token and CTA to both CTAs by st.async, which completes on the receiver's
+//    mbarrier: a cluster barrier would make every step wait for all of its
+//    global stores (46 us against 36 at 8192 x 2048).  128x1 max-abs (dg, du, h, per column): each thread's four
+//    tokens go to shared memory, and one thread per column takes the maximum of
+//    the 32 token quads.
 //  - One thread per group turns a max-abs into its scale, so that the two IEEE
 //    divisions are done once per group.
 //  - The transposed codes pass through shared memory: a thread's 4 tokens of a
 //    column are one 32-bit word; word w of column row r sits at w ^ f(r), which
 //    spreads a warp's words over all banks on the way in and keeps 16-byte
 //    units whole on the way out, where eight lanes write a column's 128 bytes.
-// An abandoned wait leaves the loop's barriers in place (the cluster's CTAs
-// make the same number of steps) and only stops the copies and the stores.
+// An abandoned wait only stops the copies and the stores; every thread still
+// walks the loop and its CTA barriers to the end.
 constexpr int kChan = 64;                      // columns of h per CTA
 constexpr int kBwdThreads = 256;               // 32 token quads x 8 column octets
 constexpr int kBwdCtasPerSm = 2;
 constexpr uint32_t kRawBytes = 128 * kChan * 2;  // one input's tile of a CTA
 constexpr uint32_t kXposeBytes = kChan * 128;    // one transposed tile of codes
+constexpr uint32_t kPartBytes = 32 * kChan * 4;  // one array's column maxima by token quad
 
 struct BwdArgs {
   uint16_t *d;
@@ -604,6 +606,17 @@ __device__ __forceinline__ uint64_t bf16_pair(uint32_t w) {
   return pack_f32x2(bf16_lo(w), bf16_hi(w));
 }
 
+// One FP32 value into CTA `rank`'s shared memory; its four bytes count towards
+// the mbarrier at the same offset there as `local_bar` here.
+__device__ __forceinline__ void st_async_f32(uint32_t local_addr, uint32_t local_bar, uint32_t rank,
+                                             float v) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+          mapa_shared(local_addr, rank)),
+      "r"(__float_as_uint(v)), "r"(mapa_shared(local_bar, rank))
+      : "memory");
+}
+
 template <bool kRows, bool kCols, bool kH>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, kBwdCtasPerSm)
     swiglu_bwd_kernel(const __grid_constant__ CUtensorMap tmD,
@@ -614,19 +627,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, kBwdCta
   uint8_t *raw = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(dsm_raw) + 127) & ~static_cast<uintptr_t>(127));
   uint32_t *xpose = reinterpret_cast<uint32_t *>(raw + 3 * kRawBytes);
+  // column maxima [token quad][array][position]; position 32 i + 4 l + e holds
+  // column 8 l + 4 i + e, so that the eight lanes of a quad store whole rows
+  float *col_part = reinterpret_cast<float *>(raw + 3 * kRawBytes + kColArrays * kXposeBytes);
+  constexpr int kPartRow = (kColArrays > 0 ? kColArrays : 1) * kChan;
+  // by step parity: the other CTA is at most one step ahead of what is read here,
+  // since it needs all of this CTA's values of a step to go on
   __shared__ float row_amax[2][2][2][128];  // [step parity][CTA of the cluster][dg, du][token]
   __shared__ float row_inv[2][128];
-  __shared__ __align__(16) uint32_t col_bits[3][kChan];
   __shared__ __align__(16) float col_inv[3][kChan];
-  __shared__ uint64_t full;
+  __shared__ uint64_t full, rows_in[2];
   __shared__ int abort_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int l8 = lane & 7;                     // column octet
   const int quad = 4 * warp + (lane >> 3);     // token quad
   const uint32_t rank = cluster_ctarank();
-  if (kRows) cluster_arrive_relaxed();
-
   // tile t = (token block t / ncb, column block t % ncb), column blocks fastest;
   // this cluster takes every (gridDim.x / 2)-th, walked incrementally
   const uint32_t ncb = static_cast<uint32_t>(p.ncb), ntb = static_cast<uint32_t>(p.ntb);
@@ -654,15 +670,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, kBwdCta
   if (tid == 0) {
     abort_flag = 0;
     mbar_init(smem_u32(&full), 1);
+    mbar_init(smem_u32(&rows_in[0]), 1);
+    mbar_init(smem_u32(&rows_in[1]), 1);
     fence_barrier_init();
     if (tb < ntb) {
       issue(cb, tb);
       pending = true;
     }
   }
-  for (int i = tid; i < 3 * kChan; i += kBwdThreads) (&col_bits[0][0])[i] = 0u;
-  __syncthreads();
-  if (kRows) cluster_wait();  // every CTA of the cluster has started
+  // barriers initialised in both CTAs before either sends
+  if (kRows) cluster_sync_all();
+  else __syncthreads();
 
   const uint64_t log2e2 = pack_f32x2(-1.4426950408889634f, -1.4426950408889634f);
   const uint64_t one2 = pack_f32x2(1.0f, 1.0f), neg2 = pack_f32x2(-1.0f, -1.0f);
@@ -718,6 +736,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, kBwdCta
 
     // ---- max-abs of the groups
     if (kRows) {
+      if (tid == 0) mbar_arrive_expect_tx(smem_u32(&rows_in[it & 1]), 2 * 256 * 4);
+      float m[8];  // token i of this thread's four: dg at 2i, du at 2i + 1
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float a = 0.0f, b = 0.0f;
@@ -727,49 +747,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, kBwdCta
           a = max3_abs(a, x.x, x.y);
           b = max3_abs(b, y.x, y.y);
         }
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) {
-          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-          b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
-        }
-        // lanes 0-1 of a token take dg to the two CTAs, lanes 2-3 du
-        if (l8 < 4)
-          st_cluster_f32(smem_u32(&row_amax[it & 1][rank][l8 >> 1][4 * quad + i]),
-                         static_cast<uint32_t>(l8 & 1), l8 < 2 ? a : b);
+        m[2 * i] = a;
+        m[2 * i + 1] = b;
       }
+      // halving exchange over the eight lanes of the quad: lane l ends with the
+      // maximum of m[l] over the lanes
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) {
+        const bool up = (l8 & o) != 0;
+#pragma unroll
+        for (int k = 0; k < o; ++k) {
+          const float keep = up ? m[k + o] : m[k], give = up ? m[k] : m[k + o];
+          m[k] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o));
+        }
+      }
+      const uint32_t at = smem_u32(&row_amax[it & 1][rank][l8 & 1][4 * quad + (l8 >> 1)]);
+      st_async_f32(at, smem_u32(&rows_in[it & 1]), 0, m[0]);
+      st_async_f32(at, smem_u32(&rows_in[it & 1]), 1, m[0]);
     }
 #pragma unroll
     for (int k = 0; k < kColArrays; ++k) {
+      float m[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float v[4];
+      for (int j = 0; j < 4; ++j) {
+        float2 v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 x =
-              unpack_f32x2(kH && k == kH0 ? h[i][j / 2] : k == 0 ? dg[i][j / 2] : du[i][j / 2]);
-          v[i] = j & 1 ? x.y : x.x;
-        }
-        float a = max3_abs(max3_abs(v[0], v[1], v[2]), v[3], 0.0f);
-        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 8));
-        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16));
-        // the warp's four token quads share the atomics
-        if ((lane >> 3) == (j & 3)) atomicMax(&col_bits[k][8 * l8 + j], __float_as_uint(a));
+        for (int i = 0; i < 4; ++i)
+          v[i] = unpack_f32x2(kH && k == kH0 ? h[i][j] : k == 0 ? dg[i][j] : du[i][j]);
+        m[2 * j] = max3_abs(max3_abs(v[0].x, v[1].x, v[2].x), v[3].x, 0.0f);
+        m[2 * j + 1] = max3_abs(max3_abs(v[0].y, v[1].y, v[2].y), v[3].y, 0.0f);
       }
+      float4 *dst = reinterpret_cast<float4 *>(col_part + quad * kPartRow + k * kChan) + l8;
+      dst[0] = make_float4(m[0], m[1], m[2], m[3]);
+      dst[8] = make_float4(m[4], m[5], m[6], m[7]);
     }
-    if (kRows) cluster_sync_all();
-    else __syncthreads();
-    // every thread has read the raw tile: the next one may come
+    __syncthreads();
+    // every thread has read the raw tile (and used what it read): the next one
+    // may come
     const uint32_t cbc = cb;
     step();
     if (tid == 0 && ok && tb < ntb) {
-      fence_proxy_async_shared();
       issue(cb, tb);
       pending = true;
     }
     if (!kRows && kColArrays == 0) continue;
 
     // ---- scales, one group per thread at a time
+    if (kColArrays > 0 && tid < kColArrays * kChan) {
+      const int k = tid / kChan, pos = tid % kChan;
+      const int cc = 8 * ((pos & 31) >> 2) + 4 * (pos >> 5) + (pos & 3);
+      float a = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 32; i += 2)
+        a = max3_abs(a, col_part[i * kPartRow + tid], col_part[(i + 1) * kPartRow + tid]);
+      float sc, inv;
+      group_scale(a, p.pow2 != 0, sc, inv);
+      col_inv[k][cc] = inv;
+      if (ok) {
+        if (kH && k == kH0) p.shT[(t0 / 128) * p.ld_shT + c0 + cc] = sc;
+        else p.sT[(t0 / 128) * p.ld_sT + k * p.F + c0 + cc] = sc;
+      }
+    }
     if (kRows) {
+      const bool in = mbar_wait_bounded(smem_u32(&rows_in[it & 1]), (it >> 1) & 1u, &abort_flag,
+                                        &g_glu_status, p.timeout_ns, FP8Q_ERR_TIMEOUT);
+      ok = __all_sync(0xffffffffu, in) && ok;
       const int k = tid >> 7, t = tid & 127;
       const float a = fmaxf(row_amax[it & 1][0][k][t], row_amax[it & 1][1][k][t]);
       float sc, inv;
@@ -777,17 +819,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, kBwdCta
       row_inv[k][t] = inv;
       if (rank == 0 && ok && t0 + t < p.T)
         p.s[(static_cast<int64_t>(k) * p.ncb + cbc) * p.ld_s + t0 + t] = sc;
-    }
-    if (kColArrays > 0 && tid < kColArrays * kChan) {
-      const int k = tid / kChan, cc = tid % kChan;
-      float sc, inv;
-      group_scale(__uint_as_float(col_bits[k][cc]), p.pow2 != 0, sc, inv);
-      col_bits[k][cc] = 0u;
-      col_inv[k][cc] = inv;
-      if (ok) {
-        if (kH && k == kH0) p.shT[(t0 / 128) * p.ld_shT + c0 + cc] = sc;
-        else p.sT[(t0 / 128) * p.ld_sT + k * p.F + c0 + cc] = sc;
-      }
     }
     __syncthreads();
 
@@ -844,6 +875,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, kBwdCta
       }
     }
   }
+  if (kRows) cluster_sync_all();  // the other CTA no longer sends here
   // a copy still in flight after an abandoned wait lands before the CTA's shared
   // memory goes
   if (tid == 0 && pending) {
@@ -857,7 +889,8 @@ template <bool kRows, bool kCols, bool kH>
 fp8q_status launch_bwd(const CUtensorMap &tmD, const CUtensorMap &tmG, const BwdArgs &a,
                        cudaStream_t s) {
   auto kern = swiglu_bwd_kernel<kRows, kCols, kH>;
-  constexpr size_t smem = 128 + 3 * kRawBytes + ((kCols ? 2 : 0) + (kH ? 1 : 0)) * kXposeBytes;
+  constexpr size_t smem =
+      128 + 3 * kRawBytes + ((kCols ? 2 : 0) + (kH ? 1 : 0)) * (kXposeBytes + kPartBytes);
   static bool attr_set[kMaxDevices] = {};
   static std::mutex mu;
   int dev = 0;
