@@ -55,10 +55,20 @@ struct GluIn {
 fp8q_status gemm_glu(const GluIn &in, const GluOut &out, cudaStream_t s);
 fp8q_status gemm_mx_glu(const GluIn &in, const GluOut &out, cudaStream_t s);
 
-// silu(g) * u.  exp and the quotient are the fast forms (a few FP32 ulps, far
-// below the rounding of any output); exp(-g) = inf for g < -88 gives -0 * u,
-// where the exact value is below 1e-36 * u.
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+// 1 / (1 + exp(-g)) of a pair, by the hardware's exp2 and reciprocal (a few FP32
+// ulps and |g| ulps of the exponent's product, far below the rounding of any
+// output).  exp(-g) = inf for g < -88 gives 0, where the exact value is below
+// 1e-37.
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t g) {
+  const float2 x = unpack_f32x2(fmul2(g, pack_f32x2(-1.4426950408889634f, -1.4426950408889634f)));
+  const float2 d =
+      unpack_f32x2(fadd2(pack_f32x2(ex2_ftz(x.x), ex2_ftz(x.y)), pack_f32x2(1.0f, 1.0f)));
+  return pack_f32x2(rcp_ftz(d.x), rcp_ftz(d.y));
+}
+// silu(g) * u of a pair.
+__device__ __forceinline__ uint64_t gate2(uint64_t g, uint64_t u) {
+  return fmul2(fmul2(g, sigmoid2(g)), u);
+}
 
 // Row max-abs exchange between the two epilogue warps of a 128-column group.
 struct GluExchange {
@@ -100,10 +110,9 @@ __device__ __forceinline__ bool glu_store(uint64_t (&acc)[64], const GluOut &o, 
   float amax = 0.0f;
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
-    const float2 g = unpack_f32x2(acc[i]), u = unpack_f32x2(acc[32 + i]);
-    const float h0 = silu(g.x) * u.x, h1 = silu(g.y) * u.y;
-    amax = fmaxf(amax, fmaxf(fabsf(h0), fabsf(h1)));
-    acc[i] = pack_f32x2(h0, h1);
+    acc[i] = gate2(acc[i], acc[32 + i]);
+    const float2 v = unpack_f32x2(acc[i]);
+    amax = max3_abs(amax, v.x, v.y);
   }
   if (o.h) {
 #pragma unroll
@@ -144,11 +153,8 @@ __device__ __forceinline__ bool glu_store(uint64_t (&acc)[64], const GluOut &o, 
     for (int k = 0; k < 4; ++k) {
       uint32_t w[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 a = unpack_f32x2(fmul2(acc[8 * k + 2 * e], inv2));
-        const float2 b = unpack_f32x2(fmul2(acc[8 * k + 2 * e + 1], inv2));
-        w[e] = pack_e4m3x4(a.x, a.y, b.x, b.y);
-      }
+      for (int e = 0; e < 4; ++e)
+        w[e] = codes4(fmul2(acc[8 * k + 2 * e], inv2), fmul2(acc[8 * k + 2 * e + 1], inv2));
       v[k] = make_uint4(w[0], w[1], w[2], w[3]);
     }
     warp_store_block64<1, false>(buf, v, o.q, o.ldq, row0, row_end, col0, o.F, lane);

@@ -402,6 +402,33 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// max(|a|, |b|, |c|)
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
 // ---------------------------------------------------------------- E4M3
 // Two FP32 -> two E4M3 bytes (round to nearest-even, saturate to +-448):
@@ -415,6 +442,21 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
   return pack_e4m3x2(a, b) | (pack_e4m3x2(c, d) << 16);
 }
 
+// Four FP32 values -> four E4M3 codes, a in the low byte.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+__device__ __forceinline__ uint32_t codes4(uint64_t ab, uint64_t cd) {
+  const float2 x = unpack_f32x2(ab), y = unpack_f32x2(cd);
+  return codes4(x.x, x.y, y.x, y.y);
+}
 // ---------------------------------------------------------------- scales
 // Scale of one group from its max-abs value (FP32 mode: s = a/448, inv =
 // 448/a, IEEE divisions; POW2 mode: s = 2^e with the smallest e such that

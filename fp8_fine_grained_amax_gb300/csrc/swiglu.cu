@@ -332,19 +332,23 @@ __global__ void __cluster_dims__(2 * kFewSplit, 1, 1)
     const int j = warp + kWarps * k, m = m0 + quarter * C::kQuarter + j;
     h[k][0] = h[k][1] = 0.0f;
     if (j >= C::kQuarter || m >= p.M) continue;  // warp-uniform
-    float amax = 0.0f;
+    float2 gv = make_float2(0.0f, 0.0f), uv = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int s = 0; s < kFewSplit; ++s) {
+      const float *src = recv + (s * C::kQuarter + j) * 128 + lane;
+      gv.x += src[0];
+      gv.y += src[32];
+      uv.x += src[64];
+      uv.y += src[96];
+    }
+    const float2 hv = unpack_f32x2(gate2(pack_f32x2(gv.x, gv.y), pack_f32x2(uv.x, uv.y)));
+    h[k][0] = hv.x;
+    h[k][1] = hv.y;
+    float amax = fmaxf(fabsf(hv.x), fabsf(hv.y));
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int col = lane + 32 * e;
-      float g = 0.0f, u = 0.0f;
-#pragma unroll
-      for (int s = 0; s < kFewSplit; ++s) {
-        const float *src = recv + (s * C::kQuarter + j) * 128 + col;
-        g += src[0];
-        u += src[64];
-      }
-      h[k][e] = silu(g) * u;
-      amax = fmaxf(amax, fabsf(h[k][e]));
+      const float g = e ? gv.y : gv.x, u = e ? uv.y : uv.x;
       if (p.out.gu) {
         uint16_t *row = static_cast<uint16_t *>(p.out.gu) + static_cast<int64_t>(m) * p.out.ld_gu;
         row[c0 + col] = bf16_bits(g);
@@ -561,47 +565,6 @@ struct BwdArgs {
 __device__ __forceinline__ uint32_t xpose_word(uint32_t r, uint32_t w) {
   return r * 32u + (w ^ (4u * ((r >> 3) & 7u)));
 }
-// max(|a|, |b|, |c|)
-__device__ __forceinline__ float max3_abs(float a, float b, float c) {
-  float d;
-  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ float ex2_ftz(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float rcp_ftz(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-// Four FP32 values -> four E4M3 codes, a in the low byte.
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
-      "mov.b32 %0, {lo, hi};\n\t}"
-      : "=r"(r)
-      : "f"(a), "f"(b), "f"(c), "f"(d));
-  return r;
-}
-__device__ __forceinline__ uint32_t codes4(uint64_t ab, uint64_t cd) {
-  const float2 x = unpack_f32x2(ab), y = unpack_f32x2(cd);
-  return codes4(x.x, x.y, y.x, y.y);
-}
 __device__ __forceinline__ uint64_t bf16_pair(uint32_t w) {
   return pack_f32x2(bf16_lo(w), bf16_hi(w));
 }
@@ -682,7 +645,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, kBwdCta
   if (kRows) cluster_sync_all();
   else __syncthreads();
 
-  const uint64_t log2e2 = pack_f32x2(-1.4426950408889634f, -1.4426950408889634f);
   const uint64_t one2 = pack_f32x2(1.0f, 1.0f), neg2 = pack_f32x2(-1.0f, -1.0f);
   bool ok = true;
   for (uint32_t it = 0; tb < ntb; ++it) {
@@ -706,9 +668,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, kBwdCta
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint64_t y = bf16_pair(wd[k]), g = bf16_pair(wg[k]), u = bf16_pair(wu[k]);
-        const float2 x = unpack_f32x2(fmul2(g, log2e2));
-        const float2 e = unpack_f32x2(fadd2(pack_f32x2(ex2_ftz(x.x), ex2_ftz(x.y)), one2));
-        const uint64_t s = pack_f32x2(rcp_ftz(e.x), rcp_ftz(e.y));
+        const uint64_t s = sigmoid2(g);
         const uint64_t sl = fmul2(g, s);  // silu(g)
         du[i][k] = fmul2(y, sl);
         dg[i][k] = fmul2(fmul2(y, u), fma2(sl, fma2(s, neg2, one2), s));
