@@ -79,32 +79,74 @@ __device__ __forceinline__ void glu_exchange_init(GluExchange &x) {
   for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&x.bar[i]), 2);
 }
 
+// Tensor maps of the results: gu and h in boxes of 64 columns (128-byte swizzle),
+// q in boxes of 64 columns (64-byte swizzle), 32 rows each.
+struct GluMaps {
+  CUtensorMap gu, h, q;
+};
+
+// Eight packed pairs -> 16 BF16 values (32 bytes) as two 16-byte units.
+__device__ __forceinline__ uint4 bf16_unit(const uint64_t *v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = unpack_f32x2(v[e]);
+    __nv_bfloat162 p = __floats2bfloat162_rn(f.x, f.y);
+    w[e] = *reinterpret_cast<uint32_t *>(&p);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// 64 columns of this lane's row (32 pairs) into a 32-row x 128-byte box.
+__device__ __forceinline__ void stage_box(uint32_t box, const uint64_t *v, int lane) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    st_shared_v4(box + lane * 128 + 16 * (k ^ (lane & 7)), bf16_unit(v + 4 * k));
+}
+// 64 columns of this lane's row to global memory, 64 bytes of each row at a time.
+__device__ __forceinline__ void store_rows(uint32_t buf, const uint64_t *v, void *c, int64_t ldc,
+                                           int row0, int row_end, int col0, int n, int lane) {
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const uint4 u[4] = {bf16_unit(v + 16 * b), bf16_unit(v + 16 * b + 4), bf16_unit(v + 16 * b + 8),
+                        bf16_unit(v + 16 * b + 12)};
+    warp_store_block64<2, false>(buf, u, c, ldc, row0, row_end, col0 + 32 * b, n, lane);
+  }
+}
+
 // Store the results of one warp's 32 rows x 64 columns of h.  acc: this
 // thread's row, 64 gate values then 64 up values as packed FP32 pairs.  buf:
-// the warp's 2 KB staging buffer.  uses counts this warp's exchanges.  Returns
-// false when a bounded wait gave up.  All branches are warp-uniform and the
-// same for the two warps of a group.
-__device__ __forceinline__ bool glu_store(uint64_t (&acc)[64], const GluOut &o, uint32_t buf,
-                                          int row0, int row_end, int col0, int ew, int lane,
-                                          GluExchange &x, uint32_t &uses, volatile int *abort_flag,
-                                          int *status_word, uint64_t timeout_ns) {
+// the warp's staging buffer (1024-byte aligned): 8 KB with kTma, where whole
+// blocks leave as TMA tensor stores that drain while the next tile is folded
+// (8192 x 2048 x 7168 with gu and codes: 220 us with coalesced stores), else
+// 2 KB.  tma: this block may leave that way (warp-uniform; the maps clip at the
+// tensor's last row only).  uses counts this warp's exchanges.  Returns false
+// when a bounded wait gave up.  All branches are warp-uniform and the same for
+// the two warps of a group.
+template <bool kTma>
+__device__ __forceinline__ bool glu_store(uint64_t (&acc)[64], const GluOut &o, const GluMaps *maps,
+                                          bool tma, uint32_t buf, int row0, int row_end, int col0,
+                                          int ew, int lane, GluExchange &x, uint32_t &uses,
+                                          volatile int *abort_flag, int *status_word,
+                                          uint64_t timeout_ns) {
+  if (kTma) {  // the last tile's stores have read the buffer
+    if (lane == 0) bulk_wait_group_read<0>();
+    __syncwarp();
+  }
   if (o.gu) {
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {  // 32 columns (64 bytes) at a time: gate, gate, up, up
-      uint4 v[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = unpack_f32x2(acc[16 * b + 4 * k + e]);
-          __nv_bfloat162 p = __floats2bfloat162_rn(f.x, f.y);
-          w[e] = *reinterpret_cast<uint32_t *>(&p);
-        }
-        v[k] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (kTma && tma) {
+      stage_box(buf, acc, lane);
+      stage_box(buf + 4096, acc + 32, lane);
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        const uint64_t pol = l2_evict_first_policy();
+        tma_store_2d_hint(&maps->gu, buf, col0, row0, pol);
+        tma_store_2d_hint(&maps->gu, buf + 4096, o.F + col0, row0, pol);
+        bulk_commit_group();
       }
-      warp_store_block64<2, false>(buf, v, o.gu, o.ld_gu, row0, row_end,
-                                   (b >> 1) * o.F + col0 + 32 * (b & 1), 2 * o.F, lane);
+    } else {
+      store_rows(buf, acc, o.gu, o.ld_gu, row0, row_end, col0, o.F, lane);
+      store_rows(buf, acc + 32, o.gu, o.ld_gu, row0, row_end, o.F + col0, 2 * o.F, lane);
     }
   }
   float amax = 0.0f;
@@ -114,33 +156,26 @@ __device__ __forceinline__ bool glu_store(uint64_t (&acc)[64], const GluOut &o, 
     const float2 v = unpack_f32x2(acc[i]);
     amax = max3_abs(amax, v.x, v.y);
   }
+  if (!o.h && !o.q) return true;
+  if (o.q) {
+    // this warp's maxima are on their way while h is stored; the buffer of this
+    // parity was last read two uses ago, before the partner arrived for the
+    // previous use
+    x.amax[uses & 1u][ew][lane] = amax;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&x.bar[ew & 3]));
+  }
+  if (kTma) {  // gu's stores have read the buffer
+    if (lane == 0) bulk_wait_group_read<0>();
+    __syncwarp();
+  }
   if (o.h) {
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      uint4 v[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = unpack_f32x2(acc[16 * b + 4 * k + e]);
-          __nv_bfloat162 p = __floats2bfloat162_rn(f.x, f.y);
-          w[e] = *reinterpret_cast<uint32_t *>(&p);
-        }
-        v[k] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      warp_store_block64<2, false>(buf, v, o.h, o.ldh, row0, row_end, col0 + 32 * b, o.F, lane);
-    }
+    if (kTma && tma) stage_box(buf, acc, lane);
+    else store_rows(buf, acc, o.h, o.ldh, row0, row_end, col0, o.F, lane);
   }
   if (o.q) {
-    // the buffer of this parity was last read two uses ago, before the partner
-    // arrived for the previous use
     const uint32_t par = uses & 1u;
-    const int quarter = ew & 3;
-    x.amax[par][ew][lane] = amax;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&x.bar[quarter]));
-    const bool got = mbar_wait_bounded(smem_u32(&x.bar[quarter]), par, abort_flag, status_word,
+    const bool got = mbar_wait_bounded(smem_u32(&x.bar[ew & 3]), par, abort_flag, status_word,
                                        timeout_ns, FP8Q_ERR_TIMEOUT);
     if (!__all_sync(0xffffffffu, got)) return false;
     ++uses;
@@ -157,9 +192,25 @@ __device__ __forceinline__ bool glu_store(uint64_t (&acc)[64], const GluOut &o, 
         w[e] = codes4(fmul2(acc[8 * k + 2 * e], inv2), fmul2(acc[8 * k + 2 * e + 1], inv2));
       v[k] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    warp_store_block64<1, false>(buf, v, o.q, o.ldq, row0, row_end, col0, o.F, lane);
+    if (kTma && tma) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        st_shared_v4(buf + 4096 + lane * 64 + 16 * (k ^ ((lane >> 1) & 3)), v[k]);
+    } else {
+      warp_store_block64<1, false>(buf, v, o.q, o.ldq, row0, row_end, col0, o.F, lane);
+    }
     if (ew < 4 && row0 + lane < row_end)
       o.s[static_cast<int64_t>(col0 / 128) * o.ld_s + row0 + lane] = sc;
+  }
+  if (kTma && tma) {
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      const uint64_t pol = l2_evict_first_policy();
+      if (o.h) tma_store_2d_hint(&maps->h, buf, col0, row0, pol);
+      if (o.q) tma_store_2d_hint(&maps->q, buf + 4096, col0, row0, pol);
+      bulk_commit_group();
+    }
   }
   return true;
 }

@@ -47,6 +47,7 @@
 
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "fp8q.h"
 #include "fp8q_glu.cuh"
@@ -225,7 +226,8 @@ template <int kBScale, bool kOutF32, bool kGrouped, bool kPair, bool kAccum = fa
           bool kTmaOut = false, bool kGlu = false>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8q_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                     const __grid_constant__ CUtensorMap tmC, const GemmArgs p) {
+                     const __grid_constant__ std::conditional_t<kGlu, GluMaps, CUtensorMap> tmC,
+                     const GemmArgs p) {
   using C = Cfg<kPair>;
   static_assert(!kGlu || (kPair && kBScale == FP8Q_BSCALE_BLOCK && !kAccum && !kTmaOut),
                 "the gated form runs on CTA pairs with block scales");
@@ -470,10 +472,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       if constexpr (kGlu) {
         const int wrow0 = tl.a_row + row_in_tile - lane;
+        // grouped: rows past the expert's end belong to the next one
+        const bool tma = !kGrouped || wrow0 + 32 <= tl.row_end;
         if (wrow0 < tl.row_end)
-          ok = glu_store(acc, p.glu, smem_u32(sC) + static_cast<uint32_t>(ew) * kStageWarpBytes,
-                         wrow0, tl.row_end, ncol0, ew, lane, ctl->glu, glu_uses, abort_flag,
-                         &g_status, p.timeout_ns);
+          ok = glu_store<true>(acc, p.glu, &tmC, tma,
+                               smem_u32(sC) + static_cast<uint32_t>(ew) * kStageWarpBytes, wrow0,
+                               tl.row_end, ncol0, ew, lane, ctl->glu, glu_uses, abort_flag,
+                               &g_status, p.timeout_ns);
         continue;
       }
       if (kFrag && kOutF32 && !kGrouped) {
@@ -780,8 +785,9 @@ bool make_tmap_c(CUtensorMap *m, void *base, uint64_t rows, uint64_t cols, uint6
 // CTA pair) per SM that can hold one, never more than there are tiles.
 template <int kBScale, bool kOutF32, bool kGrouped, bool kPair, bool kAccum = false,
           bool kTmaOut = false, bool kGlu = false>
-fp8q_status launch(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc,
-                   const GemmArgs &args, int64_t work_tiles, cudaStream_t s) {
+fp8q_status launch(const CUtensorMap &ta, const CUtensorMap &tb,
+                   const std::conditional_t<kGlu, GluMaps, CUtensorMap> &tc, const GemmArgs &args,
+                   int64_t work_tiles, cudaStream_t s) {
   auto kern = fp8q_gemm_kernel<kBScale, kOutF32, kGrouped, kPair, kAccum, kTmaOut, kGlu>;
   const size_t smem = smem_bytes(kGrouped, kPair);
   static int max_units[kMaxDevices] = {};  // co-resident CTAs (or CTA pairs) per device
@@ -923,12 +929,17 @@ fp8q_status gemm_glu(const GluIn &in, const GluOut &out, cudaStream_t s) {
   const int64_t tiles =
       (static_cast<int64_t>(args.tiles_m) + (grouped ? in.G : 0)) * args.tiles_n;
   if (tiles >= (1ll << 31)) return FP8Q_ERR_SHAPE;
-  // no C tensor: its map slot repeats A's
+  GluMaps maps{ta, ta, ta};  // results that are left out keep a copy of A's map
+  if ((out.gu && !make_tmap_c(&maps.gu, out.gu, in.M, 2 * in.F, out.ld_gu, false)) ||
+      (out.h && !make_tmap_c(&maps.h, out.h, in.M, in.F, out.ldh, false)) ||
+      (out.q && !make_tmap_2d(&maps.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, out.q, in.M, in.F, out.ldq, 64,
+                              32, CU_TENSOR_MAP_SWIZZLE_64B)))
+    return FP8Q_ERR_CUDA;
   if (grouped)
-    return launch<FP8Q_BSCALE_BLOCK, false, true, true, false, false, true>(ta, tb, ta, args,
+    return launch<FP8Q_BSCALE_BLOCK, false, true, true, false, false, true>(ta, tb, maps, args,
                                                                             tiles, s);
-  return launch<FP8Q_BSCALE_BLOCK, false, false, true, false, false, true>(ta, tb, ta, args, tiles,
-                                                                           s);
+  return launch<FP8Q_BSCALE_BLOCK, false, false, true, false, false, true>(ta, tb, maps, args,
+                                                                           tiles, s);
 }
 
 }  // namespace fp8q

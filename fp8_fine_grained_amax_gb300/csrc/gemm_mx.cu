@@ -522,8 +522,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 64; ++i)
           acc[i] = pack_u32x2(v[i / 8][2 * (i % 8)], v[i / 8][2 * (i % 8) + 1]);
-        return !warp_ok || glu_store(acc, p.glu, buf, wrow0, tl.row_end, ncol0, ew, lane, ctl->glu,
-                                     glu_uses, abort_flag, &g_mx_status, p.timeout_ns);
+        return !warp_ok || glu_store<false>(acc, p.glu, nullptr, false, buf, wrow0, tl.row_end, ncol0,
+                                            ew, lane, ctl->glu, glu_uses, abort_flag, &g_mx_status,
+                                            p.timeout_ns);
       } else if (kOutF32 && kPrep) {
         // FP32 out, per-column scales: these warps hold no raw scales, so the
         // whole row of kEpiCols values is read first and the accumulator is
