@@ -1,7 +1,8 @@
-"""Thin ctypes binding of libfp8q (include/fp8q.h), same names as the C ABI.
+"""Thin binding of libfp8q (include/fp8q.h), same names as the C ABI.
 
 Argument marshalling only: every step of the computation runs in the CUDA
-kernels of libfp8q.so.  Tensors are torch CUDA tensors (torch supplies device
+kernels of libfp8q.so.  The gated feed-forward and Newton-Schulz calls marshal
+in a compiled module (csrc/torch_calls.cpp), the others through ctypes.  Tensors are torch CUDA tensors (torch supplies device
 memory and the current stream); outputs that are not passed in are allocated
 with torch.  E4M3 tensors are torch.uint8 (raw codes; ``.view(torch.float8_e4m3fn)``
 gives the FP8 dtype).  A failing call raises FP8QError; there is no fallback.
@@ -344,108 +345,69 @@ class SwigluGrads(NamedTuple):
     shT: Optional[torch.Tensor]  # f32 [T/128][F]
 
 
-# The calls below marshal up to 18 tensors each; a small call costs more time
-# here than on the device, so each tensor is looked at once.
-_U8, _BF16, _F32T = torch.uint8, torch.bfloat16, torch.float32
-_empty = torch.empty
+# The calls below look at up to 18 tensors and make up to 8 new ones; a small
+# call would spend longer on that in Python than on the device, so it is done in
+# csrc/torch_calls.cpp, which calls the same C ABI.
+_torch_calls = None
 
 
-def _mat(t, rows, cols, dtype, name):
-    """(address, row pitch) of a caller's matrix, whose shape and type must be as
-    given; the strides of one-long axes do not count."""
-    if t.dtype is not dtype or t.shape != (rows, cols):
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {(rows, cols)}")
-    st = t.stride()
-    if cols > 1 and rows and st[1] != 1:
-        raise ValueError(f"{name} must have a contiguous last dimension")
-    return t.data_ptr() or None, st[0] if rows > 1 else cols
+def _calls():
+    global _torch_calls
+    if _torch_calls is None:
+        load_library()
+        try:
+            from . import _torch_calls as module
+        except ImportError as e:
+            raise RuntimeError(
+                f"_torch_calls.so cannot be loaded from {_HERE} ({e}): build it with "
+                "`python -m fp8_fine_grained_amax_gb300.build`") from e
+        _torch_calls = module
+    return _torch_calls
 
 
-def _raw_current_stream(stream):
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
-def _glu_call(entry, a, sa, b_args, M, F, K, dev, with_h, with_gu, with_codes, scale_mode, h, gu, q,
-              s, stream):
-    # results: the caller's, checked, or new ones
-    p_h = p_gu = p_q = p_s = None
-    ld_h, ld_gu, ld_q, ld_s = F, 2 * F, F, M
-    if h is not None:
-        p_h, ld_h = _mat(h, M, F, _BF16, "h")
-    elif with_h:
-        h = _empty((M, F), dtype=_BF16, device=dev)
-        p_h = h.data_ptr()
-    if gu is not None:
-        p_gu, ld_gu = _mat(gu, M, 2 * F, _BF16, "gu")
-    elif with_gu:
-        gu = _empty((M, 2 * F), dtype=_BF16, device=dev)
-        p_gu = gu.data_ptr()
-    if q is not None:
-        p_q, ld_q = _mat(q, M, F, _U8, "q")
-    elif with_codes:
-        q = _empty((M, F), dtype=_U8, device=dev)
-        p_q = q.data_ptr()
-    if s is not None:
-        p_s, ld_s = _mat(s, F // 128, M, _F32T, "s")
-    elif q is not None:
-        s = _empty((F // 128, M), dtype=_F32T, device=dev)
-        p_s = s.data_ptr()
-    p_a, ld_a = _mat(a, M, K, _U8, "a")
-    p_sa, ld_sa = _mat(sa, K // 128, M, _F32T, "sa")
-    st = getattr(_lib or load_library(), entry)(
-        p_a, ld_a, p_sa, ld_sa, *b_args, p_h, ld_h, p_gu, ld_gu, p_q, ld_q, p_s, ld_s, scale_mode, M,
-        F, K, _raw_current_stream(stream))
-    if st:
-        raise FP8QError(st, entry)
-    return SwigluOut(h, gu, q, s)
+def _swiglu(pow2, entry, a, sa, b, sb, offs, with_h, with_gu, with_codes, scale_mode, h, gu, q, s,
+            stream):
+    r = (_torch_calls or _calls()).swiglu(pow2, a, sa, b, sb, offs, with_h, with_gu, with_codes,
+                                          scale_mode, h, gu, q, s, _handle(stream))
+    if type(r) is int:
+        raise FP8QError(r, entry)
+    return tuple.__new__(SwigluOut, r)
 
 
 def fp8q_gemm_swiglu(a, sa, b, sb, *, with_h=True, with_gu=False, with_codes=False,
-                     scale_mode=FP8Q_SCALE_FP32, h=None, gu=None, q=None, s=None, stream=None,
-                     _entry="fp8q_gemm_swiglu"):
+                     scale_mode=FP8Q_SCALE_FP32, h=None, gu=None, q=None, s=None, stream=None):
     """h = silu(X Wg^T) * (X Wu^T) from codes a uint8 [M][K] (sa f32 [K/128][M]) and the stacked
     projections b uint8 [2F][K] (sb f32 [2F/128][K/128]) -> SwigluOut(h, gu, q, s)."""
-    M, K = a.shape
-    N = b.shape[0]
-    if N % 2:
-        raise ValueError("b must hold both projections: [2F][K]")
-    p_b, ld_b = _mat(b, N, K, _U8, "b")
-    p_sb, ld_sb = _mat(sb, N // 128, K // 128, _F32T, "sb")
-    return _glu_call(_entry, a, sa, (p_b, ld_b, p_sb, ld_sb), M, N // 2, K, a.device, with_h, with_gu,
-                     with_codes, scale_mode, h, gu, q, s, stream)
+    return _swiglu(False, "fp8q_gemm_swiglu", a, sa, b, sb, None, with_h, with_gu, with_codes,
+                   scale_mode, h, gu, q, s, stream)
 
 
-def fp8q_gemm_swiglu_pow2(a, sa, b, sb, **kw):
+def fp8q_gemm_swiglu_pow2(a, sa, b, sb, *, with_h=True, with_gu=False, with_codes=False,
+                          scale_mode=FP8Q_SCALE_FP32, h=None, gu=None, q=None, s=None, stream=None):
     """fp8q_gemm_swiglu for power-of-two input scales on the block-scaled MMA."""
-    return fp8q_gemm_swiglu(a, sa, b, sb, _entry="fp8q_gemm_swiglu_pow2", **kw)
+    return _swiglu(True, "fp8q_gemm_swiglu_pow2", a, sa, b, sb, None, with_h, with_gu, with_codes,
+                   scale_mode, h, gu, q, s, stream)
 
 
 def fp8q_grouped_gemm_swiglu(a, sa, b, sb, offs, *, with_h=True, with_gu=False, with_codes=False,
                              scale_mode=FP8Q_SCALE_FP32, h=None, gu=None, q=None, s=None,
-                             stream=None, _entry="fp8q_grouped_gemm_swiglu"):
+                             stream=None):
     """fp8q_gemm_swiglu per expert: b uint8 [G][2F][K], sb f32 [G][2F/128][K/128], offs int32
     [G+1] on the device.  Rows outside [offs[0], offs[G]) are left as is."""
-    M, K = a.shape
-    G, N, Kb = b.shape
-    st = b.stride()
-    if b.dtype is not _U8 or Kb != K or N % 2 or (b.numel() and (st[2] != 1 or st[0] != N * st[1])):
-        raise ValueError("b must be uint8 [G][2F][K], its last dimension contiguous and its experts "
-                         "back to back")
-    if sb.dtype is not _F32T or sb.shape != (G, N // 128, K // 128) or not sb.is_contiguous():
-        raise ValueError("sb must be a contiguous float32 [G][2F/128][K/128] tensor")
-    if offs.dtype is not torch.int32 or offs.shape != (G + 1,) or not offs.is_contiguous():
-        raise ValueError("offs must be a contiguous int32 [G+1] tensor")
-    return _glu_call(_entry, a, sa,
-                     (b.data_ptr() or None, st[1], sb.data_ptr() or None, offs.data_ptr(), G), M,
-                     N // 2, K, a.device, with_h, with_gu, with_codes, scale_mode, h, gu, q, s, stream)
+    return _swiglu(False, "fp8q_grouped_gemm_swiglu", a, sa, b, sb, offs, with_h, with_gu, with_codes,
+                   scale_mode, h, gu, q, s, stream)
 
 
-def fp8q_grouped_gemm_swiglu_pow2(a, sa, b, sb, offs, **kw):
+def fp8q_grouped_gemm_swiglu_pow2(a, sa, b, sb, offs, *, with_h=True, with_gu=False,
+                                  with_codes=False, scale_mode=FP8Q_SCALE_FP32, h=None, gu=None,
+                                  q=None, s=None, stream=None):
     """fp8q_grouped_gemm_swiglu for power-of-two input scales on the block-scaled MMA."""
-    return fp8q_grouped_gemm_swiglu(a, sa, b, sb, offs, _entry="fp8q_grouped_gemm_swiglu_pow2",
-                                    **kw)
+    return _swiglu(True, "fp8q_grouped_gemm_swiglu_pow2", a, sa, b, sb, offs, with_h, with_gu,
+                   with_codes, scale_mode, h, gu, q, s, stream)
 
 
 def fp8q_swiglu_bwd(dh, gu, *, with_d=False, with_rows=True, with_cols=True, with_h=True,
@@ -454,66 +416,15 @@ def fp8q_swiglu_bwd(dh, gu, *, with_d=False, with_rows=True, with_cols=True, wit
     """Backward of h = silu(g) * u: dh BF16 [T][F], gu BF16 [T][2F] -> SwigluGrads, any of the
     BF16 gradient d (with_d), its 1x128 codes (with_rows), its transposed 128x1 codes (with_cols)
     and the transposed 128x1 codes of h (with_h; both need T % 128 == 0)."""
-    T, F = dh.shape
-    N = 2 * F
-    p_dh, ld_dh = _mat(dh, T, F, _BF16, "dh")
-    p_gu, ld_gu = _mat(gu, T, N, _BF16, "gu")
-    dev = dh.device
-    p_d = p_q = p_s = p_qT = p_sT = p_hT = p_shT = None
-    ld_d, ld_q, ld_s, ld_qT, ld_sT, ld_hT, ld_shT = N, N, T, T, N, T, F
-    if d is not None:
-        p_d, ld_d = _mat(d, T, N, _BF16, "d")
-    elif with_d:
-        d = _empty((T, N), dtype=_BF16, device=dev)
-        p_d = d.data_ptr()
-    if q is not None:
-        p_q, ld_q = _mat(q, T, N, _U8, "q")
-    elif with_rows:
-        q = _empty((T, N), dtype=_U8, device=dev)
-        p_q = q.data_ptr()
-    if s is not None:
-        p_s, ld_s = _mat(s, N // 128, T, _F32T, "s")
-    elif q is not None:
-        s = _empty((N // 128, T), dtype=_F32T, device=dev)
-        p_s = s.data_ptr()
-    if qT is not None:
-        p_qT, ld_qT = _mat(qT, N, T, _U8, "qT")
-    elif with_cols:
-        qT = _empty((N, T), dtype=_U8, device=dev)
-        p_qT = qT.data_ptr()
-    if sT is not None:
-        p_sT, ld_sT = _mat(sT, T // 128, N, _F32T, "sT")
-    elif qT is not None:
-        sT = _empty((T // 128, N), dtype=_F32T, device=dev)
-        p_sT = sT.data_ptr()
-    if hT is not None:
-        p_hT, ld_hT = _mat(hT, F, T, _U8, "hT")
-    elif with_h:
-        hT = _empty((F, T), dtype=_U8, device=dev)
-        p_hT = hT.data_ptr()
-    if shT is not None:
-        p_shT, ld_shT = _mat(shT, T // 128, F, _F32T, "shT")
-    elif hT is not None:
-        shT = _empty((T // 128, F), dtype=_F32T, device=dev)
-        p_shT = shT.data_ptr()
-    st = (_lib or load_library()).fp8q_swiglu_bwd(
-        p_dh, ld_dh, p_gu, ld_gu, p_d, ld_d, p_q, ld_q, p_s, ld_s, p_qT, ld_qT, p_sT, ld_sT, p_hT,
-        ld_hT, p_shT, ld_shT, T, F, scale_mode, _raw_current_stream(stream))
-    if st:
-        raise FP8QError(st, "fp8q_swiglu_bwd")
-    return SwigluGrads(d, q, s, qT, sT, hT, shT)
+    r = (_torch_calls or _calls()).swiglu_bwd(dh, gu, with_d, with_rows, with_cols, with_h, scale_mode,
+                                              d, q, s, qT, sT, hT, shT, _handle(stream))
+    if type(r) is int:
+        raise FP8QError(r, "fp8q_swiglu_bwd")
+    return tuple.__new__(SwigluGrads, r)
 
 
 def fp8q_newton_schulz_workspace_bytes(batch: int, m: int, n: int) -> int:
     return int(load_library().fp8q_newton_schulz_workspace_bytes(batch, m, n))
-
-
-def _pitches(t, m, n, name):
-    """Row and matrix pitch of a matrix or a batch of matrices."""
-    st = t.stride()
-    if n > 1 and m and st[-1] != 1:
-        raise ValueError(f"{name} must have a contiguous last dimension")
-    return st[-2] if m > 1 else n, st[0] if len(st) == 3 else 0
 
 
 def fp8q_newton_schulz(g, *, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7,
@@ -521,29 +432,12 @@ def fp8q_newton_schulz(g, *, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7
     """Orthogonalised update of g ([m][n] or a batch [B][m][n], FP32 or BF16): `steps` steps
     X <- aX + (bA + cA^2)X, A = X X^T, from X = g / (|g|_F + eps) -> BF16 or FP32, g's shape.
     A workspace tensor is allocated with torch when not given."""
-    if g.dim() not in (2, 3) or g.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError("g must be an FP32 or BF16 matrix or batch of matrices")
-    dt = torch.bfloat16 if out_dtype == FP8Q_OUT_BF16 else torch.float32
-    if out is None:
-        out = torch.empty(g.shape, dtype=dt, device=g.device)
-    elif out.shape != g.shape or out.dtype != dt:
-        raise ValueError("out must have g's shape and the type out_dtype names")
-    B = g.shape[0] if g.dim() == 3 else 1
-    m, n = g.shape[-2:]
-    ld_g, stride_g = _pitches(g, m, n, "g")
-    ld_o, stride_o = _pitches(out, m, n, "out")
-    lib = _lib or load_library()
-    if workspace is None:
-        nbytes = lib.fp8q_newton_schulz_workspace_bytes(B, m, n)
-        workspace = _empty((max(nbytes, 1),), dtype=_U8, device=g.device)
     a, b, c = coeffs
-    _check(lib.fp8q_newton_schulz(
-        g.data_ptr() or None, ld_g, stride_g,
-        FP8Q_OUT_FP32 if g.dtype is _F32T else FP8Q_OUT_BF16, out.data_ptr() or None, ld_o, stride_o,
-        out_dtype, B, m, n, steps, a, b, c, eps, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _raw_current_stream(stream)),
-        "fp8q_newton_schulz")
-    return out
+    r = (_torch_calls or _calls()).newton_schulz(g, steps, a, b, c, eps, out_dtype, out, workspace,
+                                                 _handle(stream))
+    if type(r) is int:
+        raise FP8QError(r, "fp8q_newton_schulz")
+    return r
 
 
 def fp8q_cast_e4m3(x, *, q=None, stream=None):

@@ -25,6 +25,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfp8q.so")
+# The argument marshalling of the newer calls as a CPython module (linked
+# against the library and torch).
+EXT = os.path.join(PKG, "_torch_calls.so")
+EXT_SOURCE = "torch_calls.cpp"
 SOURCES = ["gemm.cu", "gemm_mx.cu", "quant.cu", "swiglu.cu", "newton_schulz.cu", "api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -44,9 +48,9 @@ def _inputs():
 
 
 def _up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(EXT)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -58,6 +62,37 @@ def _compile(src: str) -> tuple[str, str]:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
     return obj, r.stderr
+
+
+def _compile_ext() -> str:
+    """Object file of the CPython module (torch's headers, host code only)."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    obj = os.path.join(BUILD, "torch_calls.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    inc = [*include_paths(), sysconfig.get_paths()["include"], cuda, INCLUDE]
+    cmd = [shutil.which("g++") or "g++", "-O1", "-std=c++17", "-fPIC", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{d}" for d in inc], "-c", os.path.join(CSRC, EXT_SOURCE), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {EXT_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_ext(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = EXT + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, f"-L{PKG}", "-l:libfp8q.so",
+           f"-L{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of {EXT_SOURCE} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
 
 
 def launch_regs_of(gemm_src: str) -> int:
@@ -90,7 +125,8 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and _up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        ext = ex.submit(_compile_ext)
         results = dict(zip(SOURCES, ex.map(_compile, SOURCES)))
     check_gemm_registers(results["gemm.cu"][1], launch_regs_of(os.path.join(CSRC, "gemm.cu")))
     check_gemm_registers(results["gemm_mx.cu"][1], launch_regs_of(os.path.join(CSRC, "gemm_mx.cu")),
@@ -101,11 +137,12 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         for src, (_, log) in results.items():
             print(f"== {src}\n{log}")
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *[results[s][0] for s in SOURCES]]
+    cmd = [nvcc(), *ARCH, "-shared", "-Xlinker", "-soname=libfp8q.so", "-o", tmp, *[results[s][0] for s in SOURCES]]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_ext(ext.result())
     return LIB
 
 

@@ -1,0 +1,330 @@
+// torch_calls.cpp -- the argument marshalling of the gated feed-forward and
+// Newton-Schulz bindings as a CPython module: tensors in, libfp8q's C ABI called
+// on torch's current stream, result tensors out.  No step of the computation is
+// here.  A small call takes longer to marshal than to run; looking at up to 18
+// tensors and making up to 8 new ones costs 20 to 33 us per call in Python on a
+// Grace core, 9 to 19 us here.
+//
+// Every function takes positional arguments (binding.py gives them their names
+// and defaults) and returns the tuple of results, or the fp8q_status as an int
+// where the call failed.  Wrong tensors raise ValueError.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <string>
+
+#include "fp8q.h"
+
+namespace {
+
+struct Mat {
+  void *p = nullptr;
+  int64_t ld = 0;
+};
+
+bool fail(const std::string &what) {
+  PyErr_SetString(PyExc_ValueError, what.c_str());
+  return false;
+}
+
+const at::Tensor *tensor(PyObject *o, const char *name) {
+  if (!THPVariable_Check(o)) {
+    PyErr_Format(PyExc_TypeError, "%s must be a torch.Tensor", name);
+    return nullptr;
+  }
+  return &THPVariable_Unpack(o);
+}
+
+// Address and row pitch of a matrix whose shape and type must be as given; the
+// strides of one-long axes do not count.
+bool mat(const at::Tensor &t, int64_t rows, int64_t cols, at::ScalarType dtype, const char *name,
+         Mat &m) {
+  if (t.scalar_type() != dtype || t.dim() != 2 || t.size(0) != rows || t.size(1) != cols)
+    return fail(std::string(name) + " must be a " + c10::toString(dtype) + " tensor of shape (" +
+                std::to_string(rows) + ", " + std::to_string(cols) + ")");
+  if (!t.is_cuda()) return fail(std::string(name) + " must be on a CUDA device");
+  if (cols > 1 && rows > 0 && t.stride(1) != 1)
+    return fail(std::string(name) + " must have a contiguous last dimension");
+  m.p = t.numel() ? t.data_ptr() : nullptr;
+  m.ld = rows > 1 ? t.stride(0) : cols;
+  return true;
+}
+bool mat(PyObject *o, int64_t rows, int64_t cols, at::ScalarType dtype, const char *name, Mat &m) {
+  const at::Tensor *t = tensor(o, name);
+  return t && mat(*t, rows, cols, dtype, name, m);
+}
+
+at::Tensor new_tensor(at::IntArrayRef size, at::ScalarType dtype, at::Device dev) {
+  return at::Tensor(at::detail::empty_cuda(size, dtype, dev, c10::nullopt));
+}
+
+// Results of a call: the caller's tensor, checked, a new one, or None.
+struct Results {
+  static constexpr int kMost = 8;
+  PyObject *o[kMost] = {};
+  int n = 0;
+  ~Results() {
+    for (int i = 0; i < n; ++i) Py_XDECREF(o[i]);
+  }
+  bool add(PyObject *given, bool wanted, int64_t rows, int64_t cols, at::ScalarType dtype,
+           at::Device dev, const char *name, Mat &m, bool &present) {
+    if (given != Py_None) {
+      if (!mat(given, rows, cols, dtype, name, m)) return false;
+      Py_INCREF(given);
+      o[n++] = given;
+      present = true;
+    } else if (wanted) {
+      at::Tensor t = new_tensor({rows, cols}, dtype, dev);
+      m.p = t.data_ptr();
+      m.ld = cols;
+      o[n++] = THPVariable_Wrap(std::move(t));
+      present = true;
+    } else {
+      Py_INCREF(Py_None);
+      o[n++] = Py_None;
+      present = false;
+    }
+    return o[n - 1] != nullptr;
+  }
+  PyObject *tuple(fp8q_status st) {
+    if (st != FP8Q_OK) return PyLong_FromLong(st);
+    PyObject *t = PyTuple_New(n);
+    if (!t) return nullptr;
+    for (int i = 0; i < n; ++i) PyTuple_SET_ITEM(t, i, o[i]);
+    n = 0;
+    return t;
+  }
+};
+
+// torch's current stream, or the given stream's handle.
+bool stream_of(PyObject *o, at::Device dev, void *&s) {
+  if (o == Py_None) {
+    s = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+    return true;
+  }
+  s = PyLong_AsVoidPtr(o);
+  return !(s == nullptr && PyErr_Occurred());
+}
+
+PyObject *wrong_count(const char *name) {
+  PyErr_Format(PyExc_TypeError, "%s: wrong number of arguments", name);
+  return nullptr;
+}
+
+// (pow2, a, sa, b, sb, offs, with_h, with_gu, with_codes, scale_mode, h, gu, q, s, stream)
+PyObject *swiglu_impl(PyObject *const *v, Py_ssize_t n) {
+  if (n != 15) return wrong_count("swiglu");
+  const bool pow2 = v[0] == Py_True;
+  const at::Tensor *a = tensor(v[1], "a"), *b = tensor(v[3], "b"), *sb = tensor(v[4], "sb");
+  if (!a || !b || !sb) return nullptr;
+  const bool grouped = v[5] != Py_None;
+  if (a->dim() != 2 || b->dim() != (grouped ? 3 : 2)) {
+    fail(grouped ? "a must be [M][K] and b [G][2F][K]" : "a must be [M][K] and b [2F][K]");
+    return nullptr;
+  }
+  const int64_t M = a->size(0), K = a->size(1), N = b->size(-2), F = N / 2;
+  if (N % 2 || b->size(-1) != K) {
+    fail("b must hold both projections: [2F][K] rows, with a's K");
+    return nullptr;
+  }
+  const at::Device dev = a->device();
+  Mat ma, msa, mb, msb;
+  if (!mat(*a, M, K, at::kByte, "a", ma) || !mat(v[2], K / 128, M, at::kFloat, "sa", msa))
+    return nullptr;
+  const int32_t *offs = nullptr;
+  int64_t G = 1;
+  if (grouped) {
+    G = b->size(0);
+    const at::Tensor *to = tensor(v[5], "offs");
+    if (!to) return nullptr;
+    if (b->scalar_type() != at::kByte ||
+        (b->numel() && (b->stride(2) != 1 || b->stride(0) != N * b->stride(1)))) {
+      fail("b must be uint8 [G][2F][K], its last dimension contiguous and its experts back to back");
+      return nullptr;
+    }
+    if (sb->scalar_type() != at::kFloat || sb->dim() != 3 || sb->size(0) != G ||
+        sb->size(1) != N / 128 || sb->size(2) != K / 128 || !sb->is_contiguous()) {
+      fail("sb must be a contiguous float32 [G][2F/128][K/128] tensor");
+      return nullptr;
+    }
+    if (to->scalar_type() != at::kInt || to->dim() != 1 || to->size(0) != G + 1 ||
+        !to->is_contiguous()) {
+      fail("offs must be a contiguous int32 [G+1] tensor");
+      return nullptr;
+    }
+    if (!b->is_cuda() || !sb->is_cuda() || !to->is_cuda()) {
+      fail("b, sb and offs must be on a CUDA device");
+      return nullptr;
+    }
+    mb.p = b->numel() ? b->data_ptr() : nullptr;
+    mb.ld = b->stride(1);
+    msb.p = sb->numel() ? sb->data_ptr() : nullptr;
+    offs = to->data_ptr<int32_t>();
+  } else if (!mat(*b, N, K, at::kByte, "b", mb) ||
+             !mat(*sb, N / 128, K / 128, at::kFloat, "sb", msb)) {
+    return nullptr;
+  }
+  const int mode = static_cast<int>(PyLong_AsLong(v[9]));
+  void *stream = nullptr;
+  if ((mode == -1 && PyErr_Occurred()) || !stream_of(v[14], dev, stream)) return nullptr;
+  Results r;
+  Mat h, gu, q, s;
+  bool has_h, has_gu, has_q, has_s;
+  if (!r.add(v[10], v[6] == Py_True, M, F, at::kBFloat16, dev, "h", h, has_h) ||
+      !r.add(v[11], v[7] == Py_True, M, 2 * F, at::kBFloat16, dev, "gu", gu, has_gu) ||
+      !r.add(v[12], v[8] == Py_True, M, F, at::kByte, dev, "q", q, has_q) ||
+      !r.add(v[13], has_q, F / 128, M, at::kFloat, dev, "s", s, has_s))
+    return nullptr;
+  fp8q_status st;
+  float *fs = static_cast<float *>(s.p);
+  const float *fsa = static_cast<const float *>(msa.p), *fsb = static_cast<const float *>(msb.p);
+  if (grouped)
+    st = (pow2 ? fp8q_grouped_gemm_swiglu_pow2 : fp8q_grouped_gemm_swiglu)(
+        ma.p, ma.ld, fsa, msa.ld, mb.p, mb.ld, fsb, offs, static_cast<int>(G), h.p, h.ld, gu.p,
+        gu.ld, q.p, q.ld, fs, s.ld, mode, M, F, K, stream);
+  else
+    st = (pow2 ? fp8q_gemm_swiglu_pow2 : fp8q_gemm_swiglu)(
+        ma.p, ma.ld, fsa, msa.ld, mb.p, mb.ld, fsb, msb.ld, h.p, h.ld, gu.p, gu.ld, q.p, q.ld, fs,
+        s.ld, mode, M, F, K, stream);
+  return r.tuple(st);
+}
+
+// (dh, gu, with_d, with_rows, with_cols, with_h, scale_mode, d, q, s, qT, sT, hT, shT, stream)
+PyObject *bwd_impl(PyObject *const *v, Py_ssize_t n) {
+  if (n != 15) return wrong_count("swiglu_bwd");
+  const at::Tensor *dh = tensor(v[0], "dh");
+  if (!dh) return nullptr;
+  if (dh->dim() != 2) {
+    fail("dh must be [T][F]");
+    return nullptr;
+  }
+  const int64_t T = dh->size(0), F = dh->size(1), N = 2 * F;
+  const at::Device dev = dh->device();
+  Mat mdh, mgu;
+  if (!mat(*dh, T, F, at::kBFloat16, "dh", mdh) || !mat(v[1], T, N, at::kBFloat16, "gu", mgu))
+    return nullptr;
+  const int mode = static_cast<int>(PyLong_AsLong(v[6]));
+  void *stream = nullptr;
+  if ((mode == -1 && PyErr_Occurred()) || !stream_of(v[14], dev, stream)) return nullptr;
+  Results r;
+  Mat d, q, s, qT, sT, hT, shT;
+  bool has_d, has_q, has_qT, has_hT, has;
+  if (!r.add(v[7], v[2] == Py_True, T, N, at::kBFloat16, dev, "d", d, has_d) ||
+      !r.add(v[8], v[3] == Py_True, T, N, at::kByte, dev, "q", q, has_q) ||
+      !r.add(v[9], has_q, N / 128, T, at::kFloat, dev, "s", s, has) ||
+      !r.add(v[10], v[4] == Py_True, N, T, at::kByte, dev, "qT", qT, has_qT) ||
+      !r.add(v[11], has_qT, T / 128, N, at::kFloat, dev, "sT", sT, has) ||
+      !r.add(v[12], v[5] == Py_True, F, T, at::kByte, dev, "hT", hT, has_hT) ||
+      !r.add(v[13], has_hT, T / 128, F, at::kFloat, dev, "shT", shT, has))
+    return nullptr;
+  return r.tuple(fp8q_swiglu_bwd(mdh.p, mdh.ld, mgu.p, mgu.ld, d.p, d.ld, q.p, q.ld,
+                                 static_cast<float *>(s.p), s.ld, qT.p, qT.ld,
+                                 static_cast<float *>(sT.p), sT.ld, hT.p, hT.ld,
+                                 static_cast<float *>(shT.p), shT.ld, T, F, mode, stream));
+}
+
+// Row and matrix pitch of a matrix or a batch of matrices.
+bool pitches(const at::Tensor &t, const char *name, int64_t &ld, int64_t &stride) {
+  const int64_t m = t.size(-2), n = t.size(-1);
+  if (n > 1 && m > 0 && t.stride(-1) != 1)
+    return fail(std::string(name) + " must have a contiguous last dimension");
+  ld = m > 1 ? t.stride(-2) : n;
+  stride = t.dim() == 3 ? t.stride(0) : 0;
+  return true;
+}
+
+// (g, steps, a, b, c, eps, out_dtype, out, workspace, stream)
+PyObject *newton_schulz_impl(PyObject *const *v, Py_ssize_t n) {
+  if (n != 10) return wrong_count("newton_schulz");
+  const at::Tensor *g = tensor(v[0], "g");
+  if (!g) return nullptr;
+  if ((g->dim() != 2 && g->dim() != 3) ||
+      (g->scalar_type() != at::kFloat && g->scalar_type() != at::kBFloat16) || !g->is_cuda()) {
+    fail("g must be an FP32 or BF16 matrix or batch of matrices on a CUDA device");
+    return nullptr;
+  }
+  const at::Device dev = g->device();
+  const int steps = static_cast<int>(PyLong_AsLong(v[1]));
+  const double a = PyFloat_AsDouble(v[2]), b = PyFloat_AsDouble(v[3]), c = PyFloat_AsDouble(v[4]),
+               eps = PyFloat_AsDouble(v[5]);
+  const int out_dtype = static_cast<int>(PyLong_AsLong(v[6]));
+  void *stream = nullptr;
+  if (PyErr_Occurred() || !stream_of(v[9], dev, stream)) return nullptr;
+  const at::ScalarType od = out_dtype == FP8Q_OUT_BF16 ? at::kBFloat16 : at::kFloat;
+  at::Tensor out;
+  if (v[7] != Py_None) {
+    const at::Tensor *t = tensor(v[7], "out");
+    if (!t) return nullptr;
+    if (t->sizes() != g->sizes() || t->scalar_type() != od || !t->is_cuda()) {
+      fail("out must have g's shape and the type out_dtype names, on a CUDA device");
+      return nullptr;
+    }
+    out = *t;
+  } else {
+    out = new_tensor(g->sizes(), od, dev);
+  }
+  int64_t ld_g, stride_g, ld_o, stride_o;
+  if (!pitches(*g, "g", ld_g, stride_g) || !pitches(out, "out", ld_o, stride_o)) return nullptr;
+  const int64_t B = g->dim() == 3 ? g->size(0) : 1, m = g->size(-2), nn = g->size(-1);
+  at::Tensor ws;
+  if (v[8] != Py_None) {
+    const at::Tensor *t = tensor(v[8], "workspace");
+    if (!t) return nullptr;
+    if (!t->is_cuda() || !t->is_contiguous()) {
+      fail("workspace must be a contiguous tensor on a CUDA device");
+      return nullptr;
+    }
+    ws = *t;
+  } else {
+    const int64_t bytes = fp8q_newton_schulz_workspace_bytes(B, m, nn);
+    ws = new_tensor({bytes > 0 ? bytes : 1}, at::kByte, dev);
+  }
+  const bool any = g->numel() > 0;
+  const fp8q_status st = fp8q_newton_schulz(
+      any ? g->data_ptr() : nullptr, ld_g, stride_g,
+      g->scalar_type() == at::kFloat ? FP8Q_OUT_FP32 : FP8Q_OUT_BF16,
+      any ? out.data_ptr() : nullptr, ld_o, stride_o, out_dtype, B, m, nn, steps,
+      static_cast<float>(a), static_cast<float>(b), static_cast<float>(c), static_cast<float>(eps),
+      ws.data_ptr(), static_cast<int64_t>(ws.nbytes()), stream);
+  if (st != FP8Q_OK) return PyLong_FromLong(st);
+  if (v[7] != Py_None) {
+    Py_INCREF(v[7]);
+    return v[7];
+  }
+  return THPVariable_Wrap(std::move(out));
+}
+
+// No C++ exception (an allocation that fails, say) leaves through CPython.
+template <PyObject *(*kImpl)(PyObject *const *, Py_ssize_t)>
+PyObject *guarded(PyObject *, PyObject *const *v, Py_ssize_t n) {
+  try {
+    return kImpl(v, n);
+  } catch (const c10::OutOfMemoryError &e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
+  } catch (const std::exception &e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
+PyMethodDef methods[] = {
+    {"swiglu", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<swiglu_impl>)),
+     METH_FASTCALL, nullptr},
+    {"swiglu_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<bwd_impl>)),
+     METH_FASTCALL, nullptr},
+    {"newton_schulz",
+     reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<newton_schulz_impl>)),
+     METH_FASTCALL, nullptr},
+    {nullptr, nullptr, 0, nullptr}};
+
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, methods,
+                      nullptr,               nullptr,        nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__torch_calls(void) { return PyModule_Create(&module); }
