@@ -307,9 +307,8 @@ constexpr int kCtlRegs = 56, kEpiRegs = 224;
 static_assert(kCtlRegs + 2 * kEpiRegs <= 3 * kLaunchRegs, "register split must fit the launch");
 constexpr uint64_t kDrainNs = 1000000000ull;
 // Staging of one epilogue warp: its 32 rows x 128 columns as FP16, in blocks of
-// 32 columns (2 KB each; also a padded FP32 block of the final result).
+// 32 columns (2 KB each; also half an FP32 block of the final result).
 constexpr uint32_t kStageBlock = 2048, kStageWarp = 4 * kStageBlock;
-static_assert(4 * kStageBlock >= 32 * 33 * 4, "a padded FP32 block fits");
 constexpr int64_t kSlotFloats = 2 * 128 * 256;
 
 struct alignas(8) Ctl {
@@ -481,6 +480,12 @@ __device__ __forceinline__ uint32_t unit_at(uint32_t block, uint32_t r, uint32_t
   return block + r * 64 + 16 * (k ^ ((r >> 1) & 3));
 }
 
+__device__ __forceinline__ uint16_t ld_shared_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 // A warp's old values, 32 rows x 128 columns: lane l fetches 16-byte unit l % 4
 // of rows l / 4 + 8 i of each 32-column block.  Pitches are multiples of 8, so a
 // unit that begins inside the matrix may be read to its end.
@@ -529,24 +534,26 @@ __device__ __forceinline__ void store_staged(const Epi &e, uint16_t *m, int64_t 
   __syncwarp();
   const int r0 = e.row0 + (e.lane >> 2);
   uint16_t *dst = m + static_cast<int64_t>(r0) * ld + cbase + 8 * (e.lane & 3);
+#pragma unroll 1
+  for (int c = 0; c < blocks; ++c, dst += 32) {
+    const int left = cols - (cbase + 32 * c + 8 * (e.lane & 3));
+    uint4 u[4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
+    for (int i = 0; i < 4; ++i)
+      u[i] = ld_shared_v4(unit_at(e.stage + c * kStageBlock, (e.lane >> 2) + 8 * i, e.lane & 3));
+    if (left >= 8) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int left = cols - (cbase + 32 * c + 8 * (e.lane & 3));
-      if (c >= blocks || r0 + 8 * i >= rows || left <= 0) continue;
-      const uint4 u =
-          ld_shared_v4(unit_at(e.stage + c * kStageBlock, (e.lane >> 2) + 8 * i, e.lane & 3));
-      uint16_t *at = dst + 8 * i * ld + 32 * c;
-      if (left >= 8) {
-        *reinterpret_cast<uint4 *>(at) = u;
-      } else {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int k = 0; k < 7; ++k)
-          if (k < left) at[k] = static_cast<uint16_t>(k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xFFFFu);
+      for (int i = 0; i < 4; ++i)
+        if (r0 + 8 * i < rows) *reinterpret_cast<uint4 *>(dst + 8 * i * ld) = u[i];
+    } else if (left > 0) {
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        if (r0 + 8 * i >= rows) break;
+        const uint32_t at = unit_at(e.stage + c * kStageBlock, (e.lane >> 2) + 8 * i, e.lane & 3);
+        for (int k = 0; k < left; ++k) dst[8 * i * ld + k] = ld_shared_u16(at + 2 * k);
       }
     }
+  }
 }
 // A lane's row of a block, transposed: column runs are contiguous over the lanes.
 __device__ __forceinline__ void store_mirror(const Epi &e, const uint32_t (&w)[16], __half *m,
@@ -580,17 +587,22 @@ __device__ __forceinline__ void store_out(const Epi &e, const float (&v)[32], co
     }
     return;
   }
-  __syncwarp();
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {  // 16 rows at a time: 2 KB
+    __syncwarp();
+    if ((e.lane >> 4) == half) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) st[e.lane * 33 + i] = v[i];
-  __syncwarp();
-  if (col0 + e.lane < p.q) {
-    const int n = min(32, p.p - e.row0);
-    for (int i = 0; i < n; ++i) {
-      const int64_t at = base + static_cast<int64_t>(e.row0 + i) * p.ldo + col0 + e.lane;
-      const float f = st[i * 33 + e.lane];
-      if (p.out_f32) static_cast<float *>(p.out)[at] = f;
-      else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(f);
+      for (int i = 0; i < 32; ++i) st[(e.lane & 15) * 32 + (i ^ e.lane)] = v[i];
+    }
+    __syncwarp();
+    if (col0 + e.lane < p.q) {
+      const int r0 = e.row0 + 16 * half, n = min(16, p.p - r0);
+      for (int i = 0; i < n; ++i) {
+        const int64_t at = base + static_cast<int64_t>(r0 + i) * p.ldo + col0 + e.lane;
+        const float f = st[i * 32 + (e.lane ^ (16 * half + i))];
+        if (p.out_f32) static_cast<float *>(p.out)[at] = f;
+        else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(f);
+      }
     }
   }
 }
@@ -695,73 +707,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                                static_cast<uint32_t>(buf * kTile + half * (bn / 2));
-        uint32_t r[4][32];
+        // block c of the accumulator; the last one releases it
+        auto load_block = [&](int c, uint32_t (&r)[32]) {
+          tmem_ld_32x32b_x32(taddr + 32 * c, r);
+          tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c < blocks) tmem_ld_32x32b_x32(taddr + 32 * c, r[c]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[c][i]));
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(tempty0 + static_cast<uint32_t>(buf) * 8u);
-        buf ^= 1;
-        if (buf == 0) tphase ^= 1;
-
+          for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+          if (c == blocks - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty0 + static_cast<uint32_t>(buf) * 8u);
+          }
+        };
         if (!owner) {  // partial sums for the pair that began the tile
           // ... once it has added this warp's last ones
           if (given && !(ok = warp_wait(&p.sync->used[pair][rank][ew], given))) break;
           float4 *slot = slot_of(pair);
-          if (live) {
+#pragma unroll 1
+          for (int c = 0; c < blocks; ++c, slot += 8 * 32) {
+            uint32_t r[32];
+            load_block(c, r);
+            if (!live) continue;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                if (c < blocks) __stcg(slot + (8 * c + k) * 32,
-                       make_float4(__uint_as_float(r[c][4 * k]), __uint_as_float(r[c][4 * k + 1]),
-                                   __uint_as_float(r[c][4 * k + 2]),
-                                   __uint_as_float(r[c][4 * k + 3])));
+            for (int k = 0; k < 8; ++k)
+              __stcg(slot + k * 32,
+                     make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]),
+                                 __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3])));
           }
           given = static_cast<uint32_t>(phase) + 1;
           __syncwarp();
           if (lane == 0) st_release(&p.sync->part[pair][rank][ew], given);
+          buf ^= 1;
+          if (buf == 0) tphase ^= 1;
           continue;
         }
         // pairs after this one that hold the rest of the tile
         const int helpers =
             s.kb1 == walk.kblocks ? 0 : (walk.kblocks - s.kb1 + p.per[kind] - 1) / p.per[kind];
-        for (int h = 1; ok && h <= helpers; ++h) {
-          if (!(ok = warp_wait(&p.sync->part[pair + h][rank][ew], static_cast<uint32_t>(phase) + 1)))
-            break;
-          if (live) {
-            const float4 *src = slot_of(pair + h);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
+        for (int h = 1; ok && h <= helpers; ++h)
+          ok = warp_wait(&p.sync->part[pair + h][rank][ew], static_cast<uint32_t>(phase) + 1);
+        if (!ok) break;
+        const bool bf16_rows = last && p.out_vec;
+        // tiles on the diagonal hold both triangles themselves
+        const bool mirror = kind != kUpdate && s.col0 >= s.row0 + kTile;
+        if (kind == kGram) __syncwarp();  // the blocks' previous contents have been read
+        {
+          // one block at a time, the loop not unrolled: this code runs once per
+          // tile, and fetching it costs more than running it
+#pragma unroll 1
+          for (int c = 0; c < blocks; ++c) {
+            uint32_t r[32];
+            load_block(c, r);
+            if (!live) continue;
+            for (int h = 1; h <= helpers; ++h) {
+              const float4 *src = slot_of(pair + h) + 8 * 32 * c;
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                if (c >= blocks) continue;
-                const float4 f = __ldcg(src + (8 * c + k) * 32);
-                r[c][4 * k] = __float_as_uint(__uint_as_float(r[c][4 * k]) + f.x);
-                r[c][4 * k + 1] = __float_as_uint(__uint_as_float(r[c][4 * k + 1]) + f.y);
-                r[c][4 * k + 2] = __float_as_uint(__uint_as_float(r[c][4 * k + 2]) + f.z);
-                r[c][4 * k + 3] = __float_as_uint(__uint_as_float(r[c][4 * k + 3]) + f.w);
+                const float4 f = __ldcg(src + k * 32);
+                r[4 * k] = __float_as_uint(__uint_as_float(r[4 * k]) + f.x);
+                r[4 * k + 1] = __float_as_uint(__uint_as_float(r[4 * k + 1]) + f.y);
+                r[4 * k + 2] = __float_as_uint(__uint_as_float(r[4 * k + 2]) + f.z);
+                r[4 * k + 3] = __float_as_uint(__uint_as_float(r[4 * k + 3]) + f.w);
               }
-          }
-          __syncwarp();
-          if (lane == 0)
-            st_release(&p.sync->used[pair + h][rank][ew], static_cast<uint32_t>(phase) + 1);
-        }
-        if (!ok) break;
-        if (live) {
-          const bool bf16_rows = last && p.out_vec;
-          // tiles on the diagonal hold both triangles themselves
-          const bool mirror = kind != kUpdate && s.col0 >= s.row0 + kTile;
-          if (kind == kGram) __syncwarp();  // the blocks' previous contents have been read
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c >= blocks) continue;
+            }
             const int col0 = cbase + 32 * c;
             uint32_t w[16];
             if (kind == kUpdate) {
@@ -772,8 +780,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (!last || bf16_rows) {
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                  const float x = fmaf(co, f16_lo(w[k]), scale * __uint_as_float(r[c][2 * k]));
-                  const float y = fmaf(co, f16_hi(w[k]), scale * __uint_as_float(r[c][2 * k + 1]));
+                  const float x = fmaf(co, f16_lo(w[k]), scale * __uint_as_float(r[2 * k]));
+                  const float y = fmaf(co, f16_hi(w[k]), scale * __uint_as_float(r[2 * k + 1]));
                   if (last) {
                     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
                     w[k] = *reinterpret_cast<const uint32_t *>(&h);
@@ -786,9 +794,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                  r[c][i] = __float_as_uint(
-                      fmaf(co, i & 1 ? f16_hi(w[i / 2]) : f16_lo(w[i / 2]),
-                           scale * __uint_as_float(r[c][i])));
+                  r[i] = __float_as_uint(fmaf(co, i & 1 ? f16_hi(w[i / 2]) : f16_lo(w[i / 2]),
+                                              scale * __uint_as_float(r[i])));
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                if (col0 < cols) store_out(e, v, p, s.b, col0, st + c * (kStageBlock / 4));
               }
               continue;
             }
@@ -796,7 +807,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (kind == kGram) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                r[c][i] = __float_as_uint((1.0f / kS) * __uint_as_float(r[c][i]));
+                r[i] = __float_as_uint((1.0f / kS) * __uint_as_float(r[i]));
             } else {
               const float cs = p.c / kS, co = fmaf(cs, d_row, p.b);
               read_row(e, c, w);
@@ -804,7 +815,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                   if (i == lane)
-                    d_new = fmaf(p.b, d_row, cs * fmaf(d_row, d_row, __uint_as_float(r[c][i])));
+                    d_new = fmaf(p.b, d_row, cs * fmaf(d_row, d_row, __uint_as_float(r[i])));
               }
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
@@ -816,7 +827,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < 4; ++j) {
                   const int i = 4 * k + j;
                   const float o = i & 1 ? f16_hi(w[i / 2]) : f16_lo(w[i / 2]);
-                  r[c][i] = __float_as_uint(fmaf(co + dc[j], o, cs * __uint_as_float(r[c][i])));
+                  r[i] = __float_as_uint(fmaf(co + dc[j], o, cs * __uint_as_float(r[i])));
                 }
               }
             }
@@ -826,39 +837,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (i == lane) {
-                  if (kind == kGram) d_new = __uint_as_float(r[c][i]);
-                  r[c][i] = 0u;
+                  if (kind == kGram) d_new = __uint_as_float(r[i]);
+                  r[i] = 0u;
                 }
               if (row < p.p)
                 __stcg((kind == kGram ? p.da : p.db) + static_cast<int64_t>(s.b) * p.lda + row, d_new);
             }
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const __half2 h = __floats2half2_rn(__uint_as_float(r[c][2 * k]),
-                                                  __uint_as_float(r[c][2 * k + 1]));
+              const __half2 h = __floats2half2_rn(__uint_as_float(r[2 * k]),
+                                                  __uint_as_float(r[2 * k + 1]));
               w[k] = *reinterpret_cast<const uint32_t *>(&h);
             }
             write_row(e, c, w);
             if (mirror) store_mirror(e, w, (kind == kGram ? p.am : p.bm) + amat, p.lda, p.p, col0);
           }
-          if (!last) {
-            __half *dst = kind == kUpdate ? p.x[cur ^ 1] + xmat : (kind == kGram ? p.am : p.bm) + amat;
-            store_staged(e, reinterpret_cast<uint16_t *>(dst), kind == kUpdate ? p.ldx : p.lda, p.p,
-                         cols, cbase, blocks);
-          } else if (bf16_rows) {
-            store_staged(e, static_cast<uint16_t *>(p.out) + static_cast<int64_t>(s.b) * p.out_stride,
-                         p.ldo, p.p, cols, cbase, blocks);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (c < blocks && cbase + 32 * c < cols) {
-                float v[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[c][i]);
-                store_out(e, v, p, s.b, cbase + 32 * c, st);
-              }
+          if (live && (!last || bf16_rows)) {
+            uint16_t *dst = static_cast<uint16_t *>(p.out) + static_cast<int64_t>(s.b) * p.out_stride;
+            int64_t ld = p.ldo;
+            if (!last) {
+              dst = reinterpret_cast<uint16_t *>(
+                  kind == kUpdate ? p.x[cur ^ 1] + xmat : (kind == kGram ? p.am : p.bm) + amat);
+              ld = kind == kUpdate ? p.ldx : p.lda;
+            }
+            store_staged(e, dst, ld, p.p, cols, cbase, blocks);
           }
         }
+        for (int h = 1; h <= helpers; ++h) {  // the slots may be written again
+          __syncwarp();
+          if (lane == 0)
+            st_release(&p.sync->used[pair + h][rank][ew], static_cast<uint32_t>(phase) + 1);
+        }
+        buf ^= 1;
+        if (buf == 0) tphase ^= 1;
         // warp 2 counts the tile as done.  A warp is at most two tiles ahead of
         // another (two accumulators), so four barriers are enough.
         __syncwarp();
