@@ -286,7 +286,15 @@ __global__ void __launch_bounds__(256) ns_load_tall_kernel(const In *__restrict_
 //    memory before it waits for the accumulator, the results replace them
 //    there, and global accesses are whole 64-byte pieces of rows.
 //  - Data written by other SMs in an earlier phase is read past L1 (ld.cg), and
-//    by TMA after a proxy fence on both sides of the counter.
+//    by TMA after a proxy fence behind the counter.  One thread per CTA polls the
+//    counter and tells the epilogue warps through shared memory.
+//  - The operand ring takes what the epilogue's staging leaves: 5 stages of 32 KB
+//    for 256-wide tiles, 8 of 24 KB for 128, 10 of 20 KB for 64.  A stage's copy
+//    takes about 1.2 us from issue to arrival, so that with 5 stages no tile
+//    could run faster than 0.24 us per K block (128-wide tiles: 0.17 us of MMAs).
+//    Changing the layout between phases drains the ring, which a single matrix
+//    does anyway; a batch, whose phases overlap, keeps its widest tile's layout
+//    (16 of 896 x 640: 204 us, 240 with changes).
 //  - The tile width is chosen per phase kind (see Plan): 256 columns feed the
 //    tensor cores best (62 bytes of operands per clock and SM), narrower tiles
 //    cover the matrix with less waste and finish sooner where there are few.
@@ -297,7 +305,7 @@ constexpr int kGram = 0, kPoly = 1, kUpdate = 2;  // A = X X^T | B = bA + cA^2 |
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kTile = 256;               // rows of a pair's tile, and its largest width
-constexpr int kStages = 5;
+constexpr int kMaxStages = 10;
 constexpr uint32_t kOpBytes = 128 * 128;  // one operand's share of a CTA: 128 x 64 FP16
 constexpr int kMaxPairs = 76;            // slots for partial sums
 // Register split as in the GEMMs: built for kLaunchRegs (checked by the build),
@@ -306,19 +314,31 @@ constexpr int kLaunchRegs = 168;
 constexpr int kCtlRegs = 56, kEpiRegs = 224;
 static_assert(kCtlRegs + 2 * kEpiRegs <= 3 * kLaunchRegs, "register split must fit the launch");
 constexpr uint64_t kDrainNs = 1000000000ull;
-// Staging of one epilogue warp: its 32 rows x 128 columns as FP16, in blocks of
-// 32 columns (2 KB each; also half an FP32 block of the final result).
-constexpr uint32_t kStageBlock = 2048, kStageWarp = 4 * kStageBlock;
+// Staging of one epilogue warp: its rows and columns as FP16, in blocks of 32 x
+// 32 (2 KB each; also half an FP32 block of the final result).
+constexpr uint32_t kStageBlock = 2048;
+// Shared memory from a 1024-byte boundary on: the ring, upwards, and at the end
+// the staging of the kind's tile width.
+constexpr uint32_t kArena = 224 * 1024;
+__host__ __device__ constexpr uint32_t staging_bytes(int bn) { return kEpiWarps * (bn / 64) * kStageBlock; }
+__host__ __device__ constexpr uint32_t ring_stage(int bn) { return kOpBytes + bn / 2 * 128; }
+__host__ __device__ constexpr int ring_stages(int bn) {
+  return static_cast<int>((kArena - staging_bytes(bn)) / ring_stage(bn)) < kMaxStages
+             ? static_cast<int>((kArena - staging_bytes(bn)) / ring_stage(bn))
+             : kMaxStages;
+}
+static_assert(ring_stages(256) == 5 && ring_stages(128) == 8 && ring_stages(64) == 10, "ring depths");
 constexpr int64_t kSlotFloats = 2 * 128 * 256;
 
 struct alignas(8) Ctl {
-  uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
-  uint64_t stored[4];  // a tile's results are written, by tile number mod 4
+  uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drain;
+  // counts, not barrier phases: writer and reader may be any number of steps apart
+  uint32_t stored[kEpiWarps];  // tiles whose results a warp has written
+  uint32_t ready;              // segments whose matrix is ready for its phase
   uint32_t tmem_base;
   int abort_flag;
 };
-constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * 2 * kOpBytes +
-                         kEpiWarps * kStageWarp + sizeof(Ctl);
+constexpr size_t kSmem = 1024 + kArena + sizeof(Ctl);
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
 // Counters in the workspace, zeroed by the set-up kernel of each call; after
@@ -333,6 +353,7 @@ struct NsArgs {
   int kb_q, kb_p;          // 64-wide K blocks along q and p
   int row_tiles;           // 256-row tiles along p
   int bn[3], tiles[3];     // by phase kind: tile width, tiles per matrix,
+  int layout[3];           // the width that the ring and the staging are laid out for,
   int per[3];              // units per pair of an even split, or 0: whole tiles
   float a, b, c;
   __half *x[2], *am, *bm;
@@ -412,6 +433,30 @@ __device__ __forceinline__ bool wait_count(const uint32_t *p, uint32_t want,
   const uint64_t t0 = global_timer_ns();
   while (true) {
     if (ld_acquire(p) >= want) return true;
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > limit_ns) {
+      *abort_flag = 1;
+      atomicExch(&g_ns_status, FP8Q_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
+// The same for a counter in shared memory.
+__device__ __forceinline__ uint32_t ld_acquire_shared(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_release_shared(uint32_t addr, uint32_t v) {
+  asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ bool wait_shared(uint32_t addr, uint32_t want, volatile int *abort_flag,
+                                            uint64_t limit_ns) {
+  if (ld_acquire_shared(addr) >= want) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (ld_acquire_shared(addr) >= want) return true;
     if (*abort_flag) return false;
     if (global_timer_ns() - t0 > limit_ns) {
       *abort_flag = 1;
@@ -555,6 +600,19 @@ __device__ __forceinline__ void store_staged(const Epi &e, uint16_t *m, int64_t 
     }
   }
 }
+// r[lane], by halving.
+__device__ __forceinline__ float own_column(const uint32_t (&r)[32], int lane) {
+  uint32_t v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = lane & 16 ? r[i + 16] : r[i];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = lane & 8 ? v[i + 8] : v[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = lane & 4 ? v[i + 4] : v[i];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) v[i] = lane & 2 ? v[i + 2] : v[i];
+  return __uint_as_float(lane & 1 ? v[1] : v[0]);
+}
 // A lane's row of a block, transposed: column runs are contiguous over the lanes.
 __device__ __forceinline__ void store_mirror(const Epi &e, const uint32_t (&w)[16], __half *m,
                                              int64_t ld, int n, int col0) {
@@ -612,9 +670,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const uint32_t sL = smem_u32(smem), sR = sL + kStages * kOpBytes;
-  uint8_t *staging = smem + static_cast<size_t>(kStages) * 2 * kOpBytes;
-  Ctl *ctl = reinterpret_cast<Ctl *>(staging + kEpiWarps * kStageWarp);
+  const uint32_t ring = smem_u32(smem);
+  Ctl *ctl = reinterpret_cast<Ctl *>(smem + kArena);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int *abort_flag = &ctl->abort_flag;
   const uint32_t rank = cluster_ctarank();
@@ -622,7 +679,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int phases = 3 * p.steps;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(smem_u32(&ctl->full[i]), 1);
       mbar_init(smem_u32(&ctl->empty[i]), 1);
     }
@@ -632,7 +689,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&ctl->drain), 1);
     ctl->abort_flag = 0;
-    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&ctl->stored[i]), kEpiWarps);
+    for (int i = 0; i < kEpiWarps; ++i) ctl->stored[i] = 0;
+    ctl->ready = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane < static_cast<int>(sizeof(Maps) / sizeof(CUtensorMap)))
@@ -652,8 +710,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
     const uint32_t tempty0 = mapa_shared(smem_u32(&ctl->tempty[0]), 0);
     Epi e;
-    float *st = reinterpret_cast<float *>(staging + ew * kStageWarp);
-    e.stage = smem_u32(st);
     e.lane = lane;
     // this warp's part of a pair's slot of partial sums, as float4
     auto slot_of = [&](int pr) {
@@ -665,7 +721,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool got = lane != 0 || wait_count(count, want, abort_flag, p.timeout_ns);
       return __all_sync(0xffffffffu, got) != 0;
     };
-    int buf = 0, tile_no = 0;
+    int buf = 0, tile_no = 0, seg_no = 0;
     uint32_t tphase = 0, given = 0;  // given: phase + 1 of this warp's last partial sums
     bool ok = true;
     for (int phase = 0; ok && phase < phases; ++phase) {
@@ -673,7 +729,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool last = phase + 1 == phases;
       Walk walk(p, phase, pair);
       Segment s;
-      while (walk.next(p, s)) {
+      const uint32_t staging = staging_bytes(p.layout[kind]);
+      uint8_t *stage = smem + kArena - staging + staging / kEpiWarps * ew;
+      e.stage = smem_u32(stage);
+      for (; walk.next(p, s); ++seg_no) {
         e.row0 = s.row0 + static_cast<int>(rank) * 128 + quarter * 32;
         const int bn = p.bn[kind], blocks = bn / 64;  // 32-column blocks of this warp
         const int row = e.row0 + lane, cbase = s.col0 + half * (bn / 2);
@@ -688,7 +747,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (owner && live && kind != kGram) {
           // old values are on their way, or in place, before the accumulator is
           // waited for: under the MMAs' own traffic a load takes over a microsecond
-          if (!(ok = warp_wait(&p.done[s.b], walk.ready))) break;
+          const bool there = lane != 0 || wait_shared(smem_u32(&ctl->ready),
+                                                      static_cast<uint32_t>(seg_no) + 1, abort_flag,
+                                                      p.timeout_ns);
+          if (!(ok = __all_sync(0xffffffffu, there))) break;
           if (row < p.p) d_row = __ldcg(diag + row);
           if (kind == kPoly) {  // the pitch is whole
             const int dc = cbase + 4 * lane;
@@ -799,7 +861,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 float v[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-                if (col0 < cols) store_out(e, v, p, s.b, col0, st + c * (kStageBlock / 4));
+                if (col0 < cols) store_out(e, v, p, s.b, col0, reinterpret_cast<float *>(stage + c * kStageBlock));
               }
               continue;
             }
@@ -811,12 +873,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             } else {
               const float cs = p.c / kS, co = fmaf(cs, d_row, p.b);
               read_row(e, c, w);
-              if (e.row0 == col0) {  // b d_A + c/S (sum + d_A^2) on the diagonal
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (i == lane)
-                    d_new = fmaf(p.b, d_row, cs * fmaf(d_row, d_row, __uint_as_float(r[i])));
-              }
+              if (e.row0 == col0)  // b d_A + c/S (sum + d_A^2) on the diagonal
+                d_new = fmaf(p.b, d_row, cs * fmaf(d_row, d_row, own_column(r, lane)));
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 const float dc[4] = {__shfl_sync(0xffffffffu, d_col.x, 8 * c + k),
@@ -831,15 +889,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
               }
             }
-            if (e.row0 == col0) {
-              // the diagonal crosses this block (both begin at multiples of 32): its
-              // values leave as FP32, the FP16 matrix holds zeros there
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i == lane) {
-                  if (kind == kGram) d_new = __uint_as_float(r[i]);
-                  r[i] = 0u;
-                }
+            // the diagonal crosses this block (both begin at multiples of 32): its
+            // values leave as FP32, the FP16 matrix holds zeros there
+            const bool on_diag = e.row0 == col0;
+            if (on_diag) {
+              if (kind == kGram) d_new = own_column(r, lane);
               if (row < p.p)
                 __stcg((kind == kGram ? p.da : p.db) + static_cast<int64_t>(s.b) * p.lda + row, d_new);
             }
@@ -850,6 +904,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               w[k] = *reinterpret_cast<const uint32_t *>(&h);
             }
             write_row(e, c, w);
+            if (on_diag)
+              st_shared_u16(unit_at(e.stage + c * kStageBlock, lane, lane >> 3) + 2 * (lane & 7), 0u);
             if (mirror) store_mirror(e, w, (kind == kGram ? p.am : p.bm) + amat, p.lda, p.p, col0);
           }
           if (live && (!last || bf16_rows)) {
@@ -870,10 +926,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         buf ^= 1;
         if (buf == 0) tphase ^= 1;
-        // warp 2 counts the tile as done.  A warp is at most two tiles ahead of
-        // another (two accumulators), so four barriers are enough.
+        // warp 2 counts the tile as done
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl->stored[tile_no & 3]));
+        if (lane == 0)
+          st_release_shared(smem_u32(&ctl->stored[ew]), static_cast<uint32_t>(tile_no) + 1);
         ++tile_no;
       }
     }
@@ -886,47 +942,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ================================================== TMA producer
     if (lane == 0) {
-      int st = 0;
-      uint32_t ring = 0, armed = 0, armed_phase = 0;
+      int st = 0, seg_no = 0, tile_no = 0, before = p.layout[0];
+      uint32_t phases_of = 0, armed = 0;  // bit i: parity of stage i's next use; used so far
       bool ok = true;
+      auto wait_empty = [&](int i) {
+        return mbar_wait_bounded(smem_u32(&ctl->empty[i]), ((phases_of >> i) & 1u) ^ 1u, abort_flag,
+                                 &g_ns_status, p.timeout_ns, FP8Q_ERR_TIMEOUT);
+      };
       for (int phase = 0; ok && phase < phases; ++phase) {
         const int kind = phase % 3, cur = (phase / 3) & 1;
         const CUtensorMap *ml = kind == kGram ? &maps.x[cur] : kind == kPoly ? &maps.a : &maps.b;
         const CUtensorMap *mr = kind == kGram   ? &maps.xr[cur]
                                 : kind == kPoly ? &maps.ar
                                                 : &maps.xn[cur];
-        const int half_cols = p.bn[kind] / 2;
-        const uint32_t tx = 2 * (kOpBytes + static_cast<uint32_t>(half_cols) * 128);
+        const int half_cols = p.bn[kind] / 2, layout = p.layout[kind], stages = ring_stages(layout);
+        const uint32_t stage_bytes = ring_stage(layout), tx = 2 * ring_stage(p.bn[kind]);
+        if (layout != before) {
+          // another layout: every stage has been used up, and the last tile's
+          // results have left the staging that the ring may now reach into
+          for (int i = 0; ok && i < kMaxStages; ++i)
+            if (armed >> i & 1u) ok = wait_empty(i);
+          for (int i = 0; ok && i < kEpiWarps; ++i)
+            ok = wait_shared(smem_u32(&ctl->stored[i]), static_cast<uint32_t>(tile_no), abort_flag,
+                             p.timeout_ns);
+          if (!ok) break;
+          before = layout;
+          st = 0;
+        }
         Walk walk(p, phase, pair);
         Segment s;
         while (ok && walk.next(p, s)) {
           if (!(ok = wait_count(&p.done[s.b], walk.ready, abort_flag, p.timeout_ns))) break;
+          st_release_shared(smem_u32(&ctl->ready), static_cast<uint32_t>(++seg_no));
+          if (s.kb0 == 0) ++tile_no;
           fence_proxy_async_all();
           for (int kb = s.kb0; kb < s.kb1; ++kb) {
-            if (!mbar_wait_bounded(smem_u32(&ctl->empty[st]), ring ^ 1, abort_flag, &g_ns_status,
-                                   p.timeout_ns, FP8Q_ERR_TIMEOUT)) {
-              ok = false;
-              break;
-            }
+            if (!(ok = wait_empty(st))) break;
             const uint32_t fb = smem_u32(&ctl->full[st]);
             if (rank == 0) mbar_arrive_expect_tx(fb, tx);
-            const uint32_t fb0 = mapa_shared(fb, 0);
-            tma_load_3d_pair(sL + st * kOpBytes, ml, fb0, kb * 64,
-                             s.row0 + static_cast<int>(rank) * 128, s.b);
+            const uint32_t fb0 = mapa_shared(fb, 0), sl = ring + st * stage_bytes, sr = sl + kOpBytes;
+            tma_load_3d_pair(sl, ml, fb0, kb * 64, s.row0 + static_cast<int>(rank) * 128, s.b);
             const int rc = s.col0 + static_cast<int>(rank) * half_cols;
             if (kind != kUpdate) {
-              tma_load_3d_pair(sR + st * kOpBytes, mr, fb0, kb * 64, rc, s.b);
+              tma_load_3d_pair(sr, mr, fb0, kb * 64, rc, s.b);
             } else {
-              tma_load_3d_pair(sR + st * kOpBytes, mr, fb0, rc, kb * 64, s.b);
-              if (half_cols > 64)
-                tma_load_3d_pair(sR + st * kOpBytes + 8192, mr, fb0, rc + 64, kb * 64, s.b);
+              tma_load_3d_pair(sr, mr, fb0, rc, kb * 64, s.b);
+              if (half_cols > 64) tma_load_3d_pair(sr + 8192, mr, fb0, rc + 64, kb * 64, s.b);
             }
             armed |= 1u << st;
-            armed_phase = (armed_phase & ~(1u << st)) | (ring << st);
-            if (++st == kStages) {
-              st = 0;
-              ring ^= 1;
-            }
+            phases_of ^= 1u << st;
+            if (++st == stages) st = 0;
           }
         }
       }
@@ -934,8 +999,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // this CTA's copies land before it exits (the leading CTA's barriers
         // see both CTAs' copies; the other waits long enough for any copy)
         if (rank == 0)
-          for (int i = 0; i < kStages; ++i)
-            if (armed & (1u << i)) mbar_wait_drain(smem_u32(&ctl->full[i]), (armed_phase >> i) & 1);
+          for (int i = 0; i < kMaxStages; ++i)
+            if (armed >> i & 1u)
+              mbar_wait_drain(smem_u32(&ctl->full[i]), ((phases_of >> i) & 1u) ^ 1u);
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < 1000000ull) {
         }
@@ -944,36 +1010,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 2) {
     // ================================================== counts of done tiles
     // One device-wide fence per tile covers all epilogue warps' writes, seen
-    // through the barrier; the epilogue does not wait for it (1.5 us).
-    if (lane == 0) {
-      int tile_no = 0;
-      bool ok = true;
-      for (int phase = 0; ok && phase + 1 < phases; ++phase) {
-        Walk walk(p, phase, pair);
-        Segment s;
-        while (ok && walk.next(p, s)) {
-          if (s.kb0 != 0) continue;  // the pair that began the tile counts it
-          ok = mbar_wait_bounded(smem_u32(&ctl->stored[tile_no & 3]),
-                                 static_cast<uint32_t>(tile_no >> 2) & 1u, abort_flag, &g_ns_status,
-                                 p.timeout_ns, FP8Q_ERR_TIMEOUT);
-          if (!ok) break;
-          fence_proxy_async_all();
+    // through their counts; the epilogue does not wait for it (about 1 us).
+    int tile_no = 0;
+    bool ok = true;
+    for (int phase = 0; ok && phase + 1 < phases; ++phase) {
+      Walk walk(p, phase, pair);
+      Segment s;
+      while (ok && walk.next(p, s)) {
+        if (s.kb0 != 0) continue;  // the pair that began the tile counts it
+        ++tile_no;
+        const bool there =
+            lane >= kEpiWarps || wait_shared(smem_u32(&ctl->stored[lane]),
+                                             static_cast<uint32_t>(tile_no), abort_flag, p.timeout_ns);
+        if (!(ok = __all_sync(0xffffffffu, there))) break;
+        if (lane == 0) {
           __threadfence();
           red_release(&p.done[s.b]);
-          ++tile_no;
         }
       }
     }
   } else if (warp == 1) {
     // ================================================== MMA issuer
     if (lane == 0 && rank == 0) {
-      int st = 0, buf = 0;
-      uint32_t ring = 0, tphase = 0;
+      int st = 0, buf = 0, before = p.layout[0];
+      uint32_t phases_of = 0, tphase = 0;  // bit i: parity of stage i's next use
       bool ok = true, issued = false;
       for (int phase = 0; ok && phase < phases; ++phase) {
         Walk walk(p, phase, pair);
         const bool n_major = walk.kind == kUpdate;
-        const uint32_t idesc = idesc_f16(256, p.bn[walk.kind], n_major);
+        const int layout = p.layout[walk.kind], stages = ring_stages(layout);
+        const uint32_t idesc = idesc_f16(256, p.bn[walk.kind], n_major),
+                       stage_bytes = ring_stage(layout);
+        if (layout != before) {
+          before = layout;
+          st = 0;
+        }
         Segment s;
         while (ok && walk.next(p, s)) {
           if (!mbar_wait_bounded(smem_u32(&ctl->tempty[buf]), tphase ^ 1, abort_flag, &g_ns_status,
@@ -984,15 +1055,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t d = tmem_base + static_cast<uint32_t>(buf * kTile);
           for (int kb = s.kb0; kb < s.kb1; ++kb) {
-            if (!mbar_wait_bounded(smem_u32(&ctl->full[st]), ring, abort_flag, &g_ns_status,
-                                   p.timeout_ns, FP8Q_ERR_TIMEOUT)) {
+            if (!mbar_wait_bounded(smem_u32(&ctl->full[st]), (phases_of >> st) & 1u, abort_flag,
+                                   &g_ns_status, p.timeout_ns, FP8Q_ERR_TIMEOUT)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint64_t ad = smem_desc_sw128(sL + st * kOpBytes);
-            const uint64_t bd = n_major ? smem_desc_sw128_mn(sR + st * kOpBytes, 8192)
-                                        : smem_desc_sw128(sR + st * kOpBytes);
+            const uint32_t sl = ring + st * stage_bytes;
+            const uint64_t ad = smem_desc_sw128(sl);
+            const uint64_t bd = n_major ? smem_desc_sw128_mn(sl + kOpBytes, 8192)
+                                        : smem_desc_sw128(sl + kOpBytes);
             const uint64_t bstep = n_major ? 128 : 2;  // 16 K: 16 rows of 128 bytes, or 32 bytes
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -1000,10 +1072,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                            kb != s.kb0 || k != 0 ? 1u : 0u);
             mma_commit_pair_multicast(smem_u32(&ctl->empty[st]), 0x3);
             issued = true;
-            if (++st == kStages) {
-              st = 0;
-              ring ^= 1;
-            }
+            phases_of ^= 1u << st;
+            if (++st == stages) st = 0;
           }
           if (!ok) break;
           mma_commit_pair_multicast(smem_u32(&ctl->tfull[buf]), 0x3);
@@ -1069,8 +1139,8 @@ int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // Tile width and share of each phase kind, by an estimate of its time: rounds of
 // tiles, each the longer of its MMAs and its epilogue, and the last epilogue.  A
-// K block of a 256-row tile measured 0.34 us at 256 columns (tensor cores), 0.25
-// at 128 and 0.2 at 64 (operand traffic); an epilogue about 0.8 us and 0.55 per 64
+// K block of a 256-row tile measured 0.34 us at 256 columns (tensor cores), 0.2
+// at 128 and 0.14 at 64 (operand traffic); an epilogue about 1.5 us and 0.45 per 64
 // columns; handing split tiles over 9 us (every pair's 256 KB of partial sums go
 // through L2 at once).
 struct Plan {
@@ -1091,8 +1161,8 @@ Plan plan_of(int64_t batch, int64_t p, int64_t q, int64_t pairs) {
       int64_t tiles = row_tiles * n;
       if (k != kUpdate) tiles -= kTile / bn * (row_tiles * (row_tiles - 1) / 2);
       const int64_t all = tiles * batch, rounds = (all + pairs - 1) / pairs;
-      const double block = bn == 256 ? 0.34 : bn == 128 ? 0.25 : 0.2;
-      const double epi = 0.8 + 0.55 * (bn / 64);
+      const double block = bn == 256 ? 0.34 : bn == 128 ? 0.2 : 0.14;
+      const double epi = 1.5 + 0.45 * (bn / 64);
       const double mma = block * static_cast<double>(kblocks);
       double t = static_cast<double>(rounds) * (mma > epi ? mma : epi) + epi;
       int64_t per = 0;
@@ -1232,6 +1302,9 @@ extern "C" fp8q_status fp8q_newton_schulz(const void *g, int64_t ldg, int64_t g_
   const Plan plan = plan_of(batch, l.p, l.q, pairs);
   for (int k = 0; k < 3; ++k) {
     v.bn[k] = plan.bn[k];
+    v.layout[k] = plan.bn[k];
+    for (int j = 0; batch > 1 && j < 3; ++j)
+      if (plan.bn[j] > v.layout[k]) v.layout[k] = plan.bn[j];
     v.tiles[k] = static_cast<int>(plan.tiles[k]);
     v.per[k] = static_cast<int>(plan.per[k]);
   }
