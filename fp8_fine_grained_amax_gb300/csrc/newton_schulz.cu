@@ -54,7 +54,7 @@ fp8q_status ns_status_take(cudaStream_t s) {
 namespace {
 
 constexpr float kS = 256.0f;        // scale of the stored FP16 matrices
-constexpr int kMaxParts = 304;      // partial sums of squares per matrix
+constexpr int kMaxParts = 608;      // partial sums of squares per matrix
 
 // ------------------------------------------------------------------ set-up
 __device__ __forceinline__ float load_in(const float *p) { return __ldg(p); }
@@ -89,9 +89,11 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // Sum of squares of matrix blockIdx.y, part blockIdx.x of gridDim.x; a warp
-// takes whole rows.  kVec: rows begin on 16-byte boundaries.  The order is
-// fixed, so repeated calls agree.  Also zeroes the counters that the steps
-// kernel of this call uses.
+// takes pieces of a row (8 loads per lane with kVec false, 4 or 8 with kVec),
+// all of a piece's loads in flight.  kVec: rows begin on 16-byte boundaries.  The order is fixed, so repeated calls
+// agree.  Also zeroes the counters that the steps kernel of this call uses.
+template <bool kVec>
+constexpr int kPieceOf = kVec ? 1024 : 256;
 template <typename In, bool kVec>
 __global__ void __launch_bounds__(256) ns_sumsq_kernel(const In *__restrict__ g, int64_t ldg,
                                                        int64_t batch_stride, int64_t m, int64_t n,
@@ -99,38 +101,35 @@ __global__ void __launch_bounds__(256) ns_sumsq_kernel(const In *__restrict__ g,
                                                        uint32_t *__restrict__ counters,
                                                        int n_counters) {
   constexpr int V = kVec ? kVecOf<In> : 1;
+  constexpr int kPiece = kPieceOf<kVec>, kLoads = kPiece / 32 / V;
   __shared__ float sums[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int i = threadIdx.x; i < n_counters; i += 256) counters[i] = 0u;
   const In *base = g + blockIdx.y * batch_stride;
+  const int64_t pieces = (n + kPiece - 1) / kPiece, items = m * pieces;
   float acc = 0.0f;
-  for (int64_t r = blockIdx.x * 8 + warp; r < m; r += 8 * gridDim.x) {
-    const In *row = base + r * ldg;
-    const int64_t whole = n / V * V;
-    int64_t c = lane * V;
-    if constexpr (kVec) {
-      for (; c + 7 * 32 * V < whole; c += 8 * 32 * V) {  // eight loads in flight
-        float v[8][V];
+  for (int64_t it = blockIdx.x * 8 + warp; it < items; it += 8 * gridDim.x) {
+    const int64_t r = it / pieces, c0 = (it - r * pieces) * kPiece;
+    const In *row = base + r * ldg + c0;
+    const int left = static_cast<int>(n - c0 < kPiece ? n - c0 : kPiece);
+    float v[kLoads][V];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) load_vec(row + c + i * 32 * V, v[i]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int j = 0; j < V; ++j) acc = fmaf(v[i][j], v[i][j], acc);
+    for (int i = 0; i < kLoads; ++i) {
+      const int c = (i * 32 + lane) * V;
+      if constexpr (kVec) {
+        if (c + V <= left) {
+          load_vec(row + c, v[i]);
+          continue;
+        }
       }
-      for (; c < whole; c += 32 * V) {
-        float v[V];
-        load_vec(row + c, v);
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc = fmaf(v[j], v[j], acc);
-      }
-      c = whole + lane;
+      for (int j = 0; j < V; ++j) v[i][j] = c + j < left ? load_in(row + c + j) : 0.0f;
     }
-    for (; c < n; c += 32) {
-      const float v = load_in(row + c);
-      acc = fmaf(v, v, acc);
-    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc = fmaf(v[i][j], v[i][j], acc);
   }
   acc = warp_sum(acc);
   if (lane == 0) sums[warp] = acc;
@@ -1227,8 +1226,8 @@ fp8q_status load_x(const In *g, int64_t ldg, int64_t bs, int64_t batch, int64_t 
                    float eps, const Layout &l, uint8_t *ws, cudaStream_t s) {
   float *part = reinterpret_cast<float *>(ws + l.part);
   __half *x = reinterpret_cast<__half *>(ws + l.x0);
-  const int64_t row_blocks = (m + 7) / 8;
-  const int parts = static_cast<int>(row_blocks < kMaxParts ? row_blocks : kMaxParts);
+  const int64_t blocks = (m * ((n + kPieceOf<kVec> - 1) / kPieceOf<kVec>) + 7) / 8;
+  const int parts = static_cast<int>(blocks < kMaxParts ? blocks : kMaxParts);
   const unsigned b = static_cast<unsigned>(batch);
   if (fp8q_status st = launch_on(ns_sumsq_kernel<In, kVec>, dim3(parts, b), dim3(256), 0, s, g, ldg,
                                  bs, m, n, part, reinterpret_cast<uint32_t *>(ws + l.sync),

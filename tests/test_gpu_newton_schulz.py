@@ -100,6 +100,27 @@ def test_batch_and_single_matrices(m, n):
     assert fq.fp8q_newton_schulz(g[:0]).shape == (0, m, n)
 
 
+@pytest.mark.parametrize("B,m,n", [(400, 40, 50), (200, 64, 200), (90, 130, 70), (40, 300, 320),
+                                   (20, 520, 300)])
+def test_many_small_matrices(B, m, n):
+    # several rounds of tiles per pair, one or a few K blocks each: the kernel's
+    # producer, MMA, epilogue and counting warps run far apart from one another
+    g = gradient(B, m, n, seed=11).cuda()
+    x = fq.fp8q_newton_schulz(g)
+    assert rel(x, reference(g.cpu())) <= TOL[x.dtype]
+    assert torch.equal(x, fq.fp8q_newton_schulz(g))
+
+
+@pytest.mark.parametrize("m,n", [(1100, 1900), (1700, 2300), (768, 9000), (9001, 260), (100, 20000),
+                                 (1280, 16384)])
+def test_split_and_wide_tiles(m, n):
+    # long sums and more than one tile width in one call
+    g = gradient(m, n, seed=12)
+    x = fq.fp8q_newton_schulz(g.cuda(), out_dtype=fq.FP8Q_OUT_FP32)
+    assert rel(x, reference(g)) <= TOL[torch.float32]
+    assert torch.equal(x, fq.fp8q_newton_schulz(g.cuda(), out_dtype=fq.FP8Q_OUT_FP32))
+
+
 def test_tall_is_the_transpose_of_wide():
     g = gradient(130, 300, seed=5).cuda()
     assert torch.equal(fq.fp8q_newton_schulz(g.t().contiguous()).t(), fq.fp8q_newton_schulz(g))
