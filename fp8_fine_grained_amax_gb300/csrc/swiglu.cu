@@ -74,8 +74,10 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t local_addr, uint32_t ran
 // 256-row tiles of the GEMMs would leave most SMs idle.  Here the weights are
 // the MMA's M side and the tokens its N side: a CTA takes 64 columns of h (64
 // gate rows and the 64 up rows of the same columns: one 128-row operand), N
-// tokens, and a quarter of the K-groups; a cluster of eight CTAs covers the
-// 1x128 group of h (two column halves) times the four K quarters.
+// tokens, and one of S parts of the K-groups; a cluster of 2 S CTAs covers the
+// 1x128 group of h (two column halves).  S is the most, up to four, that keeps
+// every CTA resident at once (two per SM): all of them then stream until the
+// end, where a second wave would leave SMs idle.
 //   warp 0     TMA producer: weights and tokens per K-group into a ring that
 //              keeps 64 to 160 KB per SM on their way, which is what streaming
 //              at the memory's rate needs
@@ -83,23 +85,22 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t local_addr, uint32_t ran
 //              K = 32) into one of four TMEM buffers
 //   warps 2-5  fold: each thread one weight row, acc += P * sa * sb in FP32,
 //              the tokens' scales broadcast through shared memory
-// Then the K quarters are summed: each CTA sends its sums of a quarter of the
+// Then the K parts are summed: each CTA sends its sums of the S-th part of the
 // tokens to the CTA that finishes them (distributed shared memory, every sum
 // has its own place, added in K order), which gates them; for the codes the two
 // column halves of a group exchange one max-abs per token.
-constexpr int kFewSplit = 4;       // CTAs along K
 constexpr int kFewThreads = 192;
 constexpr int kFewBufs = 4;        // TMEM buffers
 
-template <int N>
+template <int N, int S>
 struct Few {
   static constexpr uint32_t kWBytes = 128 * 128, kXBytes = N * 128;
   // ring depth: what two CTAs per SM leave room for (three shallower ones
   // measured slower: 24 tokens of 7168 x 7168 28.6 us, against 24.5)
   static constexpr int kStages = N == 16 ? 5 : N == 32 ? 4 : 3;
   static constexpr int kPerSm = 2;
-  static constexpr int kQuarter = N / kFewSplit;  // tokens finished by a CTA
-  static constexpr uint32_t kRecv = kFewSplit * kQuarter * 128 * 4;
+  static constexpr int kShare = N / S;  // tokens finished by a CTA
+  static constexpr uint32_t kRecv = S * kShare * 128 * 4;
   static constexpr uint32_t kCols = kFewBufs * N;
   static constexpr size_t kSmem = 1024 + kStages * (kWBytes + kXBytes) + kRecv;
   static_assert(kPerSm * (kSmem + 4096) <= 227 * 1024, "shared memory");
@@ -128,18 +129,18 @@ __device__ __forceinline__ float pow2_of(float s, bool &bad) {
   return __uint_as_float((e < 0xFFu ? e : 0xFEu) << 23);
 }
 
-template <int N, bool kPow2>
-__global__ void __cluster_dims__(2 * kFewSplit, 1, 1)
-    __launch_bounds__(kFewThreads, Few<N>::kPerSm)
+template <int N, int S, bool kPow2>
+__global__ void __cluster_dims__(2 * S, 1, 1)
+    __launch_bounds__(kFewThreads, Few<N, S>::kPerSm)
         glu_few_tokens_kernel(const __grid_constant__ CUtensorMap tmW,
                               const __grid_constant__ CUtensorMap tmX, const FewArgs p) {
-  using C = Few<N>;
+  using C = Few<N, S>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[C::kStages], empty[C::kStages], tfull[kFewBufs], tempty[kFewBufs], drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ __align__(16) float s_sa[4][2][N];          // per fold warp, double-buffered
-  __shared__ float s_amax[2][C::kQuarter];               // [column half][token]
+  __shared__ float s_amax[2][C::kShare];               // [column half][token]
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sW = smem_u32(smem), sX = sW + C::kStages * C::kWBytes;
@@ -147,12 +148,12 @@ __global__ void __cluster_dims__(2 * kFewSplit, 1, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int *abort_flag = &s_abort;
   const int rank = static_cast<int>(cluster_ctarank());
-  const int half = rank >> 2, quarter = rank & 3;        // column half, K quarter
-  const int group = static_cast<int>(blockIdx.x) / (2 * kFewSplit);
+  const int half = rank / S, part = rank % S;  // column half, K part
+  const int group = static_cast<int>(blockIdx.x) / (2 * S);
   const int F = p.out.F, c0 = group * 128 + half * 64;   // first column of h
   const int m0 = static_cast<int>(blockIdx.y) * N;       // first token
-  const int per = (p.num_kb + kFewSplit - 1) / kFewSplit;
-  const int kb0 = min(quarter * per, p.num_kb), kb1 = min(kb0 + per, p.num_kb);
+  const int per = (p.num_kb + S - 1) / S;
+  const int kb0 = min(part * per, p.num_kb), kb1 = min(kb0 + per, p.num_kb);
 
   cluster_arrive_relaxed();
   if (threadIdx.x == 0) {
@@ -296,15 +297,15 @@ __global__ void __cluster_dims__(2 * kFewSplit, 1, 1)
     tc_fence_before();
     __syncwarp();
     cluster_wait();  // every CTA of the cluster has started
-    // token n's sums go to the CTA that finishes it, at [K quarter][token][row]
+    // token n's sums go to the CTA that finishes it, at [K part][token][row]
     const uint32_t mine = smem_u32(recv) + static_cast<uint32_t>(
-        (quarter * C::kQuarter * 128 + fw * 32 + lane) * 4);
+        (part * C::kShare * 128 + fw * 32 + lane) * 4);
 #pragma unroll
-    for (int d = 0; d < kFewSplit; ++d) {
-      const uint32_t dst = mapa_shared(mine, static_cast<uint32_t>(half * kFewSplit + d));
+    for (int d = 0; d < S; ++d) {
+      const uint32_t dst = mapa_shared(mine, static_cast<uint32_t>(half * S + d));
 #pragma unroll
-      for (int j = 0; j < C::kQuarter; ++j) {
-        const int n = d * C::kQuarter + j;
+      for (int j = 0; j < C::kShare; ++j) {
+        const int n = d * C::kShare + j;
         if (m0 + n < p.M) {
           const float2 v = unpack_f32x2(acc[n / 2]);
           asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + j * 512), "f"(n & 1 ? v.y : v.x)
@@ -323,19 +324,19 @@ __global__ void __cluster_dims__(2 * kFewSplit, 1, 1)
     tmem_dealloc(tmem, C::kCols);
   }
 
-  // ---- this CTA's quarter of the tokens: 64 columns of h, two per lane
+  // ---- this CTA's part of the tokens: 64 columns of h, two per lane
   constexpr int kWarps = kFewThreads / 32;
-  constexpr int kTok = (C::kQuarter + kWarps - 1) / kWarps;  // tokens per warp
+  constexpr int kTok = (C::kShare + kWarps - 1) / kWarps;  // tokens per warp
   float h[kTok][2];
 #pragma unroll
   for (int k = 0; k < kTok; ++k) {
-    const int j = warp + kWarps * k, m = m0 + quarter * C::kQuarter + j;
+    const int j = warp + kWarps * k, m = m0 + part * C::kShare + j;
     h[k][0] = h[k][1] = 0.0f;
-    if (j >= C::kQuarter || m >= p.M) continue;  // warp-uniform
+    if (j >= C::kShare || m >= p.M) continue;  // warp-uniform
     float2 gv = make_float2(0.0f, 0.0f), uv = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int s = 0; s < kFewSplit; ++s) {
-      const float *src = recv + (s * C::kQuarter + j) * 128 + lane;
+    for (int s = 0; s < S; ++s) {
+      const float *src = recv + (s * C::kShare + j) * 128 + lane;
       gv.x += src[0];
       gv.y += src[32];
       uv.x += src[64];
@@ -362,7 +363,7 @@ __global__ void __cluster_dims__(2 * kFewSplit, 1, 1)
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       if (lane < 2)  // to both column halves of the group
-        st_cluster_f32(smem_u32(&s_amax[half][j]), static_cast<uint32_t>(lane * kFewSplit + quarter),
+        st_cluster_f32(smem_u32(&s_amax[half][j]), static_cast<uint32_t>(lane * S + part),
                        amax);
     }
   }
@@ -370,8 +371,8 @@ __global__ void __cluster_dims__(2 * kFewSplit, 1, 1)
   cluster_sync_all();
 #pragma unroll
   for (int k = 0; k < kTok; ++k) {
-    const int j = warp + kWarps * k, m = m0 + quarter * C::kQuarter + j;
-    if (j >= C::kQuarter || m >= p.M) continue;
+    const int j = warp + kWarps * k, m = m0 + part * C::kShare + j;
+    if (j >= C::kShare || m >= p.M) continue;
     float sc, inv;
     group_scale(fmaxf(s_amax[0][j], s_amax[1][j]), p.out.pow2 != 0, sc, inv);
     uint8_t *row = p.out.q + static_cast<int64_t>(m) * p.out.ldq + c0;
@@ -383,10 +384,10 @@ __global__ void __cluster_dims__(2 * kFewSplit, 1, 1)
   }
 }
 
-template <int N, bool kPow2>
+template <int N, int S, bool kPow2>
 fp8q_status launch_few(const GluIn &in, const GluOut &out, cudaStream_t s) {
-  using C = Few<N>;
-  auto kern = glu_few_tokens_kernel<N, kPow2>;
+  using C = Few<N, S>;
+  auto kern = glu_few_tokens_kernel<N, S, kPow2>;
   static bool attr_set[kMaxDevices] = {};
   static std::mutex mu;
   int dev = 0;
@@ -418,23 +419,34 @@ fp8q_status launch_few(const GluIn &in, const GluOut &out, cudaStream_t s) {
   a.num_kb = static_cast<int>(in.K / 128);
   a.out = out;
   a.timeout_ns = wait_timeout_ns().load();
-  const dim3 grid(static_cast<unsigned>(in.F / 128 * 2 * kFewSplit),
+  const dim3 grid(static_cast<unsigned>(in.F / 128 * 2 * S),
                   static_cast<unsigned>((in.M + N - 1) / N));
   return launch_on(kern, grid, dim3(kFewThreads), C::kSmem, s, tw, tx, a);
 }
 
-template <bool kPow2>
+template <int S, bool kPow2>
 fp8q_status launch_few(const GluIn &in, const GluOut &out, cudaStream_t s) {
-  return in.M <= 16   ? launch_few<16, kPow2>(in, out, s)
-         : in.M <= 32 ? launch_few<32, kPow2>(in, out, s)
-                      : launch_few<64, kPow2>(in, out, s);
+  return in.M <= 16   ? launch_few<16, S, kPow2>(in, out, s)
+         : in.M <= 32 ? launch_few<32, S, kPow2>(in, out, s)
+                      : launch_few<64, S, kPow2>(in, out, s);
+}
+template <bool kPow2>
+fp8q_status launch_few(const GluIn &in, const GluOut &out, int sm_count, cudaStream_t s) {
+  const int64_t ctas = in.F / 64 * ((in.M + 63) / 64), room = 2 * static_cast<int64_t>(sm_count);
+  return 4 * ctas <= room   ? launch_few<4, kPow2>(in, out, s)
+         : 2 * ctas <= room ? launch_few<2, kPow2>(in, out, s)
+                            : launch_few<1, kPow2>(in, out, s);
 }
 
-// Blocks of 64 tokens share the weights through L2, so a little more than one
-// wave of the few-token kernel's CTAs (two per SM) still beats the GEMMs' tiles,
-// which take the time of a whole K loop however few they are.
+// Up to 64 tokens, and for more while blocks of 64 tokens times blocks of 64
+// columns are at most 128: the blocks share the weights through L2, and the GEMMs'
+// tiles take the time of a whole K loop however few they are.  K = 7168, both
+// sides measured (few-token kernel / tiles): F = 2048, 256 tokens (128 blocks)
+// 21 / 31 us, 384 tokens (192) 37 / 33; F = 640, 512 tokens (80) 18 / 31, 1024
+// tokens (160) 32 / 31; F = 7168, 128 tokens (224) 52 / 35; K = 1024, F = 7168,
+// 128 tokens 12 / 9.
 bool few_tokens(const GluIn &in) {
-  return in.M <= 64 || in.F / 16 * ((in.M + 63) / 64) <= 512;
+  return in.M <= 64 || in.F / 64 * ((in.M + 63) / 64) <= 128;
 }
 
 bool valid_mode(int m) { return m == FP8Q_SCALE_FP32 || m == FP8Q_SCALE_POW2; }
@@ -471,7 +483,8 @@ fp8q_status glu_entry(const GluIn &in, const GluOut &o, int scale_mode, bool pow
   if (fp8q_status st = device_info(dev)) return st;
   auto s = static_cast<cudaStream_t>(stream);
   if (!grouped && few_tokens(in))
-    return pow2 ? launch_few<true>(in, o, s) : launch_few<false>(in, o, s);
+    return pow2 ? launch_few<true>(in, o, dev.sm_count, s)
+                : launch_few<false>(in, o, dev.sm_count, s);
   return pow2 && in.K > 0 ? gemm_mx_glu(in, o, s) : gemm_glu(in, o, s);
 }
 
