@@ -443,7 +443,7 @@ fp8q_status launch_few(const GluIn &in, const GluOut &out, int sm_count, cudaStr
 // tiles take the time of a whole K loop however few they are.  K = 7168, both
 // sides measured (few-token kernel / tiles): F = 2048, 256 tokens (128 blocks)
 // 21 / 31 us, 384 tokens (192) 37 / 33; F = 640, 512 tokens (80) 18 / 31, 1024
-// tokens (160) 32 / 31; F = 7168, 128 tokens (224) 52 / 35; K = 1024, F = 7168,
+// tokens (160) 32 / 31; F = 7168, 192 tokens (336) 62 / 36; K = 1024, F = 7168,
 // 128 tokens 12 / 9.
 bool few_tokens(const GluIn &in) {
   return in.M <= 64 || in.F / 64 * ((in.M + 63) / 64) <= 128;

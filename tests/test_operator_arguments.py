@@ -116,3 +116,26 @@ def test_workspace_size(lib):
     assert need <= f(1, 2048, 7168) <= need + 76 * 256 * 256 * 4 + 32768
     assert f(1, 8, 8) <= 256 * 256 * 4 + 32768
     assert f(-1, 8, 8) == 0 and f(1, 1 << 21, 8) == 0 and f(4096, 1 << 16, 1 << 16) == 0
+
+
+def test_marshalling_module_loads_and_names_its_calls(lib, B):
+    m = B._calls()
+    for name in ("swiglu", "swiglu_bwd", "newton_schulz"):
+        with pytest.raises(TypeError):
+            getattr(m, name)()
+
+
+def test_binding_refuses_what_is_not_on_a_gpu(lib):
+    import torch
+
+    import fp8_fine_grained_amax_gb300 as fq
+    a, sa = torch.zeros(4, 256, dtype=torch.uint8), torch.ones(2, 4)
+    b, sb = torch.zeros(256, 256, dtype=torch.uint8), torch.ones(2, 2)
+    with pytest.raises(ValueError, match="CUDA"):
+        fq.fp8q_gemm_swiglu(a, sa, b, sb)
+    with pytest.raises(TypeError):
+        fq.fp8q_gemm_swiglu([1], sa, b, sb)
+    with pytest.raises(ValueError, match="CUDA"):
+        fq.fp8q_swiglu_bwd(torch.zeros(128, 128).bfloat16(), torch.zeros(128, 256).bfloat16())
+    with pytest.raises(ValueError, match="CUDA"):
+        fq.fp8q_newton_schulz(torch.zeros(8, 8))
