@@ -237,6 +237,16 @@ __device__ __forceinline__ void warp_store_block64(uint32_t buf, const uint4 (&u
   }
 }
 
+// Programmatic dependent launch: wait until the kernel before this one on the
+// stream is done (nothing to wait for under an ordinary launch); let the next
+// one start setting itself up.
+__device__ __forceinline__ void wait_for_previous_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_kernel_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __device__ __forceinline__ void prefetch_tmap(const void *tmap) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
 }

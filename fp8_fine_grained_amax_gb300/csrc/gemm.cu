@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     else tmem_alloc(smem_u32(&ctl->tmem_base), kTmemCols);
     tc_fence_before();
   }
+  if (kGlu) wait_for_previous_kernel();
   // barriers initialised and TMEM allocated in every CTA before any CTA of the
   // pair signals a peer
   __syncwarp();
@@ -613,6 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    if (kGlu) let_next_kernel_start();
     // every tensor store of this warp has written global memory
     if (lane == 0) bulk_wait_group_all();
     // teardown (epilogue side): TMEM reads are complete
@@ -795,7 +797,7 @@ fp8q_status launch(const CUtensorMap &ta, const CUtensorMap &tb,
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return FP8Q_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -825,6 +827,11 @@ fp8q_status launch(const CUtensorMap &ta, const CUtensorMap &tb,
       }
       max_units[dev] = n;
     }
+  }
+  if (kGlu) {  // as launch_dependent
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
   }
   const int64_t units = work_tiles < max_units[dev] ? work_tiles : max_units[dev];
   cfg.gridDim = dim3(static_cast<unsigned>(units * (kPair ? 2 : 1)), 1, 1);

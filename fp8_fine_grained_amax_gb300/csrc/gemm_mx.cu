@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
   }
   __syncwarp();
+  if (kGlu) wait_for_previous_kernel();
   cluster_sync_all();
   // grouped: clamp the expert offsets into [0, M] and build the m-tile prefix
   int total_tiles;
@@ -632,6 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       prev_buf = i % kAccBufs;
     }
     if (ok && prev_t >= 0) ok = drain(prev_t, prev_buf);
+    if (kGlu) let_next_kernel_start();
     __syncwarp();
     tc_fence_before();
     cluster_sync_all();
@@ -817,7 +819,7 @@ fp8q_status launch_mx(const CUtensorMap &ta, const CUtensorMap &tb, const MxArgs
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FP8Q_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;  // CTA pairs
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
@@ -839,6 +841,11 @@ fp8q_status launch_mx(const CUtensorMap &ta, const CUtensorMap &tb, const MxArgs
         return FP8Q_ERR_UNSUPPORTED;
       max_pairs[dev] = n;
     }
+  }
+  if (kGlu) {  // as launch_dependent
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
   }
   const int64_t pairs = tiles < max_pairs[dev] ? tiles : max_pairs[dev];
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);

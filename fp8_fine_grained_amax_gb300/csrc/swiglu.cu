@@ -180,6 +180,8 @@ __global__ void __cluster_dims__(2 * S, 1, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
+  wait_for_previous_kernel();
+  let_next_kernel_start();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -421,7 +423,7 @@ fp8q_status launch_few(const GluIn &in, const GluOut &out, cudaStream_t s) {
   a.timeout_ns = wait_timeout_ns().load();
   const dim3 grid(static_cast<unsigned>(in.F / 128 * 2 * S),
                   static_cast<unsigned>((in.M + N - 1) / N));
-  return launch_on(kern, grid, dim3(kFewThreads), C::kSmem, s, tw, tx, a);
+  return launch_dependent(kern, grid, dim3(kFewThreads), C::kSmem, s, tw, tx, a);
 }
 
 template <int S, bool kPow2>
@@ -649,10 +651,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, kBwdCta
     mbar_init(smem_u32(&rows_in[0]), 1);
     mbar_init(smem_u32(&rows_in[1]), 1);
     fence_barrier_init();
-    if (tb < ntb) {
-      issue(cb, tb);
-      pending = true;
-    }
+  }
+  wait_for_previous_kernel();
+  if (tid == 0 && tb < ntb) {
+    issue(cb, tb);
+    pending = true;
   }
   // barriers initialised in both CTAs before either sends
   if (kRows) cluster_sync_all();
@@ -848,6 +851,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, kBwdCta
       }
     }
   }
+  let_next_kernel_start();
   if (kRows) cluster_sync_all();  // the other CTA no longer sends here
   // a copy still in flight after an abandoned wait lands before the CTA's shared
   // memory goes
@@ -881,8 +885,8 @@ fp8q_status launch_bwd(const CUtensorMap &tmD, const CUtensorMap &tmG, const Bwd
   if (fp8q_status st = device_info(info)) return st;
   const int64_t tiles = static_cast<int64_t>(a.ncb) * a.ntb;
   const int64_t room = static_cast<int64_t>(info.sm_count) * kBwdCtasPerSm / 2;
-  return launch_on(kern, dim3(static_cast<unsigned>(2 * (tiles < room ? tiles : room))),
-                   dim3(kBwdThreads), smem, s, tmD, tmG, a);
+  return launch_dependent(kern, dim3(static_cast<unsigned>(2 * (tiles < room ? tiles : room))),
+                          dim3(kBwdThreads), smem, s, tmD, tmG, a);
 }
 
 template <bool kRows, bool kCols>
