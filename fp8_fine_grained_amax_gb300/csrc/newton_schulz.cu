@@ -104,6 +104,8 @@ __global__ void __launch_bounds__(256) ns_sumsq_kernel(const In *__restrict__ g,
   constexpr int kPiece = kPieceOf<kVec>, kLoads = kPiece / 32 / V;
   __shared__ float sums[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  wait_for_previous_kernel();
+  let_next_kernel_start();
   if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int i = threadIdx.x; i < n_counters; i += 256) counters[i] = 0u;
   const In *base = g + blockIdx.y * batch_stride;
@@ -141,6 +143,8 @@ __global__ void __launch_bounds__(256) ns_sumsq_kernel(const In *__restrict__ g,
 }
 
 // S / (|g|_F + eps) of matrix blockIdx.z from its partial sums, to every thread.
+// (The partial sums are the previous kernel's; the matrix itself is not, but the
+// kernel before that one may be writing it still: nothing is read ahead.)
 __device__ __forceinline__ float ns_scale(const float *part, int parts, float eps, float *shared) {
   if (threadIdx.x < 32) {
     float v = 0.0f;
@@ -173,6 +177,8 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const In *__restrict__ g, 
                                                       int64_t ldx) {
   constexpr int V = kVecOf<In>;
   __shared__ float s_scale;
+  wait_for_previous_kernel();
+  let_next_kernel_start();
   const In *base = g + blockIdx.z * batch_stride;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + 8 * (threadIdx.x & 31);
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 32 + (threadIdx.x >> 5);
@@ -222,6 +228,8 @@ __global__ void __launch_bounds__(256) ns_load_tall_kernel(const In *__restrict_
   constexpr int kRows = 256 / kLanes;    // rows per pass
   __shared__ float s_scale;
   __shared__ float tile[64][65];
+  wait_for_previous_kernel();
+  let_next_kernel_start();
   const In *base = g + blockIdx.z * batch_stride;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 64, c0 = static_cast<int64_t>(blockIdx.x) * 64;
   const int tid = threadIdx.x, j0 = V * (tid % kLanes);
@@ -699,6 +707,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_before();
   }
   __syncwarp();
+  wait_for_previous_kernel();
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
@@ -1229,16 +1238,16 @@ fp8q_status load_x(const In *g, int64_t ldg, int64_t bs, int64_t batch, int64_t 
   const int64_t blocks = (m * ((n + kPieceOf<kVec> - 1) / kPieceOf<kVec>) + 7) / 8;
   const int parts = static_cast<int>(blocks < kMaxParts ? blocks : kMaxParts);
   const unsigned b = static_cast<unsigned>(batch);
-  if (fp8q_status st = launch_on(ns_sumsq_kernel<In, kVec>, dim3(parts, b), dim3(256), 0, s, g, ldg,
+  if (fp8q_status st = launch_dependent(ns_sumsq_kernel<In, kVec>, dim3(parts, b), dim3(256), 0, s, g, ldg,
                                  bs, m, n, part, reinterpret_cast<uint32_t *>(ws + l.sync),
                                  static_cast<int>(sizeof(Sync) / 4 + batch)))
     return st;
   if (m > n)
-    return launch_on(ns_load_tall_kernel<In, kVec>,
+    return launch_dependent(ns_load_tall_kernel<In, kVec>,
                      dim3(static_cast<unsigned>((n + 63) / 64), static_cast<unsigned>((m + 63) / 64), b),
                      dim3(256), 0, s, g, ldg, bs, m, n, static_cast<const float *>(part), parts, eps,
                      x, l.ldx);
-  return launch_on(ns_load_kernel<In, kVec>,
+  return launch_dependent(ns_load_kernel<In, kVec>,
                    dim3(static_cast<unsigned>((n + 255) / 256), static_cast<unsigned>((m + 31) / 32), b),
                    dim3(256), 0, s, g, ldg, bs, m, n, static_cast<const float *>(part), parts, eps, x,
                    l.ldx);
@@ -1344,11 +1353,13 @@ extern "C" fp8q_status fp8q_newton_schulz(const void *g, int64_t ldg, int64_t g_
     return st;
   // the pairs wait for one another: a cooperative launch runs all of them at once
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as launch_dependent
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;

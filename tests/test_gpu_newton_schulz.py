@@ -185,6 +185,22 @@ def test_streams_capture_and_kept_workspace():
     assert torch.equal(again, want) and torch.equal(captured, want)
 
 
+def test_two_streams_at_once():
+    # each call fills the GPU with kernels that wait for their own CTAs
+    gs = [gradient(1500, 2000, seed=20 + i).cuda() for i in range(2)]
+    want = [fq.fp8q_newton_schulz(g) for g in gs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in gs]
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(fq.fp8q_newton_schulz(gs[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])
+
+
 def test_binding_refuses():
     g = gradient(8, 16).cuda()
     with pytest.raises(ValueError):
