@@ -17,6 +17,7 @@
 #include <cstdint>
 
 #include "fp8q.h"
+#include "fp8q_host.cuh"
 #include "fp8q_ptx.cuh"
 
 namespace fp8q {
@@ -84,6 +85,17 @@ __device__ __forceinline__ void glu_exchange_init(GluExchange &x) {
 struct GluMaps {
   CUtensorMap gu, h, q;
 };
+// Results that are left out keep a copy of `any`.
+inline bool make_glu_maps(GluMaps &m, const CUtensorMap &any, const GluIn &in, const GluOut &out) {
+  m = GluMaps{any, any, any};
+  return (!out.gu ||
+          make_tmap_2d(&m.gu, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out.gu, in.M, 2 * in.F,
+                       out.ld_gu * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B)) &&
+         (!out.h || make_tmap_2d(&m.h, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out.h, in.M, in.F,
+                                 out.ldh * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B)) &&
+         (!out.q || make_tmap_2d(&m.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, out.q, in.M, in.F, out.ldq,
+                                 64, 32, CU_TENSOR_MAP_SWIZZLE_64B));
+}
 
 // Eight packed pairs -> 16 BF16 values (32 bytes) as two 16-byte units.
 __device__ __forceinline__ uint4 bf16_unit(const uint64_t *v) {
@@ -115,25 +127,22 @@ __device__ __forceinline__ void store_rows(uint32_t buf, const uint64_t *v, void
 
 // Store the results of one warp's 32 rows x 64 columns of h.  acc: this
 // thread's row, 64 gate values then 64 up values as packed FP32 pairs.  buf:
-// the warp's staging buffer (1024-byte aligned): 8 KB with kTma, where whole
-// blocks leave as TMA tensor stores that drain while the next tile is folded
-// (8192 x 2048 x 7168 with gu and codes: 220 us with coalesced stores), else
-// 2 KB.  tma: this block may leave that way (warp-uniform; the maps clip at the
-// tensor's last row only).  uses counts this warp's exchanges.  Returns false
+// the warp's staging buffer (8 KB, 1024-byte aligned).  Whole blocks leave as TMA
+// tensor stores that drain while the next tile is folded (8192 x 2048 x 7168 with
+// gu and codes: 213 us, 220 with coalesced stores).  tma: this block may leave
+// that way (warp-uniform; the maps clip at the tensor's last row only).  uses counts this warp's exchanges.  Returns false
 // when a bounded wait gave up.  All branches are warp-uniform and the same for
 // the two warps of a group.
-template <bool kTma>
 __device__ __forceinline__ bool glu_store(uint64_t (&acc)[64], const GluOut &o, const GluMaps *maps,
                                           bool tma, uint32_t buf, int row0, int row_end, int col0,
                                           int ew, int lane, GluExchange &x, uint32_t &uses,
                                           volatile int *abort_flag, int *status_word,
                                           uint64_t timeout_ns) {
-  if (kTma) {  // the last tile's stores have read the buffer
-    if (lane == 0) bulk_wait_group_read<0>();
-    __syncwarp();
-  }
+  // the last tile's stores have read the buffer
+  if (lane == 0) bulk_wait_group_read<0>();
+  __syncwarp();
   if (o.gu) {
-    if (kTma && tma) {
+    if (tma) {
       stage_box(buf, acc, lane);
       stage_box(buf + 4096, acc + 32, lane);
       fence_proxy_async_shared();
@@ -165,12 +174,11 @@ __device__ __forceinline__ bool glu_store(uint64_t (&acc)[64], const GluOut &o, 
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&x.bar[ew & 3]));
   }
-  if (kTma) {  // gu's stores have read the buffer
-    if (lane == 0) bulk_wait_group_read<0>();
-    __syncwarp();
-  }
+  // gu's stores have read the buffer
+  if (lane == 0) bulk_wait_group_read<0>();
+  __syncwarp();
   if (o.h) {
-    if (kTma && tma) stage_box(buf, acc, lane);
+    if (tma) stage_box(buf, acc, lane);
     else store_rows(buf, acc, o.h, o.ldh, row0, row_end, col0, o.F, lane);
   }
   if (o.q) {
@@ -192,7 +200,7 @@ __device__ __forceinline__ bool glu_store(uint64_t (&acc)[64], const GluOut &o, 
         w[e] = codes4(fmul2(acc[8 * k + 2 * e], inv2), fmul2(acc[8 * k + 2 * e + 1], inv2));
       v[k] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    if (kTma && tma) {
+    if (tma) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         st_shared_v4(buf + 4096 + lane * 64 + 16 * (k ^ ((lane >> 1) & 3)), v[k]);
@@ -202,7 +210,7 @@ __device__ __forceinline__ bool glu_store(uint64_t (&acc)[64], const GluOut &o, 
     if (ew < 4 && row0 + lane < row_end)
       o.s[static_cast<int64_t>(col0 / 128) * o.ld_s + row0 + lane] = sc;
   }
-  if (kTma && tma) {
+  if (tma) {
     fence_proxy_async_shared();
     __syncwarp();
     if (lane == 0) {

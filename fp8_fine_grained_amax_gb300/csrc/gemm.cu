@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // grouped: rows past the expert's end belong to the next one
         const bool tma = !kGrouped || wrow0 + 32 <= tl.row_end;
         if (wrow0 < tl.row_end)
-          ok = glu_store<true>(acc, p.glu, &tmC, tma,
+          ok = glu_store(acc, p.glu, &tmC, tma,
                                smem_u32(sC) + static_cast<uint32_t>(ew) * kStageWarpBytes, wrow0,
                                tl.row_end, ncol0, ew, lane, ctl->glu, glu_uses, abort_flag,
                                &g_status, p.timeout_ns);
@@ -936,12 +936,8 @@ fp8q_status gemm_glu(const GluIn &in, const GluOut &out, cudaStream_t s) {
   const int64_t tiles =
       (static_cast<int64_t>(args.tiles_m) + (grouped ? in.G : 0)) * args.tiles_n;
   if (tiles >= (1ll << 31)) return FP8Q_ERR_SHAPE;
-  GluMaps maps{ta, ta, ta};  // results that are left out keep a copy of A's map
-  if ((out.gu && !make_tmap_c(&maps.gu, out.gu, in.M, 2 * in.F, out.ld_gu, false)) ||
-      (out.h && !make_tmap_c(&maps.h, out.h, in.M, in.F, out.ldh, false)) ||
-      (out.q && !make_tmap_2d(&maps.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, out.q, in.M, in.F, out.ldq, 64,
-                              32, CU_TENSOR_MAP_SWIZZLE_64B)))
-    return FP8Q_ERR_CUDA;
+  GluMaps maps;
+  if (!make_glu_maps(maps, ta, in, out)) return FP8Q_ERR_CUDA;
   if (grouped)
     return launch<FP8Q_BSCALE_BLOCK, false, true, true, false, false, true>(ta, tb, maps, args,
                                                                             tiles, s);

@@ -50,6 +50,7 @@
 
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "fp8q.h"
 #include "fp8q_glu.cuh"
@@ -155,6 +156,12 @@ constexpr size_t kGroupTables = 3 * (kMaxGroups + 1) * sizeof(int);
 // Output staging: 2 KB per epilogue warp (32 rows x 64 bytes) for coalesced
 // stores of the drained accumulator.
 constexpr size_t kStageBytes = kEpiWarps * 2048;
+// Gated GEMM: a shallower ring leaves 8 KB per warp for whole blocks of results,
+// which leave as TMA tensor stores (fp8q_glu.cuh).  K = 128, where a tile is all
+// epilogue: 2678 x 3968 with h and gu 28 us with 2 KB and coalesced stores.
+constexpr int kGluStages = 4;
+constexpr size_t kGluStageBytes = kEpiWarps * 8192;
+struct NoMaps {};
 constexpr size_t kSmemBytes = 1024 + kRingBytes + kStageBytes + sizeof(MxCtl);
 
 __device__ __forceinline__ void mbar_wait_drain(uint32_t bar, uint32_t parity) {
@@ -230,7 +237,10 @@ __device__ __forceinline__ MxTile mx_tile_of(int t, const MxArgs &p, const int *
 template <int kBScale, bool kOutF32, bool kAccum, bool kGrouped = false, bool kGlu = false>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8q_gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA,
-                        const __grid_constant__ CUtensorMap tmB, const MxArgs p) {
+                        const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ std::conditional_t<kGlu, GluMaps, NoMaps> maps,
+                        const MxArgs p) {
+  constexpr int kRing = kGlu ? kGluStages : kStages;  // ring depth
   // per-column B scales of a dense GEMM are prepared in warps 2-3
   constexpr bool kPrep = kBScale == FP8Q_BSCALE_ROW && !kGrouped;
   static_assert(!kGlu || (kBScale == FP8Q_BSCALE_BLOCK && !kOutF32 && !kAccum && BN == 256),
@@ -239,10 +249,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t *sA = smem;
-  uint8_t *sB = smem + kStages * kABytes;
-  uint8_t *sC = smem + kRingBytes;  // output staging (1024-byte aligned)
+  uint8_t *sB = smem + kRing * kABytes;
+  uint8_t *sC = smem + static_cast<size_t>(kRing) * (kABytes + kBBytes);  // output staging (1024-byte aligned)
   uint32_t *prep_b = reinterpret_cast<uint32_t *>(sC + kStageBytes);  // [slot][8][32]
-  MxCtl *ctl = reinterpret_cast<MxCtl *>(sC + kStageBytes + (kPrep ? kPrepBytes : 0));
+  MxCtl *ctl = reinterpret_cast<MxCtl *>(sC + (kGlu ? kGluStageBytes : kStageBytes) +
+                                         (kPrep ? kPrepBytes : 0));
   int *s_lo = reinterpret_cast<int *>(ctl + 1);  // grouped only (see mx_tile_of)
   int *s_hi = s_lo + (kMaxGroups + 1);
   int *s_pre = s_hi + (kMaxGroups + 1);
@@ -255,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nst = (p.num_kb + kGroupsPerStage - 1) / kGroupsPerStage;  // scale stages per tile
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kRing; ++i) {
       mbar_init(smem_u32(&ctl->full[i]), 1);
       mbar_init(smem_u32(&ctl->empty[i]), 1);
     }
@@ -523,9 +534,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 64; ++i)
           acc[i] = pack_u32x2(v[i / 8][2 * (i % 8)], v[i / 8][2 * (i % 8) + 1]);
-        return !warp_ok || glu_store<false>(acc, p.glu, nullptr, false, buf, wrow0, tl.row_end, ncol0,
-                                            ew, lane, ctl->glu, glu_uses, abort_flag, &g_mx_status,
-                                            p.timeout_ns);
+        // grouped: rows past the expert's end belong to the next one
+        const bool tma = !kGrouped || wrow0 + 32 <= tl.row_end;
+        return !warp_ok || glu_store(acc, p.glu, &maps, tma,
+                                     smem_u32(sC) + static_cast<uint32_t>(ew) * 8192u, wrow0,
+                                     tl.row_end, ncol0, ew, lane, ctl->glu, glu_uses, abort_flag,
+                                     &g_mx_status, p.timeout_ns);
       } else if (kOutF32 && kPrep) {
         // FP32 out, per-column scales: these warps hold no raw scales, so the
         // whole row of kEpiCols values is read first and the accumulator is
@@ -633,7 +647,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       prev_buf = i % kAccBufs;
     }
     if (ok && prev_t >= 0) ok = drain(prev_t, prev_buf);
-    if (kGlu) let_next_kernel_start();
+    if (kGlu) {
+      let_next_kernel_start();
+      // every tensor store of this warp has written global memory
+      if (lane == 0) bulk_wait_group_all();
+    }
     __syncwarp();
     tc_fence_before();
     cluster_sync_all();
@@ -673,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           armed |= 1u << stage;
           armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) {
+          if (++stage == kRing) {
             stage = 0;
             phase ^= 1;
           }
@@ -681,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) {
         if (rank == 0) {
-          for (int s = 0; s < kStages; ++s)
+          for (int s = 0; s < kRing; ++s)
             if (armed & (1u << s)) mbar_wait_drain(smem_u32(&ctl->full[s]), (armed_phase >> s) & 1);
         }
         spin_ns(1000000);
@@ -783,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           issued = true;
-          if (++stage == kStages) {
+          if (++stage == kRing) {
             stage = 0;
             phase ^= 1;
           }
@@ -809,10 +827,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ host
 template <int kBScale, bool kOutF32, bool kAccum, bool kGrouped = false, bool kGlu = false>
 fp8q_status launch_mx(const CUtensorMap &ta, const CUtensorMap &tb, const MxArgs &args,
-                      int64_t tiles, cudaStream_t s) {
+                      int64_t tiles, cudaStream_t s,
+                      const std::conditional_t<kGlu, GluMaps, NoMaps> &maps = {}) {
   auto kern = fp8q_gemm_mx_kernel<kBScale, kOutF32, kAccum, kGrouped, kGlu>;
-  constexpr size_t smem = kSmemBytes + (kGrouped ? kGroupTables : 0) +
-                          (kBScale == FP8Q_BSCALE_ROW && !kGrouped ? kPrepBytes : 0);
+  constexpr size_t smem =
+      (kGlu ? 1024 + kGluStages * (kABytes + kBBytes) + kGluStageBytes + sizeof(MxCtl) : kSmemBytes) +
+      (kGrouped ? kGroupTables : 0) + (kBScale == FP8Q_BSCALE_ROW && !kGrouped ? kPrepBytes : 0);
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
   static int max_pairs[kMaxDevices] = {};
   static std::mutex mu;
@@ -849,7 +869,8 @@ fp8q_status launch_mx(const CUtensorMap &ta, const CUtensorMap &tb, const MxArgs
   }
   const int64_t pairs = tiles < max_pairs[dev] ? tiles : max_pairs[dev];
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
-  return cudaLaunchKernelEx(&cfg, kern, ta, tb, args) == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kern, ta, tb, maps, args) == cudaSuccess ? FP8Q_OK
+                                                                           : FP8Q_ERR_CUDA;
 }
 
 template <bool kAccum>
@@ -967,9 +988,11 @@ fp8q_status gemm_mx_glu(const GluIn &in, const GluOut &out, cudaStream_t s) {
   const int64_t tiles =
       (static_cast<int64_t>(args.tiles_m) + (grouped ? in.G : 0)) * args.tiles_n;
   if (tiles >= (1ll << 31)) return FP8Q_ERR_SHAPE;
+  GluMaps maps;
+  if (!make_glu_maps(maps, ta, in, out)) return FP8Q_ERR_CUDA;
   return grouped
-             ? launch_mx<FP8Q_BSCALE_BLOCK, false, false, true, true>(ta, tb, args, tiles, s)
-             : launch_mx<FP8Q_BSCALE_BLOCK, false, false, false, true>(ta, tb, args, tiles, s);
+             ? launch_mx<FP8Q_BSCALE_BLOCK, false, false, true, true>(ta, tb, args, tiles, s, maps)
+             : launch_mx<FP8Q_BSCALE_BLOCK, false, false, false, true>(ta, tb, args, tiles, s, maps);
 }
 
 fp8q_status mx_status_take(cudaStream_t s) {
