@@ -137,7 +137,11 @@ struct GemmArgs {
   const int32_t *offs;  // grouped only
   int G;
   uint64_t timeout_ns;
-  GluOut glu;  // gated GEMM only: N = F, tiles of 128 columns of h
+};
+// The gated form's additions stay out of the plain kernels' types and code
+// (if constexpr): with them in common the plain GEMMs lost 1 to 3 %.
+struct GluGemmArgs : GemmArgs {
+  GluOut glu;  // N = F, tiles of 128 columns of h
 };
 
 // Shared-memory control block, after the operand ring and the output staging.
@@ -152,7 +156,9 @@ struct alignas(8) SmemCtl {
   // per-column B scales (Wgrad): each epilogue warp stages the scales of its
   // own columns for the current K-group, double-buffered
   alignas(16) float sb_warp[kEpiWarps][2][kEpiCols];
-  GluExchange glu;  // gated GEMM only
+};
+struct GluSmemCtl : SmemCtl {
+  GluExchange glu;
 };
 
 // Output staging: 8 KB per epilogue warp: its 32 rows x 128 BF16 columns as
@@ -161,11 +167,11 @@ struct alignas(8) SmemCtl {
 constexpr uint32_t kStageWarpBytes = 8192;
 constexpr uint32_t kStageCBytes = kEpiWarps * kStageWarpBytes;
 
-__host__ __device__ constexpr size_t smem_bytes(bool grouped, bool pair) {
+__host__ __device__ constexpr size_t smem_bytes(bool grouped, bool pair, bool glu = false) {
   return 1024 /* alignment slack */ + (pair ? Cfg<true>::kTileBytes : Cfg<false>::kTileBytes) +
-         kStageCBytes + sizeof(SmemCtl) + (grouped ? 2 * (kMaxGroups + 1) * sizeof(int) : 0);
+         kStageCBytes + (glu ? sizeof(GluSmemCtl) : sizeof(SmemCtl)) + (grouped ? 2 * (kMaxGroups + 1) * sizeof(int) : 0);
 }
-static_assert(smem_bytes(true, true) <= 227 * 1024 && smem_bytes(true, false) <= 227 * 1024,
+static_assert(smem_bytes(true, true, true) <= 227 * 1024 && smem_bytes(true, false) <= 227 * 1024,
               "shared memory per CTA");
 
 struct Tile {
@@ -227,8 +233,9 @@ template <int kBScale, bool kOutF32, bool kGrouped, bool kPair, bool kAccum = fa
 __global__ void __launch_bounds__(kThreads, 1)
     fp8q_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ std::conditional_t<kGlu, GluMaps, CUtensorMap> tmC,
-                     const GemmArgs p) {
+                     const std::conditional_t<kGlu, GluGemmArgs, GemmArgs> p) {
   using C = Cfg<kPair>;
+  using Ctl = std::conditional_t<kGlu, GluSmemCtl, SmemCtl>;
   static_assert(!kGlu || (kPair && kBScale == FP8Q_BSCALE_BLOCK && !kAccum && !kTmaOut),
                 "the gated form runs on CTA pairs with block scales");
   extern __shared__ uint8_t smem_raw[];
@@ -237,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *sA = smem;
   uint8_t *sB = smem + C::kStages * C::kABytes;
   uint8_t *sC = smem + C::kTileBytes;  // output staging (1024-byte aligned)
-  SmemCtl *ctl = reinterpret_cast<SmemCtl *>(sC + kStageCBytes);
+  Ctl *ctl = reinterpret_cast<Ctl *>(sC + kStageCBytes);
   int *s_lo = reinterpret_cast<int *>(ctl + 1);  // grouped only (see tile_of)
   int *s_prefix = s_lo + (kMaxGroups + 1);
 
@@ -258,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->tempty[i]), C::kTemptyCount);
     }
     mbar_init(smem_u32(&ctl->drain), 1);
-    if (kGlu) glu_exchange_init(ctl->glu);
+    if constexpr (kGlu) glu_exchange_init(ctl->glu);
     ctl->abort_flag = 0;
     fence_barrier_init();
   }
@@ -272,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     else tmem_alloc(smem_u32(&ctl->tmem_base), kTmemCols);
     tc_fence_before();
   }
-  if (kGlu) wait_for_previous_kernel();
+  if constexpr (kGlu) wait_for_previous_kernel();
   // barriers initialised and TMEM allocated in every CTA before any CTA of the
   // pair signals a peer
   __syncwarp();
@@ -335,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int tb = 0;
     uint32_t tphase = 0;
     uint32_t sb_iter = 0;
-    uint32_t glu_uses = 0;
+    [[maybe_unused]] uint32_t glu_uses = 0;
     bool ok = true;
     for (int t = tile_first; ok && t < total_tiles; t += tile_step) {
       const Tile tl = tile_of<kGrouped, C::kTileM, kGlu>(t, p, s_lo, s_prefix);
@@ -362,14 +369,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            : p.sb + ncol0 + 16 * (lane & 7) + 2 * (lane >> 3);
       const int64_t sb_step = kBScale == FP8Q_BSCALE_BLOCK ? 1 : p.ld_sb;
       // gated form: the up projection's block, NB rows of blocks further down
-      const int64_t sb_up = static_cast<int64_t>(NB) * (kGrouped ? p.num_kb : p.ld_sb);
+      [[maybe_unused]] int64_t sb_up = 0;
+      if constexpr (kGlu) sb_up = static_cast<int64_t>(NB) * (kGrouped ? p.num_kb : p.ld_sb);
       // per-column kind: this lane's first column
       const int ncol = ncol0 + 16 * (lane & 7) + 2 * (lane >> 3);
       auto load_sa = [&]() { return sa_in ? __ldg(sa_ptr) : 0.0f; };
       auto load_sb = [&]() {
         return kBScale != FP8Q_BSCALE_ROW && sb_in ? __ldg(sb_ptr) : 0.0f;
       };
-      auto load_sbu = [&]() { return kGlu ? __ldg(sb_ptr + sb_up) : 0.0f; };
       auto load_sb4 = [&]() {
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (kBScale == FP8Q_BSCALE_ROW) {
@@ -386,19 +393,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < kEpiCols / 2; ++j) acc[j] = 0ull;
       float sa_nx = p.num_kb > 0 ? load_sa() : 0.0f;
       float sb_nx = p.num_kb > 0 ? load_sb() : 0.0f;
-      float sbu_nx = p.num_kb > 0 ? load_sbu() : 0.0f;
+      [[maybe_unused]] float sbu_nx = 0.0f;
+      if constexpr (kGlu) sbu_nx = p.num_kb > 0 ? __ldg(sb_ptr + sb_up) : 0.0f;
       float4 sb4_nx = p.num_kb > 0 ? load_sb4() : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 
       for (int kb = 0; kb < p.num_kb; ++kb) {
         // the scales of group kb were loaded one iteration ago; fetch kb+1 now
-        const float sa_v = sa_nx, sb_v = sb_nx, sbu_v = sbu_nx;
+        const float sa_v = sa_nx, sb_v = sb_nx;
+        [[maybe_unused]] const float sbu_v = sbu_nx;
         const float4 sb4 = sb4_nx;
         if (kb + 1 < p.num_kb) {
           sa_ptr += p.ld_sa;
           sb_ptr += sb_step;
           sa_nx = load_sa();
           sb_nx = load_sb();
-          sbu_nx = load_sbu();
+          if constexpr (kGlu) sbu_nx = __ldg(sb_ptr + sb_up);
           sb4_nx = load_sb4();
         }
         if (kBScale == FP8Q_BSCALE_ROW) {
@@ -408,7 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         const uint64_t scale2 = pack_f32x2(sa_v * sb_v, sa_v * sb_v);
-        const uint64_t scale2u = kGlu ? pack_f32x2(sa_v * sbu_v, sa_v * sbu_v) : scale2;
+        [[maybe_unused]] uint64_t scale2u = 0;
+        if constexpr (kGlu) scale2u = pack_f32x2(sa_v * sbu_v, sa_v * sbu_v);
         uint64_t sa2f[4];  // per-column kind: this thread's four row scales, packed twice
         if (kFrag) {
 #pragma unroll
@@ -614,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (kGlu) let_next_kernel_start();
+    if constexpr (kGlu) let_next_kernel_start();
     // every tensor store of this warp has written global memory
     if (lane == 0) bulk_wait_group_all();
     // teardown (epilogue side): TMEM reads are complete
@@ -649,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t fb0 = mapa_shared(fb, 0);
             tma_load_2d_pair(smem_u32(sA + stage * C::kABytes), &tmA, fb0, kb * BK,
                              tl.a_row + static_cast<int>(rank) * BM);
-            if (kGlu) {
+            if constexpr (kGlu) {
               // 64 gate rows, then the up rows of the same 64 columns of h
               const int brow = tl.b_row + static_cast<int>(rank) * (BN / 4);
               tma_load_2d_pair(smem_u32(sB + stage * C::kBBytes), &tmB, fb0, kb * BK, brow);
@@ -788,10 +798,11 @@ bool make_tmap_c(CUtensorMap *m, void *base, uint64_t rows, uint64_t cols, uint6
 template <int kBScale, bool kOutF32, bool kGrouped, bool kPair, bool kAccum = false,
           bool kTmaOut = false, bool kGlu = false>
 fp8q_status launch(const CUtensorMap &ta, const CUtensorMap &tb,
-                   const std::conditional_t<kGlu, GluMaps, CUtensorMap> &tc, const GemmArgs &args,
+                   const std::conditional_t<kGlu, GluMaps, CUtensorMap> &tc,
+                   const std::conditional_t<kGlu, GluGemmArgs, GemmArgs> &args,
                    int64_t work_tiles, cudaStream_t s) {
   auto kern = fp8q_gemm_kernel<kBScale, kOutF32, kGrouped, kPair, kAccum, kTmaOut, kGlu>;
-  const size_t smem = smem_bytes(kGrouped, kPair);
+  const size_t smem = smem_bytes(kGrouped, kPair, kGlu);
   static int max_units[kMaxDevices] = {};  // co-resident CTAs (or CTA pairs) per device
   static std::mutex mu;
   int dev = 0;
@@ -907,7 +918,7 @@ fp8q_status gemm_glu(const GluIn &in, const GluOut &out, cudaStream_t s) {
   const bool grouped = in.offs != nullptr;
   DeviceInfo dev;
   if (fp8q_status st = device_info(dev)) return st;
-  if (dev.max_smem_optin < static_cast<int>(smem_bytes(grouped, true)))
+  if (dev.max_smem_optin < static_cast<int>(smem_bytes(grouped, true, true)))
     return FP8Q_ERR_UNSUPPORTED;
   // K == 0: no loads happen; describe a dummy 1 x 128 tensor so the maps are valid
   const bool k0 = in.K == 0;
@@ -918,7 +929,7 @@ fp8q_status gemm_glu(const GluIn &in, const GluOut &out, cudaStream_t s) {
       !make_tmap_u8(&tb, k0 ? any : in.b, k0 ? 1 : brows, k0 ? 128 : in.K, k0 ? 128 : in.ldb,
                     BN / 4))
     return FP8Q_ERR_CUDA;
-  GemmArgs args{};
+  GluGemmArgs args{};
   args.sa = in.sa;
   args.ld_sa = in.ld_sa;
   args.sb = in.sb;

@@ -120,7 +120,10 @@ struct MxArgs {
   const int32_t *offs;  // grouped only: expert row offsets [G + 1] (device)
   int G;
   uint64_t timeout_ns;
-  GluOut glu;           // gated GEMM only: N = F, tiles of 128 columns of h
+};
+// The gated form's additions stay out of the plain kernels' types and code.
+struct GluMxArgs : MxArgs {
+  GluOut glu;  // N = F, tiles of 128 columns of h
 };
 
 // Per-column B scale preparation (dense GEMMs with FP8Q_BSCALE_ROW): every
@@ -148,7 +151,9 @@ struct alignas(8) MxCtl {
   uint64_t pfree[kPrepSlots];   // every CTA: the four B producer warps read them
   uint32_t tmem_base;
   int abort_flag;
-  GluExchange glu;  // gated GEMM only
+};
+struct GluMxCtl : MxCtl {
+  GluExchange glu;
 };
 
 constexpr int kMaxGroups = 1024;
@@ -239,7 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fp8q_gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ std::conditional_t<kGlu, GluMaps, NoMaps> maps,
-                        const MxArgs p) {
+                        const std::conditional_t<kGlu, GluMxArgs, MxArgs> p) {
+  using Ctl = std::conditional_t<kGlu, GluMxCtl, MxCtl>;
   constexpr int kRing = kGlu ? kGluStages : kStages;  // ring depth
   // per-column B scales of a dense GEMM are prepared in warps 2-3
   constexpr bool kPrep = kBScale == FP8Q_BSCALE_ROW && !kGrouped;
@@ -252,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *sB = smem + kRing * kABytes;
   uint8_t *sC = smem + static_cast<size_t>(kRing) * (kABytes + kBBytes);  // output staging (1024-byte aligned)
   uint32_t *prep_b = reinterpret_cast<uint32_t *>(sC + kStageBytes);  // [slot][8][32]
-  MxCtl *ctl = reinterpret_cast<MxCtl *>(sC + (kGlu ? kGluStageBytes : kStageBytes) +
+  Ctl *ctl = reinterpret_cast<Ctl *>(sC + (kGlu ? kGluStageBytes : kStageBytes) +
                                          (kPrep ? kPrepBytes : 0));
   int *s_lo = reinterpret_cast<int *>(ctl + 1);  // grouped only (see mx_tile_of)
   int *s_hi = s_lo + (kMaxGroups + 1);
@@ -283,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->pready[i]), 2);
       mbar_init(smem_u32(&ctl->pfree[i]), 4);
     }
-    if (kGlu) glu_exchange_init(ctl->glu);
+    if constexpr (kGlu) glu_exchange_init(ctl->glu);
     ctl->abort_flag = 0;
     fence_barrier_init();
   }
@@ -296,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
   }
   __syncwarp();
-  if (kGlu) wait_for_previous_kernel();
+  if constexpr (kGlu) wait_for_previous_kernel();
   cluster_sync_all();
   // grouped: clamp the expert offsets into [0, M] and build the m-tile prefix
   int total_tiles;
@@ -342,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ss = 0;           // next scale stage slot to write
     uint32_t sphase = 0;  // its phase
     uint32_t tphase = 0;  // bit b: phase of tfull[b]
-    uint32_t glu_uses = 0;
+    [[maybe_unused]] uint32_t glu_uses = 0;
     bool ok = true;
 
     // Scale production walks a cursor over (tile, stage) in the order the MMA
@@ -647,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       prev_buf = i % kAccBufs;
     }
     if (ok && prev_t >= 0) ok = drain(prev_t, prev_buf);
-    if (kGlu) {
+    if constexpr (kGlu) {
       let_next_kernel_start();
       // every tensor store of this warp has written global memory
       if (lane == 0) bulk_wait_group_all();
@@ -679,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t fb0 = mapa_shared(fb, 0);
           tma_load_2d_pair(smem_u32(sA + stage * kABytes), &tmA, fb0, kb * BK,
                            tl.m0 + static_cast<int>(rank) * BM);
-          if (kGlu) {
+          if constexpr (kGlu) {
             // 64 gate rows, then the up rows of the same 64 columns of h
             const int brow = tl.b_row + static_cast<int>(rank) * (BN / 4);
             tma_load_2d_pair(smem_u32(sB + stage * kBBytes), &tmB, fb0, kb * BK, brow);
@@ -826,12 +832,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ host
 template <int kBScale, bool kOutF32, bool kAccum, bool kGrouped = false, bool kGlu = false>
-fp8q_status launch_mx(const CUtensorMap &ta, const CUtensorMap &tb, const MxArgs &args,
-                      int64_t tiles, cudaStream_t s,
+fp8q_status launch_mx(const CUtensorMap &ta, const CUtensorMap &tb,
+                      const std::conditional_t<kGlu, GluMxArgs, MxArgs> &args, int64_t tiles,
+                      cudaStream_t s,
                       const std::conditional_t<kGlu, GluMaps, NoMaps> &maps = {}) {
   auto kern = fp8q_gemm_mx_kernel<kBScale, kOutF32, kAccum, kGrouped, kGlu>;
   constexpr size_t smem =
-      (kGlu ? 1024 + kGluStages * (kABytes + kBBytes) + kGluStageBytes + sizeof(MxCtl) : kSmemBytes) +
+      (kGlu ? 1024 + kGluStages * (kABytes + kBBytes) + kGluStageBytes + sizeof(GluMxCtl) : kSmemBytes) +
       (kGrouped ? kGroupTables : 0) + (kBScale == FP8Q_BSCALE_ROW && !kGrouped ? kPrepBytes : 0);
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
   static int max_pairs[kMaxDevices] = {};
@@ -971,7 +978,7 @@ fp8q_status gemm_mx_glu(const GluIn &in, const GluOut &out, cudaStream_t s) {
                     static_cast<uint64_t>(in.G) * 2 * in.F, in.K, in.ldb, 128, BN / 4,
                     CU_TENSOR_MAP_SWIZZLE_128B))
     return FP8Q_ERR_CUDA;
-  MxArgs args{};
+  GluMxArgs args{};
   args.sa = in.sa;
   args.ld_sa = in.ld_sa;
   args.sb = in.sb;
