@@ -243,8 +243,8 @@ template <int kBScale, bool kOutF32, bool kAccum, bool kGrouped = false, bool kG
 __global__ void __launch_bounds__(kThreads, 1)
     fp8q_gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB,
-                        const __grid_constant__ std::conditional_t<kGlu, GluMaps, NoMaps> maps,
-                        const std::conditional_t<kGlu, GluMxArgs, MxArgs> p) {
+                        const std::conditional_t<kGlu, GluMxArgs, MxArgs> p,
+                        const __grid_constant__ std::conditional_t<kGlu, GluMaps, NoMaps> maps) {
   using Ctl = std::conditional_t<kGlu, GluMxCtl, MxCtl>;
   constexpr int kRing = kGlu ? kGluStages : kStages;  // ring depth
   // per-column B scales of a dense GEMM are prepared in warps 2-3
@@ -876,7 +876,7 @@ fp8q_status launch_mx(const CUtensorMap &ta, const CUtensorMap &tb,
   }
   const int64_t pairs = tiles < max_pairs[dev] ? tiles : max_pairs[dev];
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
-  return cudaLaunchKernelEx(&cfg, kern, ta, tb, maps, args) == cudaSuccess ? FP8Q_OK
+  return cudaLaunchKernelEx(&cfg, kern, ta, tb, args, maps) == cudaSuccess ? FP8Q_OK
                                                                            : FP8Q_ERR_CUDA;
 }
 
