@@ -14,9 +14,12 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <optional>
 #include <string>
 
 #include "fp8q.h"
@@ -60,9 +63,48 @@ bool mat(PyObject *o, int64_t rows, int64_t cols, at::ScalarType dtype, const ch
   return t && mat(*t, rows, cols, dtype, name, m);
 }
 
-at::Tensor new_tensor(at::IntArrayRef size, at::ScalarType dtype, at::Device dev) {
-  return at::Tensor(at::detail::empty_cuda(size, dtype, dev, c10::nullopt));
-}
+// Where a call runs, and where the memory that it takes for itself comes from:
+// the stream of its kernels.  torch hands freed memory out again in the order of
+// the stream it was taken on, so memory of the current stream would be reused
+// while kernels on another one still work in it.
+class Place {
+ public:
+  // torch's current stream, or the given stream's handle.
+  bool set(PyObject *stream, at::Device device) {
+    dev = device;
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(dev.index());
+    handle = current.stream();
+    if (stream == Py_None) return true;
+    handle = PyLong_AsVoidPtr(stream);
+    if (handle == nullptr && PyErr_Occurred()) return false;
+    if (handle != current.stream()) {
+      other = c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), dev.index());
+      reader = current;
+    }
+    return true;
+  }
+  // Scratch: nothing but this call's kernels uses it.
+  at::Tensor scratch(int64_t bytes) const { return take({bytes}, at::kByte); }
+  // A result: the caller may go on with it on the current stream (once that
+  // stream waits for the other one) and drop it there.
+  at::Tensor result(at::IntArrayRef size, at::ScalarType dtype) const {
+    at::Tensor t = take(size, dtype);
+    if (reader && t.nbytes() > 0)
+      c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *reader);
+    return t;
+  }
+
+  at::Device dev{at::kCUDA, 0};
+  void *handle = nullptr;
+
+ private:
+  at::Tensor take(at::IntArrayRef size, at::ScalarType dtype) const {
+    std::optional<c10::cuda::CUDAStreamGuard> on;
+    if (other) on.emplace(*other);
+    return at::Tensor(at::detail::empty_cuda(size, dtype, dev, c10::nullopt));
+  }
+  std::optional<c10::cuda::CUDAStream> other, reader;  // set where they differ
+};
 
 // Results of a call: the caller's tensor, checked, a new one, or None.
 struct Results {
@@ -73,14 +115,14 @@ struct Results {
     for (int i = 0; i < n; ++i) Py_XDECREF(o[i]);
   }
   bool add(PyObject *given, bool wanted, int64_t rows, int64_t cols, at::ScalarType dtype,
-           at::Device dev, const char *name, Mat &m, bool &present) {
+           const Place &place, const char *name, Mat &m, bool &present) {
     if (given != Py_None) {
       if (!mat(given, rows, cols, dtype, name, m)) return false;
       Py_INCREF(given);
       o[n++] = given;
       present = true;
     } else if (wanted) {
-      at::Tensor t = new_tensor({rows, cols}, dtype, dev);
+      at::Tensor t = place.result({rows, cols}, dtype);
       m.p = t.data_ptr();
       m.ld = cols;
       o[n++] = THPVariable_Wrap(std::move(t));
@@ -101,16 +143,6 @@ struct Results {
     return t;
   }
 };
-
-// torch's current stream, or the given stream's handle.
-bool stream_of(PyObject *o, at::Device dev, void *&s) {
-  if (o == Py_None) {
-    s = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
-    return true;
-  }
-  s = PyLong_AsVoidPtr(o);
-  return !(s == nullptr && PyErr_Occurred());
-}
 
 PyObject *wrong_count(const char *name) {
   PyErr_Format(PyExc_TypeError, "%s: wrong number of arguments", name);
@@ -171,15 +203,15 @@ PyObject *swiglu_impl(PyObject *const *v, Py_ssize_t n) {
     return nullptr;
   }
   const int mode = static_cast<int>(PyLong_AsLong(v[9]));
-  void *stream = nullptr;
-  if ((mode == -1 && PyErr_Occurred()) || !stream_of(v[14], dev, stream)) return nullptr;
+  Place place;
+  if ((mode == -1 && PyErr_Occurred()) || !place.set(v[14], dev)) return nullptr;
   Results r;
   Mat h, gu, q, s;
   bool has_h, has_gu, has_q, has_s;
-  if (!r.add(v[10], v[6] == Py_True, M, F, at::kBFloat16, dev, "h", h, has_h) ||
-      !r.add(v[11], v[7] == Py_True, M, 2 * F, at::kBFloat16, dev, "gu", gu, has_gu) ||
-      !r.add(v[12], v[8] == Py_True, M, F, at::kByte, dev, "q", q, has_q) ||
-      !r.add(v[13], has_q, F / 128, M, at::kFloat, dev, "s", s, has_s))
+  if (!r.add(v[10], v[6] == Py_True, M, F, at::kBFloat16, place, "h", h, has_h) ||
+      !r.add(v[11], v[7] == Py_True, M, 2 * F, at::kBFloat16, place, "gu", gu, has_gu) ||
+      !r.add(v[12], v[8] == Py_True, M, F, at::kByte, place, "q", q, has_q) ||
+      !r.add(v[13], has_q, F / 128, M, at::kFloat, place, "s", s, has_s))
     return nullptr;
   fp8q_status st;
   float *fs = static_cast<float *>(s.p);
@@ -187,11 +219,11 @@ PyObject *swiglu_impl(PyObject *const *v, Py_ssize_t n) {
   if (grouped)
     st = (pow2 ? fp8q_grouped_gemm_swiglu_pow2 : fp8q_grouped_gemm_swiglu)(
         ma.p, ma.ld, fsa, msa.ld, mb.p, mb.ld, fsb, offs, static_cast<int>(G), h.p, h.ld, gu.p,
-        gu.ld, q.p, q.ld, fs, s.ld, mode, M, F, K, stream);
+        gu.ld, q.p, q.ld, fs, s.ld, mode, M, F, K, place.handle);
   else
     st = (pow2 ? fp8q_gemm_swiglu_pow2 : fp8q_gemm_swiglu)(
         ma.p, ma.ld, fsa, msa.ld, mb.p, mb.ld, fsb, msb.ld, h.p, h.ld, gu.p, gu.ld, q.p, q.ld, fs,
-        s.ld, mode, M, F, K, stream);
+        s.ld, mode, M, F, K, place.handle);
   return r.tuple(st);
 }
 
@@ -210,23 +242,23 @@ PyObject *bwd_impl(PyObject *const *v, Py_ssize_t n) {
   if (!mat(*dh, T, F, at::kBFloat16, "dh", mdh) || !mat(v[1], T, N, at::kBFloat16, "gu", mgu))
     return nullptr;
   const int mode = static_cast<int>(PyLong_AsLong(v[6]));
-  void *stream = nullptr;
-  if ((mode == -1 && PyErr_Occurred()) || !stream_of(v[14], dev, stream)) return nullptr;
+  Place place;
+  if ((mode == -1 && PyErr_Occurred()) || !place.set(v[14], dev)) return nullptr;
   Results r;
   Mat d, q, s, qT, sT, hT, shT;
   bool has_d, has_q, has_qT, has_hT, has;
-  if (!r.add(v[7], v[2] == Py_True, T, N, at::kBFloat16, dev, "d", d, has_d) ||
-      !r.add(v[8], v[3] == Py_True, T, N, at::kByte, dev, "q", q, has_q) ||
-      !r.add(v[9], has_q, N / 128, T, at::kFloat, dev, "s", s, has) ||
-      !r.add(v[10], v[4] == Py_True, N, T, at::kByte, dev, "qT", qT, has_qT) ||
-      !r.add(v[11], has_qT, T / 128, N, at::kFloat, dev, "sT", sT, has) ||
-      !r.add(v[12], v[5] == Py_True, F, T, at::kByte, dev, "hT", hT, has_hT) ||
-      !r.add(v[13], has_hT, T / 128, F, at::kFloat, dev, "shT", shT, has))
+  if (!r.add(v[7], v[2] == Py_True, T, N, at::kBFloat16, place, "d", d, has_d) ||
+      !r.add(v[8], v[3] == Py_True, T, N, at::kByte, place, "q", q, has_q) ||
+      !r.add(v[9], has_q, N / 128, T, at::kFloat, place, "s", s, has) ||
+      !r.add(v[10], v[4] == Py_True, N, T, at::kByte, place, "qT", qT, has_qT) ||
+      !r.add(v[11], has_qT, T / 128, N, at::kFloat, place, "sT", sT, has) ||
+      !r.add(v[12], v[5] == Py_True, F, T, at::kByte, place, "hT", hT, has_hT) ||
+      !r.add(v[13], has_hT, T / 128, F, at::kFloat, place, "shT", shT, has))
     return nullptr;
   return r.tuple(fp8q_swiglu_bwd(mdh.p, mdh.ld, mgu.p, mgu.ld, d.p, d.ld, q.p, q.ld,
                                  static_cast<float *>(s.p), s.ld, qT.p, qT.ld,
                                  static_cast<float *>(sT.p), sT.ld, hT.p, hT.ld,
-                                 static_cast<float *>(shT.p), shT.ld, T, F, mode, stream));
+                                 static_cast<float *>(shT.p), shT.ld, T, F, mode, place.handle));
 }
 
 // Row and matrix pitch of a matrix or a batch of matrices.
@@ -254,8 +286,8 @@ PyObject *newton_schulz_impl(PyObject *const *v, Py_ssize_t n) {
   const double a = PyFloat_AsDouble(v[2]), b = PyFloat_AsDouble(v[3]), c = PyFloat_AsDouble(v[4]),
                eps = PyFloat_AsDouble(v[5]);
   const int out_dtype = static_cast<int>(PyLong_AsLong(v[6]));
-  void *stream = nullptr;
-  if (PyErr_Occurred() || !stream_of(v[9], dev, stream)) return nullptr;
+  Place place;
+  if (PyErr_Occurred() || !place.set(v[9], dev)) return nullptr;
   const at::ScalarType od = out_dtype == FP8Q_OUT_BF16 ? at::kBFloat16 : at::kFloat;
   at::Tensor out;
   if (v[7] != Py_None) {
@@ -267,7 +299,7 @@ PyObject *newton_schulz_impl(PyObject *const *v, Py_ssize_t n) {
     }
     out = *t;
   } else {
-    out = new_tensor(g->sizes(), od, dev);
+    out = place.result(g->sizes(), od);
   }
   int64_t ld_g, stride_g, ld_o, stride_o;
   if (!pitches(*g, "g", ld_g, stride_g) || !pitches(out, "out", ld_o, stride_o)) return nullptr;
@@ -283,7 +315,7 @@ PyObject *newton_schulz_impl(PyObject *const *v, Py_ssize_t n) {
     ws = *t;
   } else {
     const int64_t bytes = fp8q_newton_schulz_workspace_bytes(B, m, nn);
-    ws = new_tensor({bytes > 0 ? bytes : 1}, at::kByte, dev);
+    ws = place.scratch(bytes > 0 ? bytes : 1);
   }
   const bool any = g->numel() > 0;
   const fp8q_status st = fp8q_newton_schulz(
@@ -291,7 +323,7 @@ PyObject *newton_schulz_impl(PyObject *const *v, Py_ssize_t n) {
       g->scalar_type() == at::kFloat ? FP8Q_OUT_FP32 : FP8Q_OUT_BF16,
       any ? out.data_ptr() : nullptr, ld_o, stride_o, out_dtype, B, m, nn, steps,
       static_cast<float>(a), static_cast<float>(b), static_cast<float>(c), static_cast<float>(eps),
-      ws.data_ptr(), static_cast<int64_t>(ws.nbytes()), stream);
+      ws.data_ptr(), static_cast<int64_t>(ws.nbytes()), place.handle);
   if (st != FP8Q_OK) return PyLong_FromLong(st);
   if (v[7] != Py_None) {
     Py_INCREF(v[7]);
