@@ -4,7 +4,9 @@ Argument marshalling only: every step of the computation runs in the CUDA
 kernels of libfp8q.so.  The gated feed-forward and Newton-Schulz calls marshal
 in a compiled module (csrc/torch_calls.cpp), the others through ctypes.  Tensors are torch CUDA tensors (torch supplies device
 memory and the current stream); outputs that are not passed in are allocated
-with torch.  E4M3 tensors are torch.uint8 (raw codes; ``.view(torch.float8_e4m3fn)``
+with torch.  ``stream`` names another stream than the current one: the call, and
+the memory that it takes for results and scratch, are then that stream's, as
+under ``torch.cuda.stream``.  E4M3 tensors are torch.uint8 (raw codes; ``.view(torch.float8_e4m3fn)``
 gives the FP8 dtype).  A failing call raises FP8QError; there is no fallback.
 """
 from __future__ import annotations
@@ -135,6 +137,24 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _new(shape, dtype, device, stream):
+    """A tensor for a call's result or scratch, from the memory of the stream that the call runs on.
+
+    torch hands freed memory out again in the order of the stream it was taken on: memory of the
+    current stream could be reused there while the call still works in it on another one.  The
+    caller may go on with a result on the current stream, once that waits for the other one."""
+    if stream is not None:
+        current = torch.cuda.current_stream(device)
+        if stream.cuda_stream != current.cuda_stream:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+            with torch.cuda.stream(stream):
+                t = torch.empty(shape, dtype=dtype, device=device)
+            t.record_stream(current)
+            return t
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _rows_ld(t, name):
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError(f"{name} must be 2-D with a contiguous last dimension")
@@ -145,9 +165,9 @@ def fp8q_quant_act(x, *, scale_mode=FP8Q_SCALE_FP32, q=None, sa=None, stream=Non
     """1x128 quantisation of BF16 x [M][K] -> (q uint8 [M][K], sa f32 [K/128][M])."""
     M, K = x.shape
     if q is None:
-        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        q = _new((M, K), torch.uint8, x.device, stream)
     if sa is None:
-        sa = torch.empty((K // 128, M), dtype=torch.float32, device=x.device)
+        sa = _new((K // 128, M), torch.float32, x.device, stream)
     _check(load_library().fp8q_quant_act(
         _ptr(x), M, K, _rows_ld(x, "x"), _ptr(q), _rows_ld(q, "q"), _ptr(sa),
         _rows_ld(sa, "sa") if sa.numel() else M, scale_mode, _stream(stream)), "fp8q_quant_act")
@@ -161,14 +181,14 @@ def fp8q_quant_act_T(x, *, scale_mode=FP8Q_SCALE_FP32, with_rows=False, qT=None,
     T, C = x.shape
     dev = x.device
     if qT is None:
-        qT = torch.empty((C, T), dtype=torch.uint8, device=dev)
+        qT = _new((C, T), torch.uint8, dev, stream)
     if sT is None:
-        sT = torch.empty((T // 128, C), dtype=torch.float32, device=dev)
+        sT = _new((T // 128, C), torch.float32, dev, stream)
     if with_rows:
         if q_rows is None:
-            q_rows = torch.empty((T, C), dtype=torch.uint8, device=dev)
+            q_rows = _new((T, C), torch.uint8, dev, stream)
         if s_rows is None:
-            s_rows = torch.empty((C // 128, T), dtype=torch.float32, device=dev)
+            s_rows = _new((C // 128, T), torch.float32, dev, stream)
     _check(load_library().fp8q_quant_act_T(
         _ptr(x), T, C, _rows_ld(x, "x"), _ptr(qT), _rows_ld(qT, "qT") if qT.numel() else T,
         _ptr(sT), _rows_ld(sT, "sT") if sT.numel() else C,
@@ -186,9 +206,9 @@ def fp8q_requant_act_T(q, s_rows, *, scale_mode=FP8Q_SCALE_FP32, qT=None, sT=Non
     s_rows f32 [C/128][T] -> (qT uint8 [C][T], sT f32 [T/128][C])."""
     T, C = q.shape
     if qT is None:
-        qT = torch.empty((C, T), dtype=torch.uint8, device=q.device)
+        qT = _new((C, T), torch.uint8, q.device, stream)
     if sT is None:
-        sT = torch.empty((T // 128, C), dtype=torch.float32, device=q.device)
+        sT = _new((T // 128, C), torch.float32, q.device, stream)
     _check(load_library().fp8q_requant_act_T(
         _ptr(q), T, C, _rows_ld(q, "q"), _ptr(s_rows),
         _rows_ld(s_rows, "s_rows") if s_rows.numel() else T, _ptr(qT),
@@ -204,11 +224,11 @@ def fp8q_quant_weight(w, *, scale_mode=FP8Q_SCALE_FP32, with_transpose=False, q=
     N, K = w.shape
     dev = w.device
     if q is None:
-        q = torch.empty((N, K), dtype=torch.uint8, device=dev)
+        q = _new((N, K), torch.uint8, dev, stream)
     if sb is None:
-        sb = torch.empty(((N + 127) // 128, K // 128), dtype=torch.float32, device=dev)
+        sb = _new(((N + 127) // 128, K // 128), torch.float32, dev, stream)
     if with_transpose and qT is None:
-        qT = torch.empty((K, N), dtype=torch.uint8, device=dev)
+        qT = _new((K, N), torch.uint8, dev, stream)
     _check(load_library().fp8q_quant_weight(
         _ptr(w), N, K, _rows_ld(w, "w"), _ptr(q), _rows_ld(q, "q"),
         _ptr(qT) if with_transpose else None,
@@ -231,12 +251,12 @@ def fp8q_quant_tensor(x, *, scale_mode=FP8Q_SCALE_FP32, q=None, s=None, workspac
     M, K = x.shape
     dev = x.device
     if q is None:
-        q = torch.empty((M, K), dtype=torch.uint8, device=dev)
+        q = _new((M, K), torch.uint8, dev, stream)
     if s is None:
-        s = torch.empty((1,), dtype=torch.float32, device=dev)
+        s = _new((1,), torch.float32, dev, stream)
     nbytes = fp8q_quant_tensor_workspace_bytes(M, K)
     if workspace is None:
-        workspace = torch.empty((max(nbytes, 4),), dtype=torch.uint8, device=dev)
+        workspace = _new((max(nbytes, 4),), torch.uint8, dev, stream)
     _check(load_library().fp8q_quant_tensor(
         _ptr(x), M, K, _rows_ld(x, "x"), _ptr(q), _rows_ld(q, "q"), _ptr(s), _ptr(workspace),
         workspace.numel() * workspace.element_size(), scale_mode, _stream(stream)),
@@ -262,7 +282,7 @@ def fp8q_gemm(a, sa, b, sb, *, bscale_kind=FP8Q_BSCALE_BLOCK, out_dtype=FP8Q_OUT
     N = b.shape[0]
     if c is None:
         dt = torch.bfloat16 if out_dtype == FP8Q_OUT_BF16 else torch.float32
-        c = torch.empty((M, N), dtype=dt, device=a.device)
+        c = _new((M, N), dt, a.device, stream)
     ld_sa = _rows_ld(sa, "sa") if sa.numel() else M
     ld_sb = _rows_ld(sb, "sb") if sb.numel() else 1
     _check(getattr(load_library(), _entry)(
@@ -310,7 +330,7 @@ def fp8q_grouped_gemm(a, sa, b, sb, offs, *, out_dtype=FP8Q_OUT_BF16, c=None, st
     G, N, _ = b.shape
     if c is None:
         dt = torch.bfloat16 if out_dtype == FP8Q_OUT_BF16 else torch.float32
-        c = torch.empty((M, N), dtype=dt, device=a.device)
+        c = _new((M, N), dt, a.device, stream)
     if b.stride(2) != 1 or b.stride(0) != N * b.stride(1):
         raise ValueError("b must be [G][N][ldb] with experts packed back to back")
     _check(getattr(load_library(), _entry)(
@@ -443,7 +463,7 @@ def fp8q_newton_schulz(g, *, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7
 def fp8q_cast_e4m3(x, *, q=None, stream=None):
     """FP32 -> E4M3 codes (RNE, saturate), no scaling."""
     if q is None:
-        q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        q = _new(x.shape, torch.uint8, x.device, stream)
     _check(load_library().fp8q_cast_e4m3(_ptr(x), x.numel(), _ptr(q), _stream(stream)),
            "fp8q_cast_e4m3")
     return q
