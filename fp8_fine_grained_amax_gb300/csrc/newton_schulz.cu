@@ -473,6 +473,15 @@ __device__ __forceinline__ bool wait_shared(uint32_t addr, uint32_t want, volati
   }
 }
 
+// True for the whole warp where every lane's wait came true.  What the waiting
+// lanes acquired is ordered before the other lanes' accesses by __syncwarp; a
+// vote alone orders no memory.
+__device__ __forceinline__ bool warp_acquired(bool got) {
+  const bool all = __all_sync(0xffffffffu, got) != 0;
+  __syncwarp();
+  return all;
+}
+
 // One pair's walk over its units of a phase, as segments of tiles.
 struct Segment {
   int b, row0, col0;  // matrix, first row and column of the tile
@@ -727,7 +736,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // lane 0 waits for a counter; the answer goes to the whole warp
     auto warp_wait = [&](const uint32_t *count, uint32_t want) {
       const bool got = lane != 0 || wait_count(count, want, abort_flag, p.timeout_ns);
-      return __all_sync(0xffffffffu, got) != 0;
+      return warp_acquired(got);
     };
     int buf = 0, tile_no = 0, seg_no = 0;
     uint32_t tphase = 0, given = 0;  // given: phase + 1 of this warp's last partial sums
@@ -758,7 +767,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const bool there = lane != 0 || wait_shared(smem_u32(&ctl->ready),
                                                       static_cast<uint32_t>(seg_no) + 1, abort_flag,
                                                       p.timeout_ns);
-          if (!(ok = __all_sync(0xffffffffu, there))) break;
+          if (!(ok = warp_acquired(there))) break;
           if (row < p.p) d_row = __ldcg(diag + row);
           if (kind == kPoly) {  // the pitch is whole
             const int dc = cbase + 4 * lane;
@@ -1030,7 +1039,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool there =
             lane >= kEpiWarps || wait_shared(smem_u32(&ctl->stored[lane]),
                                              static_cast<uint32_t>(tile_no), abort_flag, p.timeout_ns);
-        if (!(ok = __all_sync(0xffffffffu, there))) break;
+        if (!(ok = warp_acquired(there))) break;
         if (lane == 0) {
           __threadfence();
           red_release(&p.done[s.b]);
