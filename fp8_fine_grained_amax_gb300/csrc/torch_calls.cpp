@@ -144,6 +144,17 @@ struct Results {
   }
 };
 
+// Flags by their truth, as Python takes them (1, a numpy bool, ...).
+template <int N>
+bool flags(PyObject *const *o, bool (&v)[N]) {
+  for (int i = 0; i < N; ++i) {
+    const int t = PyObject_IsTrue(o[i]);
+    if (t < 0) return false;
+    v[i] = t != 0;
+  }
+  return true;
+}
+
 PyObject *wrong_count(const char *name) {
   PyErr_Format(PyExc_TypeError, "%s: wrong number of arguments", name);
   return nullptr;
@@ -204,13 +215,14 @@ PyObject *swiglu_impl(PyObject *const *v, Py_ssize_t n) {
   }
   const int mode = static_cast<int>(PyLong_AsLong(v[9]));
   Place place;
-  if ((mode == -1 && PyErr_Occurred()) || !place.set(v[14], dev)) return nullptr;
+  bool want[3];  // h, gu, codes
+  if ((mode == -1 && PyErr_Occurred()) || !flags(v + 6, want) || !place.set(v[14], dev)) return nullptr;
   Results r;
   Mat h, gu, q, s;
   bool has_h, has_gu, has_q, has_s;
-  if (!r.add(v[10], v[6] == Py_True, M, F, at::kBFloat16, place, "h", h, has_h) ||
-      !r.add(v[11], v[7] == Py_True, M, 2 * F, at::kBFloat16, place, "gu", gu, has_gu) ||
-      !r.add(v[12], v[8] == Py_True, M, F, at::kByte, place, "q", q, has_q) ||
+  if (!r.add(v[10], want[0], M, F, at::kBFloat16, place, "h", h, has_h) ||
+      !r.add(v[11], want[1], M, 2 * F, at::kBFloat16, place, "gu", gu, has_gu) ||
+      !r.add(v[12], want[2], M, F, at::kByte, place, "q", q, has_q) ||
       !r.add(v[13], has_q, F / 128, M, at::kFloat, place, "s", s, has_s))
     return nullptr;
   fp8q_status st;
@@ -243,16 +255,17 @@ PyObject *bwd_impl(PyObject *const *v, Py_ssize_t n) {
     return nullptr;
   const int mode = static_cast<int>(PyLong_AsLong(v[6]));
   Place place;
-  if ((mode == -1 && PyErr_Occurred()) || !place.set(v[14], dev)) return nullptr;
+  bool want[4];  // d, rows, cols, h
+  if ((mode == -1 && PyErr_Occurred()) || !flags(v + 2, want) || !place.set(v[14], dev)) return nullptr;
   Results r;
   Mat d, q, s, qT, sT, hT, shT;
   bool has_d, has_q, has_qT, has_hT, has;
-  if (!r.add(v[7], v[2] == Py_True, T, N, at::kBFloat16, place, "d", d, has_d) ||
-      !r.add(v[8], v[3] == Py_True, T, N, at::kByte, place, "q", q, has_q) ||
+  if (!r.add(v[7], want[0], T, N, at::kBFloat16, place, "d", d, has_d) ||
+      !r.add(v[8], want[1], T, N, at::kByte, place, "q", q, has_q) ||
       !r.add(v[9], has_q, N / 128, T, at::kFloat, place, "s", s, has) ||
-      !r.add(v[10], v[4] == Py_True, N, T, at::kByte, place, "qT", qT, has_qT) ||
+      !r.add(v[10], want[2], N, T, at::kByte, place, "qT", qT, has_qT) ||
       !r.add(v[11], has_qT, T / 128, N, at::kFloat, place, "sT", sT, has) ||
-      !r.add(v[12], v[5] == Py_True, F, T, at::kByte, place, "hT", hT, has_hT) ||
+      !r.add(v[12], want[3], F, T, at::kByte, place, "hT", hT, has_hT) ||
       !r.add(v[13], has_hT, T / 128, F, at::kFloat, place, "shT", shT, has))
     return nullptr;
   return r.tuple(fp8q_swiglu_bwd(mdh.p, mdh.ld, mgu.p, mgu.ld, d.p, d.ld, q.p, q.ld,

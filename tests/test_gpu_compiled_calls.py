@@ -1,5 +1,6 @@
 """What the compiled marshalling of the gated feed-forward and Newton-Schulz calls does with its
 arguments, with the caller's streams, and with the interpreter."""
+import numpy as np
 import pytest
 import torch
 
@@ -24,6 +25,25 @@ def gated_operands(M=5, F=128, K=256):
     a = torch.randn(M, K, generator=g).to(torch.float8_e4m3fn).view(torch.uint8)
     b = torch.randn(2 * F, K, generator=g).to(torch.float8_e4m3fn).view(torch.uint8)
     return a.cuda(), torch.ones(K // 128, M).cuda(), b.cuda(), torch.ones(2 * F // 128, K // 128).cuda()
+
+
+# ------------------------------------------------------------------ arguments
+@pytest.mark.parametrize("yes,no", [(True, False), (1, 0), (np.bool_(True), np.bool_(False)), ("y", "")])
+def test_flags_are_taken_by_their_truth(yes, no):
+    r = fq.fp8q_gemm_swiglu(*gated_operands(), with_h=no, with_gu=yes, with_codes=yes)
+    assert [t is not None for t in r] == [False, True, True, True]
+    r = fq.fp8q_gemm_swiglu(*gated_operands(), with_h=yes, with_gu=no, with_codes=no)
+    assert [t is not None for t in r] == [True, False, False, False]
+    dh, gu = torch.ones(128, 128).bfloat16().cuda(), torch.ones(128, 256).bfloat16().cuda()
+    r = fq.fp8q_swiglu_bwd(dh, gu, with_d=yes, with_rows=no, with_cols=no, with_h=yes)
+    assert [t is not None for t in r] == [True, False, False, False, False, True, True]
+    r = fq.fp8q_swiglu_bwd(dh, gu, with_d=no, with_rows=yes, with_cols=yes, with_h=no)
+    assert [t is not None for t in r] == [False, True, True, True, True, False, False]
+
+
+def test_a_flag_without_truth_raises():
+    with pytest.raises(ValueError):
+        fq.fp8q_gemm_swiglu(*gated_operands(), with_gu=np.ones(2))
 
 
 # ------------------------------------------------------------------ streams
