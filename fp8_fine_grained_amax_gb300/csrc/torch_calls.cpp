@@ -19,6 +19,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <climits>
 #include <optional>
 #include <string>
 
@@ -155,6 +156,16 @@ bool flags(PyObject *const *o, bool (&v)[N]) {
   return true;
 }
 
+// A Python int as a C int; what does not fit becomes the nearest that does, which
+// is out of range for every argument here, and the call refuses it.
+bool int_of(PyObject *o, int &v) {
+  int past = 0;
+  const long x = PyLong_AsLongAndOverflow(o, &past);
+  if (x == -1 && past == 0 && PyErr_Occurred()) return false;
+  v = past > 0 || x > INT_MAX ? INT_MAX : past < 0 || x < INT_MIN ? INT_MIN : static_cast<int>(x);
+  return true;
+}
+
 PyObject *wrong_count(const char *name) {
   PyErr_Format(PyExc_TypeError, "%s: wrong number of arguments", name);
   return nullptr;
@@ -213,10 +224,10 @@ PyObject *swiglu_impl(PyObject *const *v, Py_ssize_t n) {
              !mat(*sb, N / 128, K / 128, at::kFloat, "sb", msb)) {
     return nullptr;
   }
-  const int mode = static_cast<int>(PyLong_AsLong(v[9]));
+  int mode = 0;
   Place place;
   bool want[3];  // h, gu, codes
-  if ((mode == -1 && PyErr_Occurred()) || !flags(v + 6, want) || !place.set(v[14], dev)) return nullptr;
+  if (!int_of(v[9], mode) || !flags(v + 6, want) || !place.set(v[14], dev)) return nullptr;
   Results r;
   Mat h, gu, q, s;
   bool has_h, has_gu, has_q, has_s;
@@ -253,10 +264,10 @@ PyObject *bwd_impl(PyObject *const *v, Py_ssize_t n) {
   Mat mdh, mgu;
   if (!mat(*dh, T, F, at::kBFloat16, "dh", mdh) || !mat(v[1], T, N, at::kBFloat16, "gu", mgu))
     return nullptr;
-  const int mode = static_cast<int>(PyLong_AsLong(v[6]));
+  int mode = 0;
   Place place;
   bool want[4];  // d, rows, cols, h
-  if ((mode == -1 && PyErr_Occurred()) || !flags(v + 2, want) || !place.set(v[14], dev)) return nullptr;
+  if (!int_of(v[6], mode) || !flags(v + 2, want) || !place.set(v[14], dev)) return nullptr;
   Results r;
   Mat d, q, s, qT, sT, hT, shT;
   bool has_d, has_q, has_qT, has_hT, has;
@@ -295,10 +306,10 @@ PyObject *newton_schulz_impl(PyObject *const *v, Py_ssize_t n) {
     return nullptr;
   }
   const at::Device dev = g->device();
-  const int steps = static_cast<int>(PyLong_AsLong(v[1]));
+  int steps = 0, out_dtype = 0;
+  if (!int_of(v[1], steps) || !int_of(v[6], out_dtype)) return nullptr;
   const double a = PyFloat_AsDouble(v[2]), b = PyFloat_AsDouble(v[3]), c = PyFloat_AsDouble(v[4]),
                eps = PyFloat_AsDouble(v[5]);
-  const int out_dtype = static_cast<int>(PyLong_AsLong(v[6]));
   Place place;
   if (PyErr_Occurred() || !place.set(v[9], dev)) return nullptr;
   const at::ScalarType od = out_dtype == FP8Q_OUT_BF16 ? at::kBFloat16 : at::kFloat;

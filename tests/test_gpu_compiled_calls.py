@@ -46,6 +46,21 @@ def test_a_flag_without_truth_raises():
         fq.fp8q_gemm_swiglu(*gated_operands(), with_gu=np.ones(2))
 
 
+@pytest.mark.parametrize("far", [1 << 32, -(1 << 32), 1 << 80])
+def test_numbers_past_an_int_are_refused(far):
+    # the low 32 bits alone would be a valid mode, count or type
+    a, sa, b, sb = gated_operands()
+    dh, gu = torch.ones(128, 128).bfloat16().cuda(), torch.ones(128, 256).bfloat16().cuda()
+    g = torch.ones(8, 16).cuda()
+    for call in (lambda: fq.fp8q_gemm_swiglu(a, sa, b, sb, scale_mode=far),
+                 lambda: fq.fp8q_swiglu_bwd(dh, gu, scale_mode=far),
+                 lambda: fq.fp8q_newton_schulz(g, steps=far + 5),
+                 lambda: fq.fp8q_newton_schulz(g, out_dtype=far)):
+        with pytest.raises(fq.FP8QError) as err:
+            call()
+        assert err.value.status == B.FP8Q_ERR_INVALID
+
+
 # ------------------------------------------------------------------ streams
 def home_of(t):
     """Handle of the stream that a tensor's memory was taken on."""
