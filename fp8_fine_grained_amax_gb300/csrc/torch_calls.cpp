@@ -362,7 +362,11 @@ PyObject *guarded(PyObject *, PyObject *const *v, Py_ssize_t n) {
   try {
     return kImpl(v, n);
   } catch (const c10::OutOfMemoryError &e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
+    PyObject *torch = PyImport_ImportModule("torch");
+    PyObject *type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    if (type) PyErr_SetString(type, e.what_without_backtrace());
+    Py_XDECREF(type);
+    Py_XDECREF(torch);
   } catch (const std::exception &e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   }

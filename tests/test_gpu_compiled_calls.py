@@ -61,6 +61,16 @@ def test_numbers_past_an_int_are_refused(far):
         assert err.value.status == B.FP8Q_ERR_INVALID
 
 
+def test_out_of_memory_is_torchs_own_error():
+    # a workspace of more than the card holds; g and out are views of one matrix
+    g = torch.zeros(1, 4096, 4096, dtype=torch.bfloat16, device="cuda").expand(3000, -1, -1)
+    need = fq.fp8q_newton_schulz_workspace_bytes(3000, 4096, 4096)
+    assert need > torch.cuda.get_device_properties(0).total_memory
+    with pytest.raises(torch.OutOfMemoryError):
+        fq.fp8q_newton_schulz(g, out=torch.empty_like(g[:1]).expand(3000, -1, -1))
+    assert torch.equal(fq.fp8q_newton_schulz(g[0]), torch.zeros_like(g[0]))
+
+
 # ------------------------------------------------------------------ streams
 def home_of(t):
     """Handle of the stream that a tensor's memory was taken on."""
