@@ -107,42 +107,62 @@ class Place {
   std::optional<c10::cuda::CUDAStream> other, reader;  // set where they differ
 };
 
+// The interpreter's other threads run while this lives: an allocation may wait
+// for the device, a launch for room in its queue.
+struct NoGil {
+  PyThreadState *const state = PyEval_SaveThread();
+  ~NoGil() { PyEval_RestoreThread(state); }
+};
+
 // Results of a call: the caller's tensor, checked, a new one, or None.
-struct Results {
-  static constexpr int kMost = 8;
-  PyObject *o[kMost] = {};
-  int n = 0;
-  ~Results() {
-    for (int i = 0; i < n; ++i) Py_XDECREF(o[i]);
-  }
+class Results {
+ public:
   bool add(PyObject *given, bool wanted, int64_t rows, int64_t cols, at::ScalarType dtype,
-           const Place &place, const char *name, Mat &m, bool &present) {
+           const char *name, Mat &m, bool &present) {
+    One &r = all_[n_++];
+    present = wanted || given != Py_None;
     if (given != Py_None) {
-      if (!mat(given, rows, cols, dtype, name, m)) return false;
-      Py_INCREF(given);
-      o[n++] = given;
-      present = true;
-    } else if (wanted) {
-      at::Tensor t = place.result({rows, cols}, dtype);
-      m.p = t.data_ptr();
-      m.ld = cols;
-      o[n++] = THPVariable_Wrap(std::move(t));
-      present = true;
-    } else {
-      Py_INCREF(Py_None);
-      o[n++] = Py_None;
-      present = false;
+      r.given = given;
+      return mat(given, rows, cols, dtype, name, m);
     }
-    return o[n - 1] != nullptr;
+    if (wanted) {
+      m.ld = cols;
+      r.rows = rows;
+      r.dtype = dtype;
+      r.wanted = &m;
+    }
+    return true;
+  }
+  // Make the new ones (needs no GIL).
+  void make(const Place &place) {
+    for (int i = 0; i < n_; ++i)
+      if (Mat *m = all_[i].wanted) {
+        all_[i].made = place.result({all_[i].rows, m->ld}, all_[i].dtype);
+        m->p = all_[i].made.data_ptr();
+      }
   }
   PyObject *tuple(fp8q_status st) {
     if (st != FP8Q_OK) return PyLong_FromLong(st);
-    PyObject *t = PyTuple_New(n);
-    if (!t) return nullptr;
-    for (int i = 0; i < n; ++i) PyTuple_SET_ITEM(t, i, o[i]);
-    n = 0;
+    PyObject *t = PyTuple_New(n_);
+    for (int i = 0; t && i < n_; ++i) {
+      PyObject *o = all_[i].wanted ? THPVariable_Wrap(std::move(all_[i].made))
+                                   : Py_NewRef(all_[i].given ? all_[i].given : Py_None);
+      if (o) PyTuple_SET_ITEM(t, i, o);
+      else Py_CLEAR(t);
+    }
     return t;
   }
+
+ private:
+  struct One {
+    PyObject *given = nullptr;
+    Mat *wanted = nullptr;  // of the new one
+    int64_t rows = 0;
+    at::ScalarType dtype = at::kByte;
+    at::Tensor made;
+  };
+  One all_[8];
+  int n_ = 0;
 };
 
 // Flags by their truth, as Python takes them (1, a numpy bool, ...).
@@ -231,22 +251,26 @@ PyObject *swiglu_impl(PyObject *const *v, Py_ssize_t n) {
   Results r;
   Mat h, gu, q, s;
   bool has_h, has_gu, has_q, has_s;
-  if (!r.add(v[10], want[0], M, F, at::kBFloat16, place, "h", h, has_h) ||
-      !r.add(v[11], want[1], M, 2 * F, at::kBFloat16, place, "gu", gu, has_gu) ||
-      !r.add(v[12], want[2], M, F, at::kByte, place, "q", q, has_q) ||
-      !r.add(v[13], has_q, F / 128, M, at::kFloat, place, "s", s, has_s))
+  if (!r.add(v[10], want[0], M, F, at::kBFloat16, "h", h, has_h) ||
+      !r.add(v[11], want[1], M, 2 * F, at::kBFloat16, "gu", gu, has_gu) ||
+      !r.add(v[12], want[2], M, F, at::kByte, "q", q, has_q) ||
+      !r.add(v[13], has_q, F / 128, M, at::kFloat, "s", s, has_s))
     return nullptr;
-  fp8q_status st;
-  float *fs = static_cast<float *>(s.p);
   const float *fsa = static_cast<const float *>(msa.p), *fsb = static_cast<const float *>(msb.p);
-  if (grouped)
-    st = (pow2 ? fp8q_grouped_gemm_swiglu_pow2 : fp8q_grouped_gemm_swiglu)(
-        ma.p, ma.ld, fsa, msa.ld, mb.p, mb.ld, fsb, offs, static_cast<int>(G), h.p, h.ld, gu.p,
-        gu.ld, q.p, q.ld, fs, s.ld, mode, M, F, K, place.handle);
-  else
-    st = (pow2 ? fp8q_gemm_swiglu_pow2 : fp8q_gemm_swiglu)(
-        ma.p, ma.ld, fsa, msa.ld, mb.p, mb.ld, fsb, msb.ld, h.p, h.ld, gu.p, gu.ld, q.p, q.ld, fs,
-        s.ld, mode, M, F, K, place.handle);
+  fp8q_status st;
+  {
+    NoGil free;
+    r.make(place);
+    float *fs = static_cast<float *>(s.p);
+    if (grouped)
+      st = (pow2 ? fp8q_grouped_gemm_swiglu_pow2 : fp8q_grouped_gemm_swiglu)(
+          ma.p, ma.ld, fsa, msa.ld, mb.p, mb.ld, fsb, offs, static_cast<int>(G), h.p, h.ld, gu.p,
+          gu.ld, q.p, q.ld, fs, s.ld, mode, M, F, K, place.handle);
+    else
+      st = (pow2 ? fp8q_gemm_swiglu_pow2 : fp8q_gemm_swiglu)(
+          ma.p, ma.ld, fsa, msa.ld, mb.p, mb.ld, fsb, msb.ld, h.p, h.ld, gu.p, gu.ld, q.p, q.ld,
+          fs, s.ld, mode, M, F, K, place.handle);
+  }
   return r.tuple(st);
 }
 
@@ -271,18 +295,24 @@ PyObject *bwd_impl(PyObject *const *v, Py_ssize_t n) {
   Results r;
   Mat d, q, s, qT, sT, hT, shT;
   bool has_d, has_q, has_qT, has_hT, has;
-  if (!r.add(v[7], want[0], T, N, at::kBFloat16, place, "d", d, has_d) ||
-      !r.add(v[8], want[1], T, N, at::kByte, place, "q", q, has_q) ||
-      !r.add(v[9], has_q, N / 128, T, at::kFloat, place, "s", s, has) ||
-      !r.add(v[10], want[2], N, T, at::kByte, place, "qT", qT, has_qT) ||
-      !r.add(v[11], has_qT, T / 128, N, at::kFloat, place, "sT", sT, has) ||
-      !r.add(v[12], want[3], F, T, at::kByte, place, "hT", hT, has_hT) ||
-      !r.add(v[13], has_hT, T / 128, F, at::kFloat, place, "shT", shT, has))
+  if (!r.add(v[7], want[0], T, N, at::kBFloat16, "d", d, has_d) ||
+      !r.add(v[8], want[1], T, N, at::kByte, "q", q, has_q) ||
+      !r.add(v[9], has_q, N / 128, T, at::kFloat, "s", s, has) ||
+      !r.add(v[10], want[2], N, T, at::kByte, "qT", qT, has_qT) ||
+      !r.add(v[11], has_qT, T / 128, N, at::kFloat, "sT", sT, has) ||
+      !r.add(v[12], want[3], F, T, at::kByte, "hT", hT, has_hT) ||
+      !r.add(v[13], has_hT, T / 128, F, at::kFloat, "shT", shT, has))
     return nullptr;
-  return r.tuple(fp8q_swiglu_bwd(mdh.p, mdh.ld, mgu.p, mgu.ld, d.p, d.ld, q.p, q.ld,
-                                 static_cast<float *>(s.p), s.ld, qT.p, qT.ld,
-                                 static_cast<float *>(sT.p), sT.ld, hT.p, hT.ld,
-                                 static_cast<float *>(shT.p), shT.ld, T, F, mode, place.handle));
+  fp8q_status st;
+  {
+    NoGil free;
+    r.make(place);
+    st = fp8q_swiglu_bwd(mdh.p, mdh.ld, mgu.p, mgu.ld, d.p, d.ld, q.p, q.ld,
+                         static_cast<float *>(s.p), s.ld, qT.p, qT.ld, static_cast<float *>(sT.p),
+                         sT.ld, hT.p, hT.ld, static_cast<float *>(shT.p), shT.ld, T, F, mode,
+                         place.handle);
+  }
+  return r.tuple(st);
 }
 
 // Row and matrix pitch of a matrix or a batch of matrices.
@@ -322,12 +352,7 @@ PyObject *newton_schulz_impl(PyObject *const *v, Py_ssize_t n) {
       return nullptr;
     }
     out = *t;
-  } else {
-    out = place.result(g->sizes(), od);
   }
-  int64_t ld_g, stride_g, ld_o, stride_o;
-  if (!pitches(*g, "g", ld_g, stride_g) || !pitches(out, "out", ld_o, stride_o)) return nullptr;
-  const int64_t B = g->dim() == 3 ? g->size(0) : 1, m = g->size(-2), nn = g->size(-1);
   at::Tensor ws;
   if (v[8] != Py_None) {
     const at::Tensor *t = tensor(v[8], "workspace");
@@ -337,17 +362,27 @@ PyObject *newton_schulz_impl(PyObject *const *v, Py_ssize_t n) {
       return nullptr;
     }
     ws = *t;
-  } else {
-    const int64_t bytes = fp8q_newton_schulz_workspace_bytes(B, m, nn);
-    ws = place.scratch(bytes > 0 ? bytes : 1);
   }
+  const int64_t B = g->dim() == 3 ? g->size(0) : 1, m = g->size(-2), nn = g->size(-1);
+  int64_t ld_g, stride_g, ld_o = nn, stride_o = m * nn;
+  if (!pitches(*g, "g", ld_g, stride_g) || (out.defined() && !pitches(out, "out", ld_o, stride_o)))
+    return nullptr;
   const bool any = g->numel() > 0;
-  const fp8q_status st = fp8q_newton_schulz(
-      any ? g->data_ptr() : nullptr, ld_g, stride_g,
-      g->scalar_type() == at::kFloat ? FP8Q_OUT_FP32 : FP8Q_OUT_BF16,
-      any ? out.data_ptr() : nullptr, ld_o, stride_o, out_dtype, B, m, nn, steps,
-      static_cast<float>(a), static_cast<float>(b), static_cast<float>(c), static_cast<float>(eps),
-      ws.data_ptr(), static_cast<int64_t>(ws.nbytes()), place.handle);
+  fp8q_status st;
+  {
+    NoGil free;
+    if (!out.defined()) out = place.result(g->sizes(), od);
+    if (!ws.defined()) {
+      const int64_t bytes = fp8q_newton_schulz_workspace_bytes(B, m, nn);
+      ws = place.scratch(bytes > 0 ? bytes : 1);
+    }
+    st = fp8q_newton_schulz(
+        any ? g->data_ptr() : nullptr, ld_g, stride_g,
+        g->scalar_type() == at::kFloat ? FP8Q_OUT_FP32 : FP8Q_OUT_BF16,
+        any ? out.data_ptr() : nullptr, ld_o, stride_o, out_dtype, B, m, nn, steps,
+        static_cast<float>(a), static_cast<float>(b), static_cast<float>(c),
+        static_cast<float>(eps), ws.data_ptr(), static_cast<int64_t>(ws.nbytes()), place.handle);
+  }
   if (st != FP8Q_OK) return PyLong_FromLong(st);
   if (v[7] != Py_None) {
     Py_INCREF(v[7]);

@@ -1,5 +1,8 @@
 """What the compiled marshalling of the gated feed-forward and Newton-Schulz calls does with its
 arguments, with the caller's streams, and with the interpreter."""
+import threading
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -173,3 +176,43 @@ def test_another_stream_inside_a_capture():
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------ interpreter
+def test_other_threads_run_while_a_call_waits():
+    # behind a kernel that sleeps, launches fill the queue until a call has to
+    # wait in the driver; Python threads go on meanwhile
+    dh, gu = torch.ones(128, 128).bfloat16().cuda(), torch.ones(128, 256).bfloat16().cuda()
+    d = torch.empty(128, 256).bfloat16().cuda()
+
+    def call():
+        fq.fp8q_swiglu_bwd(dh, gu, with_rows=False, with_cols=False, with_h=False, d=d)
+
+    call()
+    torch.cuda.synchronize()
+    stop, gaps = threading.Event(), [0.0]
+
+    def tick():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(1e-3)
+            now = time.perf_counter()
+            gaps[0] = max(gaps[0], now - last)
+            last = now
+
+    t = threading.Thread(target=tick)
+    t.start()
+    torch.cuda._sleep(2_000_000_000)  # about a second
+    held = 0.0
+    for _ in range(6000):
+        t0 = time.perf_counter()
+        call()
+        held = max(held, time.perf_counter() - t0)
+        if held > 0.2:
+            break
+    stop.set()
+    t.join()
+    torch.cuda.synchronize()
+    if held < 0.2:
+        pytest.skip(f"no call had to wait ({held:.3f} s at most)")
+    assert gaps[0] < held / 2, (gaps[0], held)
