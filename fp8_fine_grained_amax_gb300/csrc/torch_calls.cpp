@@ -47,21 +47,23 @@ const at::Tensor *tensor(PyObject *o, const char *name) {
 
 // Address and row pitch of a matrix whose shape and type must be as given; the
 // strides of one-long axes do not count.
-bool mat(const at::Tensor &t, int64_t rows, int64_t cols, at::ScalarType dtype, const char *name,
-         Mat &m) {
+bool mat(const at::Tensor &t, int64_t rows, int64_t cols, at::ScalarType dtype, at::Device dev,
+         const char *name, Mat &m) {
   if (t.scalar_type() != dtype || t.dim() != 2 || t.size(0) != rows || t.size(1) != cols)
     return fail(std::string(name) + " must be a " + c10::toString(dtype) + " tensor of shape (" +
                 std::to_string(rows) + ", " + std::to_string(cols) + ")");
   if (!t.is_cuda()) return fail(std::string(name) + " must be on a CUDA device");
+  if (t.device() != dev) return fail(std::string(name) + " must be on " + dev.str());
   if (cols > 1 && rows > 0 && t.stride(1) != 1)
     return fail(std::string(name) + " must have a contiguous last dimension");
   m.p = t.numel() ? t.data_ptr() : nullptr;
   m.ld = rows > 1 ? t.stride(0) : cols;
   return true;
 }
-bool mat(PyObject *o, int64_t rows, int64_t cols, at::ScalarType dtype, const char *name, Mat &m) {
+bool mat(PyObject *o, int64_t rows, int64_t cols, at::ScalarType dtype, at::Device dev,
+         const char *name, Mat &m) {
   const at::Tensor *t = tensor(o, name);
-  return t && mat(*t, rows, cols, dtype, name, m);
+  return t && mat(*t, rows, cols, dtype, dev, name, m);
 }
 
 // Where a call runs, and where the memory that it takes for itself comes from:
@@ -73,14 +75,15 @@ class Place {
   // torch's current stream, or the given stream's handle.
   bool set(PyObject *stream, at::Device device) {
     dev = device;
+    on_device_.emplace(device);  // the library launches on the device that is current
     const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(dev.index());
     handle = current.stream();
     if (stream == Py_None) return true;
     handle = PyLong_AsVoidPtr(stream);
     if (handle == nullptr && PyErr_Occurred()) return false;
     if (handle != current.stream()) {
-      other = c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), dev.index());
-      reader = current;
+      other_ = c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), dev.index());
+      reader_ = current;
     }
     return true;
   }
@@ -90,8 +93,8 @@ class Place {
   // stream waits for the other one) and drop it there.
   at::Tensor result(at::IntArrayRef size, at::ScalarType dtype) const {
     at::Tensor t = take(size, dtype);
-    if (reader && t.nbytes() > 0)
-      c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *reader);
+    if (reader_ && t.nbytes() > 0)
+      c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *reader_);
     return t;
   }
 
@@ -101,10 +104,11 @@ class Place {
  private:
   at::Tensor take(at::IntArrayRef size, at::ScalarType dtype) const {
     std::optional<c10::cuda::CUDAStreamGuard> on;
-    if (other) on.emplace(*other);
+    if (other_) on.emplace(*other_);
     return at::Tensor(at::detail::empty_cuda(size, dtype, dev, c10::nullopt));
   }
-  std::optional<c10::cuda::CUDAStream> other, reader;  // set where they differ
+  std::optional<c10::cuda::CUDAGuard> on_device_;
+  std::optional<c10::cuda::CUDAStream> other_, reader_;  // set where they differ
 };
 
 // The interpreter's other threads run while this lives: an allocation may wait
@@ -118,12 +122,12 @@ struct NoGil {
 class Results {
  public:
   bool add(PyObject *given, bool wanted, int64_t rows, int64_t cols, at::ScalarType dtype,
-           const char *name, Mat &m, bool &present) {
+           at::Device dev, const char *name, Mat &m, bool &present) {
     One &r = all_[n_++];
     present = wanted || given != Py_None;
     if (given != Py_None) {
       r.given = given;
-      return mat(given, rows, cols, dtype, name, m);
+      return mat(given, rows, cols, dtype, dev, name, m);
     }
     if (wanted) {
       m.ld = cols;
@@ -209,7 +213,7 @@ PyObject *swiglu_impl(PyObject *const *v, Py_ssize_t n) {
   }
   const at::Device dev = a->device();
   Mat ma, msa, mb, msb;
-  if (!mat(*a, M, K, at::kByte, "a", ma) || !mat(v[2], K / 128, M, at::kFloat, "sa", msa))
+  if (!mat(*a, M, K, at::kByte, dev, "a", ma) || !mat(v[2], K / 128, M, at::kFloat, dev, "sa", msa))
     return nullptr;
   const int32_t *offs = nullptr;
   int64_t G = 1;
@@ -232,16 +236,16 @@ PyObject *swiglu_impl(PyObject *const *v, Py_ssize_t n) {
       fail("offs must be a contiguous int32 [G+1] tensor");
       return nullptr;
     }
-    if (!b->is_cuda() || !sb->is_cuda() || !to->is_cuda()) {
-      fail("b, sb and offs must be on a CUDA device");
+    if (b->device() != dev || sb->device() != dev || to->device() != dev) {
+      fail("b, sb and offs must be on a's CUDA device");
       return nullptr;
     }
     mb.p = b->numel() ? b->data_ptr() : nullptr;
     mb.ld = b->stride(1);
     msb.p = sb->numel() ? sb->data_ptr() : nullptr;
     offs = to->data_ptr<int32_t>();
-  } else if (!mat(*b, N, K, at::kByte, "b", mb) ||
-             !mat(*sb, N / 128, K / 128, at::kFloat, "sb", msb)) {
+  } else if (!mat(*b, N, K, at::kByte, dev, "b", mb) ||
+             !mat(*sb, N / 128, K / 128, at::kFloat, dev, "sb", msb)) {
     return nullptr;
   }
   int mode = 0;
@@ -251,10 +255,10 @@ PyObject *swiglu_impl(PyObject *const *v, Py_ssize_t n) {
   Results r;
   Mat h, gu, q, s;
   bool has_h, has_gu, has_q, has_s;
-  if (!r.add(v[10], want[0], M, F, at::kBFloat16, "h", h, has_h) ||
-      !r.add(v[11], want[1], M, 2 * F, at::kBFloat16, "gu", gu, has_gu) ||
-      !r.add(v[12], want[2], M, F, at::kByte, "q", q, has_q) ||
-      !r.add(v[13], has_q, F / 128, M, at::kFloat, "s", s, has_s))
+  if (!r.add(v[10], want[0], M, F, at::kBFloat16, dev, "h", h, has_h) ||
+      !r.add(v[11], want[1], M, 2 * F, at::kBFloat16, dev, "gu", gu, has_gu) ||
+      !r.add(v[12], want[2], M, F, at::kByte, dev, "q", q, has_q) ||
+      !r.add(v[13], has_q, F / 128, M, at::kFloat, dev, "s", s, has_s))
     return nullptr;
   const float *fsa = static_cast<const float *>(msa.p), *fsb = static_cast<const float *>(msb.p);
   fp8q_status st;
@@ -286,7 +290,7 @@ PyObject *bwd_impl(PyObject *const *v, Py_ssize_t n) {
   const int64_t T = dh->size(0), F = dh->size(1), N = 2 * F;
   const at::Device dev = dh->device();
   Mat mdh, mgu;
-  if (!mat(*dh, T, F, at::kBFloat16, "dh", mdh) || !mat(v[1], T, N, at::kBFloat16, "gu", mgu))
+  if (!mat(*dh, T, F, at::kBFloat16, dev, "dh", mdh) || !mat(v[1], T, N, at::kBFloat16, dev, "gu", mgu))
     return nullptr;
   int mode = 0;
   Place place;
@@ -295,13 +299,13 @@ PyObject *bwd_impl(PyObject *const *v, Py_ssize_t n) {
   Results r;
   Mat d, q, s, qT, sT, hT, shT;
   bool has_d, has_q, has_qT, has_hT, has;
-  if (!r.add(v[7], want[0], T, N, at::kBFloat16, "d", d, has_d) ||
-      !r.add(v[8], want[1], T, N, at::kByte, "q", q, has_q) ||
-      !r.add(v[9], has_q, N / 128, T, at::kFloat, "s", s, has) ||
-      !r.add(v[10], want[2], N, T, at::kByte, "qT", qT, has_qT) ||
-      !r.add(v[11], has_qT, T / 128, N, at::kFloat, "sT", sT, has) ||
-      !r.add(v[12], want[3], F, T, at::kByte, "hT", hT, has_hT) ||
-      !r.add(v[13], has_hT, T / 128, F, at::kFloat, "shT", shT, has))
+  if (!r.add(v[7], want[0], T, N, at::kBFloat16, dev, "d", d, has_d) ||
+      !r.add(v[8], want[1], T, N, at::kByte, dev, "q", q, has_q) ||
+      !r.add(v[9], has_q, N / 128, T, at::kFloat, dev, "s", s, has) ||
+      !r.add(v[10], want[2], N, T, at::kByte, dev, "qT", qT, has_qT) ||
+      !r.add(v[11], has_qT, T / 128, N, at::kFloat, dev, "sT", sT, has) ||
+      !r.add(v[12], want[3], F, T, at::kByte, dev, "hT", hT, has_hT) ||
+      !r.add(v[13], has_hT, T / 128, F, at::kFloat, dev, "shT", shT, has))
     return nullptr;
   fp8q_status st;
   {
@@ -347,8 +351,8 @@ PyObject *newton_schulz_impl(PyObject *const *v, Py_ssize_t n) {
   if (v[7] != Py_None) {
     const at::Tensor *t = tensor(v[7], "out");
     if (!t) return nullptr;
-    if (t->sizes() != g->sizes() || t->scalar_type() != od || !t->is_cuda()) {
-      fail("out must have g's shape and the type out_dtype names, on a CUDA device");
+    if (t->sizes() != g->sizes() || t->scalar_type() != od || t->device() != dev) {
+      fail("out must have g's shape and the type out_dtype names, on g's CUDA device");
       return nullptr;
     }
     out = *t;
@@ -357,8 +361,8 @@ PyObject *newton_schulz_impl(PyObject *const *v, Py_ssize_t n) {
   if (v[8] != Py_None) {
     const at::Tensor *t = tensor(v[8], "workspace");
     if (!t) return nullptr;
-    if (!t->is_cuda() || !t->is_contiguous()) {
-      fail("workspace must be a contiguous tensor on a CUDA device");
+    if (t->device() != dev || !t->is_contiguous()) {
+      fail("workspace must be a contiguous tensor on g's CUDA device");
       return nullptr;
     }
     ws = *t;

@@ -74,6 +74,29 @@ def test_out_of_memory_is_torchs_own_error():
     assert torch.equal(fq.fp8q_newton_schulz(g[0]), torch.zeros_like(g[0]))
 
 
+def test_every_operand_is_on_the_first_ones_device():
+    # with one card, host memory is the only other place
+    a, sa, b, sb = gated_operands()
+    b3, sb3 = b[None], sb[None]
+    offs = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    dh, gu = torch.ones(128, 128).bfloat16().cuda(), torch.ones(128, 256).bfloat16().cuda()
+    g = torch.ones(8, 16).cuda()
+    ws = torch.empty(fq.fp8q_newton_schulz_workspace_bytes(1, 8, 16), dtype=torch.uint8)
+    for call in (lambda: fq.fp8q_gemm_swiglu(a, sa.cpu(), b, sb), lambda: fq.fp8q_gemm_swiglu(a, sa, b.cpu(), sb),
+                 lambda: fq.fp8q_gemm_swiglu(a, sa, b, sb.cpu()),
+                 lambda: fq.fp8q_gemm_swiglu(a, sa, b, sb, h=torch.empty(5, 128).bfloat16()),
+                 lambda: fq.fp8q_grouped_gemm_swiglu(a, sa, b3.cpu(), sb3, offs),
+                 lambda: fq.fp8q_grouped_gemm_swiglu(a, sa, b3, sb3.cpu(), offs),
+                 lambda: fq.fp8q_grouped_gemm_swiglu(a, sa, b3, sb3, offs.cpu()),
+                 lambda: fq.fp8q_swiglu_bwd(dh, gu.cpu()),
+                 lambda: fq.fp8q_swiglu_bwd(dh, gu, q=torch.empty(128, 256, dtype=torch.uint8)),
+                 lambda: fq.fp8q_newton_schulz(g, out=torch.empty(8, 16).bfloat16()),
+                 lambda: fq.fp8q_newton_schulz(g, workspace=ws)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    assert fq.fp8q_grouped_gemm_swiglu(a, sa, b3, sb3, offs).h.shape == (5, 128)
+
+
 # ------------------------------------------------------------------ streams
 def home_of(t):
     """Handle of the stream that a tensor's memory was taken on."""
