@@ -150,7 +150,12 @@ __device__ __forceinline__ float ns_scale(const float *part, int parts, float ep
     float v = 0.0f;
     for (int i = threadIdx.x; i < parts; i += 32) v += part[blockIdx.z * kMaxParts + i];
     v = warp_sum(v);
-    if (threadIdx.x == 0) *shared = kS / (sqrtf(v) + eps);
+    if (threadIdx.x == 0) {
+      // below 2^-119 only where v is 0: the quotient would overflow, and 0 * inf is
+      // no zero.  (eps = 0 and a zero matrix: 0 / 0, as the formula has it.)
+      const float norm = sqrtf(v) + eps;
+      *shared = norm > 0.0f && norm < 0x1p-119f ? 0x1p127f : kS / norm;
+    }
   }
   __syncthreads();
   return *shared;
