@@ -18,6 +18,7 @@ import os
 import re
 import shutil
 import subprocess
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,7 +27,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfp8q.so")
 # The argument marshalling of the newer calls as a CPython module (linked
-# against the library and torch).
+# against the library and torch).  The other calls need neither it nor torch's
+# headers: where it does not build, the library still does.
 EXT = os.path.join(PKG, "_torch_calls.so")
 EXT_SOURCE = "torch_calls.cpp"
 SOURCES = ["gemm.cu", "gemm_mx.cu", "quant.cu", "swiglu.cu", "newton_schulz.cu", "api.cu"]
@@ -40,18 +42,18 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found (set NVCC or put CUDA's bin on PATH)")
 
 
-def _inputs():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "fp8q.h"))
-    files.append(os.path.abspath(__file__))
-    return files
+def _current(target: str, inputs) -> bool:
+    """Whether `target` is there and no older than what it is made from."""
+    files = [*inputs, os.path.join(INCLUDE, "fp8q.h"), os.path.abspath(__file__)]
+    return os.path.exists(target) and all(os.path.getmtime(f) <= os.path.getmtime(target) for f in files)
 
 
-def _up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(EXT)):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+def _lib_current() -> bool:
+    return _current(LIB, [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != EXT_SOURCE])
+
+
+def _ext_current() -> bool:
+    return _current(EXT, [os.path.join(CSRC, EXT_SOURCE)])
 
 
 def _compile(src: str) -> tuple[str, str]:
@@ -121,13 +123,28 @@ def check_gemm_registers(ptxas_log: str, expected: int, kernel: str = "fp8q_gemm
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
-    """Compile (if stale) and return the path of libfp8q.so."""
-    if not force and _up_to_date():
+    """Compile what is stale and return the path of libfp8q.so.  A marshalling
+    module that does not build is a warning; its calls raise when they are used."""
+    stale_lib, stale_ext = force or not _lib_current(), force or not _ext_current()
+    if not (stale_lib or stale_ext):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        ext = ex.submit(_compile_ext)
-        results = dict(zip(SOURCES, ex.map(_compile, SOURCES)))
+        ext = ex.submit(_compile_ext) if stale_ext else None
+        if stale_lib:
+            _link_library(dict(zip(SOURCES, ex.map(_compile, SOURCES))), verbose)
+    if ext is not None:
+        try:
+            _link_ext(ext.result())
+        except Exception as e:
+            if os.path.exists(EXT):
+                os.remove(EXT)  # made from other sources
+            warnings.warn(f"the marshalling module was not built: {e}", RuntimeWarning, stacklevel=2)
+    return LIB
+
+
+def _link_library(results, verbose: bool) -> None:
+    """libfp8q.so from each source's object file and ptxas report."""
     check_gemm_registers(results["gemm.cu"][1], launch_regs_of(os.path.join(CSRC, "gemm.cu")))
     check_gemm_registers(results["gemm_mx.cu"][1], launch_regs_of(os.path.join(CSRC, "gemm_mx.cu")),
                          "fp8q_gemm_mx_kernel")
@@ -137,13 +154,12 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         for src, (_, log) in results.items():
             print(f"== {src}\n{log}")
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-shared", "-Xlinker", "-soname=libfp8q.so", "-o", tmp, *[results[s][0] for s in SOURCES]]
+    cmd = [nvcc(), *ARCH, "-shared", "-Xlinker", "-soname=libfp8q.so", "-o", tmp,
+           *[results[s][0] for s in SOURCES]]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_ext(ext.result())
-    return LIB
 
 
 if __name__ == "__main__":
