@@ -18,6 +18,7 @@ import os
 import re
 import shutil
 import subprocess
+import sys
 import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -31,6 +32,7 @@ LIB = os.path.join(PKG, "libfp8q.so")
 # headers: where it does not build, the library still does.
 EXT = os.path.join(PKG, "_torch_calls.so")
 EXT_SOURCE = "torch_calls.cpp"
+EXT_MADE_FOR = os.path.join(BUILD, "torch_calls.made_for")  # the torch and the interpreter that EXT is linked against
 SOURCES = ["gemm.cu", "gemm_mx.cu", "quant.cu", "swiglu.cu", "newton_schulz.cu", "api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -52,8 +54,16 @@ def _lib_current() -> bool:
     return _current(LIB, [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != EXT_SOURCE])
 
 
+def _made_for() -> str:
+    import torch
+    return f"torch {torch.__version__} in {os.path.dirname(torch.__file__)}, python {sys.version}"
+
+
 def _ext_current() -> bool:
-    return _current(EXT, [os.path.join(CSRC, EXT_SOURCE)])
+    if not _current(EXT, [os.path.join(CSRC, EXT_SOURCE)]) or not os.path.exists(EXT_MADE_FOR):
+        return False
+    with open(EXT_MADE_FOR) as f:
+        return f.read() == _made_for()
 
 
 def _compile(src: str) -> tuple[str, str]:
@@ -95,6 +105,8 @@ def _link_ext(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link of {EXT_SOURCE} failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, EXT)
+    with open(EXT_MADE_FOR, "w") as f:
+        f.write(_made_for())
 
 
 def launch_regs_of(gemm_src: str) -> int:
@@ -138,7 +150,7 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
             _link_ext(ext.result())
         except Exception as e:
             if os.path.exists(EXT):
-                os.remove(EXT)  # made from other sources
+                os.remove(EXT)  # made from other sources or for another torch
             warnings.warn(f"the marshalling module was not built: {e}", RuntimeWarning, stacklevel=2)
     return LIB
 

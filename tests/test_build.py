@@ -3,6 +3,7 @@ import os
 import shutil
 
 import pytest
+import torch
 
 from fp8_fine_grained_amax_gb300 import build
 
@@ -47,3 +48,9 @@ def test_an_older_module_does_not_stay_where_the_new_one_fails(built, monkeypatc
     with pytest.warns(RuntimeWarning):
         build.build_library()
     assert not os.path.exists(build.EXT)
+
+
+def test_the_module_is_rebuilt_for_another_torch(built, monkeypatch):
+    monkeypatch.setattr(torch, "__version__", "0.0.0+other")
+    build.build_library()
+    assert built == ["module", "link"]
