@@ -168,6 +168,8 @@ constexpr int kGluStages = 4;
 constexpr size_t kGluStageBytes = kEpiWarps * 8192;
 struct NoMaps {};
 constexpr size_t kSmemBytes = 1024 + kRingBytes + kStageBytes + sizeof(MxCtl);
+constexpr size_t kGluSmemBytes =
+    1024 + kGluStages * (kABytes + kBBytes) + kGluStageBytes + sizeof(GluMxCtl);
 
 __device__ __forceinline__ void mbar_wait_drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = global_timer_ns();
@@ -838,8 +840,8 @@ fp8q_status launch_mx(const CUtensorMap &ta, const CUtensorMap &tb,
                       const std::conditional_t<kGlu, GluMaps, NoMaps> &maps = {}) {
   auto kern = fp8q_gemm_mx_kernel<kBScale, kOutF32, kAccum, kGrouped, kGlu>;
   constexpr size_t smem =
-      (kGlu ? 1024 + kGluStages * (kABytes + kBBytes) + kGluStageBytes + sizeof(GluMxCtl) : kSmemBytes) +
-      (kGrouped ? kGroupTables : 0) + (kBScale == FP8Q_BSCALE_ROW && !kGrouped ? kPrepBytes : 0);
+      (kGlu ? kGluSmemBytes : kSmemBytes) + (kGrouped ? kGroupTables : 0) +
+      (kBScale == FP8Q_BSCALE_ROW && !kGrouped ? kPrepBytes : 0);
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
   static int max_pairs[kMaxDevices] = {};
   static std::mutex mu;
@@ -969,7 +971,7 @@ fp8q_status gemm_mx_glu(const GluIn &in, const GluOut &out, cudaStream_t s) {
   const bool grouped = in.offs != nullptr;
   DeviceInfo dev;
   if (fp8q_status st = device_info(dev)) return st;
-  if (dev.max_smem_optin < static_cast<int>(kSmemBytes + (grouped ? kGroupTables : 0)))
+  if (dev.max_smem_optin < static_cast<int>(kGluSmemBytes + (grouped ? kGroupTables : 0)))
     return FP8Q_ERR_UNSUPPORTED;
   CUtensorMap ta, tb;
   if (!make_tmap_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, in.a, in.M, in.K, in.lda, 128, BM,
