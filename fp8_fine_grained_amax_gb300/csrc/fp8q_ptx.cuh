@@ -192,9 +192,8 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
 // segments instead of 32 scattered pieces, with an L2 evict-first hint.  The
 // block starts at (row0, col0); rows >= row_end and columns >= n are left
 // alone.  kEsz: element size (2 or 4); kAccum (FP32 only): C += values, one
-// FP32 addition per element; kOnce: nothing reads the block back soon (the
-// evict-first hint).
-template <int kEsz, bool kAccum, bool kOnce = true>
+// FP32 addition per element.
+template <int kEsz, bool kAccum>
 __device__ __forceinline__ void warp_store_block64(uint32_t buf, const uint4 (&u)[4], void *c,
                                                    int64_t ldc, int row0, int row_end, int col0,
                                                    int n, int lane) {
@@ -221,8 +220,7 @@ __device__ __forceinline__ void warp_store_block64(uint32_t buf, const uint4 (&u
         v.z = __float_as_uint(__fadd_rn(old.z, __uint_as_float(v.z)));
         v.w = __float_as_uint(__fadd_rn(old.w, __uint_as_float(v.w)));
       }
-      if (kOnce) st_global_v4_hint(dst, v, l2_evict_first_policy());
-      else *reinterpret_cast<uint4 *>(dst) = v;
+      st_global_v4_hint(dst, v, l2_evict_first_policy());
     } else {
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
       for (int e = 0; e < kUnitCols && col + e < n; ++e) {
