@@ -90,8 +90,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // Sum of squares of matrix blockIdx.y, part blockIdx.x of gridDim.x; a warp
 // takes pieces of a row (8 loads per lane with kVec false, 4 or 8 with kVec),
-// all of a piece's loads in flight.  kVec: rows begin on 16-byte boundaries.  The order is fixed, so repeated calls
-// agree.  Also zeroes the counters that the steps kernel of this call uses.
+// all of a piece's loads in flight.  kVec: rows begin on 16-byte boundaries.  The
+// order is fixed, so repeated calls agree.  Also zeroes the counters that the steps kernel of this call uses.
 template <bool kVec>
 constexpr int kPieceOf = kVec ? 1024 : 256;
 template <typename In, bool kVec>
@@ -1164,7 +1164,10 @@ int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 // K block of a 256-row tile measured 0.34 us at 256 columns (tensor cores), 0.2
 // at 128 and 0.14 at 64 (operand traffic); an epilogue about 1.5 us and 0.45 per 64
 // columns; handing split tiles over 9 us (every pair's 256 KB of partial sums go
-// through L2 at once).
+// through L2 at once).  With every SM reading operands at once (the Gram product of
+// a 2048 x 7168 update, about 14 TB/s from L2) a 128-wide block takes 0.27, not 0.2:
+// by that figure the estimate would be 33 us for its 128-wide tiles and 31 for an
+// even split of 256-wide ones; which of the two is faster has not been measured.
 struct Plan {
   int bn[3];
   int64_t tiles[3], per[3], pairs;

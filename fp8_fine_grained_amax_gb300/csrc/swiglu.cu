@@ -6,8 +6,9 @@
 //             h = silu(g) * u,  silu(g) = g s,  s = 1 / (1 + exp(-g))
 //   backward  du = dh g s,  dg = dh u s (1 + g (1 - s))
 //
-// The forward pass for more than kFewTokens tokens runs on the tensor-core
-// GEMMs of gemm.cu / gemm_mx.cu with the gated epilogue of fp8q_glu.cuh.
+// Larger forward passes (few_tokens() below has the rule) and all of experts run
+// on the tensor-core GEMMs of gemm.cu / gemm_mx.cu with the gated epilogue of
+// fp8q_glu.cuh.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -70,9 +71,10 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t local_addr, uint32_t ran
 // 1x128 group of h (two column halves).  S is the most, up to four, that keeps
 // every CTA resident at once (two per SM): all of them then stream until the
 // end, where a second wave would leave SMs idle.
-//   warp 0     TMA producer: weights and tokens per K-group into a ring that
-//              keeps 64 to 160 KB per SM on their way, which is what streaming
-//              at the memory's rate needs
+//   warp 0     TMA producer: weights and tokens per K-group into rings of 180,
+//              160 or 144 KB per SM (two CTAs; 16, 32, 64 tokens; 160, 128 or 96
+//              KB of it weights), so much on its way being what streaming at the
+//              memory's rate needs
 //   warp 1     MMA issuer: per K-group 4 x tcgen05.mma (M = 128, N tokens,
 //              K = 32) into one of four TMEM buffers
 //   warps 2-5  fold: each thread one weight row, acc += P * sa * sb in FP32,
@@ -530,9 +532,9 @@ GluOut glu_out(void *h, int64_t ldh, void *gu, int64_t ld_gu, void *q, int64_t l
 //    eight threads (each ends with one of the eight maxima), then one value per
 //    token and CTA to both CTAs by st.async, which completes on the receiver's
 //    mbarrier: a cluster barrier would make every step wait for all of its
-//    global stores (46 us against 36 at 8192 x 2048).  128x1 max-abs (dg, du, h, per column): each thread's four
-//    tokens go to shared memory, and one thread per column takes the maximum of
-//    the 32 token quads.
+//    global stores (46 us against 36 at 8192 x 2048).
+//  - 128x1 max-abs (dg, du, h, per column): each thread's four tokens go to shared
+//    memory, and one thread per column takes the maximum of the 32 token quads.
 //  - One thread per group turns a max-abs into its scale, so that the two IEEE
 //    divisions are done once per group.
 //  - The transposed codes pass through shared memory: a thread's 4 tokens of a
