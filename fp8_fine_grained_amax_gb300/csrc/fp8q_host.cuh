@@ -133,13 +133,11 @@ inline bool make_tmap_2d(CUtensorMap *m, CUtensorMapDataType type, const void *b
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Read (and clear) the quantisers' device status word; defined in quant.cu.
-fp8q_status quant_status_take(cudaStream_t s);
-// The same for the power-of-two (block-scaled MMA) GEMM; defined in gemm_mx.cu.
-fp8q_status mx_status_take(cudaStream_t s);
-// The same for the few-token gated feed-forward kernel; defined in swiglu.cu.
-fp8q_status glu_status_take(cudaStream_t s);
-// The same for the Newton-Schulz kernels; defined in newton_schulz.cu.
-fp8q_status ns_status_take(cudaStream_t s);
+// Address of a device status word on the current device (null on failure):
+// 0, or the fp8q_status of a failure since fp8q_sync_status() last took it.
+int *quant_status_word();  // quant.cu
+int *mx_status_word();     // gemm_mx.cu: power-of-two GEMM
+int *glu_status_word();    // swiglu.cu: few-token gated kernel and backward pass
+int *ns_status_word();     // newton_schulz.cu
 
 }  // namespace fp8q

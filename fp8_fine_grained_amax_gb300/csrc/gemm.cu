@@ -45,6 +45,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 #include <type_traits>
@@ -758,6 +759,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Every status word taken (read and cleared) in one go, for one copy to the host:
+// a blocking copy per word costs 9 us each.  Calls from several threads at once
+// use different slots.
+constexpr int kStatusWords = 5, kTakeSlots = 64;
+struct StatusWords {
+  int *w[kStatusWords];
+};
+__device__ int g_taken[kTakeSlots][kStatusWords];
+__global__ void take_status_kernel(const StatusWords words, unsigned slot) {
+  if (threadIdx.x < kStatusWords) g_taken[slot][threadIdx.x] = atomicExch(words.w[threadIdx.x], 0);
+}
+
 // One CTA waits on an mbarrier that nothing completes, with the same bounded
 // wait as the GEMM; it must give up and record FP8Q_ERR_TIMEOUT.
 __global__ void wait_timeout_probe_kernel(uint64_t timeout_ns) {
@@ -1083,20 +1096,25 @@ extern "C" fp8q_status fp8q_grouped_gemm(const void *a, int64_t lda, const float
 }
 
 extern "C" fp8q_status fp8q_sync_status(void *stream) {
+  static std::atomic<unsigned> calls{0};
   auto s = static_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(s) != cudaSuccess) return FP8Q_ERR_CUDA;
-  int v = 0;
-  if (cudaMemcpyFromSymbol(&v, g_status, sizeof(int)) != cudaSuccess) return FP8Q_ERR_CUDA;
-  if (v != 0) {
-    const int zero = 0;
-    if (cudaMemcpyToSymbol(g_status, &zero, sizeof(int)) != cudaSuccess) return FP8Q_ERR_CUDA;
-  }
-  const fp8q_status q = quant_status_take(s);
-  const fp8q_status x = mx_status_take(s);
-  const fp8q_status g = glu_status_take(s);
-  const fp8q_status n = ns_status_take(s);
-  if (v != 0) return static_cast<fp8q_status>(v);
-  return q != FP8Q_OK ? q : x != FP8Q_OK ? x : g != FP8Q_OK ? g : n;
+  void *own = nullptr;
+  if (cudaGetSymbolAddress(&own, g_status) != cudaSuccess) return FP8Q_ERR_CUDA;
+  const StatusWords words = {{static_cast<int *>(own), quant_status_word(), mx_status_word(),
+                              glu_status_word(), ns_status_word()}};
+  for (int *w : words.w)
+    if (!w) return FP8Q_ERR_CUDA;
+  const unsigned slot = calls.fetch_add(1) % kTakeSlots;
+  int v[kStatusWords] = {};
+  if (fp8q_status st = launch_on(take_status_kernel, dim3(1), dim3(32), 0, s, words, slot)) return st;
+  if (cudaMemcpyFromSymbolAsync(v, g_taken, sizeof v, slot * sizeof v, cudaMemcpyDeviceToHost, s) !=
+          cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return FP8Q_ERR_CUDA;
+  for (int w : v)
+    if (w != 0) return static_cast<fp8q_status>(w);
+  return FP8Q_OK;
 }
 
 extern "C" void fp8q_set_wait_timeout_ns(uint64_t ns) {

@@ -1004,15 +1004,9 @@ fp8q_status gemm_mx_glu(const GluIn &in, const GluOut &out, cudaStream_t s) {
              : launch_mx<FP8Q_BSCALE_BLOCK, false, false, false, true>(ta, tb, args, tiles, s, maps);
 }
 
-fp8q_status mx_status_take(cudaStream_t s) {
-  if (cudaStreamSynchronize(s) != cudaSuccess) return FP8Q_ERR_CUDA;
-  int v = 0;
-  if (cudaMemcpyFromSymbol(&v, g_mx_status, sizeof(int)) != cudaSuccess) return FP8Q_ERR_CUDA;
-  if (v != 0) {
-    const int zero = 0;
-    if (cudaMemcpyToSymbol(g_mx_status, &zero, sizeof(int)) != cudaSuccess) return FP8Q_ERR_CUDA;
-  }
-  return static_cast<fp8q_status>(v);
+int *mx_status_word() {
+  void *p = nullptr;
+  return cudaGetSymbolAddress(&p, g_mx_status) == cudaSuccess ? static_cast<int *>(p) : nullptr;
 }
 
 }  // namespace fp8q

@@ -38,17 +38,9 @@ namespace fp8q {
 // Device status word of these kernels (read by fp8q_sync_status).
 __device__ int g_ns_status;
 
-fp8q_status ns_status_take(cudaStream_t s) {
-  int v = 0;
-  if (cudaMemcpyFromSymbolAsync(&v, g_ns_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s) !=
-          cudaSuccess ||
-      cudaStreamSynchronize(s) != cudaSuccess)
-    return FP8Q_ERR_CUDA;
-  if (v != 0) {
-    const int zero = 0;
-    if (cudaMemcpyToSymbol(g_ns_status, &zero, sizeof(int)) != cudaSuccess) return FP8Q_ERR_CUDA;
-  }
-  return static_cast<fp8q_status>(v);
+int *ns_status_word() {
+  void *p = nullptr;
+  return cudaGetSymbolAddress(&p, g_ns_status) == cudaSuccess ? static_cast<int *>(p) : nullptr;
 }
 
 namespace {

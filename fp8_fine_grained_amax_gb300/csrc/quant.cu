@@ -35,17 +35,9 @@ namespace fp8q {
 // their bounded waits gave up (read and cleared by fp8q_sync_status()).
 __device__ int g_quant_status;
 
-fp8q_status quant_status_take(cudaStream_t s) {
-  int v = 0;
-  if (cudaMemcpyFromSymbolAsync(&v, g_quant_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s) !=
-          cudaSuccess ||
-      cudaStreamSynchronize(s) != cudaSuccess)
-    return FP8Q_ERR_CUDA;
-  if (v != 0) {
-    const int zero = 0;
-    if (cudaMemcpyToSymbol(g_quant_status, &zero, sizeof(int)) != cudaSuccess) return FP8Q_ERR_CUDA;
-  }
-  return static_cast<fp8q_status>(v);
+int *quant_status_word() {
+  void *p = nullptr;
+  return cudaGetSymbolAddress(&p, g_quant_status) == cudaSuccess ? static_cast<int *>(p) : nullptr;
 }
 
 namespace {
