@@ -75,7 +75,8 @@ class Place {
   // torch's current stream, or the given stream's handle.
   bool set(PyObject *stream, at::Device device) {
     dev = device;
-    on_device_.emplace(device);  // the library launches on the device that is current
+    // the library launches on the device that is current
+    if (c10::cuda::current_device() != dev.index()) on_device_.emplace(device);
     const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(dev.index());
     handle = current.stream();
     if (stream == Py_None) return true;
