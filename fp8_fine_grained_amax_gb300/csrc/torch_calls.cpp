@@ -2,9 +2,9 @@
 // Newton-Schulz bindings as a CPython module: tensors in, libfp8q's C ABI called
 // on torch's current stream, result tensors out.  No step of the computation is
 // here.  A small call takes longer to marshal than to run; looking at up to 18
-// tensors and making up to 8 new ones costs, on a Grace core, 2.5 us with the
-// results given (launch included) and 0.9 us more per new tensor, against 9 us
-// and 1.6 us per tensor from Python through ctypes.
+// tensors and making up to 8 new ones costs, on a Grace core, 3.0 to 3.5 us with
+// the results given (launch included) and 0.8 to 0.9 us more per new tensor,
+// against 9 us and 1.6 us per tensor from Python through ctypes.
 //
 // Every function takes positional arguments (binding.py gives them their names
 // and defaults) and returns the tuple of results, or the fp8q_status as an int

@@ -410,9 +410,11 @@ fp8q_status fp8q_newton_schulz(const void *g, int64_t ldg, int64_t g_stride, int
 fp8q_status fp8q_cast_e4m3(const float *x, int64_t n, void *q, void *stream);
 
 /*
- * Synchronise `stream`, then read and clear this device's status word.
+ * Synchronise `stream`, then read and clear this device's status words (one
+ * small kernel and one copy on `stream`, which must not be capturing).
  * Returns FP8Q_ERR_TIMEOUT if a kernel's bounded wait gave up since the last
- * call, FP8Q_ERR_CUDA if synchronisation failed, else FP8Q_OK.
+ * call, FP8Q_ERR_INVALID if a power-of-two call met another scale,
+ * FP8Q_ERR_CUDA if synchronisation failed, else FP8Q_OK.
  */
 fp8q_status fp8q_sync_status(void *stream);
 
