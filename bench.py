@@ -33,10 +33,12 @@ captured once as a CUDA graph and replayed (--no-graph launches it from the
 host instead), so that the device runs the kernels back to back rather than
 waiting on host launch overhead; the per-kernel times come from timing events
 between the kernels inside the graph.  The per-kernel times, the
-roofline of the dominant kernel, an end-to-end number through host buffers,
-the clocks sampled during the timed region, the error of the result against
-the CPU oracle, the CPU oracle's own throughput, and (one GPU) the same
-per-kernel measurement for every other workload are added.
+roofline of the dominant kernel, an end-to-end number through host buffers (the
+copies of the next step's inputs and the last one's result run beside the
+kernels, over two sets of device buffers), the clocks sampled during the timed
+region, the error of the result against the CPU oracle, the CPU oracle's own
+throughput, and (one GPU) every other workload's value, measured in the same
+way, are added; --details FILE keeps the other workloads' per-kernel tables.
 
   python bench.py [--gpus N] [--steps K] [--warmup W] [--workload NAME]
   python bench.py --impl reference ...   # the CPU oracle as the reference arm
@@ -1195,8 +1197,7 @@ def run_ours(args, rank, world, local):
                         peak_source=src),
         "e2e": {"value": round(whole_job_value(work, world, e2e_ms, scale), 2), "unit": wl.unit,
                 "h2d_bytes_per_step": bi, "d2h_bytes_per_step": bo,
-                "ms_per_step": round(e2e_ms, 4), "steps": e2e_steps,
-                "pipeline": "H2D(i+1) and D2H(i-1) overlap kernels(i); 2 device buffer sets"},
+                "ms_per_step": round(e2e_ms, 4), "steps": e2e_steps},
         "gpu_launches": len(ks) * args.steps * reps,
         "buffer_copies": len(copies),
         "clocks": clocks,
@@ -1214,11 +1215,21 @@ def run_ours(args, rank, world, local):
         for _, name in CONFIG_WORKLOADS:
             if name != wl.name:
                 others[name] = measure_other(name, dev, stream, args, clk, hbm, fp8_peak)
-        line["workloads"] = others
+        line["workloads"] = short_values(others)
+        if args.details:
+            with open(args.details, "w") as f:
+                json.dump(others, f, indent=1)
     clk.stop()
     if world > 1:
         dist.destroy_process_group()
     return line
+
+
+def short_values(others):
+    """Each workload's value alone, three digits or whole numbers: the line has to stay short enough
+    for whoever keeps only the last 3000 characters of the output.  --details keeps the rest."""
+    return {name: float(f"{r['value']:.3g}") if r["value"] < 100 else round(r["value"])
+            for name, r in others.items()}
 
 
 # ----------------------------------------------------------------- reference arm
@@ -1275,6 +1286,8 @@ def main():
                     help="also measure every other configuration's workloads (default: on for "
                          "the headline workload on one GPU)")
     ap.add_argument("--no-all-workloads", dest="all_workloads", action="store_false")
+    ap.add_argument("--details", metavar="FILE",
+                    help="write the other workloads' per-kernel tables, clocks and timing to FILE (JSON)")
     args = ap.parse_args()
     if args.warmup < 3:
         raise SystemExit("--warmup must be >= 3")
