@@ -1,8 +1,9 @@
 """Thin binding of libfp8q (include/fp8q.h), same names as the C ABI.
 
 Argument marshalling only: every step of the computation runs in the CUDA
-kernels of libfp8q.so.  The gated feed-forward and Newton-Schulz calls marshal
-in a compiled module (csrc/torch_calls.cpp), the others through ctypes.  Tensors are torch CUDA tensors (torch supplies device
+kernels of libfp8q.so.  The gated feed-forward, Newton-Schulz, norm, AdamW and
+router calls marshal in a compiled module (csrc/torch_calls.cpp), the others
+through ctypes.  Tensors are torch CUDA tensors (torch supplies device
 memory and the current stream); outputs that are not passed in are allocated
 with torch.  ``stream`` names another stream than the current one: the call, and
 the memory that it takes for results and scratch, are then that stream's, as
@@ -36,10 +37,15 @@ FP8Q_OUT_FP32 = 1
 FP8Q_BSCALE_BLOCK = 0
 FP8Q_BSCALE_BLOCK_T = 1
 FP8Q_BSCALE_ROW = 2
+FP8Q_STATE_BF16 = 0
+FP8Q_STATE_FP32 = 1
+FP8Q_STATE_E4M3 = 2
+FP8Q_SCORE_SOFTMAX = 0
+FP8Q_SCORE_SIGMOID = 1
 
 # name -> (restype, argtypes) for every entry point declared in include/fp8q.h
 _P, _I64, _INT, _U64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64
-_F32 = ctypes.c_float
+_F32, _F64 = ctypes.c_float, ctypes.c_double
 _GLU = [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _INT, _I64,
         _I64, _I64, _P]
 _GLU_GROUPED = [_P, _I64, _P, _I64, _P, _I64, _P, _P, _INT, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
@@ -74,6 +80,17 @@ SIGNATURES = {
     "fp8q_newton_schulz_workspace_bytes": (_I64, [_I64, _I64, _I64]),
     "fp8q_newton_schulz": (_INT, [_P, _I64, _I64, _INT, _P, _I64, _I64, _INT, _I64, _I64, _I64, _INT,
                                   _F32, _F32, _F32, _F32, _P, _I64, _P]),
+    "fp8q_rmsnorm": (_INT, [_P, _I64, _INT, _P, _I64, _INT, _P, _INT, _F32, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
+                            _P, _INT, _I64, _I64, _P]),
+    "fp8q_rmsnorm_bwd_workspace_bytes": (_I64, [_I64, _I64]),
+    "fp8q_rmsnorm_bwd": (_INT, [_P, _I64, _INT, _P, _I64, _INT, _P, _P, _INT, _P, _I64, _P, _I64, _INT, _P, _INT,
+                                _I64, _I64, _P, _I64, _P]),
+    "fp8q_adamw": (_INT, [_P, _I64, _INT, _INT, _INT, _F64, _F64, _F64, _F64, _F64, _I64, _P, _P, _P, _P]),
+    "fp8q_route_workspace_bytes": (_I64, [_I64, _I64]),
+    "fp8q_route": (_INT, [_P, _I64, _INT, _P, _INT, _INT, _F32, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64,
+                          _P, _I64, _P]),
+    "fp8q_route_bwd": (_INT, [_P, _I64, _INT, _P, _INT, _INT, _F32, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64,
+                              _P]),
     "fp8q_cast_e4m3": (_INT, [_P, _I64, _P, _P]),
     "fp8q_sync_status": (_INT, [_P]),
     "fp8q_set_wait_timeout_ns": (None, [_U64]),
@@ -458,6 +475,107 @@ def fp8q_newton_schulz(g, *, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7
     if type(r) is int:
         raise FP8QError(r, "fp8q_newton_schulz")
     return r
+
+
+class RmsNormOut(NamedTuple):
+    """Results of fp8q_rmsnorm; None where not asked for."""
+    r: Optional[torch.Tensor]     # [T][C] of the residual's type: x + residual
+    y: Optional[torch.Tensor]     # BF16 [T][C]
+    q: Optional[torch.Tensor]     # uint8 [T][C]: 1x128 codes of y
+    s: Optional[torch.Tensor]     # f32 [C/128][T]
+    rstd: Optional[torch.Tensor]  # f32 [T]
+
+
+class RmsNormGrads(NamedTuple):
+    """Results of fp8q_rmsnorm_bwd; None where not asked for."""
+    dx: Optional[torch.Tensor]  # [T][C]: the gradient of x and of the residual alike
+    dw: Optional[torch.Tensor]  # f32 [C]
+
+
+class Routes(NamedTuple):
+    """Results of fp8q_route."""
+    idx: torch.Tensor     # int32 [T][k]: experts by falling logit, -1 where none is left
+    weight: torch.Tensor  # f32 [T][k]
+    counts: torch.Tensor  # int32 [E]
+    offs: torch.Tensor    # int32 [E+1]: offsets of the grouped products
+    order: torch.Tensor   # int32 [T*k]: choice t * k + j of each row sorted by expert, -1 behind the last
+    slot: torch.Tensor    # int32 [T][k]: each choice's row in that order, -1 where none
+    tokens: torch.Tensor  # int32 [1]: tokens with a choice
+    loss: torch.Tensor    # f32 [1]: balance loss
+
+
+def fp8q_rmsnorm(x, w, *, residual=None, eps=1e-6, with_r=True, with_y=False, with_codes=True, with_rstd=False,
+                 scale_mode=FP8Q_SCALE_FP32, r=None, y=None, q=None, s=None, rstd=None, stream=None):
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * w for x [T][C] and residual (optional) BF16 or FP32,
+    w [C] -> RmsNormOut(r, y, q, s, rstd): h as the new residual stream (with_r, where a residual is given;
+    r=residual updates it in place), y in BF16 (with_y), y's 1x128 codes and scales (with_codes, C % 128 == 0)
+    and the rows' statistics for the backward pass (with_rstd)."""
+    out = (_torch_calls or _calls()).rmsnorm(x, w, residual, eps, with_r, with_y, with_codes, with_rstd, scale_mode,
+                                             r, y, q, s, rstd, _handle(stream))
+    if type(out) is int:
+        raise FP8QError(out, "fp8q_rmsnorm")
+    return tuple.__new__(RmsNormOut, out)
+
+
+def fp8q_rmsnorm_bwd_workspace_bytes(T: int, C: int) -> int:
+    return int(load_library().fp8q_rmsnorm_bwd_workspace_bytes(T, C))
+
+
+def fp8q_rmsnorm_bwd(dy, x, rstd, w, *, dres=None, with_dx=True, with_dw=True, out_dtype=FP8Q_OUT_BF16, dx=None,
+                     dw=None, accumulate=False, workspace=None, stream=None):
+    """Backward of fp8q_rmsnorm: dy [T][C], the normalised rows x [T][C] (the forward's r, or its x without a
+    residual), rstd f32 [T], w [C], and the residual stream's own gradient dres [T][C] (optional, of out_dtype)
+    -> RmsNormGrads(dx, dw).  accumulate adds to the dw that is given.  A workspace tensor is allocated with
+    torch when not given."""
+    out = (_torch_calls or _calls()).rmsnorm_bwd(dy, x, rstd, w, dres, with_dx, with_dw, out_dtype, dx, dw, accumulate,
+                                                 workspace, _handle(stream))
+    if type(out) is int:
+        raise FP8QError(out, "fp8q_rmsnorm_bwd")
+    return tuple.__new__(RmsNormGrads, out)
+
+
+def fp8q_adamw(params, grads, m, v, *, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, grad_scale=None,
+               m_scales=None, v_scales=None, copies=None, stream=None):
+    """One AdamW step, in place, over lists of contiguous tensors: params and grads FP32 or BF16, moments m and v
+    FP32, BF16, or uint8 codes of m and sqrt(v) with f32 scales [ceil(n/128)] in m_scales and v_scales (all zeros
+    before the first step); copies receive the new parameters in BF16.  step (an int from 1 on, or an int64 tensor)
+    and lr (a float or an f32 tensor) may be device tensors of one element, which a captured call then follows;
+    grad_scale (an f32 tensor of one element) multiplies the gradients."""
+    step_dev = step if isinstance(step, torch.Tensor) else None
+    lr_dev = lr if isinstance(lr, torch.Tensor) else None
+    st = (_torch_calls or _calls()).adamw(
+        params, grads, m, v, m_scales, v_scales, copies, 0.0 if lr_dev is not None else lr, betas[0], betas[1], eps,
+        weight_decay, 1 if step_dev is not None else step, lr_dev, step_dev, grad_scale, _handle(stream))
+    if st:
+        raise FP8QError(st, "fp8q_adamw")
+
+
+def fp8q_route_workspace_bytes(T: int, E: int) -> int:
+    return int(load_library().fp8q_route_workspace_bytes(T, E))
+
+
+def fp8q_route(logits, k, *, score=FP8Q_SCORE_SOFTMAX, normalise=True, scale=1.0, valid=None, idx=None, weight=None,
+               counts=None, offs=None, order=None, slot=None, tokens=None, loss=None, workspace=None, stream=None):
+    """Router of a mixture of experts: logits [T][E] BF16 or FP32 (-inf closes an expert to a token), valid (optional)
+    bool [T], False for padding -> Routes: the k largest logits' experts and weights, counts, the offsets and the
+    sorted order of the grouped products, and the balance loss.  A workspace tensor is allocated with torch when not
+    given."""
+    out = (_torch_calls or _calls()).route(logits, k, score, normalise, scale, valid, idx, weight, counts, offs, order,
+                                           slot, tokens, loss, workspace, _handle(stream))
+    if type(out) is int:
+        raise FP8QError(out, "fp8q_route")
+    return tuple.__new__(Routes, out)
+
+
+def fp8q_route_bwd(logits, idx, counts, tokens, *, dweight=None, dloss=None, score=FP8Q_SCORE_SOFTMAX, normalise=True,
+                   scale=1.0, valid=None, dlogits=None, stream=None):
+    """Backward of fp8q_route from the gradients of its weights (f32 [T][k]) and of its balance loss (f32, one
+    element), with its idx, counts and tokens -> dlogits [T][E] of the logits' type."""
+    out = (_torch_calls or _calls()).route_bwd(logits, idx, counts, tokens, dweight, dloss, score, normalise, scale,
+                                               valid, dlogits, _handle(stream))
+    if type(out) is int:
+        raise FP8QError(out, "fp8q_route_bwd")
+    return out[0]
 
 
 def fp8q_cast_e4m3(x, *, q=None, stream=None):

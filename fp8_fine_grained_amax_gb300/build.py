@@ -33,7 +33,8 @@ LIB = os.path.join(PKG, "libfp8q.so")
 EXT = os.path.join(PKG, "_torch_calls.so")
 EXT_SOURCE = "torch_calls.cpp"
 EXT_MADE_FOR = os.path.join(BUILD, "torch_calls.made_for")  # the torch and the interpreter that EXT is linked against
-SOURCES = ["gemm.cu", "gemm_mx.cu", "quant.cu", "swiglu.cu", "newton_schulz.cu", "api.cu"]
+SOURCES = ["gemm.cu", "gemm_mx.cu", "quant.cu", "swiglu.cu", "newton_schulz.cu", "norm.cu", "adamw.cu", "route.cu",
+           "api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

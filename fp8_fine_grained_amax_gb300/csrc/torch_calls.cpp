@@ -1,5 +1,5 @@
-// torch_calls.cpp -- the argument marshalling of the gated feed-forward and
-// Newton-Schulz bindings as a CPython module: tensors in, libfp8q's C ABI called
+// torch_calls.cpp -- the argument marshalling of the gated feed-forward,
+// Newton-Schulz, norm, AdamW and router bindings as a CPython module: tensors in, libfp8q's C ABI called
 // on torch's current stream, result tensors out.  No step of the computation is
 // here.  A small call takes longer to marshal than to run; looking at up to 18
 // tensors and making up to 8 new ones costs, on a Grace core, 3.0 to 3.5 us with
@@ -19,9 +19,11 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <climits>
 #include <optional>
 #include <string>
+#include <vector>
 
 #include "fp8q.h"
 
@@ -64,6 +66,39 @@ bool mat(PyObject *o, int64_t rows, int64_t cols, at::ScalarType dtype, at::Devi
          const char *name, Mat &m) {
   const at::Tensor *t = tensor(o, name);
   return t && mat(*t, rows, cols, dtype, dev, name, m);
+}
+
+// Address of a vector whose length and type must be as given.
+bool vec(const at::Tensor &t, int64_t n, at::ScalarType dtype, at::Device dev, const char *name,
+         void *&p) {
+  if (t.scalar_type() != dtype || t.dim() != 1 || t.size(0) != n || (n > 1 && t.stride(0) != 1))
+    return fail(std::string(name) + " must be a contiguous " + c10::toString(dtype) +
+                " tensor of shape (" + std::to_string(n) + ",)");
+  if (t.device() != dev || !t.is_cuda())
+    return fail(std::string(name) + " must be on " + (dev.is_cuda() ? dev.str() : "a CUDA device"));
+  p = n ? t.data_ptr() : nullptr;
+  return true;
+}
+
+// FP8Q_OUT_BF16 or FP8Q_OUT_FP32 for a tensor of either type.
+bool kind_of(const at::Tensor &t, const char *name, int &kind) {
+  if (t.scalar_type() != at::kBFloat16 && t.scalar_type() != at::kFloat)
+    return fail(std::string(name) + " must be BFloat16 or Float");
+  kind = t.scalar_type() == at::kFloat ? FP8Q_OUT_FP32 : FP8Q_OUT_BF16;
+  return true;
+}
+
+// One value in device memory (a tensor of one element), or null for None.
+bool scalar(PyObject *o, at::ScalarType dtype, at::Device dev, const char *name, const void *&p) {
+  p = nullptr;
+  if (o == Py_None) return true;
+  const at::Tensor *t = tensor(o, name);
+  if (!t) return false;
+  if (t->scalar_type() != dtype || t->numel() != 1 || t->device() != dev)
+    return fail(std::string(name) + " must be a " + c10::toString(dtype) + " tensor of one element on " +
+                dev.str());
+  p = t->data_ptr();
+  return true;
 }
 
 // Where a call runs, and where the memory that it takes for itself comes from:
@@ -138,12 +173,30 @@ class Results {
     }
     return true;
   }
+  // The same for a vector of n elements.
+  bool add_vec(PyObject *given, bool wanted, int64_t n, at::ScalarType dtype, at::Device dev,
+               const char *name, Mat &m) {
+    One &r = all_[n_++];
+    if (given != Py_None) {
+      r.given = given;
+      const at::Tensor *t = tensor(given, name);
+      return t && vec(*t, n, dtype, dev, name, m.p);
+    }
+    if (wanted) {
+      r.rows = n;
+      r.dtype = dtype;
+      r.vector = true;
+      r.wanted = &m;
+    }
+    return true;
+  }
   // Make the new ones (needs no GIL).
   void make(const Place &place) {
     for (int i = 0; i < n_; ++i)
       if (Mat *m = all_[i].wanted) {
-        all_[i].made = place.result({all_[i].rows, m->ld}, all_[i].dtype);
-        m->p = all_[i].made.data_ptr();
+        One &r = all_[i];
+        r.made = r.vector ? place.result({r.rows}, r.dtype) : place.result({r.rows, m->ld}, r.dtype);
+        m->p = r.made.data_ptr();
       }
   }
   PyObject *tuple(fp8q_status st) {
@@ -164,6 +217,7 @@ class Results {
     Mat *wanted = nullptr;  // of the new one
     int64_t rows = 0;
     at::ScalarType dtype = at::kByte;
+    bool vector = false;
     at::Tensor made;
   };
   One all_[8];
@@ -396,6 +450,363 @@ PyObject *newton_schulz_impl(PyObject *const *v, Py_ssize_t n) {
   return THPVariable_Wrap(std::move(out));
 }
 
+// A tensor argument of either type as rows x cols.
+bool mat_any(PyObject *o, int64_t rows, int64_t cols, at::Device dev, const char *name, Mat &m,
+             int &kind) {
+  const at::Tensor *t = tensor(o, name);
+  return t && kind_of(*t, name, kind) && mat(*t, rows, cols, t->scalar_type(), dev, name, m);
+}
+bool vec_any(PyObject *o, int64_t n, at::Device dev, const char *name, Mat &m, int &kind) {
+  const at::Tensor *t = tensor(o, name);
+  return t && kind_of(*t, name, kind) && vec(*t, n, t->scalar_type(), dev, name, m.p);
+}
+at::ScalarType type_of(int kind) { return kind == FP8Q_OUT_FP32 ? at::kFloat : at::kBFloat16; }
+
+// (x, w, residual, eps, with_r, with_y, with_codes, with_rstd, scale_mode, r, y, q, s, rstd, stream)
+PyObject *rmsnorm_impl(PyObject *const *v, Py_ssize_t n) {
+  if (n != 15) return wrong_count("rmsnorm");
+  const at::Tensor *x = tensor(v[0], "x");
+  if (!x) return nullptr;
+  if (x->dim() != 2) {
+    fail("x must be [T][C]");
+    return nullptr;
+  }
+  const int64_t T = x->size(0), C = x->size(1);
+  const at::Device dev = x->device();
+  Mat mx, mw, mres;
+  int kx = 0, kw = 0, kres = 0, mode = 0;
+  const bool has_res = v[2] != Py_None;
+  if (!mat_any(v[0], T, C, dev, "x", mx, kx) || !vec_any(v[1], C, dev, "w", mw, kw) ||
+      (has_res && !mat_any(v[2], T, C, dev, "residual", mres, kres)))
+    return nullptr;
+  const double eps = PyFloat_AsDouble(v[3]);
+  Place place;
+  bool want[4];  // r, y, codes, rstd
+  if (PyErr_Occurred() || !int_of(v[8], mode) || !flags(v + 4, want) || !place.set(v[14], dev))
+    return nullptr;
+  if (!has_res && v[9] != Py_None) {
+    fail("r is the sum with the residual: it needs one");
+    return nullptr;
+  }
+  Results out;
+  Mat r, y, q, s, rstd;
+  bool has_r, has_y, has_q, has_s;
+  if (!out.add(v[9], want[0] && has_res, T, C, type_of(kres), dev, "r", r, has_r) ||
+      !out.add(v[10], want[1], T, C, at::kBFloat16, dev, "y", y, has_y) ||
+      !out.add(v[11], want[2], T, C, at::kByte, dev, "q", q, has_q) ||
+      !out.add(v[12], has_q, C / 128, T, at::kFloat, dev, "s", s, has_s) ||
+      !out.add_vec(v[13], want[3], T, at::kFloat, dev, "rstd", rstd))
+    return nullptr;
+  fp8q_status st;
+  {
+    NoGil free;
+    out.make(place);
+    st = fp8q_rmsnorm(mx.p, mx.ld, kx, mres.p, mres.ld, kres, mw.p, kw, static_cast<float>(eps), r.p,
+                      r.ld, y.p, y.ld, q.p, q.ld, static_cast<float *>(s.p), s.ld,
+                      static_cast<float *>(rstd.p), mode, T, C, place.handle);
+  }
+  return out.tuple(st);
+}
+
+// (dy, x, rstd, w, dres, with_dx, with_dw, out_dtype, dx, dw, accumulate, workspace, stream)
+PyObject *rmsnorm_bwd_impl(PyObject *const *v, Py_ssize_t n) {
+  if (n != 13) return wrong_count("rmsnorm_bwd");
+  const at::Tensor *dy = tensor(v[0], "dy");
+  if (!dy) return nullptr;
+  if (dy->dim() != 2) {
+    fail("dy must be [T][C]");
+    return nullptr;
+  }
+  const int64_t T = dy->size(0), C = dy->size(1);
+  const at::Device dev = dy->device();
+  Mat mdy, mx, mrstd, mw, mdres;
+  int kdy = 0, kx = 0, kw = 0, kd = 0;
+  const at::Tensor *rstd = tensor(v[2], "rstd");
+  if (!rstd || !mat_any(v[0], T, C, dev, "dy", mdy, kdy) || !mat_any(v[1], T, C, dev, "x", mx, kx) ||
+      !vec(*rstd, T, at::kFloat, dev, "rstd", mrstd.p) || !vec_any(v[3], C, dev, "w", mw, kw) ||
+      !int_of(v[7], kd))
+    return nullptr;
+  const at::ScalarType od = type_of(kd);
+  if (v[4] != Py_None && !mat(v[4], T, C, od, dev, "dres", mdres)) return nullptr;
+  Place place;
+  bool want[2], accumulate[1];  // dx, dw
+  if (!flags(v + 5, want) || !flags(v + 10, accumulate) || !place.set(v[12], dev)) return nullptr;
+  if (accumulate[0] && v[9] == Py_None) {
+    fail("accumulate adds to the dw that is given");
+    return nullptr;
+  }
+  Results out;
+  Mat dx, dw;
+  bool has_dx;
+  if (!out.add(v[8], want[0], T, C, od, dev, "dx", dx, has_dx) ||
+      !out.add_vec(v[9], want[1], C, at::kFloat, dev, "dw", dw))
+    return nullptr;
+  at::Tensor ws;
+  if (v[11] != Py_None) {
+    const at::Tensor *t = tensor(v[11], "workspace");
+    if (!t) return nullptr;
+    if (t->device() != dev || !t->is_contiguous()) {
+      fail("workspace must be a contiguous tensor on dy's CUDA device");
+      return nullptr;
+    }
+    ws = *t;
+  }
+  fp8q_status st;
+  {
+    NoGil free;
+    out.make(place);
+    if (!ws.defined() && (want[1] || v[9] != Py_None))
+      ws = place.scratch(std::max<int64_t>(fp8q_rmsnorm_bwd_workspace_bytes(T, C), 1));
+    st = fp8q_rmsnorm_bwd(mdy.p, mdy.ld, kdy, mx.p, mx.ld, kx, static_cast<float *>(mrstd.p), mw.p, kw,
+                          mdres.p, mdres.ld, dx.p, dx.ld, kd, static_cast<float *>(dw.p),
+                          accumulate[0], T, C, ws.defined() ? ws.data_ptr() : nullptr,
+                          ws.defined() ? static_cast<int64_t>(ws.nbytes()) : 0, place.handle);
+  }
+  return out.tuple(st);
+}
+
+// A list or tuple of tensors.
+class List {
+ public:
+  ~List() { Py_XDECREF(items_); }
+  bool take(PyObject *o, const char *name) {
+    name_ = name;
+    items_ = PySequence_Fast(o, "");
+    if (!items_) {
+      PyErr_Format(PyExc_TypeError, "%s must be a list of tensors", name);
+      return false;
+    }
+    return true;
+  }
+  Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(items_); }
+  const at::Tensor *at(Py_ssize_t i) const { return tensor(PySequence_Fast_GET_ITEM(items_, i), name_); }
+
+ private:
+  PyObject *items_ = nullptr;
+  const char *name_ = "";
+};
+
+// Address of entry i of a list: as many values as its parameter has, dense.
+bool entry(const List &l, Py_ssize_t i, const char *name, int64_t count, at::ScalarType dtype,
+           at::Device dev, void *&p) {
+  const at::Tensor *t = l.at(i);
+  if (!t) return false;
+  if (t->scalar_type() != dtype || t->numel() != count || !t->is_contiguous() || t->device() != dev)
+    return fail(std::string(name) + "[" + std::to_string(i) + "] must be a contiguous " +
+                c10::toString(dtype) + " tensor of " + std::to_string(count) + " elements on " +
+                dev.str());
+  p = count ? t->data_ptr() : nullptr;
+  return true;
+}
+
+// (params, grads, m, v, m_scales, v_scales, copies, lr, beta1, beta2, eps, weight_decay, step,
+//  lr tensor, step tensor, grad_scale, stream)
+PyObject *adamw_impl(PyObject *const *v, Py_ssize_t n) {
+  if (n != 17) return wrong_count("adamw");
+  List params, grads, ms, vs, mscales, vscales, copies;
+  if (!params.take(v[0], "params") || !grads.take(v[1], "grads") || !ms.take(v[2], "m") ||
+      !vs.take(v[3], "v"))
+    return nullptr;
+  const Py_ssize_t count = params.size();
+  const bool has_scales = v[4] != Py_None, has_copies = v[6] != Py_None;
+  if (has_scales != (v[5] != Py_None)) {
+    fail("m_scales and v_scales go together");
+    return nullptr;
+  }
+  if ((has_scales && (!mscales.take(v[4], "m_scales") || !vscales.take(v[5], "v_scales"))) ||
+      (has_copies && !copies.take(v[6], "copies")))
+    return nullptr;
+  if (grads.size() != count || ms.size() != count || vs.size() != count ||
+      (has_scales && (mscales.size() != count || vscales.size() != count)) ||
+      (has_copies && copies.size() != count)) {
+    fail("the lists must be as long as params");
+    return nullptr;
+  }
+  double num[5];
+  for (int i = 0; i < 5; ++i) num[i] = PyFloat_AsDouble(v[7 + i]);
+  const long long step = PyLong_AsLongLong(v[12]);
+  if (PyErr_Occurred()) return nullptr;
+  if (count == 0) return PyLong_FromLong(FP8Q_OK);
+  const at::Tensor *p0 = params.at(0), *g0 = p0 ? grads.at(0) : nullptr, *m0 = g0 ? ms.at(0) : nullptr;
+  if (!m0) return nullptr;
+  int kp = 0, kg = 0, state = FP8Q_STATE_E4M3;
+  if (!kind_of(*p0, "params", kp) || !kind_of(*g0, "grads", kg)) return nullptr;
+  const bool codes = m0->scalar_type() == at::kByte;
+  if (!codes && !kind_of(*m0, "m", state)) return nullptr;
+  if (codes != has_scales) {
+    fail(codes ? "uint8 moments need m_scales and v_scales" : "only uint8 moments have scales");
+    return nullptr;
+  }
+  const at::Device dev = p0->device();
+  if (!dev.is_cuda()) {
+    fail("params must be on a CUDA device");
+    return nullptr;
+  }
+  const at::ScalarType tp = p0->scalar_type(), tg = g0->scalar_type(), tm = m0->scalar_type();
+  const void *lr_dev, *step_dev, *scale;
+  Place place;
+  if (!scalar(v[13], at::kFloat, dev, "lr", lr_dev) || !scalar(v[14], at::kLong, dev, "step", step_dev) ||
+      !scalar(v[15], at::kFloat, dev, "grad_scale", scale) || !place.set(v[16], dev))
+    return nullptr;
+  std::vector<fp8q_adamw_tensor> list(static_cast<size_t>(count));
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    fp8q_adamw_tensor &t = list[static_cast<size_t>(i)];
+    const at::Tensor *p = params.at(i);
+    if (!p) return nullptr;
+    t.n = p->numel();
+    const int64_t groups = (t.n + 127) / 128;
+    void *g = nullptr, *msc = nullptr, *vsc = nullptr;
+    t.copy = nullptr;
+    if (!entry(params, i, "params", t.n, tp, dev, t.p) || !entry(grads, i, "grads", t.n, tg, dev, g) ||
+        !entry(ms, i, "m", t.n, tm, dev, t.m) || !entry(vs, i, "v", t.n, tm, dev, t.v) ||
+        (codes && (!entry(mscales, i, "m_scales", groups, at::kFloat, dev, msc) ||
+                   !entry(vscales, i, "v_scales", groups, at::kFloat, dev, vsc))) ||
+        (has_copies && !entry(copies, i, "copies", t.n, at::kBFloat16, dev, t.copy)))
+      return nullptr;
+    t.g = g;
+    t.m_scale = static_cast<float *>(msc);
+    t.v_scale = static_cast<float *>(vsc);
+  }
+  fp8q_status st;
+  {
+    NoGil free;
+    st = fp8q_adamw(list.data(), count, kp, kg, state, num[0], num[1], num[2], num[3], num[4], step,
+                    static_cast<const float *>(lr_dev), static_cast<const int64_t *>(step_dev),
+                    static_cast<const float *>(scale), place.handle);
+  }
+  return PyLong_FromLong(st);
+}
+
+// The logits of a router and the tokens that count.
+bool router_in(PyObject *ol, PyObject *ovalid, Mat &l, int &kind, const uint8_t *&valid, int64_t &T,
+               int64_t &E, std::optional<at::Device> &dev) {
+  const at::Tensor *t = tensor(ol, "logits");
+  if (!t) return false;
+  if (t->dim() != 2) return fail("logits must be [T][E]");
+  T = t->size(0);
+  E = t->size(1);
+  dev = t->device();
+  if (!mat_any(ol, T, E, *dev, "logits", l, kind)) return false;
+  valid = nullptr;
+  if (ovalid == Py_None) return true;
+  const at::Tensor *m = tensor(ovalid, "valid");
+  if (!m) return false;
+  if (m->scalar_type() != at::kBool && m->scalar_type() != at::kByte)
+    return fail("valid must be a Bool or Byte tensor");
+  void *p = nullptr;
+  if (!vec(*m, T, m->scalar_type(), *dev, "valid", p)) return false;
+  valid = static_cast<const uint8_t *>(p);
+  return true;
+}
+
+// A result of T x k values without gaps.
+bool dense(const Mat &m, int64_t T, int64_t k, const char *name) {
+  return T <= 1 || m.ld == k || fail(std::string(name) + " must be contiguous");
+}
+
+// (logits, k, score, normalise, scale, valid, idx, weight, counts, offs, order, slot, tokens, loss,
+//  workspace, stream)
+PyObject *route_impl(PyObject *const *v, Py_ssize_t n) {
+  if (n != 16) return wrong_count("route");
+  Mat l;
+  int kind = 0, k = 0, score = 0;
+  const uint8_t *valid;
+  int64_t T, E;
+  std::optional<at::Device> at_dev;
+  if (!router_in(v[0], v[5], l, kind, valid, T, E, at_dev)) return nullptr;
+  const at::Device dev = *at_dev;
+  bool normalise[1];
+  if (!int_of(v[1], k) || !int_of(v[2], score) || !flags(v + 3, normalise)) return nullptr;
+  const double scale = PyFloat_AsDouble(v[4]);
+  Place place;
+  if (PyErr_Occurred() || !place.set(v[15], dev)) return nullptr;
+  if (E < 1 || E > 1024 || k < 1 || k > E || k > 32 || T > (int64_t{1} << 26))
+    return PyLong_FromLong(FP8Q_ERR_SHAPE);  // before results of such sizes are made
+  Results out;
+  Mat idx, weight, counts, offs, order, slot, tokens, loss;
+  bool has;
+  if (!out.add(v[6], true, T, k, at::kInt, dev, "idx", idx, has) ||
+      !out.add(v[7], true, T, k, at::kFloat, dev, "weight", weight, has) ||
+      !out.add_vec(v[8], true, E, at::kInt, dev, "counts", counts) ||
+      !out.add_vec(v[9], true, E + 1, at::kInt, dev, "offs", offs) ||
+      !out.add_vec(v[10], true, T * k, at::kInt, dev, "order", order) ||
+      !out.add(v[11], true, T, k, at::kInt, dev, "slot", slot, has) ||
+      !out.add_vec(v[12], true, 1, at::kInt, dev, "tokens", tokens) ||
+      !out.add_vec(v[13], true, 1, at::kFloat, dev, "loss", loss) || !dense(idx, T, k, "idx") ||
+      !dense(weight, T, k, "weight") || !dense(slot, T, k, "slot"))
+    return nullptr;
+  at::Tensor ws;
+  if (v[14] != Py_None) {
+    const at::Tensor *t = tensor(v[14], "workspace");
+    if (!t) return nullptr;
+    if (t->device() != dev || !t->is_contiguous()) {
+      fail("workspace must be a contiguous tensor on the logits' CUDA device");
+      return nullptr;
+    }
+    ws = *t;
+  }
+  fp8q_status st;
+  {
+    NoGil free;
+    out.make(place);
+    const int64_t need = fp8q_route_workspace_bytes(T, E);
+    if (!ws.defined() && need > 0) ws = place.scratch(need);
+    st = fp8q_route(l.p, l.ld, kind, valid, score, normalise[0], static_cast<float>(scale),
+                    static_cast<int32_t *>(idx.p), static_cast<float *>(weight.p),
+                    static_cast<int32_t *>(counts.p), static_cast<int32_t *>(offs.p),
+                    static_cast<int32_t *>(order.p), static_cast<int32_t *>(slot.p),
+                    static_cast<int32_t *>(tokens.p), static_cast<float *>(loss.p), T, E, k,
+                    ws.defined() ? ws.data_ptr() : nullptr,
+                    ws.defined() ? static_cast<int64_t>(ws.nbytes()) : 0, place.handle);
+  }
+  return out.tuple(st);
+}
+
+// (logits, idx, counts, tokens, dweight, dloss, score, normalise, scale, valid, dlogits, stream)
+PyObject *route_bwd_impl(PyObject *const *v, Py_ssize_t n) {
+  if (n != 12) return wrong_count("route_bwd");
+  Mat l, midx, mcounts, mtokens, mdw;
+  int kind = 0, score = 0;
+  const uint8_t *valid;
+  int64_t T, E;
+  std::optional<at::Device> at_dev;
+  if (!router_in(v[0], v[9], l, kind, valid, T, E, at_dev)) return nullptr;
+  const at::Device dev = *at_dev;
+  const at::Tensor *idx = tensor(v[1], "idx"), *counts = tensor(v[2], "counts"),
+                   *tokens = tensor(v[3], "tokens");
+  if (!idx || !counts || !tokens) return nullptr;
+  if (idx->dim() != 2) {
+    fail("idx must be [T][k]");
+    return nullptr;
+  }
+  const int64_t k = idx->size(1);
+  const void *dloss;
+  bool normalise[1];
+  if (!mat(*idx, T, k, at::kInt, dev, "idx", midx) || !dense(midx, T, k, "idx") ||
+      !vec(*counts, E, at::kInt, dev, "counts", mcounts.p) ||
+      !vec(*tokens, 1, at::kInt, dev, "tokens", mtokens.p) ||
+      (v[4] != Py_None && (!mat(v[4], T, k, at::kFloat, dev, "dweight", mdw) || !dense(mdw, T, k, "dweight"))) ||
+      !scalar(v[5], at::kFloat, dev, "dloss", dloss) || !int_of(v[6], score) || !flags(v + 7, normalise))
+    return nullptr;
+  const double scale = PyFloat_AsDouble(v[8]);
+  Place place;
+  if (PyErr_Occurred() || !place.set(v[11], dev)) return nullptr;
+  Results out;
+  Mat d;
+  bool has;
+  if (!out.add(v[10], true, T, E, type_of(kind), dev, "dlogits", d, has)) return nullptr;
+  fp8q_status st;
+  {
+    NoGil free;
+    out.make(place);
+    st = fp8q_route_bwd(l.p, l.ld, kind, valid, score, normalise[0], static_cast<float>(scale),
+                        static_cast<const int32_t *>(midx.p), static_cast<const int32_t *>(mcounts.p),
+                        static_cast<const int32_t *>(mtokens.p), static_cast<const float *>(mdw.p),
+                        static_cast<const float *>(dloss), d.p, d.ld, T, E, k, place.handle);
+  }
+  return out.tuple(st);
+}
+
 // No C++ exception (an allocation that fails, say) leaves through CPython.
 template <PyObject *(*kImpl)(PyObject *const *, Py_ssize_t)>
 PyObject *guarded(PyObject *, PyObject *const *v, Py_ssize_t n) {
@@ -420,6 +831,18 @@ PyMethodDef methods[] = {
      METH_FASTCALL, nullptr},
     {"newton_schulz",
      reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<newton_schulz_impl>)),
+     METH_FASTCALL, nullptr},
+    {"rmsnorm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<rmsnorm_impl>)),
+     METH_FASTCALL, nullptr},
+    {"rmsnorm_bwd",
+     reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<rmsnorm_bwd_impl>)),
+     METH_FASTCALL, nullptr},
+    {"adamw", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<adamw_impl>)),
+     METH_FASTCALL, nullptr},
+    {"route", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<route_impl>)),
+     METH_FASTCALL, nullptr},
+    {"route_bwd",
+     reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<route_bwd_impl>)),
      METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -402,6 +402,150 @@ fp8q_status fp8q_newton_schulz(const void *g, int64_t ldg, int64_t g_stride, int
                                void *stream);
 
 /*
+ * Root-mean-square norm with the residual's addition, and the FP8 operand of
+ * the product behind it, in one pass over each row:
+ *   h = x + res,  rstd = 1 / sqrt(sum(h^2) / C + eps),  y = h * rstd * w, in FP32.
+ *   x     [T][ldx] and res (optional, NULL: h = x) [T][ld_res], BF16 or FP32 each
+ *         (x_dtype, res_dtype: FP8Q_OUT_BF16 / FP8Q_OUT_FP32); w [C] BF16 or FP32.
+ * Results, each optional (NULL to skip), at least one required:
+ *   r     [T][ld_r] of res_dtype: h, the new residual stream, rounded to
+ *         nearest-even (needs res; may be res itself, with its pitch).
+ *   y     BF16 [T][ldy].
+ *   q     E4M3 [T][ldq] with s FP32 at s[(c/128) * ld_s + t]: the 1x128
+ *         quantisation, by scale_mode, of the unrounded FP32 y -- the A operand
+ *         of fp8q_gemm and of fp8q_gemm_swiglu.  C % 128 == 0.
+ *   rstd  FP32 [T], what fp8q_rmsnorm_bwd reads.
+ * The norm is of the unrounded h.  A row of zeros with eps > 0 gives zeros.
+ * T >= 0, 0 <= C <= 32768, C % 8 == 0, eps >= 0; a row's sum of squares must be
+ * an FP32 value.  Alignment: x, res, w, r, y, q 16-byte aligned; every pitch a
+ * multiple of 16 bytes.
+ */
+fp8q_status fp8q_rmsnorm(const void *x, int64_t ldx, int x_dtype, const void *res, int64_t ld_res,
+                         int res_dtype, const void *w, int w_dtype, float eps, void *r,
+                         int64_t ld_r, void *y, int64_t ldy, void *q, int64_t ldq, float *s,
+                         int64_t ld_s, float *rstd, int scale_mode, int64_t T, int64_t C,
+                         void *stream);
+
+/*
+ * Backward pass of fp8q_rmsnorm: with xh = x * rstd and c the row's mean of
+ * dy * w * xh,
+ *   dx = rstd * (dy * w - xh * c) + dres,   dw = sum over rows of dy * xh.
+ *   dy    [T][ld_dy] BF16 or FP32; x [T][ldx] BF16 or FP32: the normalised rows
+ *         (the forward's r, or its x where there was no residual);
+ *         rstd FP32 [T]; w [C] BF16 or FP32.
+ *   dres  optional (NULL: 0) [T][ld_dres] of out_dtype: the gradient that
+ *         reaches r on the residual stream itself.  May be dx itself.
+ * Results, at least one required:
+ *   dx    [T][ld_dx] of out_dtype: the gradient of x and of res alike.
+ *   dw    FP32 [C]; added to what it holds where accumulate is not 0.  Summed in
+ *         an order that depends on T and C alone.  T == 0 gives zeros.
+ *   workspace  for dw: device scratch of fp8q_rmsnorm_bwd_workspace_bytes(T, C)
+ *              bytes (0 for sizes outside the limits), 16-byte aligned, owned by
+ *              the caller; contents on entry do not matter.
+ * Limits and alignment as for fp8q_rmsnorm.
+ */
+int64_t fp8q_rmsnorm_bwd_workspace_bytes(int64_t T, int64_t C);
+fp8q_status fp8q_rmsnorm_bwd(const void *dy, int64_t ld_dy, int dy_dtype, const void *x,
+                             int64_t ldx, int x_dtype, const float *rstd, const void *w,
+                             int w_dtype, const void *dres, int64_t ld_dres, void *dx,
+                             int64_t ld_dx, int out_dtype, float *dw, int accumulate, int64_t T,
+                             int64_t C, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * One AdamW step over a list of tensors:
+ *   g' = g * grad_scale,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2,
+ *   p = p - lr * (weight_decay p + (m / (1 - beta1^step)) /
+ *                                  (sqrt(v / (1 - beta2^step)) + eps)), in FP32.
+ * All tensors of a call have the same types:
+ *   p     FP32 or BF16 (p_dtype), g FP32 or BF16 (g_dtype); BF16 values are
+ *         rounded to nearest-even.
+ *   copy  optional: BF16 [n], the new p rounded (what fp8q_quant_weight reads).
+ *   m, v  by state_kind: FP32, BF16 (rounded to nearest-even; the step takes
+ *         the unrounded values), or FP8Q_STATE_E4M3: m and sqrt(v) as E4M3 codes
+ *         with one FP32 scale per 128 consecutive values (the last group may be
+ *         shorter) in m_scale and v_scale: with a = max(amax, 2^-116) of the
+ *         group, scale = a * (1 / 448) and codes E4M3(x * (448 * (1 / a))), each
+ *         operation rounded to nearest; a positive sqrt(v) at least to the
+ *         smallest code, 2^-9, so that no denominator becomes 0 by rounding.  Zero bytes and scales are the
+ *         state before the first step.
+ * `tensors` is a HOST array, copied by the call.  Tensors are dense; none may
+ * overlap another (the p, m, v of a call are checked, FP8Q_ERR_INVALID).
+ *   lr, step   by value, or from device memory where lr_dev / step_dev are not
+ *              NULL (a captured call then follows them); step counts from 1.
+ *   grad_scale optional (NULL: 1) FP32 in device memory, e.g. a clipping factor.
+ *   0 <= beta1, beta2 < 1, eps >= 0; lr, weight_decay finite; n >= 0, the
+ *   tensors of a call below 2^42 values together.
+ * Alignment: every address at its element's; tensors whose addresses are all
+ * 16-byte aligned take wide loads.
+ */
+enum { FP8Q_STATE_BF16 = 0, FP8Q_STATE_FP32 = 1, FP8Q_STATE_E4M3 = 2 };
+typedef struct fp8q_adamw_tensor {
+  void *p;
+  const void *g;
+  void *m, *v;
+  float *m_scale, *v_scale; /* FP8Q_STATE_E4M3 only */
+  void *copy;               /* NULL: none */
+  int64_t n;
+} fp8q_adamw_tensor;
+fp8q_status fp8q_adamw(const fp8q_adamw_tensor *tensors, int64_t count, int p_dtype, int g_dtype,
+                       int state_kind, double lr, double beta1, double beta2, double eps,
+                       double weight_decay, int64_t step, const float *lr_dev,
+                       const int64_t *step_dev, const float *grad_scale, void *stream);
+
+/*
+ * Router of a mixture of experts: the choice of k experts for each token, the
+ * weights of their sum, and the sorted order that the grouped products take.
+ *   logits [T][ld] BF16 or FP32, columns [0, E).  An expert at -inf (or NaN) is
+ *          closed to the token; +inf counts as the largest FP32 value.
+ *   valid  optional (NULL: all) one byte per token, 0: a padding token, which
+ *          goes to no expert and does not count.
+ *   score  s_e = softmax(logits)_e over the open experts or sigmoid(logit_e).
+ * Results, all required:
+ *   idx    int32 [T][k]: the k largest logits in falling order, equal ones in
+ *          rising order of e; -1 where no open expert is left.
+ *   weight FP32 [T][k]: s of the choice, divided by the token's sum of them where
+ *          normalise is not 0, times scale; 0 where idx is -1.
+ *   counts int32 [E]: choices per expert.  offs int32 [E+1]: their exclusive sums,
+ *          the offsets of fp8q_grouped_gemm.
+ *   order  int32 [T*k]: choice t * k + j at each row of the order sorted by
+ *          expert, within an expert by rising t; -1 behind row offs[E].
+ *   slot   int32 [T][k]: each choice's row in that order, -1 where idx is -1.
+ *   tokens int32 [1]: tokens with a choice.
+ *   loss   FP32 [1]: the balance loss, E * sum_e f_e P_e with f_e expert e's share
+ *          of all choices and P_e the mean over those tokens of s_e / sum s; 1
+ *          where all experts are used alike, 0 without tokens.
+ * Sums of scores below 2^-126 count as 2^-126.
+ *   1 <= k <= min(E, 32), E <= 1024, 0 <= T <= 2^26, T * k < 2^31.
+ *   workspace  device scratch of fp8q_route_workspace_bytes(T, E) bytes (0 for
+ *              sizes outside the limits), 16-byte aligned, owned by the caller;
+ *              contents on entry do not matter.
+ * idx, weight, order and slot are dense.  Alignment: every address at its
+ * element's.
+ */
+enum { FP8Q_SCORE_SOFTMAX = 0, FP8Q_SCORE_SIGMOID = 1 };
+int64_t fp8q_route_workspace_bytes(int64_t T, int64_t E);
+fp8q_status fp8q_route(const void *logits, int64_t ld, int dtype, const uint8_t *valid, int score,
+                       int normalise, float scale, int32_t *idx, float *weight, int32_t *counts,
+                       int32_t *offs, int32_t *order, int32_t *slot, int32_t *tokens, float *loss,
+                       int64_t T, int64_t E, int64_t k, void *workspace, int64_t workspace_bytes,
+                       void *stream);
+
+/*
+ * Backward pass of fp8q_route: the gradient of the logits from those of the
+ * weights and of the balance loss.  The choice and the counts are constants.
+ *   logits, valid, score, normalise, scale  as the forward call took them;
+ *   idx, counts, tokens  its results.
+ *   dweight  optional (NULL: 0) FP32 [T][k];  dloss optional (NULL: 0) FP32 [1].
+ *   dlogits  [T][ld_d] of the logits' type: 0 at closed experts and padding.
+ * An idx outside [0, E) is no choice.
+ */
+fp8q_status fp8q_route_bwd(const void *logits, int64_t ld, int dtype, const uint8_t *valid,
+                           int score, int normalise, float scale, const int32_t *idx,
+                           const int32_t *counts, const int32_t *tokens, const float *dweight,
+                           const float *dloss, void *dlogits, int64_t ld_d, int64_t T, int64_t E,
+                           int64_t k, void *stream);
+
+/*
  * Plain FP32 -> E4M3 conversion of n values (round to nearest-even, saturate
  * to +-448, NaN -> 0x7F), with no scaling.  The quantisers use the same
  * conversion; this entry exposes it so it can be checked on every FP32 bit

@@ -1,0 +1,316 @@
+"""The expert router and its backward pass against plain 64-bit arithmetic.
+
+The choice, counts, offsets and order are whole numbers and have to be equal; the
+reference sorts the FP32 logits, equal ones by index.
+
+Tolerances (u = 2^-24): exp(l - m) with the difference rounded, |l - m| u, and exp's own
+2 u; sums of up to E terms, 32 in a lane and 5 levels of a tree, 40 u; a reciprocal and
+products: a weight is right to (60 + 2 |l - m|) u of itself (sigmoid: 2 |l| for the same
+reason, and its complement likewise), with 1e-37 for what underflows.
+The loss sums T such probabilities per expert, all positive: ceil(T / 152 / 16) of them
+in a warp, 16 + 152 partial sums, and the experts in a tree: at most (T / 2432 + 260 +
+2 * 60) u.  Gradients: the factors above on every term, 100 u more for the sums, of the
+sum of magnitudes.
+"""
+import pytest
+import torch
+
+B = pytest.importorskip("fp8_fine_grained_amax_gb300.binding")
+import fp8_fine_grained_amax_gb300 as fq
+from test_gpu_swiglu import padded
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+BF, FP = torch.bfloat16, torch.float32
+BIG = torch.finfo(FP).max
+SOFT, SIG = 0, 1
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from fp8_fine_grained_amax_gb300.build import build_library
+    build_library()
+    yield B.load_library()
+    assert B.fp8q_sync_status() == 0
+
+
+def near(got, want, tol, what):
+    err = (got.double().cpu() - want).abs()
+    ok = err <= tol
+    assert bool(ok.all()), f"{what}: {int((~ok).sum())} of {ok.numel()} outside, max err/tol " \
+        f"{float((err / tol.clamp_min(1e-300)).max()):.3g}"
+
+
+def make(T, E, dtype, seed, masked):
+    g = torch.Generator().manual_seed(seed)
+    l = torch.randn(T, E, generator=g) * 2 + torch.randn(E, generator=g)
+    valid = None
+    if masked and T:
+        valid = torch.rand(T, generator=g) > 0.2
+        l = torch.where((torch.rand(T, 1, generator=g) < 0.3) & (torch.rand(T, E, generator=g) < 0.6), float("-inf"), l)
+        l[torch.rand(T, generator=g) < 0.1] = float("-inf")
+    return l.to(dtype), valid
+
+
+def parts(l, valid, score):
+    """Open experts, clamped logits and the logarithms of their scores in 64 bits."""
+    may = l.float() > float("-inf")
+    if valid is not None:
+        may = may & valid[:, None]
+    x = l.double().clamp_max(BIG)
+    x = torch.where(may, x, float("-inf"))
+    log_s = torch.nn.functional.logsigmoid(x) if score == SIG else x - torch.logsumexp(x, 1, keepdim=True)
+    return may, x, torch.where(may, log_s, float("-inf"))
+
+
+def reference(l, valid, k, score, normalise, scale):
+    T, E = l.shape
+    may, x, log_s = parts(l, valid, score)
+    idx = torch.sort(x, dim=1, descending=True, stable=True).indices[:, :k]
+    has = may.gather(1, idx)
+    w = torch.where(has, log_s.gather(1, idx), float("-inf"))
+    w = torch.softmax(w, 1).nan_to_num(0.0) if normalise else torch.exp(w)
+    idx = torch.where(has, idx, -1)
+    flat = torch.where(has, idx, E).reshape(-1)
+    order = torch.sort(flat, stable=True).indices
+    slot = torch.empty_like(order)
+    slot[order] = torch.arange(T * k)
+    counts = torch.bincount(flat, minlength=E + 1)[:E]
+    n = int(counts.sum())
+    order[n:] = -1
+    tokens = int(has[:, 0].sum()) if T else 0
+    p = torch.softmax(log_s, 1).nan_to_num(0.0)
+    loss = E * float((counts / max(n, 1) * p.sum(0)).sum()) / max(tokens, 1)
+    return dict(idx=idx, weight=w * scale, counts=counts, offs=torch.cat([torch.zeros(1).long(), counts.cumsum(0)]),
+                order=order, slot=torch.where(has, slot.reshape(T, k), -1), tokens=torch.tensor([tokens]),
+                loss=torch.tensor([loss], dtype=torch.double))
+
+
+def check(r, l, valid, k, score, normalise, scale):
+    want = reference(l, valid, k, score, normalise, scale)
+    for name in ("idx", "counts", "offs", "order", "slot", "tokens"):
+        got = getattr(r, name)
+        assert got.dtype == torch.int32 and torch.equal(got.cpu().long(), want[name]), name
+    may, x, _ = parts(l, valid, score)
+    at = want["idx"].clamp_min(0)
+    val = torch.where(want["idx"] >= 0, x.gather(1, at) if l.shape[0] else x[:, :k], 0.0)
+    top = x.amax(1, keepdim=True).clamp_min(-BIG) if l.shape[0] else x[:, :1]
+    reach = (val.abs() if score == SIG else (top - val).abs()).clamp_max(200)
+    far = reach.amax(1, keepdim=True) if normalise else reach
+    near(r.weight, want["weight"], (60 + 2 * reach + 2 * far) * U * want["weight"].abs() + 1e-37 * scale, "weight")
+    near(r.loss, want["loss"], (l.shape[0] / 2432 + 380 + 2 * 40) * U * want["loss"].abs() + 1e-37, "loss")
+
+
+GRID = [(1, 1, 1, FP), (1, 256, 8, FP), (2, 8, 2, BF), (15, 3, 3, FP), (64, 64, 6, BF), (65, 64, 6, FP), (64, 33, 32, FP),
+        (66, 128, 1, BF), (333, 64, 6, BF), (777, 160, 8, FP), (1000, 7, 2, FP), (2431, 16, 1, BF), (2433, 16, 4, FP),
+        (5003, 100, 5, BF), (300, 512, 12, FP), (257, 1024, 32, FP), (70, 1000, 16, BF), (20000, 256, 8, FP)]
+
+
+@pytest.mark.parametrize("T,E,k,dtype", GRID)
+@pytest.mark.parametrize("score,normalise,masked", [(SOFT, True, False), (SIG, True, True), (SOFT, False, True),
+                                                    (SIG, False, False)])
+def test_forward(T, E, k, dtype, score, normalise, masked):
+    l, valid = make(T, E, dtype, T + E, masked)
+    r = fq.fp8q_route(l.cuda(), k, score=score, normalise=normalise, scale=2.5, valid=None if valid is None else valid.cuda())
+    check(r, l, valid, k, score, normalise, 2.5)
+
+
+@pytest.mark.parametrize("T", [5, 400])
+def test_ties_take_the_lowest_index(T):
+    for E in (8, 40, 300):
+        l = torch.zeros(T, E)
+        l[1::2] = -0.0
+        l[2] = torch.arange(E) % 3
+        l[3] = -torch.zeros(E) * (torch.arange(E) % 2)
+        check(fq.fp8q_route(l.cuda(), 5), l, None, 5, SOFT, True, 1.0)
+        l = torch.randint(0, 3, (T, E), generator=torch.Generator().manual_seed(1)).to(BF)
+        check(fq.fp8q_route(l.cuda(), 5, score=SIG), l, None, 5, SIG, True, 1.0)
+
+
+@pytest.mark.parametrize("T", [6, 300])
+@pytest.mark.parametrize("score", [SOFT, SIG])
+@pytest.mark.parametrize("dtype", [FP, BF])
+def test_infinities_nan_and_lowest_values(T, score, dtype):
+    E, k, inf = 12, 4, float("inf")
+    l, _ = make(T, E, dtype, 3, False)
+    low = torch.finfo(dtype).min
+    l[0] = -inf                      # nothing left
+    l[1] = float("nan")
+    l[2, 3:] = -inf                  # fewer than k
+    l[3, 5], l[3, 7] = inf, inf      # as large as can be
+    l[4] = low                       # a mask of the type's lowest value everywhere
+    l[5, 1:] = low
+    l[5, 0] = float("nan")
+    r = fq.fp8q_route(l.cuda(), k, score=score)
+    for name, t in r._asdict().items():
+        assert not torch.isnan(t.float()).any(), name
+    want = reference(l.nan_to_num(nan=-inf, posinf=inf, neginf=-inf), None, k, score, True, 1.0)
+    for name in ("idx", "counts", "offs", "order", "slot", "tokens"):
+        assert torch.equal(getattr(r, name).cpu().long(), want[name]), name
+    assert (r.idx[:2] == -1).all() and (r.weight[:2] == 0).all()
+    assert r.idx[2].tolist()[3:] == [-1] and r.idx[3].tolist()[:2] == [5, 7] and r.idx[4].tolist() == [0, 1, 2, 3]
+    if score == SOFT:
+        assert (r.weight[4] == 0.25).all()
+    else:  # every score underflows: no weight rather than no number
+        assert (r.weight[4] == 0).all()
+    ones = torch.ones(T, k, device="cuda")
+    d = fq.fp8q_route_bwd(l.cuda(), r.idx, r.counts, r.tokens, dweight=ones, dloss=torch.ones(1, device="cuda"),
+                          score=score)
+    assert torch.isfinite(d.float()).all() and not d[:2].any() and not d[2, 3:].any()
+
+
+@pytest.mark.parametrize("T", [3, 500])
+def test_no_valid_token(T):
+    l, _ = make(T, 16, FP, 4, False)
+    none = torch.zeros(T, dtype=torch.bool, device="cuda")
+    r = fq.fp8q_route(l.cuda(), 2, valid=none)
+    assert (r.idx == -1).all() and (r.order == -1).all() and (r.slot == -1).all() and not r.weight.any()
+    assert not r.counts.any() and not r.offs.any() and r.loss.item() == 0 and r.tokens.item() == 0
+    d = fq.fp8q_route_bwd(l.cuda(), r.idx, r.counts, r.tokens, dweight=torch.ones(T, 2, device="cuda"),
+                          dloss=torch.ones(1, device="cuda"), valid=none)
+    assert not d.any()
+
+
+def test_no_tokens():
+    r = fq.fp8q_route(torch.empty(0, 16, device="cuda"), 2)
+    assert r.idx.shape == (0, 2) and r.order.shape == (0,) and not r.counts.any() and not r.offs.any()
+    assert r.loss.item() == 0 and r.tokens.item() == 0
+    d = fq.fp8q_route_bwd(torch.empty(0, 16, device="cuda"), r.idx, r.counts, r.tokens, dloss=r.loss)
+    assert d.shape == (0, 16)
+
+
+def test_balance_loss_is_one_where_experts_are_used_alike():
+    l = torch.full((64, 8), -20.0)
+    l[torch.arange(64), torch.arange(64) % 8] = 20.0
+    assert abs(fq.fp8q_route(l.cuda(), 1).loss.item() - 1) < 1e-6
+    l[:] = -20.0
+    l[:, 3] = 20.0
+    assert abs(fq.fp8q_route(l.cuda(), 1).loss.item() - 8) < 1e-5
+
+
+@pytest.mark.parametrize("T,E,k", [(40, 24, 3), (700, 100, 6)])
+def test_strides_and_given_results(T, E, k):
+    for dtype in (FP, BF):
+        l, valid = make(T, E, dtype, 5, True)
+        want = fq.fp8q_route(l.cuda(), k, valid=valid.cuda())
+        for pad in (1, 8):
+            lv, _ = padded(T, E, 2, pad, dtype, float("nan"))
+            lv.copy_(l)
+            i = lambda *s: torch.full(s, -9, dtype=torch.int32, device="cuda")  # noqa: E731
+            given = dict(idx=i(T, k), weight=torch.zeros(T, k, device="cuda"), counts=i(E), offs=i(E + 1), order=i(T * k),
+                         slot=i(T, k), tokens=i(1), loss=torch.zeros(1, device="cuda"))
+            ws = torch.full((fq.fp8q_route_workspace_bytes(T, E) + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+            r = fq.fp8q_route(lv, k, valid=valid.cuda().byte(), workspace=ws[:-64], **given)
+            for name, t in r._asdict().items():
+                assert t is given[name] and torch.equal(t, getattr(want, name)), name
+            assert (ws[-64:] == 0xFF).all()
+            dw, one = torch.randn(T, k, device="cuda"), torch.ones((), device="cuda")
+            d0 = fq.fp8q_route_bwd(l.cuda(), r.idx, r.counts, r.tokens, dweight=dw, dloss=one, valid=valid.cuda())
+            dv, buf = padded(T, E, 2, pad, dtype, 7.0)
+            d1 = fq.fp8q_route_bwd(lv, r.idx, r.counts, r.tokens, dweight=dw, dloss=one, valid=valid.cuda(), dlogits=dv)
+            assert d1 is dv and torch.equal(d0, d1) and (buf[:, E:] == 7).all() and (buf[T:] == 7).all()
+
+
+def value(x, may, idx, counts, tokens, dw, dloss, score, normalise, scale):
+    """sum(weight * dw) + dloss * loss in 64 bits, the choice and the counts held."""
+    E = x.shape[1]
+    log_s = torch.nn.functional.logsigmoid(x) if score == SIG else torch.log_softmax(x, 1)
+    log_s = torch.where(may, log_s, float("-inf"))
+    has = idx >= 0
+    w = torch.where(has, log_s.gather(1, idx.clamp_min(0)), float("-inf"))
+    w = torch.softmax(w, 1) if normalise else torch.exp(w)
+    p = torch.softmax(log_s, 1)
+    loss = E * (counts.double() / counts.sum() * p.sum(0)).sum() / tokens
+    return (torch.where(has, w, 0.0) * dw).sum() * scale + dloss * loss
+
+
+@pytest.mark.parametrize("T,E,k,dtype", [(1, 2, 1, FP), (3, 8, 2, FP), (50, 33, 5, BF), (333, 64, 6, BF), (600, 256, 8, FP),
+                                         (100, 512, 8, FP), (64, 1000, 16, BF), (20, 128, 32, FP), (5000, 16, 4, FP)])
+@pytest.mark.parametrize("score,normalise", [(SOFT, True), (SOFT, False), (SIG, True), (SIG, False)])
+def test_backward(T, E, k, dtype, score, normalise):
+    l, valid = make(T, E, dtype, T * 3 + E, T > 3)
+    vc = None if valid is None else valid.cuda()
+    kw = dict(score=score, normalise=normalise, scale=1.5, valid=vc)
+    r = fq.fp8q_route(l.cuda(), k, **kw)
+    g = torch.Generator().manual_seed(T)
+    dw, dloss = torch.randn(T, k, generator=g), 0.7
+    may, x, log_s = parts(l, valid, score)
+    alive = may.any(1)
+    idx, counts, tokens = r.idx.cpu().long(), r.counts.cpu(), int(r.tokens)
+    n = T / max(tokens, 1)
+
+    def grads(a, b):
+        y = torch.where(may, x, -1e4)[alive].requires_grad_()
+        v = value(y, may[alive], idx[alive], counts, tokens, a * dw[alive].double(), b * dloss, score, normalise, 1.5)
+        return torch.zeros(T, E, dtype=torch.double).masked_scatter_(alive[:, None].expand(T, E),
+                                                                     torch.autograd.grad(v, y)[0]) * may
+
+    # magnitudes of the sums behind each element
+    s = torch.where(may, torch.exp(log_s), 0.0)
+    p = torch.where(alive[:, None], torch.softmax(log_s, 1), 0.0)
+    has = idx >= 0
+    u = torch.where(has, torch.exp(log_s.gather(1, idx.clamp_min(0))), 0.0)
+    if normalise:
+        u = u / u.sum(1, keepdim=True).clamp_min(1e-300)
+    mag = torch.zeros(T, E, dtype=torch.double).scatter_add_(1, idx.clamp_min(0), u * dw.abs().double() * 1.5)
+    all_u = (u * dw.abs().double() * 1.5).sum(1, keepdim=True)
+    if normalise:
+        mag = mag + torch.zeros(T, E, dtype=torch.double).scatter_add_(1, idx.clamp_min(0), u) * all_u
+    elif score == SOFT:
+        mag = mag + p * all_u
+    dp = dloss * E * counts.double() / max(int(counts.sum()), 1) / max(tokens, 1)
+    mag_l = p * (dp + (p * dp).sum(1, keepdim=True))
+    if score == SIG:
+        mag, mag_l = mag * torch.sigmoid(-x.clamp_min(-1e4)), mag_l * torch.sigmoid(-x.clamp_min(-1e4))
+    reach = torch.where(may, (x.abs() if score == SIG else x.amax(1, keepdim=True) - x), 0.0).amax(1, keepdim=True)
+    dwc, dlc = dw.cuda(), torch.tensor([dloss], device="cuda")
+    for a, b in ((1, 1), (1, 0), (0, 1)):
+        got = fq.fp8q_route_bwd(l.cuda(), r.idx, r.counts, r.tokens, dweight=dwc if a else None, dloss=dlc if b else None, **kw)
+        assert got.dtype == dtype
+        want = grads(a, b)
+        # and the reference's own rounding, 2^-53 of its terms: where the exact sum is 0 it leaves some of that
+        tol = (200 + 8 * reach) * U * (a * mag + b * mag_l) + 1e-37 + 2.0 ** -48 * (a * dw.abs().double().sum(1, keepdim=True) + b)
+        near(got, want, tol + (2.0 ** -8 * (want.abs() + tol) if dtype == BF else 0), f"dlogits {a} {b}")
+        again = fq.fp8q_route_bwd(l.cuda(), r.idx, r.counts, r.tokens, dweight=dwc if a else None, dloss=dlc if b else None, **kw)
+        assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("score,normalise", [(SOFT, True), (SOFT, False), (SIG, True), (SIG, False)])
+def test_gradients_against_differences(score, normalise):
+    T, E, k, e = 6, 10, 3, 1e-4
+    l, _ = make(T, E, FP, 6, False)
+    r = fq.fp8q_route(l.cuda(), k, score=score, normalise=normalise)
+    dw = torch.randn(T, k, generator=torch.Generator().manual_seed(7))
+    d = fq.fp8q_route_bwd(l.cuda(), r.idx, r.counts, r.tokens, dweight=dw.cuda(), dloss=torch.ones(1, device="cuda"),
+                          score=score, normalise=normalise).double().cpu()
+    may = torch.ones(T, E, dtype=torch.bool)
+    f = lambda x: float(value(x, may, r.idx.cpu().long(), r.counts.cpu(), T, dw.double(), 1.0, score, normalise, 1.0))  # noqa: E731
+    for seed in range(4):
+        v = torch.randn(T, E, generator=torch.Generator().manual_seed(seed)).double()
+        slope = (f(l.double() + e * v) - f(l.double() - e * v)) / (2 * e)
+        # third differences e^2 of order one, FP32 gradients
+        assert abs(slope - float((d * v).sum())) < 1e-6 * (1 + float(d.norm() * v.norm()))
+
+
+def test_choices_that_are_none_and_the_same_choice_twice():
+    l, _ = make(4, 8, FP, 8, False)
+    idx = torch.tensor([[1, 1], [-1, 3], [8, 2], [1 << 30, -(1 << 30)]], dtype=torch.int32, device="cuda")
+    counts = torch.ones(8, dtype=torch.int32, device="cuda")
+    dw = torch.ones(4, 2, device="cuda")
+    d = fq.fp8q_route_bwd(l.cuda(), idx, counts, torch.tensor([4], dtype=torch.int32, device="cuda"), dweight=dw,
+                          score=SIG, normalise=False).double().cpu()
+    s = torch.sigmoid(l.double())
+    want = torch.zeros(4, 8, dtype=torch.double)
+    for t, e, n in ((0, 1, 2), (1, 3, 1), (2, 2, 1)):
+        want[t, e] = n * s[t, e] * (1 - s[t, e])
+    near(d, want, 100 * U * want + 1e-37, "dlogits")
+
+
+def test_repeats_bit_by_bit():
+    l, valid = make(9000, 200, FP, 9, True)
+    first = fq.fp8q_route(l.cuda(), 8, valid=valid.cuda())
+    for _ in range(5):
+        again = fq.fp8q_route(l.cuda(), 8, valid=valid.cuda())
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
