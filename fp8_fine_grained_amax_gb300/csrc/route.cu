@@ -5,9 +5,14 @@
 //   weight_j = scale * s_j (/ sum of the chosen s),
 //   loss = E * sum_e (counts_e / sum counts) * (sum_t p_te / N).
 //
-// A warp takes a token, lane i the V experts from i * V on, in registers.  The
-// choice is k rounds of one warp-wide integer maximum over keys that order as the
-// logits do (ties: the lowest lane and register is the lowest expert).
+// A warp takes a token, lane i the V experts from i * V on, in registers.  Each
+// expert becomes one 32-bit word: the logit's upper bits in an order-preserving
+// form, and below them the expert's index, falling, so that no two words are alike
+// and the lower index is the larger word.  A lane sorts its words (two instructions
+// per comparator), and the choice is k rounds of one warp-wide maximum over the
+// lanes' largest words.  BF16 logits fit in the upper bits.  Where two FP32 logits
+// next to each other in the choice differ in their lower bits only (or not at all),
+// the token's choice is made again on whole logits.
 //
 // The order has to be the same in every run, so rows are counted, not claimed with
 // atomics: each warp goes through a contiguous part of the tokens and counts its
@@ -27,9 +32,8 @@
 namespace fp8q {
 namespace {
 
-constexpr int kWarps = 16;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxCtas = 152;     // one per SM
+constexpr int kSms = 152;         // one CTA each
+constexpr int kMaxPerCta = 65535; // tokens of a CTA: its counts are 16 bits
 constexpr int kOneCta = 64;       // tokens that one CTA takes alone
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxChoices = 32;   // one per lane
@@ -41,11 +45,11 @@ struct RouteArgs {
   const uint8_t *valid;
   int32_t *idx, *counts, *offs, *order, *slot, *tokens;
   float *weight, *loss;
-  int *cta_counts;    // [CTAs][E]
-  float *cta_probs;   // [CTAs][E]
+  uint16_t *cta_counts;  // [CTAs][E, rounded up to even]
+  float *cta_probs;      // [CTAs][E]
   int *cta_tokens;    // [CTAs]
   int64_t ld;
-  int T, E, k, ctas, per_cta, per_warp;
+  int T, E, k, ctas, per_cta;
   float scale;
   bool sigmoid, normalise, vec;
 };
@@ -61,7 +65,7 @@ __device__ __forceinline__ void load_logits(const void *row, int E, int lane, bo
     if constexpr (kBytes >= 16) {
 #pragma unroll
       for (int i = 0; i < kBytes / 16; ++i) {
-        const uint4 u = ld_stream(p + 16 * i);
+        const uint4 u = *reinterpret_cast<const uint4 *>(p + 16 * i);
         w[4 * i] = u.x;
         w[4 * i + 1] = u.y;
         w[4 * i + 2] = u.z;
@@ -94,19 +98,76 @@ __device__ __forceinline__ float logit_at(const void *row, int kind, int e) {
                        : bf16_lo(static_cast<const uint16_t *>(row)[e]);
 }
 
-// Unsigned keys in the order of the logits: 0 for a closed expert (-inf or NaN),
-// the same for both zeros; +inf becomes the largest finite value.
+// Warps of a CTA and expert words per lane: 64 registers per thread for up to 8
+// experts per lane, 128 for 16, 255 for 32.
+__host__ __device__ constexpr int warps_for(int V) { return V <= 8 ? 32 : V == 16 ? 16 : 8; }
+
+// Unsigned keys in the order of the logits, the same for both zeros.  -inf is below
+// kOpen, +inf and NaN (which the addition makes the positive one) at kSpecial or above.
+constexpr uint32_t kOpen = 0x00800000u, kSpecial = 0xFF800000u;
 __device__ __forceinline__ uint32_t key_of(float l) {
-  if (!(l > -INFINITY)) return 0;
-  l = fminf(l, kBig);
-  const uint32_t b = l == 0.0f ? 0u : __float_as_uint(l);
+  const uint32_t b = __float_as_uint(l + 0.0f);  // -0 + 0 = +0
   return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ float logit_of(uint32_t key) {
-  return __uint_as_float(key ^ (key & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu));
+
+// Falling order of V words: Batcher's odd-even merge sort.
+template <int V>
+__device__ __forceinline__ void sort_falling(uint32_t (&w)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int i = 0; i + k < V; ++i)
+        if (i >= k % p && (i - k % p) % (2 * k) < k && i / (2 * p) == (i + k) / (2 * p)) {
+          const uint32_t a = max(w[i], w[i + k]);
+          w[i + k] = min(w[i], w[i + k]);
+          w[i] = a;
+        }
 }
 
-__device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
+// The choice on whole keys: lane j gets the j-th expert, or -1.
+template <int V>
+__device__ __forceinline__ int choose_exactly(uint32_t (&key)[V], int k, int lane) {
+  int chosen = -1;
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = 0;
+    int at = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (key[v] > best) {
+        best = key[v];
+        at = v;
+      }
+    const uint32_t top = __reduce_max_sync(~0u, best);
+    if (top < kOpen) break;
+    const int owner = __ffs(__ballot_sync(~0u, best == top)) - 1;
+    if (lane == owner) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (v == at) key[v] = 0;
+    }
+    at = __shfl_sync(~0u, at, owner);
+    if (lane == j) chosen = owner * V + at;
+  }
+  return chosen;
+}
+
+// exp2 and the reciprocal are right to 2 units and 1 unit in the last place, and
+// flush what is below 2^-126 to 0; the difference and its product with log2(e) are
+// rounded once each, 2 |l - m| 2^-24 relative in the result (|l| in a sigmoid).
+constexpr float kLog2e = 1.44269504f;
+__device__ __forceinline__ float exp_above(float l, float m) { return ex2_ftz((l - m) * kLog2e); }
+__device__ __forceinline__ float exp_minus(float l) { return ex2_ftz(-kLog2e * l); }
+__device__ __forceinline__ float sigmoid(float l) { return rcp_ftz(1.0f + exp_minus(l)); }
+
+// Logits that are no numbers are closed, infinite ones the largest value.  Rare: the
+// callers look for one in the row first.
+template <int V>
+__device__ __forceinline__ void make_finite(float (&l)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) l[v] = l[v] > -INFINITY ? fminf(l[v], kBig) : -INFINITY;
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -114,6 +175,12 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(~0u, v); }
+
+// E * sum_e (counts_e / choices) * (probs_e / tokens) from the sum of their products.
+__device__ __forceinline__ float balance(float sum, int E, int choices, int tokens) {
+  return tokens > 0 ? static_cast<float>(E) * (sum / static_cast<float>(choices)) / static_cast<float>(tokens)
+                    : 0.0f;
+}
 
 // Exclusive sums over the CTA's threads (at most 1024); `part` holds 32 ints and
 // is free again after the caller's next barrier.
@@ -131,40 +198,16 @@ __device__ __forceinline__ int cta_exclusive_sum(int v, int *part) {
   return before + s - v;
 }
 
-// counts, offs, tokens and loss, by one CTA of at least E threads: thread e has
-// expert e's total, the sum of its probabilities and its first row.
-__device__ __forceinline__ void write_totals(const RouteArgs &a, int total, float probs, int first,
-                                             int tokens, float *part) {
-  const int e = threadIdx.x, lane = e & 31, warp = e >> 5, warps = blockDim.x >> 5;
-  if (e < a.E) {
-    a.counts[e] = total;
-    a.offs[e] = first;
-    if (e == a.E - 1) a.offs[a.E] = first + total;
-  }
-  const float s = warp_sum(e < a.E ? static_cast<float>(total) * probs : 0.0f);
-  const float n = warp_sum(e < a.E ? static_cast<float>(total) : 0.0f);
-  if (lane == 0) {
-    part[warp] = s;
-    part[32 + warp] = n;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    const float all = warp_sum(lane < warps ? part[lane] : 0.0f);
-    const float choices = warp_sum(lane < warps ? part[32 + lane] : 0.0f);
-    if (lane == 0) {
-      a.tokens[0] = tokens;
-      a.loss[0] = tokens > 0 ? static_cast<float>(a.E) * (all / choices) / static_cast<float>(tokens) : 0.0f;
-    }
-  }
-}
-
-// Dynamic shared memory: counts [kWarps][E], then probabilities [kWarps][E].
+// Dynamic shared memory: counts [warps][E], then probabilities [warps][E].
 template <int kKind, int V>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(32 * warps_for(V))
 route_kernel(const RouteArgs a) {
+  constexpr int kWarps = warps_for(V), kThreads = 32 * kWarps;
+  constexpr int kEach = 32 * V > kThreads ? 32 * V / kThreads : 1;  // experts per thread, at most
+  constexpr uint32_t kIndex = 32 * V - 1;                            // a word's index bits
   extern __shared__ int smem[];
-  __shared__ int tokens_of[kWarps], scan[32];
-  __shared__ float part[64];
+  __shared__ int tokens_of[kWarps], scan[32], all_rows;
+  __shared__ float part[32];
   wait_for_previous_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E, k = a.k;
   int *counts = smem;
@@ -175,70 +218,94 @@ route_kernel(const RouteArgs a) {
 
   const int64_t cta_lo = static_cast<int64_t>(blockIdx.x) * a.per_cta;
   const int64_t cta_hi = min(static_cast<int64_t>(a.T), cta_lo + a.per_cta);
-  const int64_t lo = min(cta_hi, cta_lo + static_cast<int64_t>(warp) * a.per_warp);
-  const int64_t hi = min(cta_hi, lo + a.per_warp);
-  float psum[V];
+  const int64_t n = cta_hi > cta_lo ? cta_hi - cta_lo : 0;
+  const int64_t lo = cta_lo + n * warp / kWarps, hi = cta_lo + n * (warp + 1) / kWarps;
+  const char *row = static_cast<const char *>(a.logits) + lo * a.ld * size_of(kKind);
+  float psum[V], next[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) psum[v] = 0.0f;
   int routed = 0;
+  bool next_valid = true;
+  if (lo < hi) {
+    load_logits<kKind, V>(row, E, lane, a.vec, next);
+    if (a.valid) next_valid = a.valid[lo] != 0;
+  }
 
+  const uint32_t below = kIndex - lane * V;  // index bits of the lane's first word
   for (int64_t t = lo; t < hi; ++t) {
-    const bool valid = !a.valid || a.valid[t] != 0;
     float l[V];
-    uint32_t key[V];
-    load_logits<kKind, V>(static_cast<const char *>(a.logits) + t * a.ld * size_of(kKind), E, lane, a.vec, l);
+    const bool valid = next_valid;
 #pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = valid ? key_of(l[v]) : 0u;
-    uint32_t best = 0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) best = max(best, key[v]);
-    uint32_t top = __reduce_max_sync(~0u, best);
-    routed += top != 0;
-    const float m = logit_of(top);
-
-    // scores and their sum, before the choice clears keys
-    float s[V], sum = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float x = logit_of(key[v]);
-      s[v] = key[v] == 0 ? 0.0f : a.sigmoid ? sigmoid(x) : expf(x - m);
-      sum += s[v];
+    for (int v = 0; v < V; ++v) l[v] = next[v];
+    const char *here = row;
+    row += a.ld * size_of(kKind);
+    if (t + 1 < hi) {  // in flight while this token is dealt with
+      load_logits<kKind, V>(row, E, lane, a.vec, next);
+      if (a.valid) next_valid = a.valid[t + 1] != 0;
     }
-    sum = warp_sum(sum);
-    const float inv = 1.0f / fmaxf(sum, kTiny);
-#pragma unroll
-    for (int v = 0; v < V; ++v) psum[v] = fmaf(s[v], inv, psum[v]);
-
-    // lane j keeps choice j
     int chosen = -1;
-    uint32_t chosen_key = 0;
-    for (int j = 0; j < k && top != 0; ++j) {
-      const int owner = __ffs(__ballot_sync(~0u, best == top)) - 1;
-      int at = 0;
-      if (lane == owner) {
+    float w = 0.0f;
+    if (valid) {
+      uint32_t word[V];
+      const auto make_words = [&]() {
 #pragma unroll
-        for (int v = V - 1; v >= 0; --v)
-          if (key[v] == top) at = v;
-        best = 0;
+        for (int v = 0; v < V; ++v) word[v] = (key_of(l[v]) & ~kIndex) | (below - v);
+        sort_falling(word);
+      };
+      make_words();
+      if (__reduce_max_sync(~0u, word[0]) >= kSpecial) {
+        make_finite(l);
+        make_words();
+      }
+      // lane j keeps the j-th largest word; one round more tells whether the last
+      // choice is apart from the rest
+      uint32_t kept = 0;
+      for (int j = 0; j < k + (kKind == kFp32); ++j) {
+        const uint32_t top = __reduce_max_sync(~0u, word[0]);
+        if (lane == j) kept = top;
+        if (word[0] == top) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          if (v == at) key[v] = 0;
-          best = max(best, key[v]);
+          for (int v = 0; v + 1 < V; ++v) word[v] = word[v + 1];
+          word[V - 1] = 0;
         }
       }
-      at = __shfl_sync(~0u, at, owner);
-      if (lane == j) {
-        chosen = owner * V + at;
-        chosen_key = top;
+      if (kKind == kFp32) {
+        const uint32_t ahead = __shfl_up_sync(~0u, kept, 1);
+        const bool alike = lane > 0 && lane <= k && kept >= kOpen && ((kept ^ ahead) & ~kIndex) == 0;
+        // choice 33 of 32 has no lane: with that many every choice is made exactly
+        if (__any_sync(~0u, alike) || k == 32) {
+          uint32_t key[V];
+#pragma unroll
+          for (int v = 0; v < V; ++v) key[v] = key_of(l[v]);
+          chosen = choose_exactly<V>(key, k, lane);
+        } else if (lane < k && kept >= kOpen) {
+          chosen = static_cast<int>(kIndex - (kept & kIndex));
+        }
+      } else if (lane < k && kept >= kOpen) {
+        chosen = static_cast<int>(kIndex - (kept & kIndex));
       }
-      top = __reduce_max_sync(~0u, best);
+      float x = 0.0f;
+      if (chosen >= 0) x = fminf(logit_at(here, kKind, chosen), kBig);
+      const float m = __shfl_sync(~0u, x, 0);  // the first choice is the largest
+      routed += __shfl_sync(~0u, chosen, 0) >= 0;
+
+      float s[V], sum = 0.0f;
+      if (a.sigmoid) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = sigmoid(l[v]);
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = exp_above(l[v], m);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) sum += s[v];
+      const float inv = rcp_ftz(fmaxf(warp_sum(sum), kTiny));
+#pragma unroll
+      for (int v = 0; v < V; ++v) psum[v] = fmaf(s[v], inv, psum[v]);
+
+      if (chosen >= 0) w = a.sigmoid ? sigmoid(x) : exp_above(x, m) * inv;
+      if (a.normalise) w *= rcp_ftz(fmaxf(warp_sum(w), kTiny));
     }
-    float w = 0.0f;
-    if (chosen >= 0) {
-      const float x = logit_of(chosen_key);
-      w = a.sigmoid ? sigmoid(x) : expf(x - m) * inv;
-    }
-    if (a.normalise) w = w / fmaxf(warp_sum(w), kTiny);
     if (lane < k) {
       const int64_t at = t * k + lane;
       a.idx[at] = chosen;
@@ -258,13 +325,13 @@ route_kernel(const RouteArgs a) {
   if (lane == 0) tokens_of[warp] = routed;
   __syncthreads();
 
-  // counts become the warps' first ranks
+  // counts become the warps' first ranks; thread i has the experts from i * kEach on
   const bool alone = gridDim.x == 1;
-  int totals[kMaxExperts / kThreads], tokens = 0;
-  float p_of[kMaxExperts / kThreads];
+  int total[kEach], all = 0, tokens = 0;
+  float loss = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kMaxExperts / kThreads; ++i) {
-    const int e = threadIdx.x + i * kThreads;
+  for (int i = 0; i < kEach; ++i) {
+    const int e = threadIdx.x * kEach + i;
     int run = 0;
     float p = 0.0f;
     if (e < E) {
@@ -276,135 +343,164 @@ route_kernel(const RouteArgs a) {
         p += probs[w * E + e];
       }
       if (!alone) {
-        a.cta_counts[static_cast<int64_t>(blockIdx.x) * E + e] = run;
+        a.cta_counts[static_cast<int64_t>(blockIdx.x) * (E + (E & 1)) + e] = static_cast<uint16_t>(run);
         a.cta_probs[static_cast<int64_t>(blockIdx.x) * E + e] = p;
       }
     }
-    totals[i] = run;
-    p_of[i] = p;
+    total[i] = run;
+    all += run;
+    loss = fmaf(static_cast<float>(run), p, loss);
   }
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) tokens += tokens_of[w];
   __syncthreads();
 
-  int rows = 0;
+  int *first_row = smem + kWarps * E;  // of each expert, where the probabilities were
   if (!alone) {
     if (threadIdx.x == 0) a.cta_tokens[blockIdx.x] = tokens;
   } else {
-    // one CTA: its totals are all there is; probs holds them by expert from here on
-    int *total_of = reinterpret_cast<int *>(probs);
-    float *prob_of = probs + E;
+    // one CTA: its totals are all there is
+    const int before = cta_exclusive_sum(all, scan);
+    loss = warp_sum(loss);
+    if (lane == 0) part[warp] = loss;
+    int first = before;
 #pragma unroll
-    for (int i = 0; i < kMaxExperts / kThreads; ++i) {
-      const int e = threadIdx.x + i * kThreads;
+    for (int i = 0; i < kEach; ++i) {
+      const int e = threadIdx.x * kEach + i;
       if (e < E) {
-        total_of[e] = totals[i];
-        prob_of[e] = p_of[i];
+        a.counts[e] = total[i];
+        a.offs[e] = first;
+        first_row[e] = first;
       }
+      first += total[i];
+    }
+    if (threadIdx.x == kThreads - 1) {
+      a.offs[E] = first;
+      all_rows = first;
     }
     __syncthreads();
-    // thread i sums the experts 2i and 2i + 1
-    const int e0 = 2 * threadIdx.x;
-    const int c0 = e0 < E ? total_of[e0] : 0, c1 = e0 + 1 < E ? total_of[e0 + 1] : 0;
-    const int first = cta_exclusive_sum(c0 + c1, scan);
-    float all = 0.0f;
-    if (e0 < E) {
-      a.counts[e0] = c0;
-      a.offs[e0] = first;
-      all = static_cast<float>(c0) * prob_of[e0];
-    }
-    if (e0 + 1 < E) {
-      a.counts[e0 + 1] = c1;
-      a.offs[e0 + 1] = first + c0;
-      all = fmaf(static_cast<float>(c1), prob_of[e0 + 1], all);
-    }
-    all = warp_sum(all);
-    const int n = warp_sum(c0 + c1);
-    if (lane == 0) {
-      part[warp] = all;
-      part[32 + warp] = __int_as_float(n);
-    }
-    __syncthreads();
-    float loss = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      loss += part[w];
-      rows += __float_as_int(part[32 + w]);
-    }
+    const int rows = all_rows;
     if (threadIdx.x == 0) {
-      a.offs[E] = rows;
+      loss = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) loss += part[w];
       a.tokens[0] = tokens;
-      a.loss[0] = tokens > 0 ? static_cast<float>(E) * (loss / static_cast<float>(rows)) /
-                                   static_cast<float>(tokens)
-                             : 0.0f;
+      a.loss[0] = balance(loss, E, rows, tokens);
     }
-    if (e0 < E) total_of[e0] = first;
-    if (e0 + 1 < E) total_of[e0 + 1] = first + c0;
-    __syncthreads();
     for (int i = rows + threadIdx.x; i < a.T * k; i += kThreads) a.order[i] = -1;
   }
 
   // the warp's choices again, now with their ranks in the CTA (or their rows)
-  const int *first_row = reinterpret_cast<const int *>(probs);
   for (int64_t i = lo * k + lane; i < hi * k; i += 32) {
     const int e = a.idx[i];
     if (e < 0) continue;
-    int row = a.slot[i] + mine[e];
+    int r = a.slot[i] + mine[e];
     if (alone) {
-      row += first_row[e];
-      a.order[row] = static_cast<int32_t>(i);
+      r += first_row[e];
+      a.order[r] = static_cast<int32_t>(i);
     }
-    a.slot[i] = row;
+    a.slot[i] = r;
   }
 }
 
 constexpr int kRowThreads = 1024;
 
+// add(i, load(i)) for i = first, first + step, ... below n, twenty loads in flight.
+template <typename Load, typename Add>
+__device__ __forceinline__ void in_flight(int n, int first, int step, Load load, Add add) {
+  constexpr int kBatch = 20;
+  for (int i0 = first; i0 < n; i0 += kBatch * step) {
+    decltype(load(0)) v[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      v[j] = 0;
+      if (i0 + j * step < n) v[j] = load(i0 + j * step);
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) add(i0 + j * step, v[j]);
+  }
+}
+
 // CTA b turns ranks into rows: expert e's choices of CTA b start at offs[e] plus
 // the counts of the CTAs before it.
 __global__ void __launch_bounds__(kRowThreads)
 route_rows_kernel(const RouteArgs a) {
-  __shared__ int total_of[kRowThreads], before_of[kRowThreads], scan[32];
-  __shared__ float prob_of[kRowThreads], part[64];
+  __shared__ int total_of[2 * kRowThreads], before_of[2 * kRowThreads], scan[32];
+  __shared__ float prob_of[kRowThreads], part[32];
+  __shared__ int rows;
   wait_for_previous_kernel();
   const int E = a.E, k = a.k, tid = threadIdx.x;
-  // the CTAs' counts are added up by as many groups of threads as there is room
-  // for, each taking every groups-th CTA
-  const int width = (E + 31) / 32 * 32, groups = kRowThreads / width;
-  const int e = tid % width, group = tid / width;
-  int total = 0, before = 0, tokens = 0;
-  float probs = 0.0f;
-  if (e < E && group < groups) {
-#pragma unroll 8
-    for (int b = group; b < a.ctas; b += groups) {
-      const int c = a.cta_counts[b * E + e];
-      total += c;
-      before += b < static_cast<int>(blockIdx.x) ? c : 0;
-    }
-    if (blockIdx.x == 0) {
-#pragma unroll 8
-      for (int b = group; b < a.ctas; b += groups) probs += a.cta_probs[b * E + e];
-    }
+  const bool last = blockIdx.x == gridDim.x - 1;  // writes the totals
+  // the CTAs' counts, two experts in a word, are added up by as many groups of
+  // threads as there is room for, each taking every groups-th CTA
+  const int words = (E + 1) / 2, width = (words + 31) / 32 * 32, groups = kRowThreads / width;
+  const int word = tid % width, group = tid / width;
+  int total[2] = {0, 0}, before[2] = {0, 0};
+  if (group < groups) {
+    const uint32_t *c = reinterpret_cast<const uint32_t *>(a.cta_counts) + word;
+    in_flight(a.ctas, group, groups, [&](int b) { return word < words ? c[static_cast<int64_t>(b) * words] : 0u; },
+              [&](int b, uint32_t w) {
+                const int lo = w & 0xFFFF, hi = w >> 16, here = b < static_cast<int>(blockIdx.x);
+                total[0] += lo;
+                total[1] += hi;
+                before[0] += here ? lo : 0;
+                before[1] += here ? hi : 0;
+              });
   }
-  total_of[tid] = total;
-  before_of[tid] = before;
-  prob_of[tid] = probs;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    total_of[2 * tid + h] = total[h];
+    before_of[2 * tid + h] = before[h];
+  }
+  // the probabilities in the same way, by the last CTA
+  const int wide = (E + 31) / 32 * 32, parts = kRowThreads / wide;
+  if (last) {
+    const int e = tid % wide;
+    float p = 0.0f;
+    if (tid / wide < parts)
+      in_flight(a.ctas, tid / wide, parts,
+                [&](int b) { return e < E ? a.cta_probs[static_cast<int64_t>(b) * E + e] : 0.0f; },
+                [&](int, float v) { p += v; });
+    prob_of[tid] = p;
+  }
   __syncthreads();
-  total = before = 0;
-  probs = 0.0f;
+  int mine = 0, ahead = 0;
   if (tid < E)
     for (int g = 0; g < groups; ++g) {
-      total += total_of[g * width + tid];
-      before += before_of[g * width + tid];
-      probs += prob_of[g * width + tid];
+      mine += total_of[2 * g * width + tid];
+      ahead += before_of[2 * g * width + tid];
     }
-  const int first = cta_exclusive_sum(total, scan);
+  float probs = 0.0f;
+  if (last && tid < E)
+    for (int g = 0; g < parts; ++g) probs += prob_of[g * wide + tid];
+  const int first = cta_exclusive_sum(mine, scan);
   __syncthreads();
-  if (tid < E) total_of[tid] = first + before;
-  if (tid == kRowThreads - 1) before_of[0] = first + total;
-  if (blockIdx.x == 0) {
-    for (int b = 0; b < a.ctas; ++b) tokens += a.cta_tokens[b];
-    write_totals(a, total, probs, first, tokens, part);
+  if (tid < E) total_of[tid] = first + ahead;
+  if (tid == kRowThreads - 1) rows = first + mine;
+  if (last) {
+    const int lane = tid & 31, warp = tid >> 5;
+    if (tid < E) {
+      a.counts[tid] = mine;
+      a.offs[tid] = first;
+    }
+    const float p = warp_sum(static_cast<float>(mine) * probs);
+    int tokens = 0;
+    for (int b = tid; b < a.ctas; b += kRowThreads) tokens += a.cta_tokens[b];
+    tokens = warp_sum(tokens);
+    if (lane == 0) {
+      part[warp] = p;
+      scan[warp] = tokens;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const float loss = warp_sum(part[lane]);
+      tokens = warp_sum(scan[lane]);
+      if (lane == 0) {
+        a.offs[E] = rows;
+        a.tokens[0] = tokens;
+        a.loss[0] = balance(loss, E, rows, tokens);
+      }
+    }
   }
   __syncthreads();
   const int64_t all = static_cast<int64_t>(a.T) * k;
@@ -413,11 +509,11 @@ route_rows_kernel(const RouteArgs a) {
   for (int64_t i = lo + tid; i < hi; i += kRowThreads) {
     const int x = a.idx[i];
     if (x >= 0) {
-      const int row = a.slot[i] + total_of[x];
-      a.slot[i] = row;
-      a.order[row] = static_cast<int32_t>(i);
+      const int r = a.slot[i] + total_of[x];
+      a.slot[i] = r;
+      a.order[r] = static_cast<int32_t>(i);
     }
-    if (i >= before_of[0]) a.order[i] = -1;
+    if (i >= rows) a.order[i] = -1;
   }
 }
 
@@ -444,10 +540,10 @@ struct BwdArgs {
 template <int kKind, int V>
 __global__ void __launch_bounds__(256)
 route_bwd_kernel(const BwdArgs a) {
-  extern __shared__ float us[];  // [warps][32 * V]
+  extern __shared__ __align__(16) float of_warps[];  // [warps][32 * V]
   wait_for_previous_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E, k = a.k;
-  float *u_of = us + warp * 32 * V;
+  float *u_of = of_warps + warp * 32 * V;
   float dp[V];
   {
     int c[V], n = 0;
@@ -468,49 +564,77 @@ route_bwd_kernel(const BwdArgs a) {
   }
   __syncwarp();
   const int warps = gridDim.x * (blockDim.x >> 5);
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp; t < a.T; t += warps) {
+  // lane j's choice, and the row's logits
+  struct {
+    float l[V];
+    int at;
+    float dw;
+  } next;
+  const auto fetch = [&](int64_t t) {
     const bool valid = !a.valid || a.valid[t] != 0;
+    load_logits<kKind, V>(static_cast<const char *>(a.logits) + t * a.ld * size_of(kKind), E, lane, a.vec, next.l);
+    next.at = -1;
+    next.dw = 0.0f;
+    if (lane < k && a.dweight) {
+      next.at = a.idx[t * k + lane];
+      if (next.at >= E) next.at = -1;
+      next.dw = a.dweight[t * k + lane] * a.scale;
+    }
+    if (!valid) {
+      next.at = -1;
+#pragma unroll
+      for (int v = 0; v < V; ++v) next.l[v] = -INFINITY;
+    }
+  };
+  int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp;
+  if (t < a.T) fetch(t);
+  for (; t < a.T; t += warps) {
+    float l[V], s[V], c[V];  // c: 1 - s of a sigmoid
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = next.l[v];
+    const int at = next.at;
+    const float dw = next.dw;
     const char *row = static_cast<const char *>(a.logits) + t * a.ld * size_of(kKind);
-    int at = -1;
-    float dw = 0.0f, x = 0.0f;
-    if (lane < k && a.dweight && valid) {
-      at = a.idx[t * k + lane];
-      dw = a.dweight[t * k + lane] * a.scale;
-      if (at >= 0 && at < E) {
-        x = logit_at(row, kKind, at);
-        if (!(x > -INFINITY)) at = -1;
-        x = fminf(x, kBig);
-      } else {
-        at = -1;
+    if (t + warps < a.T) fetch(t + warps);  // in flight while this token is dealt with
+
+    bool special = false;
+#pragma unroll
+    for (int v = 0; v < V; ++v) special |= !(l[v] < INFINITY);
+    if (__any_sync(~0u, special)) make_finite(l);
+    float sum = 0.0f, m = 0.0f;
+    if (a.sigmoid) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float e = exp_minus(l[v]);
+        s[v] = rcp_ftz(1.0f + e);
+        c[v] = fminf(e, 0x1p126f) * s[v];  // any value will do where s is 0
+        sum += s[v];
+      }
+    } else {
+      m = -kBig;
+#pragma unroll
+      for (int v = 0; v < V; ++v) m = fmaxf(m, l[v]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        s[v] = exp_above(l[v], m);
+        c[v] = 1.0f;
+        sum += s[v];
       }
     }
-    float l[V], s[V];
-    load_logits<kKind, V>(row, E, lane, a.vec, l);
-    float m = -kBig;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (!valid || !(l[v] > -INFINITY)) l[v] = -INFINITY;
-      l[v] = fminf(l[v], kBig);
-      m = fmaxf(m, l[v]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-    float sum = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      s[v] = !(l[v] > -INFINITY) ? 0.0f : a.sigmoid ? sigmoid(l[v]) : expf(l[v] - m);
-      sum += s[v];
-    }
-    const float inv = 1.0f / fmaxf(warp_sum(sum), kTiny);
     float pdp = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) pdp = fmaf(s[v] * inv, dp[v], pdp);
-    pdp = warp_sum(pdp);
+    for (int v = 0; v < V; ++v) pdp = fmaf(s[v], dp[v], pdp);
+    const float inv = rcp_ftz(fmaxf(warp_sum(sum), kTiny));
+    pdp = warp_sum(pdp) * inv;
 
-    float u = at < 0 ? 0.0f : a.sigmoid ? sigmoid(x) : expf(x - m) * inv;
-    if (at < 0) dw = 0.0f;
+    // lane j has choice j's score and gradient; the gradients change lanes through
+    // shared memory, all zeros but for these
+    const float x = at >= 0 ? fminf(logit_at(row, kKind, at), kBig) : 0.0f;
+    float u = at < 0 || !(x > -INFINITY) ? 0.0f : a.sigmoid ? sigmoid(x) : exp_above(x, m) * inv;
     if (a.normalise) {
-      u = u / fmaxf(warp_sum(u), kTiny);
+      u *= rcp_ftz(fmaxf(warp_sum(u), kTiny));
       u *= dw - warp_sum(u * dw);
     } else {
       u *= dw;
@@ -518,17 +642,27 @@ route_bwd_kernel(const BwdArgs a) {
     const float usum = a.sigmoid || a.normalise ? 0.0f : warp_sum(u);
     if (at >= 0) atomicAdd(u_of + at, u);
     __syncwarp();
-    float d[V];
+    float us[V];
+    if constexpr (V % 4 == 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float p = s[v] * inv;
-      d[v] = fmaf(p, dp[v] - pdp - usum, u_of[lane * V + v]);
-      if (a.sigmoid) d[v] *= sigmoid(-l[v]);
-      if (!(l[v] > -INFINITY)) d[v] = 0.0f;
+      for (int v = 0; v < V; v += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(u_of + lane * V + v);
+        us[v] = f.x;
+        us[v + 1] = f.y;
+        us[v + 2] = f.z;
+        us[v + 3] = f.w;
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) us[v] = u_of[lane * V + v];
     }
     __syncwarp();
     if (at >= 0) u_of[at] = 0.0f;
-    __syncwarp();
+    // closed experts have s = 0 and u = 0
+    const float z = pdp + usum;
+    float d[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) d[v] = fmaf(s[v] * inv, dp[v] - z, us[v]) * c[v];
 
     char *out = static_cast<char *>(a.dlogits) + t * a.ld_d * size_of(kKind);
     const int e0 = lane * V;
@@ -551,14 +685,19 @@ route_bwd_kernel(const BwdArgs a) {
   }
 }
 
+// The same for every device, so that the probabilities' sums are too.
 struct Plan {
-  int ctas, per_cta, per_warp;
+  int ctas, per_cta;
 };
-Plan plan(int64_t T) {
+Plan plan(int64_t T, int64_t E) {
+  const int warps = warps_for(E <= 256 ? 8 : E <= 512 ? 16 : 32);
   Plan p;
-  p.ctas = T <= kOneCta ? 1 : static_cast<int>(T < kMaxCtas * kWarps ? (T + kWarps - 1) / kWarps : kMaxCtas);
+  p.ctas = 1;
+  if (T > kOneCta) {
+    const int64_t full = (T + warps - 1) / warps, most = (T + kMaxPerCta - 1) / kMaxPerCta;
+    p.ctas = static_cast<int>(most > kSms ? most : full < kSms ? full : kSms);
+  }
   p.per_cta = static_cast<int>((T + p.ctas - 1) / p.ctas);
-  p.per_warp = (p.per_cta + kWarps - 1) / kWarps;
   return p;
 }
 
@@ -568,12 +707,13 @@ bool shape_ok(int64_t T, int64_t E) {
 
 template <int kKind, int V>
 fp8q_status launch_route(const RouteArgs &a, cudaStream_t s) {
+  constexpr int kWarps = warps_for(V), kMost = kWarps * 32 * V * 8;
   const size_t smem = static_cast<size_t>(kWarps) * a.E * (sizeof(int) + sizeof(float));
   const auto kern = route_kernel<kKind, V>;
-  if (smem > 40 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kWarps * kMaxExperts * 8) != cudaSuccess)
+  if (kMost > 40 * 1024 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess)
     return FP8Q_ERR_CUDA;
-  if (fp8q_status st = launch_dependent(kern, dim3(a.ctas), dim3(kThreads), smem, s, a)) return st;
+  if (fp8q_status st = launch_dependent(kern, dim3(a.ctas), dim3(32 * kWarps), smem, s, a)) return st;
   if (a.ctas == 1) return FP8Q_OK;
   return launch_dependent(route_rows_kernel, dim3(a.ctas), dim3(kRowThreads), 0, s, a);
 }
@@ -590,7 +730,7 @@ fp8q_status launch_route(const RouteArgs &a, cudaStream_t s) {
 
 template <int kKind, int V>
 fp8q_status launch_bwd(const BwdArgs &a, cudaStream_t s) {
-  const int warps = 8, need = (a.T + warps - 1) / warps, most = kMaxCtas * 8;
+  const int warps = 8, need = (a.T + warps - 1) / warps, most = kSms * 4;
   const size_t smem = static_cast<size_t>(warps) * 32 * V * sizeof(float);
   return launch_dependent(route_bwd_kernel<kKind, V>, dim3(need < most ? need : most), dim3(32 * warps),
                           smem, s, a);
@@ -621,8 +761,8 @@ using namespace fp8q;
 
 extern "C" int64_t fp8q_route_workspace_bytes(int64_t T, int64_t E) {
   if (!shape_ok(T, E)) return 0;
-  const Plan p = plan(T);
-  return p.ctas <= 1 ? 0 : (2 * E + 1) * static_cast<int64_t>(p.ctas) * 4;
+  const Plan p = plan(T, E);
+  return p.ctas <= 1 ? 0 : ((E + 1) / 2 + E + 1) * static_cast<int64_t>(p.ctas) * 4;
 }
 
 extern "C" fp8q_status fp8q_route(const void *logits, int64_t ld, int dtype, const uint8_t *valid,
@@ -648,7 +788,7 @@ extern "C" fp8q_status fp8q_route(const void *logits, int64_t ld, int dtype, con
     return FP8Q_ERR_ALIGN;
   DeviceInfo dev;
   if (fp8q_status st = device_info(dev)) return st;
-  const Plan p = plan(T);
+  const Plan p = plan(T, E);
   RouteArgs a{};
   a.logits = logits;
   a.valid = valid;
@@ -660,16 +800,15 @@ extern "C" fp8q_status fp8q_route(const void *logits, int64_t ld, int dtype, con
   a.tokens = tokens;
   a.weight = weight;
   a.loss = loss;
-  a.cta_counts = static_cast<int *>(workspace);
-  a.cta_probs = static_cast<float *>(workspace) + E * p.ctas;
-  a.cta_tokens = static_cast<int *>(workspace) + 2 * E * p.ctas;
+  a.cta_counts = static_cast<uint16_t *>(workspace);
+  a.cta_probs = static_cast<float *>(workspace) + (E + 1) / 2 * p.ctas;
+  a.cta_tokens = static_cast<int *>(workspace) + ((E + 1) / 2 + E) * p.ctas;
   a.ld = ld;
   a.T = static_cast<int>(T);
   a.E = static_cast<int>(E);
   a.k = static_cast<int>(k);
   a.ctas = p.ctas;
   a.per_cta = p.per_cta;
-  a.per_warp = p.per_warp;
   a.scale = scale;
   a.sigmoid = score == FP8Q_SCORE_SIGMOID;
   a.normalise = normalise != 0;
