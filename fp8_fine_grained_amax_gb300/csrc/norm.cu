@@ -56,6 +56,31 @@ struct NormArgs {
   bool w_fp32, pow2;
 };
 
+// y of one vector and its code, all lanes of the warp together (the 16 lanes of a
+// group are all in the row, or none is).
+__device__ __forceinline__ void finish8(const NormArgs &a, int64_t row, int vec, bool in, float rstd,
+                                        const float (&w)[8], float (&h)[8]) {
+  if (in) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = h[e] * rstd * w[e];
+    if (a.y) store8<kBf16>(a.y, row * a.ldy + 8 * vec, h);
+  }
+  if (!a.q) return;
+  float m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) m = max3_abs(m, h[e], h[e + 1]);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+  float s, inv;
+  group_scale(m, a.pow2, s, inv);
+  if (!in) return;
+  if ((vec & 15) == 0) a.s[static_cast<int64_t>(vec >> 4) * a.ld_s + row] = s;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) h[e] *= inv;
+  *reinterpret_cast<uint2 *>(a.q + row * a.ldq + 8 * vec) =
+      make_uint2(codes4(h[0], h[1], h[2], h[3]), codes4(h[4], h[5], h[6], h[7]));
+}
+
 // kX, kRes: kinds of x and of the residual; V: 8-column vectors per thread.
 template <int kX, int kRes, int V, bool kWarpRow>
 __global__ void __launch_bounds__(kWarpRow ? 32 * kRowWarps : 1024)
@@ -115,30 +140,109 @@ rmsnorm_kernel(const NormArgs a) {
     const int vec = first + i * step;
     const bool in = vec < a.nvec;  // the same for the 16 lanes of a group
     float w[8];
-    if (in) {
-      load8_w(a.w, a.w_fp32, 8 * vec, w);
+    if (in) load8_w(a.w, a.w_fp32, 8 * vec, w);
+    finish8(a, row, vec, in, rstd, w, h[i]);
+  }
+}
+
+// One 16-byte piece of a row into this thread's own place of the ring.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// One array's part of a ring: per stage and thread the 16 or 32 bytes of its
+// vector, in planes of 16 bytes (no bank conflicts).  A thread reads back only what
+// it has copied itself, so the ring needs no barrier.
+template <int kKind>
+struct RingPart {
+  static constexpr int kPlanes = kKind == kNone ? 0 : kKind == kBf16 ? 1 : 2;
+  __device__ __forceinline__ static void fetch(uint32_t at, int threads, const void *base, int64_t from) {
+    const char *p = static_cast<const char *>(base) + from * size_of(kKind);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[i][e] = h[i][e] * rstd * w[e];
-      if (a.y) store8<kBf16>(a.y, row * a.ldy + 8 * vec, h[i]);
+    for (int i = 0; i < kPlanes; ++i) copy16(at + i * threads * 16, p + 16 * i);
+  }
+  __device__ __forceinline__ static void values(uint32_t at, int threads, float (&v)[8]) {
+    if constexpr (kKind == kBf16) unpack8(ld_shared_v4(at), v);
+    else unpack8(ld_shared_v4(at), ld_shared_v4(at + threads * 16), v);
+  }
+};
+
+// Rows of up to 8192 columns, one vector per thread: CTA b takes rows b,
+// b + gridDim, ..., with kStages - 1 rows on their way into shared memory while one
+// is dealt with.
+template <int kX, int kRes, int kStages>
+__global__ void __launch_bounds__(1024)
+rmsnorm_rows_kernel(const NormArgs a) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float part[2][32];
+  using X = RingPart<kX>;
+  using R = RingPart<kRes>;
+  wait_for_previous_kernel();
+  const int vec = threadIdx.x, threads = blockDim.x;
+  const bool in = vec < a.nvec;  // the same for the 16 lanes of a group
+  const uint32_t stage_bytes = (X::kPlanes + R::kPlanes) * 16 * threads;
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * 16;
+  const auto fetch = [&](int64_t row, int stage) {
+    if (in && row < a.T) {
+      const uint32_t at = mine + stage * stage_bytes;
+      X::fetch(at, threads, a.x, row * a.ldx + 8 * vec);
+      if constexpr (kRes != kNone)
+        R::fetch(at + X::kPlanes * 16 * threads, threads, a.res, row * a.ld_res + 8 * vec);
     }
-    if (a.q) {
-      float m = 0.0f;
+    copies_commit();
+  };
+  const int64_t step = gridDim.x;
+  int64_t row = blockIdx.x;
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) m = max3_abs(m, h[i][e], h[i][e + 1]);
+  for (int i = 0; i < kStages - 1; ++i) fetch(row + i * step, i);
+  float w[8] = {};
+  if (in) load8_w(a.w, a.w_fp32, 8 * vec, w);
+
+  int turn = 0, stage = 0;
+  for (; row < a.T; row += step, turn ^= 1) {
+    fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+    copies_wait<kStages - 1>();
+    float h[8] = {};
+    if (in) {
+      const uint32_t at = mine + stage * stage_bytes;
+      X::values(at, threads, h);
+      if constexpr (kRes != kNone) {
+        float z[8];
+        R::values(at + X::kPlanes * 16 * threads, threads, z);
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-      float s, inv;
-      group_scale(m, a.pow2, s, inv);
-      if (in) {
-        if ((vec & 15) == 0) a.s[static_cast<int64_t>(vec >> 4) * a.ld_s + row] = s;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] *= inv;
-        *reinterpret_cast<uint2 *>(a.q + row * a.ldq + 8 * vec) =
-            make_uint2(codes4(h[i][0], h[i][1], h[i][2], h[i][3]),
-                       codes4(h[i][4], h[i][5], h[i][6], h[i][7]));
+        for (int e = 0; e < 8; ++e) h[e] += z[e];
+        if (a.r) store8<kRes>(a.r, row * a.ld_r + 8 * vec, h);
       }
     }
+    stage = stage == kStages - 1 ? 0 : stage + 1;
+    float sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fmaf(h[e], h[e], sum);
+    sum = row_sum<false>(sum, part[turn]);
+    const float rstd = 1.0f / sqrtf(fmaf(sum, a.inv_c, a.eps));
+    if (a.rstd && vec == 0) a.rstd[row] = rstd;
+    finish8(a, row, vec, in, rstd, w, h);
   }
+}
+
+constexpr int kSms = 152;
+constexpr int kRingBytes = 216 * 1024;  // of an SM's shared memory
+
+template <typename... KArgs, typename... Args>
+fp8q_status launch_ring(void (*kern)(KArgs...), dim3 grid, int threads, int smem, cudaStream_t s,
+                        Args &&...args) {
+  if (smem > 40 * 1024 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess)
+    return FP8Q_ERR_CUDA;
+  return launch_dependent(kern, grid, dim3(threads), smem, s, args...);
 }
 
 // Threads for one row of nvec vectors, V of them each.
@@ -151,6 +255,17 @@ fp8q_status launch_norm(const NormArgs &a, cudaStream_t s) {
     if (a.nvec <= 32) return launch_dependent(rmsnorm_kernel<kX, kRes, 1, true>, grid, dim3(32 * kRowWarps), 0, s, a);
     if (a.nvec <= 64) return launch_dependent(rmsnorm_kernel<kX, kRes, 2, true>, grid, dim3(32 * kRowWarps), 0, s, a);
     return launch_dependent(rmsnorm_kernel<kX, kRes, 4, true>, grid, dim3(32 * kRowWarps), 0, s, a);
+  }
+  const int threads = row_threads(a.nvec, 1);
+  if (threads <= 1024) {
+    constexpr int kPlanes = RingPart<kX>::kPlanes + RingPart<kRes>::kPlanes;
+    const int per_sm = 1024 / threads;
+    const int stage = kPlanes * 16 * threads;
+    const int64_t most = static_cast<int64_t>(kSms) * per_sm;
+    const dim3 grid(static_cast<unsigned>(a.T < most ? a.T : most));
+    if (4 * stage * per_sm <= kRingBytes)
+      return launch_ring(rmsnorm_rows_kernel<kX, kRes, 4>, grid, threads, 4 * stage, s, a);
+    return launch_ring(rmsnorm_rows_kernel<kX, kRes, 2>, grid, threads, 2 * stage, s, a);
   }
   const dim3 grid(static_cast<unsigned>(a.T));
   return launch_dependent(rmsnorm_kernel<kX, kRes, 4, false>, grid, dim3(row_threads(a.nvec, 4)), 0, s, a);
@@ -247,39 +362,55 @@ rmsnorm_bwd_warp_kernel(const BwdArgs a) {
   }
 }
 
-// Rows of up to 8192 columns: one vector per thread, the next row's loads in
-// flight while this one is summed and written.
-template <int kDy, int kX, int kDx>
+// Rows of up to 8192 columns: one vector per thread, the next rows on their way into
+// shared memory as in the forward pass.
+template <int kDy, int kX, int kDx, int kStages>
 __global__ void __launch_bounds__(1024)
 rmsnorm_bwd_kernel(const BwdArgs a) {
-  __shared__ float sums[2][32];
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float sums[2][32], rstds[kStages][32];  // a warp's own copy of its rows' rstd
+  using Y = RingPart<kDy>;
+  using X = RingPart<kX>;
+  using D = RingPart<kDx>;
   wait_for_previous_kernel();
-  const int vec = threadIdx.x;
+  const int vec = threadIdx.x, threads = blockDim.x;
   const bool in = vec < a.nvec;
+  const uint32_t plane = 16 * threads;
+  const uint32_t stage_bytes = (Y::kPlanes + X::kPlanes + (a.dres ? D::kPlanes : 0)) * plane;
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * 16;
+  const uint32_t my_rstd = smem_u32(&rstds[0][threadIdx.x >> 5]);
+  const auto fetch = [&](int64_t row, int stage) {
+    if ((threadIdx.x & 31) == 0 && row < a.T) copy4(my_rstd + stage * 128, a.rstd + row);
+    if (in && row < a.T) {
+      const uint32_t at = mine + stage * stage_bytes;
+      Y::fetch(at, threads, a.dy, row * a.ld_dy + 8 * vec);
+      X::fetch(at + Y::kPlanes * plane, threads, a.x, row * a.ldx + 8 * vec);
+      if (a.dres)
+        D::fetch(at + (Y::kPlanes + X::kPlanes) * plane, threads, a.dres, row * a.ld_dres + 8 * vec);
+    }
+    copies_commit();
+  };
+  const int64_t step = gridDim.x;
+  int64_t row = blockIdx.x;
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(row + i * step, i);
   float w[8] = {}, dw[8] = {};
   if (in) load8_w(a.w, a.w_fp32, 8 * vec, w);
-  Raw<kDy> dy{};
-  Raw<kX> x{};
-  Raw<kDx> dres{};
-  float rstd = 0.0f;
-  const auto fetch = [&](int64_t row) {
-    rstd = a.rstd[row];
+
+  int turn = 0, stage = 0;
+  for (; row < a.T; row += step, turn ^= 1) {
+    fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+    copies_wait<kStages - 1>();
+    __syncwarp();  // the copy of rstd is lane 0's; it is overwritten after the row's barrier
+    const float rs = *(volatile float *)&rstds[stage][threadIdx.x >> 5];
+    float t[8] = {}, xh[8] = {}, d[8] = {};
     if (in) {
-      dy.load(a.dy, row * a.ld_dy + 8 * vec);
-      x.load(a.x, row * a.ldx + 8 * vec);
-      if (a.dres) dres.load(a.dres, row * a.ld_dres + 8 * vec);
+      const uint32_t at = mine + stage * stage_bytes;
+      Y::values(at, threads, t);
+      X::values(at + Y::kPlanes * plane, threads, xh);
+      if (a.dres) D::values(at + (Y::kPlanes + X::kPlanes) * plane, threads, d);
     }
-  };
-  int turn = 0;
-  int64_t row = blockIdx.x;
-  if (row < a.T) fetch(row);
-  for (; row < a.T; row += gridDim.x, turn ^= 1) {
-    float t[8], xh[8], d[8];
-    dy.values(t);
-    x.values(xh);
-    dres.values(d);
-    const float rs = rstd;
-    if (row + gridDim.x < a.T) fetch(row + gridDim.x);
+    stage = stage == kStages - 1 ? 0 : stage + 1;
     float sum = 0.0f;
     bwd_terms(t, xh, w, rs, dw, sum);
     if (!a.dx) continue;
@@ -372,7 +503,7 @@ rmsnorm_dw_kernel(const float *part, int n, int C, float *dw, bool accumulate) {
 int bwd_ctas(int64_t T, int64_t C) {
   const int64_t rows = C <= kWarpCols ? (T + kRowWarps - 1) / kRowWarps : T;
   const int64_t most =
-      152 * (C <= kWarpCols ? 4 : C <= kCtaCols ? 1024 / row_threads(static_cast<int>(C / 8), 1) : 1);
+      kSms * (C <= kWarpCols ? 4 : C <= kCtaCols ? 1024 / row_threads(static_cast<int>(C / 8), 1) : 1);
   return static_cast<int>(rows < most ? rows : most);
 }
 
@@ -389,8 +520,14 @@ fp8q_status launch_bwd(const BwdArgs &a, cudaStream_t s) {
       return launch_dependent(rmsnorm_bwd_warp_kernel<kDy, kX, kDx, 2>, grid, block, smem, s, a);
     return launch_dependent(rmsnorm_bwd_warp_kernel<kDy, kX, kDx, 4>, grid, block, smem, s, a);
   }
-  if (C <= kCtaCols)
-    return launch_dependent(rmsnorm_bwd_kernel<kDy, kX, kDx>, grid, dim3(row_threads(a.nvec, 1)), 0, s, a);
+  if (C <= kCtaCols) {
+    const int threads = row_threads(a.nvec, 1), per_sm = 1024 / threads;
+    const int planes = RingPart<kDy>::kPlanes + RingPart<kX>::kPlanes + (a.dres ? RingPart<kDx>::kPlanes : 0);
+    const int stage = planes * 16 * threads;
+    if (4 * stage * per_sm <= kRingBytes)
+      return launch_ring(rmsnorm_bwd_kernel<kDy, kX, kDx, 4>, grid, threads, 4 * stage, s, a);
+    return launch_ring(rmsnorm_bwd_kernel<kDy, kX, kDx, 2>, grid, threads, 2 * stage, s, a);
+  }
   const auto kern = rmsnorm_bwd_long_kernel<kDy, kX, kDx>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kMaxCols * sizeof(float)) != cudaSuccess)
