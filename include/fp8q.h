@@ -438,7 +438,7 @@ fp8q_status fp8q_rmsnorm(const void *x, int64_t ldx, int x_dtype, const void *re
  * Results, at least one required:
  *   dx    [T][ld_dx] of out_dtype: the gradient of x and of res alike.
  *   dw    FP32 [C]; added to what it holds where accumulate is not 0.  Summed in
- *         an order that depends on T and C alone.  T == 0 gives zeros.
+ *         an order that depends on T, C and the types alone.  T == 0 gives zeros.
  *   workspace  for dw: device scratch of fp8q_rmsnorm_bwd_workspace_bytes(T, C)
  *              bytes (0 for sizes outside the limits), 16-byte aligned, owned by
  *              the caller; contents on entry do not matter.

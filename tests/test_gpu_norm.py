@@ -13,7 +13,8 @@ Tolerances (u = 2^-24), for C columns:
   dx   : t = dy w and xh with a rounding each; c is a sum of C products, 42 terms deep at
          most, so off by 46 u of the sum of magnitudes / C; four more roundings of each
          term.
-  dw   : at most ceil(T / 152) rows one after another in a CTA and 160 partial sums: as
+  dw   : at most ceil(T / 152) rows one after another in a CTA and 912 partial sums in
+         32 parts and a tree, at most 40 deep: well below 160 more: as
          many u of the sum of magnitudes, and 3 for each product.
 """
 import pytest
