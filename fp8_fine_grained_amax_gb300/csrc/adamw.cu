@@ -124,35 +124,84 @@ __device__ __forceinline__ void put_codes(void *base, int64_t i, bool wide, int 
       if (e < left) p[e] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
   }
 }
-__device__ __forceinline__ void decode8(uint2 c, float s, float (&v)[8]) {
+// Four pairs of values: two-lane FP32 arithmetic (each lane rounded as by itself).
+using Pairs = uint64_t[4];
+__device__ __forceinline__ void pack(const float (&v)[8], Pairs &p) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = pack_f32x2(v[2 * i], v[2 * i + 1]);
+}
+__device__ __forceinline__ void unpack(const Pairs &p, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack_f32x2(p[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ uint64_t both(float v) { return pack_f32x2(v, v); }
+
+// The sum of two products that are rounded before it: a packed addition is joined with
+// a packed product into one rounding by the assembler, a scalar one is not.
+__device__ __forceinline__ uint64_t sum2(uint64_t a, uint64_t b) {
+  const float2 x = unpack_f32x2(a), y = unpack_f32x2(b);
+  return pack_f32x2(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
+}
+
+__device__ __forceinline__ void decode8(uint2 c, float s, Pairs &v) {
   const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
     const uint32_t d = decode_e4m3x2(static_cast<uint16_t>(w[h >> 1] >> (16 * (h & 1))));
-    v[2 * h] = f16_lo(d) * s;
-    v[2 * h + 1] = f16_hi(d) * s;
+    v[h] = fmul2(pack_f32x2(f16_lo(d), f16_hi(d)), both(s));
   }
 }
-// Codes of a group of 128 values, 8 in each of 16 lanes, and its scale: with a the
-// max-abs (at least 2^-116) s = a * fl(1 / 448), codes E4M3(x * fl(448 * fl(1 / a))),
-// one quotient where the quantisers' rule takes two.  Their products with a stay at
-// or below 448 (1 + 2^-22), which E4M3 rounds to 448.
-template <bool kRoot>
-__device__ __forceinline__ uint2 encode8(const float (&v)[8], float &s) {
-  float a = 0.0f, c[8], inv;
+__device__ __forceinline__ float absmax8(const Pairs &p) {
+  float m = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; e += 2) a = max3_abs(a, v[e], v[e + 1]);
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack_f32x2(p[i]);
+    m = max3_abs(m, f.x, f.y);
+  }
+  return m;
+}
+__device__ __forceinline__ uint2 codes8(const Pairs &p) { return make_uint2(codes4(p[0], p[1]), codes4(p[2], p[3])); }
+
+// Codes of groups of 128 values of m and of sqrt(v), 8 in each of 16 lanes; a scale:
+// with a the max-abs (at least 2^-116) s = a * fl(1 / 448), codes
+// E4M3(x * fl(448 * fl(1 / a))), one quotient where the quantisers' rule takes two.
+// Their products with a stay at or below 448 (1 + 2^-22), which E4M3 rounds to 448.
+// The lower eight lanes reduce m and take its scale, the upper eight the root's; s is
+// each half's own.
+__device__ __forceinline__ void encode(Pairs &m, Pairs &r, uint2 &cm, uint2 &cr, float &s) {
+  const bool upper = threadIdx.x & 8;
+  const float am = absmax8(m), ar = absmax8(r);
+  float a = upper ? ar : am;
+  a = fmaxf(a, __shfl_xor_sync(~0u, upper ? am : ar, 8));
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
+  for (int o = 4; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
   a = fmaxf(a, 0x1p-116f);
   s = a * (1.0f / 448.0f);
-  inv = __fdiv_rn(1.0f, a) * 448.0f;
+  const float inv = __fdiv_rn(1.0f, a) * 448.0f, other = __shfl_xor_sync(~0u, inv, 8);
+  const uint64_t im = both(upper ? other : inv), ir = both(upper ? inv : other), up = both(0x1p100f);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    c[e] = v[e] * inv;
-    if (kRoot && v[e] > 0.0f) c[e] = fmaxf(c[e], 0x1p-9f);
+  for (int i = 0; i < 4; ++i) {
+    m[i] = fmul2(m[i], im);
+    // at least 2^-9 where the root, 2^-75 or more, is positive
+    const float2 c = unpack_f32x2(fmul2(r[i], ir)), least = unpack_f32x2(fmul2(r[i], up));
+    r[i] = pack_f32x2(fmaxf(c.x, fminf(least.x, 0x1p-9f)), fmaxf(c.y, fminf(least.y, 0x1p-9f)));
   }
-  return make_uint2(codes4(c[0], c[1], c[2], c[3]), codes4(c[4], c[5], c[6], c[7]));
+  cm = codes8(m);
+  cr = codes8(r);
+}
+
+// The codes of a root are steps of it, so it is the correctly rounded one; for the step
+// alone an approximation to one unit in the last place does.
+template <bool kExact>
+__device__ __forceinline__ float root(float v) {
+  if constexpr (kExact) return __fsqrt_rn(v);
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 template <int kP, int kG, int kS>
@@ -180,20 +229,26 @@ adamw_kernel(const __grid_constant__ Batch batch, const Args a) {
   }
   const float scale = a.grad_scale ? *a.grad_scale : 1.0f;
 
-  float p[kUnroll][8], g[kUnroll][8], m[kUnroll][8], v[kUnroll][8];
+  constexpr bool kCodes = kS == kStateE4m3;
+  Pairs p[kUnroll], g[kUnroll], m[kUnroll], v[kUnroll];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const int64_t i = base + u * kThreads * 8, rest = t.n - i;
     const int left = rest < 8 ? static_cast<int>(rest < 0 ? 0 : rest) : 8;
     const bool wide = aligned && left == 8;
-    get8<kP>(t.p, i, wide, left, p[u]);
-    get8<kG>(t.g, i, wide, left, g[u]);
-    if constexpr (kS == kStateE4m3) {
+    float x[8];
+    get8<kP>(t.p, i, wide, left, x);
+    pack(x, p[u]);
+    get8<kG>(t.g, i, wide, left, x);
+    pack(x, g[u]);
+    if constexpr (kCodes) {
       decode8(get_codes(t.m, i, wide, left), left ? t.ms[i >> 7] : 0.0f, m[u]);
       decode8(get_codes(t.v, i, wide, left), left ? t.vs[i >> 7] : 0.0f, v[u]);
     } else {
-      get8<kS>(t.m, i, wide, left, m[u]);
-      get8<kS>(t.v, i, wide, left, v[u]);
+      get8<kS>(t.m, i, wide, left, x);
+      pack(x, m[u]);
+      get8<kS>(t.v, i, wide, left, x);
+      pack(x, v[u]);
     }
   }
 #pragma unroll
@@ -201,33 +256,40 @@ adamw_kernel(const __grid_constant__ Batch batch, const Args a) {
     const int64_t i = base + u * kThreads * 8, rest = t.n - i;
     const int left = rest < 8 ? static_cast<int>(rest < 0 ? 0 : rest) : 8;
     const bool wide = aligned && left == 8;
+    float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      // each product of the moments is rounded by itself, so that they are the same bits
+    for (int e = 0; e < 4; ++e) {
+      // each operation on the moments is rounded by itself, so that they are the same bits
       // in every compilation: a code is a step function of them
-      const float d = __fmul_rn(g[u][e], scale);
-      const float v0 = kS == kStateE4m3 ? __fmul_rn(v[u][e], v[u][e]) : v[u][e];
-      m[u][e] = __fadd_rn(__fmul_rn(a.b1, m[u][e]), __fmul_rn(a.omb1, d));
-      v[u][e] = __fadd_rn(__fmul_rn(a.b2, v0), __fmul_rn(__fmul_rn(a.omb2, d), d));
-      const float root = sqrtf(v[u][e]);
-      const float step = m[u][e] * ic1 / fmaf(root, isc2, a.eps);
-      p[u][e] = fmaf(-lr, fmaf(a.wd, p[u][e], step), p[u][e]);
-      if (kS == kStateE4m3) v[u][e] = root;
+      const uint64_t d = fmul2(g[u][e], both(scale));
+      const uint64_t v0 = kCodes ? fmul2(v[u][e], v[u][e]) : v[u][e];
+      m[u][e] = sum2(fmul2(both(a.b1), m[u][e]), fmul2(both(a.omb1), d));
+      v[u][e] = sum2(fmul2(both(a.b2), v0), fmul2(fmul2(both(a.omb2), d), d));
+      const float2 s = unpack_f32x2(v[u][e]);
+      const uint64_t r = pack_f32x2(root<kCodes>(s.x), root<kCodes>(s.y));
+      const float2 den = unpack_f32x2(fma2(r, both(isc2), both(a.eps)));
+      const float2 num = unpack_f32x2(fmul2(m[u][e], both(ic1)));
+      const uint64_t step = pack_f32x2(__fdividef(num.x, den.x), __fdividef(num.y, den.y));
+      p[u][e] = fma2(both(-lr), fma2(both(a.wd), p[u][e], step), p[u][e]);
+      if (kCodes) v[u][e] = r;
     }
-    put8<kP>(t.p, i, wide, left, p[u]);
-    if (t.copy) put8<kBf16>(t.copy, i, wide, left, p[u]);
-    if constexpr (kS == kStateE4m3) {
-      float ms, vs;
-      const uint2 cm = encode8<false>(m[u], ms), cv = encode8<true>(v[u], vs);
+    unpack(p[u], x);
+    put8<kP>(t.p, i, wide, left, x);
+    if (t.copy) put8<kBf16>(t.copy, i, wide, left, x);
+    if constexpr (kCodes) {
+      uint2 cm, cr;
+      float s;
+      encode(m[u], v[u], cm, cr, s);
       put_codes(t.m, i, wide, left, cm);
-      put_codes(t.v, i, wide, left, cv);
-      if (left && (threadIdx.x & 15) == 0) {
-        t.ms[i >> 7] = ms;
-        t.vs[i >> 7] = vs;
-      }
+      put_codes(t.v, i, wide, left, cr);
+      // the group may end before the upper lanes' own values do
+      const int64_t group = i >> 7;
+      if ((threadIdx.x & 7) == 0 && group * 128 < t.n) (threadIdx.x & 8 ? t.vs : t.ms)[group] = s;
     } else {
-      put8<kS>(t.m, i, wide, left, m[u]);
-      put8<kS>(t.v, i, wide, left, v[u]);
+      unpack(m[u], x);
+      put8<kS>(t.m, i, wide, left, x);
+      unpack(v[u], x);
+      put8<kS>(t.v, i, wide, left, x);
     }
   }
 }

@@ -161,6 +161,23 @@ def test_many_tensors(state):
     check_step(State(sizes, "fp32", "fp32", state, True, seed=2), 1)
 
 
+def test_moments_are_rounded_after_every_operation():
+    # m and v are defined as FP32 products and sums, each rounded (in 64 bits here, then to FP32): the
+    # same bits, so that 8-bit codes do not hang on how a compiler joins operations
+    st = State([100001], seed=11)
+    f = lambda t: t.float().double()  # noqa: E731
+    b1, b2 = (float(torch.tensor(b, dtype=FP)) for b in (0.9, 0.95))
+    o1, o2 = (float(torch.tensor(1 - b, dtype=FP)) for b in (0.9, 0.95))
+    scale = torch.tensor([0.3], device="cuda")
+    for step in (1, 2, 3):
+        m, v = (t.double().cpu() for t in (st.m[0], st.v[0]))
+        d = f(st.g[0].double().cpu() * float(scale))
+        st.step(step=step, grad_scale=scale, **HYPER)
+        m, v = f(f(b1 * m) + f(o1 * d)), f(f(b2 * v) + f(f(o2 * d) * d))
+        assert torch.equal(st.m[0].double().cpu(), m) and torch.equal(st.v[0].double().cpu(), v)
+        st.new_gradients()
+
+
 def test_the_same_as_one_by_one():
     for state in ("fp32", "e4m3"):
         a, b = (State([5000, 333, 20000], "fp32", "fp32", state, seed=3) for _ in range(2))
