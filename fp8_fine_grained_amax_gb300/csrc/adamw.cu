@@ -5,8 +5,8 @@
 // Every value is read and written once: 28 bytes per value with FP32 parameters,
 // gradients and moments, 16 with moments in 8 bits, 2 more for the BF16 copy.  It
 // is bound by memory.  The list travels in the launch's parameters (no copy to the
-// device, so a captured call holds it too); a CTA takes one chunk of 4096 values
-// and finds its tensor by a binary search over the chunks' prefix sums.
+// device, so a captured call holds it too); a CTA takes one chunk of values and finds
+// its tensor by a binary search over the chunks' prefix sums.
 //
 // Moments in 8 bits: m and sqrt(v) as E4M3 with an FP32 scale per 128 values.  v
 // itself spans the square of the gradients' range, which E4M3 (2^-9 to 448 below
@@ -28,10 +28,13 @@
 namespace fp8q {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 2;                     // vectors of 8 values per thread
-constexpr int kChunk = kThreads * 8 * kUnroll;
-constexpr int kBatch = 128;                    // tensors per launch
+// Eight values per thread, one chunk per CTA, three CTAs per SM.  176 M values with
+// moments in 8 bits: 467 us; CTAs of 256 threads 595, of 512 506 (496 held to 64
+// registers), of 1024 657; two vectors per thread 556.  FP32 moments take 750 to 762 us
+// in all of these, ten small tensors 8.6 to 9.3 (two vectors) and 10.7 (1024 threads).
+constexpr int kThreads = 384;
+constexpr int kChunk = kThreads * 8;
+constexpr int kBatch = 128;  // tensors per launch
 
 enum State { kStateBf16 = FP8Q_STATE_BF16, kStateFp32 = FP8Q_STATE_FP32, kStateE4m3 = FP8Q_STATE_E4M3 };
 
@@ -217,7 +220,7 @@ adamw_kernel(const __grid_constant__ Batch batch, const Args a) {
   }
   const Tensor &t = batch.t[lo];
   const bool aligned = batch.wide[lo >> 5] >> (lo & 31) & 1;
-  const int64_t base = static_cast<int64_t>(chunk - batch.first[lo]) * kChunk + threadIdx.x * 8;
+  const int64_t i = static_cast<int64_t>(chunk - batch.first[lo]) * kChunk + threadIdx.x * 8;
 
   float lr = a.lr, ic1 = a.ic1, isc2 = a.isc2;
   if (a.lr_dev) lr = *a.lr_dev;
@@ -230,67 +233,57 @@ adamw_kernel(const __grid_constant__ Batch batch, const Args a) {
   const float scale = a.grad_scale ? *a.grad_scale : 1.0f;
 
   constexpr bool kCodes = kS == kStateE4m3;
-  Pairs p[kUnroll], g[kUnroll], m[kUnroll], v[kUnroll];
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t i = base + u * kThreads * 8, rest = t.n - i;
-    const int left = rest < 8 ? static_cast<int>(rest < 0 ? 0 : rest) : 8;
-    const bool wide = aligned && left == 8;
-    float x[8];
-    get8<kP>(t.p, i, wide, left, x);
-    pack(x, p[u]);
-    get8<kG>(t.g, i, wide, left, x);
-    pack(x, g[u]);
-    if constexpr (kCodes) {
-      decode8(get_codes(t.m, i, wide, left), left ? t.ms[i >> 7] : 0.0f, m[u]);
-      decode8(get_codes(t.v, i, wide, left), left ? t.vs[i >> 7] : 0.0f, v[u]);
-    } else {
-      get8<kS>(t.m, i, wide, left, x);
-      pack(x, m[u]);
-      get8<kS>(t.v, i, wide, left, x);
-      pack(x, v[u]);
-    }
+  const int64_t rest = t.n - i;
+  const int left = rest < 8 ? static_cast<int>(rest < 0 ? 0 : rest) : 8;
+  const bool wide = aligned && left == 8;
+  Pairs p, g, m, v;
+  float x[8];
+  get8<kP>(t.p, i, wide, left, x);
+  pack(x, p);
+  get8<kG>(t.g, i, wide, left, x);
+  pack(x, g);
+  if constexpr (kCodes) {
+    decode8(get_codes(t.m, i, wide, left), left ? t.ms[i >> 7] : 0.0f, m);
+    decode8(get_codes(t.v, i, wide, left), left ? t.vs[i >> 7] : 0.0f, v);
+  } else {
+    get8<kS>(t.m, i, wide, left, x);
+    pack(x, m);
+    get8<kS>(t.v, i, wide, left, x);
+    pack(x, v);
   }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t i = base + u * kThreads * 8, rest = t.n - i;
-    const int left = rest < 8 ? static_cast<int>(rest < 0 ? 0 : rest) : 8;
-    const bool wide = aligned && left == 8;
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      // each operation on the moments is rounded by itself, so that they are the same bits
-      // in every compilation: a code is a step function of them
-      const uint64_t d = fmul2(g[u][e], both(scale));
-      const uint64_t v0 = kCodes ? fmul2(v[u][e], v[u][e]) : v[u][e];
-      m[u][e] = sum2(fmul2(both(a.b1), m[u][e]), fmul2(both(a.omb1), d));
-      v[u][e] = sum2(fmul2(both(a.b2), v0), fmul2(fmul2(both(a.omb2), d), d));
-      const float2 s = unpack_f32x2(v[u][e]);
-      const uint64_t r = pack_f32x2(root<kCodes>(s.x), root<kCodes>(s.y));
-      const float2 den = unpack_f32x2(fma2(r, both(isc2), both(a.eps)));
-      const float2 num = unpack_f32x2(fmul2(m[u][e], both(ic1)));
-      const uint64_t step = pack_f32x2(__fdividef(num.x, den.x), __fdividef(num.y, den.y));
-      p[u][e] = fma2(both(-lr), fma2(both(a.wd), p[u][e], step), p[u][e]);
-      if (kCodes) v[u][e] = r;
-    }
-    unpack(p[u], x);
-    put8<kP>(t.p, i, wide, left, x);
-    if (t.copy) put8<kBf16>(t.copy, i, wide, left, x);
-    if constexpr (kCodes) {
-      uint2 cm, cr;
-      float s;
-      encode(m[u], v[u], cm, cr, s);
-      put_codes(t.m, i, wide, left, cm);
-      put_codes(t.v, i, wide, left, cr);
-      // the group may end before the upper lanes' own values do
-      const int64_t group = i >> 7;
-      if ((threadIdx.x & 7) == 0 && group * 128 < t.n) (threadIdx.x & 8 ? t.vs : t.ms)[group] = s;
-    } else {
-      unpack(m[u], x);
-      put8<kS>(t.m, i, wide, left, x);
-      unpack(v[u], x);
-      put8<kS>(t.v, i, wide, left, x);
-    }
+  for (int e = 0; e < 4; ++e) {
+    // each operation on the moments is rounded by itself, so that they are the same bits
+    // in every compilation: a code is a step function of them
+    const uint64_t d = fmul2(g[e], both(scale));
+    const uint64_t v0 = kCodes ? fmul2(v[e], v[e]) : v[e];
+    m[e] = sum2(fmul2(both(a.b1), m[e]), fmul2(both(a.omb1), d));
+    v[e] = sum2(fmul2(both(a.b2), v0), fmul2(fmul2(both(a.omb2), d), d));
+    const float2 s = unpack_f32x2(v[e]);
+    const uint64_t r = pack_f32x2(root<kCodes>(s.x), root<kCodes>(s.y));
+    const float2 den = unpack_f32x2(fma2(r, both(isc2), both(a.eps)));
+    const float2 num = unpack_f32x2(fmul2(m[e], both(ic1)));
+    const uint64_t step = pack_f32x2(__fdividef(num.x, den.x), __fdividef(num.y, den.y));
+    p[e] = fma2(both(-lr), fma2(both(a.wd), p[e], step), p[e]);
+    if (kCodes) v[e] = r;
+  }
+  unpack(p, x);
+  put8<kP>(t.p, i, wide, left, x);
+  if (t.copy) put8<kBf16>(t.copy, i, wide, left, x);
+  if constexpr (kCodes) {
+    uint2 cm, cr;
+    float s;
+    encode(m, v, cm, cr, s);
+    put_codes(t.m, i, wide, left, cm);
+    put_codes(t.v, i, wide, left, cr);
+    // the group may end before the upper lanes' own values do
+    const int64_t group = i >> 7;
+    if ((threadIdx.x & 7) == 0 && group * 128 < t.n) (threadIdx.x & 8 ? t.vs : t.ms)[group] = s;
+  } else {
+    unpack(m, x);
+    put8<kS>(t.m, i, wide, left, x);
+    unpack(v, x);
+    put8<kS>(t.v, i, wide, left, x);
   }
 }
 
