@@ -430,6 +430,15 @@ route_rows_kernel(const RouteArgs a) {
   __shared__ int rows;
   wait_for_previous_kernel();
   const int E = a.E, k = a.k, tid = threadIdx.x;
+  const int64_t all = static_cast<int64_t>(a.T) * k;
+  const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.per_cta * k;
+  const int64_t hi = min(all, lo + static_cast<int64_t>(a.per_cta) * k);
+  // the thread's first choice, in flight while the counts are added up
+  int next_idx = -1, next_slot = 0;
+  if (lo + tid < hi) {
+    next_idx = a.idx[lo + tid];
+    next_slot = a.slot[lo + tid];
+  }
   const bool last = blockIdx.x == gridDim.x - 1;  // writes the totals
   // the CTAs' counts, two experts in a word, are added up by as many groups of
   // threads as there is room for, each taking every groups-th CTA
@@ -503,13 +512,14 @@ route_rows_kernel(const RouteArgs a) {
     }
   }
   __syncthreads();
-  const int64_t all = static_cast<int64_t>(a.T) * k;
-  const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.per_cta * k;
-  const int64_t hi = min(all, lo + static_cast<int64_t>(a.per_cta) * k);
   for (int64_t i = lo + tid; i < hi; i += kRowThreads) {
-    const int x = a.idx[i];
+    const int x = next_idx, rank = next_slot;
+    if (i + kRowThreads < hi) {
+      next_idx = a.idx[i + kRowThreads];
+      next_slot = a.slot[i + kRowThreads];
+    }
     if (x >= 0) {
-      const int r = a.slot[i] + total_of[x];
+      const int r = rank + total_of[x];
       a.slot[i] = r;
       a.order[r] = static_cast<int32_t>(i);
     }
@@ -537,32 +547,15 @@ struct BwdArgs {
 //   dl  = (u + v) (1 - s) (sigmoid)  or  u - p sum u + v (softmax, sum u = 0 if
 //         normalised).
 // Nothing is divided by a score, so small ones lose nothing.
+constexpr int bwd_ctas_per_sm(int V) { return V <= 8 ? 4 : V == 16 ? 2 : 1; }
+
 template <int kKind, int V>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, bwd_ctas_per_sm(V))
 route_bwd_kernel(const BwdArgs a) {
   extern __shared__ __align__(16) float of_warps[];  // [warps][32 * V]
   wait_for_previous_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E, k = a.k;
   float *u_of = of_warps + warp * 32 * V;
-  float dp[V];
-  {
-    int c[V], n = 0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = lane * V + v;
-      u_of[e] = 0.0f;
-      c[v] = e < E && a.dloss ? a.counts[e] : 0;
-      n += c[v];
-    }
-    n = warp_sum(n);
-    const int tokens = a.dloss ? a.tokens[0] : 0;
-    const float f = tokens > 0 && n > 0 ? a.dloss[0] * static_cast<float>(E) / static_cast<float>(n) /
-                                              static_cast<float>(tokens)
-                                        : 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) dp[v] = f * static_cast<float>(c[v]);
-  }
-  __syncwarp();
   const int warps = gridDim.x * (blockDim.x >> 5);
   // lane j's choice, and the row's logits
   struct {
@@ -588,6 +581,25 @@ route_bwd_kernel(const BwdArgs a) {
   };
   int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp;
   if (t < a.T) fetch(t);
+  float dp[V];
+  {
+    int c[V], n = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = lane * V + v;
+      u_of[e] = 0.0f;
+      c[v] = e < E && a.dloss ? a.counts[e] : 0;
+      n += c[v];
+    }
+    n = warp_sum(n);
+    const int tokens = a.dloss ? a.tokens[0] : 0;
+    const float f = tokens > 0 && n > 0 ? a.dloss[0] * static_cast<float>(E) / static_cast<float>(n) /
+                                              static_cast<float>(tokens)
+                                        : 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) dp[v] = f * static_cast<float>(c[v]);
+  }
+  __syncwarp();
   for (; t < a.T; t += warps) {
     float l[V], s[V], c[V];  // c: 1 - s of a sigmoid
 #pragma unroll
@@ -640,7 +652,18 @@ route_bwd_kernel(const BwdArgs a) {
       u *= dw;
     }
     const float usum = a.sigmoid || a.normalise ? 0.0f : warp_sum(u);
-    if (at >= 0) atomicAdd(u_of + at, u);
+    // (a choice that comes twice, which the forward pass does not make, adds up)
+    if (at >= 0) u_of[at] = __int_as_float(lane);
+    __syncwarp();
+    const bool twice = at >= 0 && __float_as_int(u_of[at]) != lane;
+    __syncwarp();
+    if (__any_sync(~0u, twice)) {
+      if (at >= 0) u_of[at] = 0.0f;
+      __syncwarp();
+      if (at >= 0) atomicAdd(u_of + at, u);
+    } else if (at >= 0) {
+      u_of[at] = u;
+    }
     __syncwarp();
     float us[V];
     if constexpr (V % 4 == 0) {
@@ -730,7 +753,7 @@ fp8q_status launch_route(const RouteArgs &a, cudaStream_t s) {
 
 template <int kKind, int V>
 fp8q_status launch_bwd(const BwdArgs &a, cudaStream_t s) {
-  const int warps = 8, need = (a.T + warps - 1) / warps, most = kSms * 4;
+  const int warps = 8, need = (a.T + warps - 1) / warps, most = kSms * bwd_ctas_per_sm(V);
   const size_t smem = static_cast<size_t>(warps) * 32 * V * sizeof(float);
   return launch_dependent(route_bwd_kernel<kKind, V>, dim3(need < most ? need : most), dim3(32 * warps),
                           smem, s, a);
