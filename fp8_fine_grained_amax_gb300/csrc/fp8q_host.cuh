@@ -50,6 +50,20 @@ inline fp8q_status device_info(DeviceInfo &out) {
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Let kKern take up to `bytes` of dynamic shared memory; asked of the runtime once per
+// device (0.35 us a time).  Every call for a kernel gives the same bytes.
+template <auto kKern>
+inline fp8q_status allow_smem(int bytes) {
+  static std::atomic<bool> done[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FP8Q_ERR_CUDA;
+  if (done[dev].load(std::memory_order_acquire)) return FP8Q_OK;
+  if (cudaFuncSetAttribute(kKern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return FP8Q_ERR_CUDA;
+  done[dev].store(true, std::memory_order_release);
+  return FP8Q_OK;
+}
+
 // Launch `kern` on stream `s` and report this launch's own outcome: the value
 // cudaLaunchKernelEx returns, not the process-wide last-error state, which may
 // hold an earlier, unrelated error that belongs to the caller (reading it with

@@ -331,13 +331,11 @@ int ring_stages(int bytes, int budget) {
 }
 constexpr int kForwardBudget = 96 * 1024, kBackwardBudget = 132 * 1024;
 
-template <typename... KArgs, typename... Args>
-fp8q_status launch_ring(void (*kern)(KArgs...), int64_t ctas, int threads, int smem, cudaStream_t s,
-                        Args &&...args) {
-  if (smem > 40 * 1024 &&
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess)
-    return FP8Q_ERR_CUDA;
-  return launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), dim3(threads), smem, s, args...);
+template <auto kKern, typename Args>
+fp8q_status launch_ring(int64_t ctas, int threads, int smem, cudaStream_t s, const Args &a) {
+  if (smem > 40 * 1024)
+    if (fp8q_status st = allow_smem<kKern>(kRingBytes)) return st;
+  return launch_dependent(kKern, dim3(static_cast<unsigned>(ctas)), dim3(threads), smem, s, a);
 }
 
 // Threads for one row of nvec vectors, V of them each.
@@ -363,9 +361,9 @@ fp8q_status launch_norm(const NormArgs &a, cudaStream_t s) {
     return launch_dependent(rmsnorm_kernel<kX, kRes, 4, false>, dim3(static_cast<unsigned>(a.T)),
                             dim3(row_threads(a.nvec, 4)), 0, s, a);
   const int64_t most = static_cast<int64_t>(kSms) * per_sm, ctas = a.T < most ? a.T : most;
-  if (V == 1) return launch_ring(rmsnorm_rows_kernel<kX, kRes, 1>, ctas, threads, smem, s, b);
-  if (V == 2) return launch_ring(rmsnorm_rows_kernel<kX, kRes, 2>, ctas, threads, smem, s, b);
-  return launch_ring(rmsnorm_rows_kernel<kX, kRes, 4>, ctas, threads, smem, s, b);
+  if (V == 1) return launch_ring<rmsnorm_rows_kernel<kX, kRes, 1>>(ctas, threads, smem, s, b);
+  if (V == 2) return launch_ring<rmsnorm_rows_kernel<kX, kRes, 2>>(ctas, threads, smem, s, b);
+  return launch_ring<rmsnorm_rows_kernel<kX, kRes, 4>>(ctas, threads, smem, s, b);
 }
 
 // ------------------------------------------------------------------ backward
@@ -634,14 +632,14 @@ fp8q_status launch_bwd(const BwdArgs &a, const BwdPlan &p, cudaStream_t s) {
   const int ring = p.stages * C * (size_of(kDy) + size_of(kX) + (a.dres ? size_of(kDx) : 0));
   if (C <= kWarpCols) {
     const int sums = kRowWarps * C * static_cast<int>(sizeof(float)), smem = kRowWarps * ring > sums ? kRowWarps * ring : sums;
-    if (p.V == 1) return launch_ring(rmsnorm_bwd_kernel<kDy, kX, kDx, 1, true>, p.ctas, p.threads, smem, s, a);
-    if (p.V == 2) return launch_ring(rmsnorm_bwd_kernel<kDy, kX, kDx, 2, true>, p.ctas, p.threads, smem, s, a);
-    return launch_ring(rmsnorm_bwd_kernel<kDy, kX, kDx, 4, true>, p.ctas, p.threads, smem, s, a);
+    if (p.V == 1) return launch_ring<rmsnorm_bwd_kernel<kDy, kX, kDx, 1, true>>(p.ctas, p.threads, smem, s, a);
+    if (p.V == 2) return launch_ring<rmsnorm_bwd_kernel<kDy, kX, kDx, 2, true>>(p.ctas, p.threads, smem, s, a);
+    return launch_ring<rmsnorm_bwd_kernel<kDy, kX, kDx, 4, true>>(p.ctas, p.threads, smem, s, a);
   }
   if (p.stages && p.V == 1)
-    return launch_ring(rmsnorm_bwd_kernel<kDy, kX, kDx, 1, false>, p.ctas, p.threads, ring, s, a);
-  if (p.stages) return launch_ring(rmsnorm_bwd_kernel<kDy, kX, kDx, 2, false>, p.ctas, p.threads, ring, s, a);
-  return launch_ring(rmsnorm_bwd_long_kernel<kDy, kX, kDx>, p.ctas, 1024, static_cast<int>(sizeof(float)) * C, s, a);
+    return launch_ring<rmsnorm_bwd_kernel<kDy, kX, kDx, 1, false>>(p.ctas, p.threads, ring, s, a);
+  if (p.stages) return launch_ring<rmsnorm_bwd_kernel<kDy, kX, kDx, 2, false>>(p.ctas, p.threads, ring, s, a);
+  return launch_ring<rmsnorm_bwd_long_kernel<kDy, kX, kDx>>(p.ctas, 1024, static_cast<int>(sizeof(float)) * C, s, a);
 }
 
 bool kind_ok(int kind) { return kind == kBf16 || kind == kFp32; }

@@ -732,11 +732,9 @@ template <int kKind, int V>
 fp8q_status launch_route(const RouteArgs &a, cudaStream_t s) {
   constexpr int kWarps = warps_for(V), kMost = kWarps * 32 * V * 8;
   const size_t smem = static_cast<size_t>(kWarps) * a.E * (sizeof(int) + sizeof(float));
-  const auto kern = route_kernel<kKind, V>;
-  if (kMost > 40 * 1024 &&
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess)
-    return FP8Q_ERR_CUDA;
-  if (fp8q_status st = launch_dependent(kern, dim3(a.ctas), dim3(32 * kWarps), smem, s, a)) return st;
+  if (smem > 40 * 1024)
+    if (fp8q_status st = allow_smem<route_kernel<kKind, V>>(kMost)) return st;
+  if (fp8q_status st = launch_dependent(route_kernel<kKind, V>, dim3(a.ctas), dim3(32 * kWarps), smem, s, a)) return st;
   if (a.ctas == 1) return FP8Q_OK;
   return launch_dependent(route_rows_kernel, dim3(a.ctas), dim3(kRowThreads), 0, s, a);
 }

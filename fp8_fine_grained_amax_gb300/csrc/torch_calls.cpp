@@ -19,7 +19,6 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <algorithm>
 #include <climits>
 #include <optional>
 #include <string>
@@ -154,9 +153,12 @@ struct NoGil {
   ~NoGil() { PyEval_RestoreThread(state); }
 };
 
-// Results of a call: the caller's tensor, checked, a new one, or None.
+// Results of a call: the caller's tensor, checked, a new one, or None.  With
+// `together` small new ones are parts of one allocation, 256 bytes apart at least: it
+// takes longer to ask the allocator for each than to run a small call.
 class Results {
  public:
+  explicit Results(bool together = false) : together_(together) {}
   bool add(PyObject *given, bool wanted, int64_t rows, int64_t cols, at::ScalarType dtype,
            at::Device dev, const char *name, Mat &m, bool &present) {
     One &r = all_[n_++];
@@ -190,8 +192,18 @@ class Results {
     }
     return true;
   }
+  // The call's own scratch, made with the results; `p` is set by make().
+  void scratch(int64_t bytes, void *&p) {
+    scratch_bytes_ = bytes;
+    scratch_ = &p;
+  }
   // Make the new ones (needs no GIL).
   void make(const Place &place) {
+    if (together_ && make_together(place)) return;
+    if (scratch_) {
+      scratch_made_ = place.scratch(scratch_bytes_);
+      *scratch_ = scratch_made_.data_ptr();
+    }
     for (int i = 0; i < n_; ++i)
       if (Mat *m = all_[i].wanted) {
         One &r = all_[i];
@@ -220,8 +232,47 @@ class Results {
     bool vector = false;
     at::Tensor made;
   };
+  static constexpr int64_t kSmall = 2 << 20;  // bytes of all results together
+  bool make_together(const Place &place) {
+    int64_t at[8], bytes = 0;
+    int count = 0;
+    for (int i = 0; i < n_; ++i) {
+      const One &r = all_[i];
+      if (!r.wanted) continue;
+      at[i] = bytes;
+      const int64_t n = r.vector ? r.rows : r.rows * r.wanted->ld;
+      if (n > kSmall) return false;
+      bytes += (n * static_cast<int64_t>(c10::elementSize(r.dtype)) + 255) / 256 * 256;
+      ++count;
+    }
+    const int64_t scratch_at = bytes;
+    if (scratch_) {
+      bytes += scratch_bytes_;
+      ++count;
+    }
+    if (count < 2 || bytes > kSmall) return false;
+    const at::Tensor block = place.result({bytes}, at::kByte);
+    char *base = static_cast<char *>(block.data_ptr());
+    for (int i = 0; i < n_; ++i) {
+      One &r = all_[i];
+      if (!r.wanted) continue;
+      r.made = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(block.storage()), block.key_set(),
+                                                        c10::scalarTypeToTypeMeta(r.dtype));
+      c10::TensorImpl *impl = r.made.unsafeGetTensorImpl();
+      impl->set_storage_offset(at[i] / static_cast<int64_t>(c10::elementSize(r.dtype)));
+      if (r.vector) impl->set_sizes_contiguous({r.rows});
+      else impl->set_sizes_contiguous({r.rows, r.wanted->ld});
+      r.wanted->p = base ? base + at[i] : nullptr;
+    }
+    if (scratch_) *scratch_ = base + scratch_at;
+    return true;
+  }
   One all_[8];
+  void **scratch_ = nullptr;
+  int64_t scratch_bytes_ = 0;
+  at::Tensor scratch_made_;
   int n_ = 0;
+  const bool together_;
 };
 
 // Flags by their truth, as Python takes them (1, a numpy bool, ...).
@@ -460,6 +511,17 @@ bool vec_any(PyObject *o, int64_t n, at::Device dev, const char *name, Mat &m, i
   const at::Tensor *t = tensor(o, name);
   return t && kind_of(*t, name, kind) && vec(*t, n, t->scalar_type(), dev, name, m.p);
 }
+// The caller's workspace.
+bool workspace(PyObject *o, at::Device dev, void *&p, int64_t &bytes) {
+  const at::Tensor *t = tensor(o, "workspace");
+  if (!t) return false;
+  if (t->device() != dev || !t->is_contiguous())
+    return fail("workspace must be a contiguous tensor on " + dev.str());
+  p = t->numel() ? t->data_ptr() : nullptr;
+  bytes = static_cast<int64_t>(t->nbytes());
+  return true;
+}
+
 at::ScalarType type_of(int kind) { return kind == FP8Q_OUT_FP32 ? at::kFloat : at::kBFloat16; }
 
 // (x, w, residual, eps, with_r, with_y, with_codes, with_rstd, scale_mode, r, y, q, s, rstd, stream)
@@ -488,7 +550,7 @@ PyObject *rmsnorm_impl(PyObject *const *v, Py_ssize_t n) {
     fail("r is the sum with the residual: it needs one");
     return nullptr;
   }
-  Results out;
+  Results out(true);
   Mat r, y, q, s, rstd;
   bool has_r, has_y, has_q, has_s;
   if (!out.add(v[9], want[0] && has_res, T, C, type_of(kres), dev, "r", r, has_r) ||
@@ -535,32 +597,27 @@ PyObject *rmsnorm_bwd_impl(PyObject *const *v, Py_ssize_t n) {
     fail("accumulate adds to the dw that is given");
     return nullptr;
   }
-  Results out;
+  Results out(true);
   Mat dx, dw;
   bool has_dx;
   if (!out.add(v[8], want[0], T, C, od, dev, "dx", dx, has_dx) ||
       !out.add_vec(v[9], want[1], C, at::kFloat, dev, "dw", dw))
     return nullptr;
-  at::Tensor ws;
+  void *ws = nullptr;
+  int64_t ws_bytes = 0;
   if (v[11] != Py_None) {
-    const at::Tensor *t = tensor(v[11], "workspace");
-    if (!t) return nullptr;
-    if (t->device() != dev || !t->is_contiguous()) {
-      fail("workspace must be a contiguous tensor on dy's CUDA device");
-      return nullptr;
-    }
-    ws = *t;
+    if (!workspace(v[11], dev, ws, ws_bytes)) return nullptr;
+  } else if (want[1] || v[9] != Py_None) {
+    ws_bytes = fp8q_rmsnorm_bwd_workspace_bytes(T, C);
+    if (ws_bytes > 0) out.scratch(ws_bytes, ws);
   }
   fp8q_status st;
   {
     NoGil free;
     out.make(place);
-    if (!ws.defined() && (want[1] || v[9] != Py_None))
-      ws = place.scratch(std::max<int64_t>(fp8q_rmsnorm_bwd_workspace_bytes(T, C), 1));
     st = fp8q_rmsnorm_bwd(mdy.p, mdy.ld, kdy, mx.p, mx.ld, kx, static_cast<float *>(mrstd.p), mw.p, kw,
                           mdres.p, mdres.ld, dx.p, dx.ld, kd, static_cast<float *>(dw.p),
-                          accumulate[0], T, C, ws.defined() ? ws.data_ptr() : nullptr,
-                          ws.defined() ? static_cast<int64_t>(ws.nbytes()) : 0, place.handle);
+                          accumulate[0], T, C, ws, ws_bytes, place.handle);
   }
   return out.tuple(st);
 }
@@ -722,7 +779,7 @@ PyObject *route_impl(PyObject *const *v, Py_ssize_t n) {
   if (PyErr_Occurred() || !place.set(v[15], dev)) return nullptr;
   if (E < 1 || E > 1024 || k < 1 || k > E || k > 32 || T > (int64_t{1} << 26))
     return PyLong_FromLong(FP8Q_ERR_SHAPE);  // before results of such sizes are made
-  Results out;
+  Results out(true);
   Mat idx, weight, counts, offs, order, slot, tokens, loss;
   bool has;
   if (!out.add(v[6], true, T, k, at::kInt, dev, "idx", idx, has) ||
@@ -735,29 +792,24 @@ PyObject *route_impl(PyObject *const *v, Py_ssize_t n) {
       !out.add_vec(v[13], true, 1, at::kFloat, dev, "loss", loss) || !dense(idx, T, k, "idx") ||
       !dense(weight, T, k, "weight") || !dense(slot, T, k, "slot"))
     return nullptr;
-  at::Tensor ws;
+  void *ws = nullptr;
+  int64_t ws_bytes = 0;
   if (v[14] != Py_None) {
-    const at::Tensor *t = tensor(v[14], "workspace");
-    if (!t) return nullptr;
-    if (t->device() != dev || !t->is_contiguous()) {
-      fail("workspace must be a contiguous tensor on the logits' CUDA device");
-      return nullptr;
-    }
-    ws = *t;
+    if (!workspace(v[14], dev, ws, ws_bytes)) return nullptr;
+  } else {
+    ws_bytes = fp8q_route_workspace_bytes(T, E);
+    if (ws_bytes > 0) out.scratch(ws_bytes, ws);
   }
   fp8q_status st;
   {
     NoGil free;
     out.make(place);
-    const int64_t need = fp8q_route_workspace_bytes(T, E);
-    if (!ws.defined() && need > 0) ws = place.scratch(need);
     st = fp8q_route(l.p, l.ld, kind, valid, score, normalise[0], static_cast<float>(scale),
                     static_cast<int32_t *>(idx.p), static_cast<float *>(weight.p),
                     static_cast<int32_t *>(counts.p), static_cast<int32_t *>(offs.p),
                     static_cast<int32_t *>(order.p), static_cast<int32_t *>(slot.p),
-                    static_cast<int32_t *>(tokens.p), static_cast<float *>(loss.p), T, E, k,
-                    ws.defined() ? ws.data_ptr() : nullptr,
-                    ws.defined() ? static_cast<int64_t>(ws.nbytes()) : 0, place.handle);
+                    static_cast<int32_t *>(tokens.p), static_cast<float *>(loss.p), T, E, k, ws, ws_bytes,
+                    place.handle);
   }
   return out.tuple(st);
 }
@@ -791,7 +843,7 @@ PyObject *route_bwd_impl(PyObject *const *v, Py_ssize_t n) {
   const double scale = PyFloat_AsDouble(v[8]);
   Place place;
   if (PyErr_Occurred() || !place.set(v[11], dev)) return nullptr;
-  Results out;
+  Results out(true);
   Mat d;
   bool has;
   if (!out.add(v[10], true, T, E, type_of(kind), dev, "dlogits", d, has)) return nullptr;
