@@ -667,6 +667,7 @@ extern "C" fp8q_status fp8q_rmsnorm(const void *x, int64_t ldx, int x_dtype, con
   if (ldx < C || (res && ld_res < C) || (r && ld_r < C) || (y && ldy < C) ||
       (q && (ldq < C || ld_s < T)))
     return FP8Q_ERR_SHAPE;
+  if (T > 0 && C == 0 && rstd) return FP8Q_ERR_SHAPE;  // a mean of nothing
   if (T == 0 || C == 0) return FP8Q_OK;
   if (!x || !w || (r && !res) || (!r && !y && !q && !rstd) || !q != !s) return FP8Q_ERR_INVALID;
   if (!rows_aligned(x, ldx, x_dtype) || !aligned16(w) ||

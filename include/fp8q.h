@@ -414,7 +414,7 @@ fp8q_status fp8q_newton_schulz(const void *g, int64_t ldg, int64_t g_stride, int
  *   q     E4M3 [T][ldq] with s FP32 at s[(c/128) * ld_s + t]: the 1x128
  *         quantisation, by scale_mode, of the unrounded FP32 y -- the A operand
  *         of fp8q_gemm and of fp8q_gemm_swiglu.  C % 128 == 0.
- *   rstd  FP32 [T], what fp8q_rmsnorm_bwd reads.
+ *   rstd  FP32 [T], what fp8q_rmsnorm_bwd reads.  Not with C == 0.
  * The norm is of the unrounded h.  A row of zeros with eps > 0 gives zeros.
  * T >= 0, 0 <= C <= 32768, C % 8 == 0, eps >= 0; a row's sum of squares must be
  * an FP32 value.  Alignment: x, res, w, r, y, q 16-byte aligned; every pitch a
@@ -520,7 +520,7 @@ fp8q_status fp8q_adamw(const fp8q_adamw_tensor *tensors, int64_t count, int p_dt
  *              sizes outside the limits), 16-byte aligned, owned by the caller;
  *              contents on entry do not matter.
  * idx, weight, order and slot are dense.  Alignment: every address at its
- * element's.
+ * element's.  The same bits in every run.
  */
 enum { FP8Q_SCORE_SOFTMAX = 0, FP8Q_SCORE_SIGMOID = 1 };
 int64_t fp8q_route_workspace_bytes(int64_t T, int64_t E);

@@ -308,6 +308,24 @@ def test_choices_that_are_none_and_the_same_choice_twice():
     near(d, want, 100 * U * want + 1e-37, "dlogits")
 
 
+def test_more_tokens_than_16_bit_counts_hold():
+    # 153 CTAs of up to 65535 tokens, every token to the same expert first
+    T, E, k = 10_000_001, 3, 2
+    l = torch.randn(T, E, device="cuda") * 0.1
+    l[:, 1] += 10
+    r = fq.fp8q_route(l, k)
+    second = torch.where(l[:, 2] > l[:, 0], 2, 0)
+    assert (r.idx[:, 0] == 1).all() and torch.equal(r.idx[:, 1].long(), second)
+    counts = torch.bincount(r.idx.reshape(-1), minlength=E)
+    assert torch.equal(r.counts.long(), counts) and r.offs.tolist() == [0, *counts.cumsum(0).tolist()]
+    assert torch.equal(r.order.long(), torch.sort(r.idx.reshape(-1), stable=True).indices)
+    assert torch.equal(r.order[r.slot.reshape(-1).long()].long(), torch.arange(T * k, device="cuda"))
+    p = torch.softmax(l.double(), 1).mean(0)
+    want = E * (counts.double() / (T * k) * p).sum()
+    # T / 153 / 32 probabilities one after another in a warp, 32 and 153 partial sums
+    assert abs(float(r.loss) - float(want)) < (T / 153 / 32 + 500) * U * float(want)
+
+
 def test_repeats_bit_by_bit():
     l, valid = make(9000, 200, FP, 9, True)
     first = fq.fp8q_route(l.cuda(), 8, valid=valid.cuda())

@@ -135,6 +135,7 @@ def test_empty_work_succeeds(lib, B):
     none = dict(x=None, res=None, w=None, r=None, y=None, q=None, s=None, rstd=None)
     for change in (dict(T=0), dict(C=0)):
         assert lib.fp8q_rmsnorm(*{**NORM, **none, **change}.values()) == B.FP8Q_OK
+    assert lib.fp8q_rmsnorm(*{**NORM, "C": 0}.values()) == B.FP8Q_ERR_SHAPE  # rstd of no columns
     assert lib.fp8q_rmsnorm_bwd(*{**NORM_BWD, "C": 0, "dy": None, "x": None, "w": None, "ws": None}.values()) == B.FP8Q_OK
     assert lib.fp8q_route_bwd(*{**ROUTE_BWD, "T": 0, "l": None, "d": None}.values()) == B.FP8Q_OK
     assert adamw(lib, None) == B.FP8Q_OK
