@@ -34,19 +34,25 @@ namespace {
 
 constexpr int kSms = 152;         // one CTA each
 constexpr int kMaxPerCta = 65535; // tokens of a CTA: its counts are 16 bits
-constexpr int kOneCta = 64;       // tokens that one CTA takes alone
+// Tokens that one CTA takes alone: two per warp (256 experts, 64 tokens: 8.0 us against
+// 10.0 in two launches; 1024 experts, eight warps: 32 tokens 22.1 against 17.4, 16 tokens
+// 15.5).  Past that 8 tokens per CTA until every SM has one (2048 tokens 11.6 us; with 16
+// per CTA 12.4).
+constexpr int kFewPerCta = 8;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxChoices = 32;   // one per lane
 constexpr float kTiny = 0x1p-126f;
 constexpr float kBig = 3.40282347e38f;
+
+__host__ __device__ constexpr int round_up(int n, int to) { return (n + to - 1) / to * to; }
 
 struct RouteArgs {
   const void *logits;
   const uint8_t *valid;
   int32_t *idx, *counts, *offs, *order, *slot, *tokens;
   float *weight, *loss;
-  uint16_t *cta_counts;  // [CTAs][E, rounded up to even]
-  float *cta_probs;      // [CTAs][E]
+  uint16_t *cta_counts;  // [E][CTAs, rounded up to 8]
+  float *cta_probs;      // [E][CTAs, rounded up to 4]
   int *cta_tokens;    // [CTAs]
   int64_t ld;
   int T, E, k, ctas, per_cta;
@@ -257,11 +263,11 @@ route_kernel(const RouteArgs a) {
         make_finite(l);
         make_words();
       }
-      // lane j keeps the j-th largest word; one round more tells whether the last
-      // choice is apart from the rest
-      uint32_t kept = 0;
+      // lane j keeps the j-th largest word; of FP32 logits one round more tells whether
+      // the last choice is apart from the rest
+      uint32_t kept = 0, top = 0;
       for (int j = 0; j < k + (kKind == kFp32); ++j) {
-        const uint32_t top = __reduce_max_sync(~0u, word[0]);
+        top = __reduce_max_sync(~0u, word[0]);
         if (lane == j) kept = top;
         if (word[0] == top) {
 #pragma unroll
@@ -269,20 +275,16 @@ route_kernel(const RouteArgs a) {
           word[V - 1] = 0;
         }
       }
-      if (kKind == kFp32) {
-        const uint32_t ahead = __shfl_up_sync(~0u, kept, 1);
-        const bool alike = lane > 0 && lane <= k && kept >= kOpen && ((kept ^ ahead) & ~kIndex) == 0;
-        // choice 33 of 32 has no lane: with that many every choice is made exactly
-        if (__any_sync(~0u, alike) || k == 32) {
+      if (lane < k && kept >= kOpen) chosen = static_cast<int>(kIndex - (kept & kIndex));
+      if constexpr (kKind == kFp32) {
+        uint32_t behind = __shfl_down_sync(~0u, kept, 1);
+        if (lane == k - 1) behind = top;
+        if (__any_sync(~0u, lane < k && behind >= kOpen && ((kept ^ behind) & ~kIndex) == 0)) {
           uint32_t key[V];
 #pragma unroll
           for (int v = 0; v < V; ++v) key[v] = key_of(l[v]);
           chosen = choose_exactly<V>(key, k, lane);
-        } else if (lane < k && kept >= kOpen) {
-          chosen = static_cast<int>(kIndex - (kept & kIndex));
         }
-      } else if (lane < k && kept >= kOpen) {
-        chosen = static_cast<int>(kIndex - (kept & kIndex));
       }
       float x = 0.0f;
       if (chosen >= 0) x = fminf(logit_at(here, kKind, chosen), kBig);
@@ -343,8 +345,8 @@ route_kernel(const RouteArgs a) {
         p += probs[w * E + e];
       }
       if (!alone) {
-        a.cta_counts[static_cast<int64_t>(blockIdx.x) * (E + (E & 1)) + e] = static_cast<uint16_t>(run);
-        a.cta_probs[static_cast<int64_t>(blockIdx.x) * E + e] = p;
+        a.cta_counts[e * round_up(a.ctas, 8) + blockIdx.x] = static_cast<uint16_t>(run);
+        a.cta_probs[e * round_up(a.ctas, 4) + blockIdx.x] = p;
       }
     }
     total[i] = run;
@@ -405,113 +407,101 @@ route_kernel(const RouteArgs a) {
 
 constexpr int kRowThreads = 1024;
 
-// add(i, load(i)) for i = first, first + step, ... below n, twenty loads in flight.
-template <typename Load, typename Add>
-__device__ __forceinline__ void in_flight(int n, int first, int step, Load load, Add add) {
-  constexpr int kBatch = 20;
-  for (int i0 = first; i0 < n; i0 += kBatch * step) {
-    decltype(load(0)) v[kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      v[j] = 0;
-      if (i0 + j * step < n) v[j] = load(i0 + j * step);
-    }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) add(i0 + j * step, v[j]);
-  }
-}
-
 // CTA b turns ranks into rows: expert e's choices of CTA b start at offs[e] plus
-// the counts of the CTAs before it.
+// the counts of the CTAs before it.  As many threads as there is room for share an
+// expert (1 to 32, next to each other) and read its counts eight CTAs at a time.  The
+// last CTA also writes the totals.
 __global__ void __launch_bounds__(kRowThreads)
 route_rows_kernel(const RouteArgs a) {
-  __shared__ int total_of[2 * kRowThreads], before_of[2 * kRowThreads], scan[32];
-  __shared__ float prob_of[kRowThreads], part[32];
+  __shared__ int first_row[kMaxExperts], scan[32], tokens_of[32];
+  __shared__ float part[32];
   __shared__ int rows;
   wait_for_previous_kernel();
-  const int E = a.E, k = a.k, tid = threadIdx.x;
-  const int64_t all = static_cast<int64_t>(a.T) * k;
-  const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.per_cta * k;
-  const int64_t hi = min(all, lo + static_cast<int64_t>(a.per_cta) * k);
+  const int E = a.E, k = a.k, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+  const bool totals = cta == a.ctas - 1;
+  const int64_t lo = static_cast<int64_t>(cta) * a.per_cta * k;
+  const int64_t hi = min(static_cast<int64_t>(a.T) * k, lo + static_cast<int64_t>(a.per_cta) * k);
   // the thread's first choice, in flight while the counts are added up
   int next_idx = -1, next_slot = 0;
   if (lo + tid < hi) {
     next_idx = a.idx[lo + tid];
     next_slot = a.slot[lo + tid];
   }
-  const bool last = blockIdx.x == gridDim.x - 1;  // writes the totals
-  // the CTAs' counts, two experts in a word, are added up by as many groups of
-  // threads as there is room for, each taking every groups-th CTA
-  const int words = (E + 1) / 2, width = (words + 31) / 32 * 32, groups = kRowThreads / width;
-  const int word = tid % width, group = tid / width;
-  int total[2] = {0, 0}, before[2] = {0, 0};
-  if (group < groups) {
-    const uint32_t *c = reinterpret_cast<const uint32_t *>(a.cta_counts) + word;
-    in_flight(a.ctas, group, groups, [&](int b) { return word < words ? c[static_cast<int64_t>(b) * words] : 0u; },
-              [&](int b, uint32_t w) {
-                const int lo = w & 0xFFFF, hi = w >> 16, here = b < static_cast<int>(blockIdx.x);
-                total[0] += lo;
-                total[1] += hi;
-                before[0] += here ? lo : 0;
-                before[1] += here ? hi : 0;
-              });
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    total_of[2 * tid + h] = total[h];
-    before_of[2 * tid + h] = before[h];
-  }
-  // the probabilities in the same way, by the last CTA
-  const int wide = (E + 31) / 32 * 32, parts = kRowThreads / wide;
-  if (last) {
-    const int e = tid % wide;
-    float p = 0.0f;
-    if (tid / wide < parts)
-      in_flight(a.ctas, tid / wide, parts,
-                [&](int b) { return e < E ? a.cta_probs[static_cast<int64_t>(b) * E + e] : 0.0f; },
-                [&](int, float v) { p += v; });
-    prob_of[tid] = p;
-  }
-  __syncthreads();
-  int mine = 0, ahead = 0;
-  if (tid < E)
-    for (int g = 0; g < groups; ++g) {
-      mine += total_of[2 * g * width + tid];
-      ahead += before_of[2 * g * width + tid];
-    }
+  int share = 1;  // threads per expert
+  while (share < 32 && 2 * share * E <= kRowThreads) share *= 2;
+  const int e = tid / share, mine = tid % share;
+  int total = 0, before = 0, tokens = 0;
   float probs = 0.0f;
-  if (last && tid < E)
-    for (int g = 0; g < parts; ++g) probs += prob_of[g * wide + tid];
-  const int first = cta_exclusive_sum(mine, scan);
-  __syncthreads();
-  if (tid < E) total_of[tid] = first + ahead;
-  if (tid == kRowThreads - 1) rows = first + mine;
-  if (last) {
-    const int lane = tid & 31, warp = tid >> 5;
-    if (tid < E) {
-      a.counts[tid] = mine;
-      a.offs[tid] = first;
-    }
-    const float p = warp_sum(static_cast<float>(mine) * probs);
-    int tokens = 0;
+  if (totals)
     for (int b = tid; b < a.ctas; b += kRowThreads) tokens += a.cta_tokens[b];
-    tokens = warp_sum(tokens);
-    if (lane == 0) {
-      part[warp] = p;
-      scan[warp] = tokens;
+  if (e < E) {
+    constexpr int kBatch = 5;
+    const uint4 *c = reinterpret_cast<const uint4 *>(a.cta_counts + e * round_up(a.ctas, 8));
+    const int n = round_up(a.ctas, 8) / 8;
+    for (int j0 = mine; j0 < n; j0 += kBatch * share) {
+      uint4 v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) v[i] = c[min(j0 + i * share, n - 1)];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int b0 = j0 + i * share < n ? 8 * (j0 + i * share) : a.ctas;
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+          const int x = (w[h / 2] >> (16 * (h & 1))) & 0xFFFF;
+          total += b0 + h < a.ctas ? x : 0;
+          before += b0 + h < cta ? x : 0;
+        }
+      }
     }
-    __syncthreads();
-    if (warp == 0) {
-      const float loss = warp_sum(part[lane]);
-      tokens = warp_sum(scan[lane]);
-      if (lane == 0) {
-        a.offs[E] = rows;
-        a.tokens[0] = tokens;
-        a.loss[0] = balance(loss, E, rows, tokens);
+    if (totals) {
+      const float4 *p = reinterpret_cast<const float4 *>(a.cta_probs + e * round_up(a.ctas, 4));
+      const int m = round_up(a.ctas, 4) / 4;
+      for (int j0 = mine; j0 < m; j0 += kBatch * share) {
+        float4 v[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) v[i] = p[min(j0 + i * share, m - 1)];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int b0 = j0 + i * share < m ? 4 * (j0 + i * share) : a.ctas;
+          const float w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) probs += b0 + h < a.ctas ? w[h] : 0.0f;
+        }
       }
     }
   }
+  for (int o = 1; o < share; o *= 2) {
+    total += __shfl_xor_sync(~0u, total, o);
+    before += __shfl_xor_sync(~0u, before, o);
+    probs += __shfl_xor_sync(~0u, probs, o);
+  }
+  const bool leads = e < E && mine == 0;  // for its expert
+  const int first = cta_exclusive_sum(leads ? total : 0, scan);
+  if (leads) first_row[e] = first + before;
+  if (tid == kRowThreads - 1) rows = first + (leads ? total : 0);
+  if (totals) {
+    if (leads) {
+      a.counts[e] = total;
+      a.offs[e] = first;
+    }
+    const float p = warp_sum(leads ? static_cast<float>(total) * probs : 0.0f);
+    tokens = warp_sum(tokens);
+    if (lane == 0) {
+      part[warp] = p;
+      tokens_of[warp] = tokens;
+    }
+  }
   __syncthreads();
+  if (totals && warp == 0) {
+    const float loss = warp_sum(part[lane]);
+    tokens = warp_sum(tokens_of[lane]);
+    if (lane == 0) {
+      a.offs[E] = rows;
+      a.tokens[0] = tokens;
+      a.loss[0] = balance(loss, E, rows, tokens);
+    }
+  }
   for (int64_t i = lo + tid; i < hi; i += kRowThreads) {
     const int x = next_idx, rank = next_slot;
     if (i + kRowThreads < hi) {
@@ -519,7 +509,7 @@ route_rows_kernel(const RouteArgs a) {
       next_slot = a.slot[i + kRowThreads];
     }
     if (x >= 0) {
-      const int r = rank + total_of[x];
+      const int r = rank + first_row[x];
       a.slot[i] = r;
       a.order[r] = static_cast<int32_t>(i);
     }
@@ -713,11 +703,10 @@ struct Plan {
   int ctas, per_cta;
 };
 Plan plan(int64_t T, int64_t E) {
-  const int warps = warps_for(E <= 256 ? 8 : E <= 512 ? 16 : 32);
   Plan p;
   p.ctas = 1;
-  if (T > kOneCta) {
-    const int64_t full = (T + warps - 1) / warps, most = (T + kMaxPerCta - 1) / kMaxPerCta;
+  if (T > 2 * warps_for(E <= 256 ? 8 : E <= 512 ? 16 : 32)) {
+    const int64_t full = (T + kFewPerCta - 1) / kFewPerCta, most = (T + kMaxPerCta - 1) / kMaxPerCta;
     p.ctas = static_cast<int>(most > kSms ? most : full < kSms ? full : kSms);
   }
   p.per_cta = static_cast<int>((T + p.ctas - 1) / p.ctas);
@@ -783,7 +772,7 @@ using namespace fp8q;
 extern "C" int64_t fp8q_route_workspace_bytes(int64_t T, int64_t E) {
   if (!shape_ok(T, E)) return 0;
   const Plan p = plan(T, E);
-  return p.ctas <= 1 ? 0 : ((E + 1) / 2 + E + 1) * static_cast<int64_t>(p.ctas) * 4;
+  return p.ctas <= 1 ? 0 : E * (2 * round_up(p.ctas, 8) + 4 * round_up(p.ctas, 4)) + 4ll * p.ctas;
 }
 
 extern "C" fp8q_status fp8q_route(const void *logits, int64_t ld, int dtype, const uint8_t *valid,
@@ -822,8 +811,8 @@ extern "C" fp8q_status fp8q_route(const void *logits, int64_t ld, int dtype, con
   a.weight = weight;
   a.loss = loss;
   a.cta_counts = static_cast<uint16_t *>(workspace);
-  a.cta_probs = static_cast<float *>(workspace) + (E + 1) / 2 * p.ctas;
-  a.cta_tokens = static_cast<int *>(workspace) + ((E + 1) / 2 + E) * p.ctas;
+  a.cta_probs = reinterpret_cast<float *>(a.cta_counts + E * round_up(p.ctas, 8));
+  a.cta_tokens = reinterpret_cast<int *>(a.cta_probs + E * round_up(p.ctas, 4));
   a.ld = ld;
   a.T = static_cast<int>(T);
   a.E = static_cast<int>(E);
