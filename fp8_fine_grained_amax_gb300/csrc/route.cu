@@ -407,6 +407,15 @@ route_kernel(const RouteArgs a) {
 
 constexpr int kRowThreads = 1024;
 
+// Sum of the first n (none if negative, eight at most) 16-bit counts.
+__device__ __forceinline__ int sum8(uint4 v, int n) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  unsigned s = 0;
+#pragma unroll
+  for (int h = 0; h < 4; ++h) s = __dp2a_lo(w[h], 2 * h + 1 < n ? 0x0101u : 2 * h < n ? 0x0001u : 0u, s);
+  return static_cast<int>(s);
+}
+
 // CTA b turns ranks into rows: expert e's choices of CTA b start at offs[e] plus
 // the counts of the CTAs before it.  As many threads as there is room for share an
 // expert (1 to 32, next to each other) and read its counts eight CTAs at a time.  The
@@ -444,14 +453,9 @@ route_rows_kernel(const RouteArgs a) {
       for (int i = 0; i < kBatch; ++i) v[i] = c[min(j0 + i * share, n - 1)];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int b0 = j0 + i * share < n ? 8 * (j0 + i * share) : a.ctas;
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-        for (int h = 0; h < 8; ++h) {
-          const int x = (w[h / 2] >> (16 * (h & 1))) & 0xFFFF;
-          total += b0 + h < a.ctas ? x : 0;
-          before += b0 + h < cta ? x : 0;
-        }
+        const int b0 = 8 * (j0 + i * share);
+        total += sum8(v[i], a.ctas - b0);
+        before += sum8(v[i], cta - b0);
       }
     }
     if (totals) {
