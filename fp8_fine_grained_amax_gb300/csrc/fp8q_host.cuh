@@ -104,6 +104,29 @@ inline fp8q_status launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 bloc
              : FP8Q_ERR_CUDA;
 }
 
+// The same for clusters of `cluster` CTAs.
+template <typename... KArgs, typename... Args>
+inline fp8q_status launch_dependent_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                            cudaStream_t s, unsigned cluster, Args &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...) == cudaSuccess
+             ? FP8Q_OK
+             : FP8Q_ERR_CUDA;
+}
+
 // Time limit of every device-side wait (fp8q_set_wait_timeout_ns).
 inline std::atomic<uint64_t> &wait_timeout_ns() {
   static std::atomic<uint64_t> ns{2000000000ull};

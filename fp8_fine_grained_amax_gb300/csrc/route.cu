@@ -19,7 +19,8 @@
 // choices per expert, which is a choice's rank among its warp's; prefix sums over a
 // CTA's warps and over the CTAs give its row.  Probabilities are summed in the same
 // fixed order.  Two launches: choices and counts per CTA, then the prefix over CTAs
-// and the rows; one launch where one CTA holds all tokens.
+// and the rows.  Few tokens take one launch, of one CTA or of a cluster of eight that
+// read each other's totals from shared memory.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -34,10 +35,7 @@ namespace {
 
 constexpr int kSms = 152;         // one CTA each
 constexpr int kMaxPerCta = 65535; // tokens of a CTA: its counts are 16 bits
-// Tokens that one CTA takes alone: two per warp (256 experts, 64 tokens: 8.0 us against
-// 10.0 in two launches; 1024 experts, eight warps: 32 tokens 22.1 against 17.4, 16 tokens
-// 15.5).  Past that 8 tokens per CTA until every SM has one (2048 tokens 11.6 us; with 16
-// per CTA 12.4).
+constexpr int kCluster = 8;
 constexpr int kFewPerCta = 8;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxChoices = 32;   // one per lane
@@ -204,15 +202,20 @@ __device__ __forceinline__ int cta_exclusive_sum(int v, int *part) {
   return before + s - v;
 }
 
+// Who else has tokens of the call: nobody (one CTA), the other CTAs of the cluster, or
+// those of a whole grid, whose rows a second launch works out.
+enum Mode { kOneCta, kOneCluster, kGrid };
+
 // Dynamic shared memory: counts [warps][E], then probabilities [warps][E].
-template <int kKind, int V>
+template <int kKind, int V, int kMode>
 __global__ void __launch_bounds__(32 * warps_for(V))
 route_kernel(const RouteArgs a) {
+  constexpr bool alone = kMode != kGrid, clustered = kMode == kOneCluster;
   constexpr int kWarps = warps_for(V), kThreads = 32 * kWarps;
   constexpr int kEach = 32 * V > kThreads ? 32 * V / kThreads : 1;  // experts per thread, at most
   constexpr uint32_t kIndex = 32 * V - 1;                            // a word's index bits
   extern __shared__ int smem[];
-  __shared__ int tokens_of[kWarps], scan[32], all_rows;
+  __shared__ int tokens_of[kWarps], scan[32], all_rows, cta_tokens, all_tokens;
   __shared__ float part[32];
   wait_for_previous_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E, k = a.k;
@@ -224,8 +227,9 @@ route_kernel(const RouteArgs a) {
 
   const int64_t cta_lo = static_cast<int64_t>(blockIdx.x) * a.per_cta;
   const int64_t cta_hi = min(static_cast<int64_t>(a.T), cta_lo + a.per_cta);
-  const int64_t n = cta_hi > cta_lo ? cta_hi - cta_lo : 0;
-  const int64_t lo = cta_lo + n * warp / kWarps, hi = cta_lo + n * (warp + 1) / kWarps;
+  // the first warps take one more: few tokens are spread over the SM's four schedulers
+  const int n = static_cast<int>(cta_hi > cta_lo ? cta_hi - cta_lo : 0), each = n / kWarps, more = n % kWarps;
+  const int64_t lo = cta_lo + warp * each + min(warp, more), hi = lo + each + (warp < more);
   const char *row = static_cast<const char *>(a.logits) + lo * a.ld * size_of(kKind);
   float psum[V], next[V];
 #pragma unroll
@@ -328,9 +332,8 @@ route_kernel(const RouteArgs a) {
   __syncthreads();
 
   // counts become the warps' first ranks; thread i has the experts from i * kEach on
-  const bool alone = gridDim.x == 1;
-  int total[kEach], all = 0, tokens = 0;
-  float loss = 0.0f;
+  int total[kEach], tokens = 0;
+  float prob[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int e = threadIdx.x * kEach + i;
@@ -344,52 +347,105 @@ route_kernel(const RouteArgs a) {
         run += c;
         p += probs[w * E + e];
       }
-      if (!alone) {
+      if constexpr (!alone) {
         a.cta_counts[e * round_up(a.ctas, 8) + blockIdx.x] = static_cast<uint16_t>(run);
         a.cta_probs[e * round_up(a.ctas, 4) + blockIdx.x] = p;
       }
     }
     total[i] = run;
-    all += run;
-    loss = fmaf(static_cast<float>(run), p, loss);
+    prob[i] = p;
   }
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) tokens += tokens_of[w];
   __syncthreads();
 
-  int *first_row = smem + kWarps * E;  // of each expert, where the probabilities were
-  if (!alone) {
+  // where the probabilities were: each expert's total, probability and first row here
+  int *total_of = smem + kWarps * E, *first_row = total_of + 2 * E;
+  float *prob_of = reinterpret_cast<float *>(total_of + E);
+  if constexpr (!alone) {
     if (threadIdx.x == 0) a.cta_tokens[blockIdx.x] = tokens;
   } else {
-    // one CTA: its totals are all there is
-    const int before = cta_exclusive_sum(all, scan);
+    const int rank = clustered ? blockIdx.x : 0;
+    int before[kEach] = {};
+    if constexpr (clustered) {
+      // the totals of the cluster's CTAs, in the order of their tokens
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int e = threadIdx.x * kEach + i;
+        if (e < E) {
+          total_of[e] = total[i];
+          prob_of[e] = prob[i];
+        }
+      }
+      if (threadIdx.x == 0) cta_tokens = tokens;
+      cluster_sync_all();
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int e = threadIdx.x * kEach + i;
+        total[i] = 0;
+        prob[i] = 0.0f;
+        if (e < E) {  // all loads in flight at once
+          uint32_t c[kCluster], p[kCluster];
+#pragma unroll
+          for (int r = 0; r < kCluster; ++r) {
+            c[r] = ld_cluster(mapa_shared(smem_u32(total_of + e), r));
+            p[r] = ld_cluster(mapa_shared(smem_u32(prob_of + e), r));
+          }
+#pragma unroll
+          for (int r = 0; r < kCluster; ++r) {
+            total[i] += static_cast<int>(c[r]);
+            before[i] += r < rank ? static_cast<int>(c[r]) : 0;
+            prob[i] += __uint_as_float(p[r]);
+          }
+        }
+      }
+    }
+    int all = 0;
+    float loss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      all += total[i];
+      loss = fmaf(static_cast<float>(total[i]), prob[i], loss);
+    }
+    int first = cta_exclusive_sum(all, scan);
     loss = warp_sum(loss);
     if (lane == 0) part[warp] = loss;
-    int first = before;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int e = threadIdx.x * kEach + i;
       if (e < E) {
-        a.counts[e] = total[i];
-        a.offs[e] = first;
-        first_row[e] = first;
+        if (rank == 0) {
+          a.counts[e] = total[i];
+          a.offs[e] = first;
+        }
+        first_row[e] = first + before[i];
       }
       first += total[i];
     }
-    if (threadIdx.x == kThreads - 1) {
-      a.offs[E] = first;
-      all_rows = first;
+    if (threadIdx.x == kThreads - 1) all_rows = first;
+    if (threadIdx.x == 0) {
+      if constexpr (clustered) {
+        tokens = 0;
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r) tokens += static_cast<int>(ld_cluster(mapa_shared(smem_u32(&cta_tokens), r)));
+      }
+      all_tokens = tokens;
     }
     __syncthreads();
+    // what this CTA read of the others has arrived: all of it went into sums that were
+    // stored before the barrier
+    if constexpr (clustered) cluster_arrive_relaxed();
     const int rows = all_rows;
-    if (threadIdx.x == 0) {
+    if (rank == 0 && threadIdx.x == 0) {
       loss = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) loss += part[w];
-      a.tokens[0] = tokens;
-      a.loss[0] = balance(loss, E, rows, tokens);
+      a.offs[E] = rows;
+      a.tokens[0] = all_tokens;
+      a.loss[0] = balance(loss, E, rows, all_tokens);
     }
-    for (int i = rows + threadIdx.x; i < a.T * k; i += kThreads) a.order[i] = -1;
+    for (int i = rows + rank * kThreads + threadIdx.x; i < a.T * k; i += (clustered ? kCluster : 1) * kThreads)
+      a.order[i] = -1;
   }
 
   // the warp's choices again, now with their ranks in the CTA (or their rows)
@@ -397,12 +453,13 @@ route_kernel(const RouteArgs a) {
     const int e = a.idx[i];
     if (e < 0) continue;
     int r = a.slot[i] + mine[e];
-    if (alone) {
+    if constexpr (alone) {
       r += first_row[e];
       a.order[r] = static_cast<int32_t>(i);
     }
     a.slot[i] = r;
   }
+  if constexpr (clustered) cluster_wait();  // a CTA's totals stay until all have read them
 }
 
 constexpr int kRowThreads = 1024;
@@ -702,14 +759,26 @@ route_bwd_kernel(const BwdArgs a) {
   }
 }
 
-// The same for every device, so that the probabilities' sums are too.
+// How a call's tokens are spread; the same for every device, so that the probabilities'
+// sums are too.  256 experts: 17 tokens take 4.8 us in one CTA and 6.1 in a cluster, 64
+// take 8.0, 6.3 and, in two launches, 9.9, 256 take 8.2 in a cluster and 9.9 in two
+// launches, 512 10.5 and 9.4.  With more than 256 experts the exchange is slower than
+// the second launch (1024 experts, 64 tokens: 22.0 and 16.6 us).
 struct Plan {
+  Mode mode;
   int ctas, per_cta;
 };
 Plan plan(int64_t T, int64_t E) {
+  const int warps = warps_for(E <= 256 ? 8 : E <= 512 ? 16 : 32);
   Plan p;
-  p.ctas = 1;
-  if (T > 2 * warps_for(E <= 256 ? 8 : E <= 512 ? 16 : 32)) {
+  if (T <= (E <= 256 ? warps : 2 * warps)) {
+    p.mode = kOneCta;
+    p.ctas = 1;
+  } else if (E <= 256 && T <= kCluster * warps) {
+    p.mode = kOneCluster;
+    p.ctas = kCluster;
+  } else {
+    p.mode = kGrid;
     const int64_t full = (T + kFewPerCta - 1) / kFewPerCta, most = (T + kMaxPerCta - 1) / kMaxPerCta;
     p.ctas = static_cast<int>(most > kSms ? most : full < kSms ? full : kSms);
   }
@@ -721,25 +790,36 @@ bool shape_ok(int64_t T, int64_t E) {
   return T >= 0 && T <= (int64_t{1} << 26) && E >= 1 && E <= kMaxExperts;
 }
 
-template <int kKind, int V>
-fp8q_status launch_route(const RouteArgs &a, cudaStream_t s) {
+template <int kKind, int V, int kMode>
+fp8q_status launch_choice(const RouteArgs &a, cudaStream_t s) {
   constexpr int kWarps = warps_for(V), kMost = kWarps * 32 * V * 8;
+  constexpr auto kern = route_kernel<kKind, V, kMode>;
   const size_t smem = static_cast<size_t>(kWarps) * a.E * (sizeof(int) + sizeof(float));
   if (smem > 40 * 1024)
-    if (fp8q_status st = allow_smem<route_kernel<kKind, V>>(kMost)) return st;
-  if (fp8q_status st = launch_dependent(route_kernel<kKind, V>, dim3(a.ctas), dim3(32 * kWarps), smem, s, a)) return st;
-  if (a.ctas == 1) return FP8Q_OK;
+    if (fp8q_status st = allow_smem<kern>(kMost)) return st;
+  if constexpr (kMode == kOneCluster)
+    return launch_dependent_cluster(kern, dim3(kCluster), dim3(32 * kWarps), smem, s, kCluster, a);
+  return launch_dependent(kern, dim3(a.ctas), dim3(32 * kWarps), smem, s, a);
+}
+
+template <int kKind, int V>
+fp8q_status launch_route(const RouteArgs &a, Mode mode, cudaStream_t s) {
+  if (mode == kOneCta) return launch_choice<kKind, V, kOneCta>(a, s);
+  if constexpr (V <= 8) {
+    if (mode == kOneCluster) return launch_choice<kKind, V, kOneCluster>(a, s);
+  }
+  if (fp8q_status st = launch_choice<kKind, V, kGrid>(a, s)) return st;
   return launch_dependent(route_rows_kernel, dim3(a.ctas), dim3(kRowThreads), 0, s, a);
 }
 
 template <int kKind>
-fp8q_status launch_route(const RouteArgs &a, cudaStream_t s) {
-  if (a.E <= 32) return launch_route<kKind, 1>(a, s);
-  if (a.E <= 64) return launch_route<kKind, 2>(a, s);
-  if (a.E <= 128) return launch_route<kKind, 4>(a, s);
-  if (a.E <= 256) return launch_route<kKind, 8>(a, s);
-  if (a.E <= 512) return launch_route<kKind, 16>(a, s);
-  return launch_route<kKind, 32>(a, s);
+fp8q_status launch_route(const RouteArgs &a, Mode mode, cudaStream_t s) {
+  if (a.E <= 32) return launch_route<kKind, 1>(a, mode, s);
+  if (a.E <= 64) return launch_route<kKind, 2>(a, mode, s);
+  if (a.E <= 128) return launch_route<kKind, 4>(a, mode, s);
+  if (a.E <= 256) return launch_route<kKind, 8>(a, mode, s);
+  if (a.E <= 512) return launch_route<kKind, 16>(a, mode, s);
+  return launch_route<kKind, 32>(a, mode, s);
 }
 
 template <int kKind, int V>
@@ -776,7 +856,7 @@ using namespace fp8q;
 extern "C" int64_t fp8q_route_workspace_bytes(int64_t T, int64_t E) {
   if (!shape_ok(T, E)) return 0;
   const Plan p = plan(T, E);
-  return p.ctas <= 1 ? 0 : E * (2 * round_up(p.ctas, 8) + 4 * round_up(p.ctas, 4)) + 4ll * p.ctas;
+  return p.mode != kGrid ? 0 : E * (2 * round_up(p.ctas, 8) + 4 * round_up(p.ctas, 4)) + 4ll * p.ctas;
 }
 
 extern "C" fp8q_status fp8q_route(const void *logits, int64_t ld, int dtype, const uint8_t *valid,
@@ -828,7 +908,7 @@ extern "C" fp8q_status fp8q_route(const void *logits, int64_t ld, int dtype, con
   a.normalise = normalise != 0;
   a.vec = row_vectors(logits, ld, dtype);
   auto st = static_cast<cudaStream_t>(stream);
-  return dtype == kBf16 ? launch_route<kBf16>(a, st) : launch_route<kFp32>(a, st);
+  return dtype == kBf16 ? launch_route<kBf16>(a, p.mode, st) : launch_route<kFp32>(a, p.mode, st);
 }
 
 extern "C" fp8q_status fp8q_route_bwd(const void *logits, int64_t ld, int dtype,

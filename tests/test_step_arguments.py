@@ -26,7 +26,7 @@ NORM = dict(x=P, ldx=256, kx=0, res=P, ld_res=256, kres=1, w=P, kw=1, eps=1e-6, 
 NORM_BWD = dict(dy=P, ld_dy=256, kdy=0, x=P, ldx=256, kx=0, rstd=P, w=P, kw=0, dres=P, ld_dres=256, dx=P, ld_dx=256,
                 kd=0, dw=P, accumulate=0, T=64, C=256, ws=P, ws_bytes=1 << 20, stream=None)
 ROUTE = dict(l=P, ld=64, kind=1, valid=P, score=0, norm=1, scale=1.0, idx=P, weight=P, counts=P, offs=P, order=P,
-             slot=P, tokens=P, loss=P, T=100, E=64, k=4, ws=P, ws_bytes=1 << 20, stream=None)
+             slot=P, tokens=P, loss=P, T=1000, E=64, k=4, ws=P, ws_bytes=1 << 20, stream=None)
 ROUTE_BWD = dict(l=P, ld=64, kind=1, valid=P, score=0, norm=1, scale=1.0, idx=P, counts=P, tokens=P, dw=P, dloss=P,
                  d=P, ld_d=64, T=100, E=64, k=4, stream=None)
 
@@ -147,7 +147,7 @@ def test_workspace_sizes(lib):
     assert f(1, 128) >= 512 and f(8192, 7168) >= 152 * 7168 * 4 and f(1 << 20, 7168) == f(1 << 21, 7168)
     assert f(-1, 128) == 0 and f(1, 12) == 0 and f(1, 1 << 20) == 0
     f = lib.fp8q_route_workspace_bytes
-    assert f(1, 256) == 0 and f(1 << 20, 256) == f(1 << 21, 256) > 0
+    assert f(1, 256) == f(256, 256) == 0 and f(1 << 20, 256) == f(1 << 21, 256) > 0
     assert f(-1, 8) == 0 and f(8, 0) == 0 and f(8, 1025) == 0
 
 
