@@ -79,19 +79,4 @@ __device__ __forceinline__ void store8(void *base, int64_t at, const float (&v)[
   }
 }
 
-// Eight values as they lie in memory.
-template <int kKind>
-struct Raw {
-  uint4 u[kKind == kBf16 ? 1 : 2];
-  __device__ __forceinline__ void load(const void *base, int64_t at) {
-    const char *p = static_cast<const char *>(base) + at * size_of(kKind);
-    u[0] = ld_stream(p);
-    if constexpr (kKind == kFp32) u[1] = ld_stream(p + 16);
-  }
-  __device__ __forceinline__ void values(float (&v)[8]) const {
-    if constexpr (kKind == kBf16) unpack8(u[0], v);
-    else unpack8(u[0], u[1], v);
-  }
-};
-
 }  // namespace fp8q
