@@ -777,7 +777,7 @@ PyObject *route_impl(PyObject *const *v, Py_ssize_t n) {
   const double scale = PyFloat_AsDouble(v[4]);
   Place place;
   if (PyErr_Occurred() || !place.set(v[15], dev)) return nullptr;
-  if (E < 1 || E > 1024 || k < 1 || k > E || k > 32 || T > (int64_t{1} << 26))
+  if (E < 1 || E > 1024 || k < 1 || k > E || k > 32 || T > (int64_t{1} << 26) || T * k > 0x7FFFFFFFll)
     return PyLong_FromLong(FP8Q_ERR_SHAPE);  // before results of such sizes are made
   Results out(true);
   Mat idx, weight, counts, offs, order, slot, tokens, loss;

@@ -466,8 +466,10 @@ fp8q_status fp8q_rmsnorm_bwd(const void *dy, int64_t ld_dy, int dy_dtype, const 
  *         shorter) in m_scale and v_scale: with a = max(amax, 2^-116) of the
  *         group, scale = a * (1 / 448) and codes E4M3(x * (448 * (1 / a))), each
  *         operation rounded to nearest; a positive sqrt(v) at least to the
- *         smallest code, 2^-9, so that no denominator becomes 0 by rounding.  Zero bytes and scales are the
- *         state before the first step.
+ *         smallest code, 2^-9, so that no denominator becomes 0 by rounding.
+ *         Zero bytes and scales are the state before the first step.
+ * A gradient that is no finite number makes its parameter NaN and leaves the
+ * others alone; with moments in 8 bits an infinite one takes its group with it.
  * `tensors` is a HOST array, copied by the call.  Tensors are dense; none may
  * overlap another (the p, m, v of a call are checked, FP8Q_ERR_INVALID).
  *   lr, step   by value, or from device memory where lr_dev / step_dev are not

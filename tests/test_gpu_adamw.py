@@ -199,8 +199,27 @@ def test_zero_gradients_and_zero_moments():
         assert all(not (t.bitwise_and(0x7F) if t.dtype == torch.uint8 else t).any() for t in st.m + st.v)
 
 
+@pytest.mark.parametrize("state", ["fp32", "bf16", "e4m3"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_gradients_that_are_no_numbers(state, bad):
+    # they show in their parameter and leave the others alone (8 bits: an infinite one the other groups)
+    a, b = (State([300, 40], "fp32", "fp32", state, seed=6) for _ in range(2))
+    a.g[0][133], b.g[0][133] = bad, 0.0
+    keep = torch.ones(300, dtype=torch.bool, device="cuda")
+    keep[133] = False
+    for step in (1, 2):
+        a.step(step=step, **HYPER)
+        b.step(step=step, **HYPER)
+        if state == "e4m3" and bad == float("inf"):
+            keep[128:256] = False
+        assert torch.isnan(a.p[0][133])
+        for x, y in zip(a.p + a.m + a.v, b.p + b.m + b.v):
+            kept = keep if x.numel() == 300 else slice(None)
+            assert torch.equal(x[kept], y[kept])
+
+
 def test_small_gradients_in_a_group_keep_their_denominator():
-    # one value of a group a million times larger than the others: their root is below half the
+    # one value of a group ten million times larger than the others: their root is below half the
     # smallest code, and a step of theirs stays of the order of lr
     st = State([128], "fp32", "fp32", "e4m3", seed=5)
     hyper = dict(lr=1e-2, betas=(0.9, 0.95), eps=1e-12, weight_decay=0.0)
