@@ -1,10 +1,11 @@
 // torch_calls.cpp -- the argument marshalling of the gated feed-forward,
-// Newton-Schulz, norm, AdamW and router bindings as a CPython module: tensors in, libfp8q's C ABI called
-// on torch's current stream, result tensors out.  No step of the computation is
-// here.  A small call takes longer to marshal than to run; looking at up to 18
-// tensors and making up to 8 new ones costs, on a Grace core, 3.0 to 3.5 us with
-// the results given (launch included) and 0.8 to 0.9 us more per new tensor,
-// against 9 us and 1.6 us per tensor from Python through ctypes.
+// Newton-Schulz, norm, AdamW and router bindings as a CPython module: tensors in,
+// libfp8q's C ABI called on torch's current stream, result tensors out.  No step of
+// the computation is here.  A small call takes longer to marshal than to run; looking
+// at up to 18 tensors and making up to 8 new ones costs, on a Grace core, 2.7 to 3.5 us
+// with the results given (launch included) and 0.8 to 0.9 us more per new tensor, against
+// 9 us and 1.6 us per tensor from Python through ctypes.  Small results of the norm and
+// router calls share an allocation: eight cost 3.6 us more, three 1.9.
 //
 // Every function takes positional arguments (binding.py gives them their names
 // and defaults) and returns the tuple of results, or the fp8q_status as an int
