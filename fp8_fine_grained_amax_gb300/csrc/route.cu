@@ -5,14 +5,15 @@
 //   weight_j = scale * s_j (/ sum of the chosen s),
 //   loss = E * sum_e (counts_e / sum counts) * (sum_t p_te / N).
 //
-// A warp takes a token, lane i the V experts from i * V on, in registers.  Each
-// expert becomes one 32-bit word: the logit's upper bits in an order-preserving
-// form, and below them the expert's index, falling, so that no two words are alike
-// and the lower index is the larger word.  A lane sorts its words (two instructions
-// per comparator), and the choice is k rounds of one warp-wide maximum over the
-// lanes' largest words.  BF16 logits fit in the upper bits.  Where two FP32 logits
-// next to each other in the choice differ in their lower bits only (or not at all),
-// the token's choice is made again on whole logits.
+// A warp takes a token, each lane V experts, in registers: of every 128 experts four next
+// to each other, so that a warp reads and writes rows without gaps.  Each expert becomes
+// one 32-bit word: the logit's upper bits in an order-preserving form, and below them the
+// expert's index, falling, so that no two words are alike and the lower index is the
+// larger word.  A lane sorts its words (two instructions per comparator), and the choice
+// is k rounds of one warp-wide maximum over the lanes' largest words.  BF16 logits fit in
+// the upper bits.  Of FP32 logits those that agree with the last choice in the upper bits
+// are taken too, and the lanes sort what they keep by the whole logits; where there are
+// more of them than lanes, the choice is made again on whole logits.
 //
 // The order has to be the same in every run, so rows are counted, not claimed with
 // atomics: each warp goes through a contiguous part of the tokens and counts its
@@ -58,61 +59,81 @@ struct RouteArgs {
   bool sigmoid, normalise, vec;
 };
 
-// V consecutive logits of a row from column lane * V on; -inf behind column E.
+// The v-th of a lane's V experts.
+__host__ __device__ constexpr int width(int V) { return V < 4 ? V : 4; }
+template <int V>
+__device__ __forceinline__ constexpr int expert(int lane, int v) {
+  constexpr int W = width(V);
+  return v / W * 32 * W + lane * W + v % W;
+}
+
+// A lane's logits of a row; -inf behind column E.  `vec`: the row starts on 16 bytes and
+// E is a multiple of four.
 template <int kKind, int V>
 __device__ __forceinline__ void load_logits(const void *row, int E, int lane, bool vec, float (&l)[V]) {
-  constexpr int kBytes = V * size_of(kKind);
-  const int e0 = lane * V;
-  if (vec && e0 + V <= E) {
-    uint32_t w[(kBytes + 3) / 4];
-    const char *p = static_cast<const char *>(row) + static_cast<int64_t>(e0) * size_of(kKind);
-    if constexpr (kBytes >= 16) {
+  constexpr int W = width(V), kBytes = W * size_of(kKind);
+  if (vec) {
 #pragma unroll
-      for (int i = 0; i < kBytes / 16; ++i) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p + 16 * i);
-        w[4 * i] = u.x;
-        w[4 * i + 1] = u.y;
-        w[4 * i + 2] = u.z;
-        w[4 * i + 3] = u.w;
+    for (int v = 0; v < V; v += W) {
+      const int e = expert<V>(lane, v);
+      uint32_t w[4] = {};
+      if (e < E) {
+        const char *p = static_cast<const char *>(row) + e * size_of(kKind);
+        if constexpr (kBytes == 16) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(p);
+          w[0] = u.x;
+          w[1] = u.y;
+          w[2] = u.z;
+          w[3] = u.w;
+        } else if constexpr (kBytes == 8) {
+          const uint2 u = *reinterpret_cast<const uint2 *>(p);
+          w[0] = u.x;
+          w[1] = u.y;
+        } else if constexpr (kBytes == 4) {
+          w[0] = *reinterpret_cast<const uint32_t *>(p);
+        } else {
+          w[0] = *reinterpret_cast<const uint16_t *>(p);
+        }
       }
-    } else if constexpr (kBytes == 8) {
-      const uint2 u = *reinterpret_cast<const uint2 *>(p);
-      w[0] = u.x;
-      w[1] = u.y;
-    } else if constexpr (kBytes == 4) {
-      w[0] = *reinterpret_cast<const uint32_t *>(p);
-    } else {
-      w[0] = *reinterpret_cast<const uint16_t *>(p);
-    }
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      l[v] = kKind == kFp32 ? __uint_as_float(w[v]) : (v & 1) ? bf16_hi(w[v / 2]) : bf16_lo(w[v / 2]);
+      for (int i = 0; i < W; ++i) {
+        const float x = kKind == kFp32 ? __uint_as_float(w[i]) : (i & 1) ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+        l[v + i] = e < E ? x : -INFINITY;
+      }
+    }
   } else {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = e0 + v;
+      const int e = expert<V>(lane, v);
       if (e >= E) l[v] = -INFINITY;
       else if constexpr (kKind == kFp32) l[v] = static_cast<const float *>(row)[e];
       else l[v] = bf16_lo(static_cast<const uint16_t *>(row)[e]);
     }
   }
 }
+// A row into the L2: its bytes are at most 32 lines.
+__device__ __forceinline__ void prefetch_row(const char *row, int bytes, int lane) {
+  if (lane * 128 < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + lane * 128));
+}
 __device__ __forceinline__ float logit_at(const void *row, int kind, int e) {
   return kind == kFp32 ? static_cast<const float *>(row)[e]
                        : bf16_lo(static_cast<const uint16_t *>(row)[e]);
 }
 
-// Warps of a CTA and expert words per lane: 64 registers per thread for up to 8
-// experts per lane, 128 for 16, 255 for 32.
-__host__ __device__ constexpr int warps_for(int V) { return V <= 8 ? 32 : V == 16 ? 16 : 8; }
+// Warps of a CTA: 64 registers per thread for up to 16 experts per lane, 128 for 32.
+// Many experts leave no room there for the next row, the sums of the probabilities and
+// the words that wait: the row waits in the L2, the others in shared memory.  (16384
+// tokens of 1024 experts, all in registers, eight warps: 73.6 us and backward 63.3, so
+// 55.1 and 28.6; of 512 31.5 and 22.6, so 28.3 and 16.3.  Backward of 256
+// experts 10.1 in registers and 10.7 so.)
+__host__ __device__ constexpr bool many(int V) { return V >= 16; }
+__host__ __device__ constexpr int warps_for(int V) { return V <= 16 ? 32 : 16; }
 
-// Where the lanes' sorted words wait for their turn: in registers, shifted in every
-// round, or, many of them, in shared memory, one column per lane and a zero behind its
-// words.  16384 tokens of 1024 experts, 8 choices: 79.8 us shifted, 73.7 queued, 32
-// choices 161.8 and 133.7; of 512 33.1 and 31.5.  Of 256 18.6 and 18.4, but one token
-// 3.9 and 4.2.
-__host__ __device__ constexpr bool queued(int V) { return V >= 16; }
-__host__ __device__ constexpr int queue_words(int V) { return queued(V) ? 32 * (V + 1) : 0; }  // of a warp
+// The lanes' sorted words, of one warp, in shared memory: one column per lane and a zero
+// behind its words.  16384 tokens of 1024 experts, 8 choices: 79.8 us with the words
+// shifted in registers every round, 73.7 so; of 256 18.6 and 18.4, but one token 3.9 and
+// 4.2.
+__host__ __device__ constexpr int queue_words(int V) { return many(V) ? 32 * (V + 1) : 0; }
 
 // Unsigned keys in the order of the logits, the same for both zeros.  -inf is below
 // kOpen, +inf and NaN (which the addition makes the positive one) at kSpecial or above.
@@ -153,16 +174,35 @@ __device__ __forceinline__ int choose_exactly(uint32_t (&key)[V], int k, int lan
       }
     const uint32_t top = __reduce_max_sync(~0u, best);
     if (top < kOpen) break;
-    const int owner = __ffs(__ballot_sync(~0u, best == top)) - 1;
-    if (lane == owner) {
+    const unsigned e = expert<V>(lane, at), first = __reduce_min_sync(~0u, best == top ? e : ~0u);
+    if (e == first) {
 #pragma unroll
       for (int v = 0; v < V; ++v)
         if (v == at) key[v] = 0;
     }
-    at = __shfl_sync(~0u, at, owner);
-    if (lane == j) chosen = owner * V + at;
+    if (lane == j) chosen = static_cast<int>(first);
   }
   return chosen;
+}
+
+// The choices of the lanes, nearly in order, into it: falling logits, equal ones by rising
+// experts, none (-1) last.  Neighbours are exchanged until two rounds change nothing.
+__device__ __forceinline__ bool comes_before(float x, int e, float y, int f) {
+  return e >= 0 && (f < 0 || x > y || (x == y && e < f));
+}
+__device__ __forceinline__ void sort_lanes(float &x, int &e, int lane) {
+  for (int odd = 0, still = 0; still < 2; odd ^= 1) {
+    const int other = ((lane - odd) ^ 1) + odd;
+    const float y = __shfl_sync(~0u, x, other & 31);
+    const int f = __shfl_sync(~0u, e, other & 31);
+    const bool paired = other >= 0 && other < 32;
+    const bool change = paired && (other > lane ? comes_before(y, f, x, e) : comes_before(x, e, y, f));
+    if (change) {
+      x = y;
+      e = f;
+    }
+    still = __any_sync(~0u, change) ? 0 : still + 1;
+  }
 }
 
 // exp2 and the reciprocal are right to 2 units and 1 unit in the last place, and
@@ -214,7 +254,8 @@ __device__ __forceinline__ int cta_exclusive_sum(int v, int *part) {
 // those of a whole grid, whose rows a second launch works out.
 enum Mode { kOneCta, kOneCluster, kGrid };
 
-// Dynamic shared memory: counts [warps][E], probabilities [warps][E], the warps' queues.
+// Dynamic shared memory: counts [warps][E], probabilities [warps][E, rounded up to 4],
+// the warps' words that wait.
 template <int kKind, int V, int kMode>
 __global__ void __launch_bounds__(32 * warps_for(V))
 route_kernel(const RouteArgs a) {
@@ -222,15 +263,19 @@ route_kernel(const RouteArgs a) {
   constexpr int kWarps = warps_for(V), kThreads = 32 * kWarps;
   constexpr int kEach = 32 * V > kThreads ? 32 * V / kThreads : 1;  // experts per thread, at most
   constexpr uint32_t kIndex = 32 * V - 1;                            // a word's index bits
-  extern __shared__ int smem[];
+  extern __shared__ __align__(16) int smem[];
   __shared__ int tokens_of[kWarps], scan[32], all_rows, cta_tokens, all_tokens;
   __shared__ float part[32];
   wait_for_previous_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E, k = a.k;
+  const int E4 = round_up(E, 4);
   int *counts = smem;
   float *probs = reinterpret_cast<float *>(smem + kWarps * E);
   int *mine = counts + warp * E;
+  float *my_probs = probs + warp * E4;
   for (int e = lane; e < E; e += 32) mine[e] = 0;
+  if constexpr (many(V))
+    for (int e = lane; e < E4; e += 32) my_probs[e] = 0.0f;
   __syncwarp();
 
   const int64_t cta_lo = static_cast<int64_t>(blockIdx.x) * a.per_cta;
@@ -239,28 +284,34 @@ route_kernel(const RouteArgs a) {
   const int n = static_cast<int>(cta_hi > cta_lo ? cta_hi - cta_lo : 0), each = n / kWarps, more = n % kWarps;
   const int64_t lo = cta_lo + warp * each + min(warp, more), hi = lo + each + (warp < more);
   const char *row = static_cast<const char *>(a.logits) + lo * a.ld * size_of(kKind);
-  float psum[V], next[V];
+  constexpr int kAhead = many(V) ? 1 : V;
+  float psum[kAhead], next[kAhead];
 #pragma unroll
-  for (int v = 0; v < V; ++v) psum[v] = 0.0f;
+  for (int v = 0; v < kAhead; ++v) psum[v] = 0.0f;
   int routed = 0;
   bool next_valid = true;
   if (lo < hi) {
-    load_logits<kKind, V>(row, E, lane, a.vec, next);
+    if constexpr (!many(V)) load_logits<kKind, V>(row, E, lane, a.vec, next);
     if (a.valid) next_valid = a.valid[lo] != 0;
   }
 
-  uint32_t *queue = reinterpret_cast<uint32_t *>(smem + 2 * kWarps * E) + warp * queue_words(V) + lane;
-  if constexpr (queued(V)) queue[32 * V] = 0;
-  const uint32_t below = kIndex - lane * V;  // index bits of the lane's first word
+  uint32_t *queue = reinterpret_cast<uint32_t *>(probs + kWarps * E4) + warp * queue_words(V) + lane;
+  if constexpr (many(V)) queue[32 * V] = 0;
+  const uint32_t below = kIndex - expert<V>(lane, 0);  // index bits of the lane's first word
   for (int64_t t = lo; t < hi; ++t) {
     float l[V];
     const bool valid = next_valid;
-#pragma unroll
-    for (int v = 0; v < V; ++v) l[v] = next[v];
     const char *here = row;
     row += a.ld * size_of(kKind);
+    if constexpr (many(V)) {
+      load_logits<kKind, V>(here, E, lane, a.vec, l);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) l[v] = next[v];
+    }
     if (t + 1 < hi) {  // in flight while this token is dealt with
-      load_logits<kKind, V>(row, E, lane, a.vec, next);
+      if constexpr (many(V)) prefetch_row(row, E * size_of(kKind), lane);
+      else load_logits<kKind, V>(row, E, lane, a.vec, next);
       if (a.valid) next_valid = a.valid[t + 1] != 0;
     }
     int chosen = -1;
@@ -269,7 +320,7 @@ route_kernel(const RouteArgs a) {
       uint32_t word[V];
       const auto make_words = [&]() {
 #pragma unroll
-        for (int v = 0; v < V; ++v) word[v] = (key_of(l[v]) & ~kIndex) | (below - v);
+        for (int v = 0; v < V; ++v) word[v] = (key_of(l[v]) & ~kIndex) | (below - expert<V>(0, v));
         sort_falling(word);
       };
       make_words();
@@ -279,16 +330,17 @@ route_kernel(const RouteArgs a) {
       }
       // lane j keeps the j-th largest word; of FP32 logits one round more tells whether
       // the last choice is apart from the rest
-      uint32_t kept = 0, top = 0;
-      if constexpr (queued(V)) {
+      if constexpr (many(V)) {
 #pragma unroll
         for (int v = 1; v < V; ++v) queue[32 * v] = word[v];
       }
-      for (int j = 0, at = 32; j < k + (kKind == kFp32); ++j) {
+      uint32_t kept = 0, top = 0;
+      int at = 32;
+      const auto round = [&](int j) {
         top = __reduce_max_sync(~0u, word[0]);
         if (lane == j) kept = top;
         if (word[0] == top) {
-          if constexpr (queued(V)) {
+          if constexpr (many(V)) {
             word[0] = queue[at];
             at += 32;
           } else {
@@ -297,16 +349,27 @@ route_kernel(const RouteArgs a) {
             word[V - 1] = 0;
           }
         }
-      }
+      };
+      for (int j = 0; j < k + (kKind == kFp32); ++j) round(j);
       if (lane < k && kept >= kOpen) chosen = static_cast<int>(kIndex - (kept & kIndex));
       if constexpr (kKind == kFp32) {
         uint32_t behind = __shfl_down_sync(~0u, kept, 1);
         if (lane == k - 1) behind = top;
         if (__any_sync(~0u, lane < k && behind >= kOpen && ((kept ^ behind) & ~kIndex) == 0)) {
-          uint32_t key[V];
+          const uint32_t last = __shfl_sync(~0u, kept, k - 1);
+          int j = k + 1;
+          while (top >= kOpen && ((top ^ last) & ~kIndex) == 0 && j < 32) round(j++);
+          if (top >= kOpen && ((top ^ last) & ~kIndex) == 0) {
+            uint32_t key[V];
 #pragma unroll
-          for (int v = 0; v < V; ++v) key[v] = key_of(l[v]);
-          chosen = choose_exactly<V>(key, k, lane);
+            for (int v = 0; v < V; ++v) key[v] = key_of(l[v]);
+            chosen = choose_exactly<V>(key, k, lane);
+          } else {
+            chosen = kept >= kOpen ? static_cast<int>(kIndex - (kept & kIndex)) : -1;
+            float x = chosen >= 0 ? logit_at(here, kKind, chosen) : 0.0f;
+            sort_lanes(x, chosen, lane);
+            if (lane >= k) chosen = -1;
+          }
         }
       }
       float x = 0.0f;
@@ -325,8 +388,21 @@ route_kernel(const RouteArgs a) {
 #pragma unroll
       for (int v = 0; v < V; ++v) sum += s[v];
       const float inv = rcp_ftz(fmaxf(warp_sum(sum), kTiny));
+      if constexpr (many(V)) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) psum[v] = fmaf(s[v], inv, psum[v]);
+        for (int v = 0; v < V; v += 4) {
+          const int e = expert<V>(lane, v);
+          if (e < E) {
+            float4 *p = reinterpret_cast<float4 *>(my_probs + e);
+            const float4 q = *p;
+            *p = make_float4(fmaf(s[v], inv, q.x), fmaf(s[v + 1], inv, q.y), fmaf(s[v + 2], inv, q.z),
+                             fmaf(s[v + 3], inv, q.w));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) psum[v] = fmaf(s[v], inv, psum[v]);
+      }
 
       if (chosen >= 0) w = a.sigmoid ? sigmoid(x) : exp_above(x, m) * inv;
       if (a.normalise) w *= rcp_ftz(fmaxf(warp_sum(w), kTiny));
@@ -344,9 +420,11 @@ route_kernel(const RouteArgs a) {
     }
     __syncwarp();
   }
+  if constexpr (!many(V)) {
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (lane * V + v < E) probs[warp * E + lane * V + v] = psum[v];
+    for (int v = 0; v < V; ++v)
+      if (expert<V>(lane, v) < E) my_probs[expert<V>(lane, v)] = psum[v];
+  }
   if (lane == 0) tokens_of[warp] = routed;
   __syncthreads();
 
@@ -364,7 +442,7 @@ route_kernel(const RouteArgs a) {
         const int c = counts[w * E + e];
         counts[w * E + e] = run;
         run += c;
-        p += probs[w * E + e];
+        p += probs[w * E4 + e];
       }
       if constexpr (!alone) {
         a.cta_counts[e * round_up(a.ctas, 8) + blockIdx.x] = static_cast<uint16_t>(run);
@@ -616,25 +694,29 @@ struct BwdArgs {
 //   dl  = (u + v) (1 - s) (sigmoid)  or  u - p sum u + v (softmax, sum u = 0 if
 //         normalised).
 // Nothing is divided by a score, so small ones lose nothing.
-constexpr int bwd_ctas_per_sm(int V) { return V <= 8 ? 4 : V == 16 ? 2 : 1; }
+constexpr int bwd_ctas_per_sm(int V) { return V <= 16 ? 4 : 2; }
 
 template <int kKind, int V>
 __global__ void __launch_bounds__(256, bwd_ctas_per_sm(V))
 route_bwd_kernel(const BwdArgs a) {
-  extern __shared__ __align__(16) float of_warps[];  // [warps][32 * V]
+  extern __shared__ __align__(16) float of_warps[];  // [warps][32 * V], many experts: and dp [32 * V]
   wait_for_previous_kernel();
+  constexpr int W = width(V), kAhead = many(V) ? 1 : V;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E, k = a.k;
-  float *u_of = of_warps + warp * 32 * V;
+  float *u_of = of_warps + warp * 32 * V, *dp_of = of_warps + (blockDim.x >> 5) * 32 * V;
   const int warps = gridDim.x * (blockDim.x >> 5);
   // lane j's choice, and the row's logits
   struct {
-    float l[V];
+    float l[kAhead];
     int at;
     float dw;
+    bool valid;
   } next;
   const auto fetch = [&](int64_t t) {
-    const bool valid = !a.valid || a.valid[t] != 0;
-    load_logits<kKind, V>(static_cast<const char *>(a.logits) + t * a.ld * size_of(kKind), E, lane, a.vec, next.l);
+    next.valid = !a.valid || a.valid[t] != 0;
+    const char *row = static_cast<const char *>(a.logits) + t * a.ld * size_of(kKind);
+    if constexpr (many(V)) prefetch_row(row, E * size_of(kKind), lane);
+    else load_logits<kKind, V>(row, E, lane, a.vec, next.l);
     next.at = -1;
     next.dw = 0.0f;
     if (lane < k && a.dweight) {
@@ -642,20 +724,15 @@ route_bwd_kernel(const BwdArgs a) {
       if (next.at >= E) next.at = -1;
       next.dw = a.dweight[t * k + lane] * a.scale;
     }
-    if (!valid) {
-      next.at = -1;
-#pragma unroll
-      for (int v = 0; v < V; ++v) next.l[v] = -INFINITY;
-    }
   };
   int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp;
   if (t < a.T) fetch(t);
-  float dp[V];
+  float dp[kAhead];
   {
     int c[V], n = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = lane * V + v;
+      const int e = expert<V>(lane, v);
       u_of[e] = 0.0f;
       c[v] = e < E && a.dloss ? a.counts[e] : 0;
       n += c[v];
@@ -665,17 +742,43 @@ route_bwd_kernel(const BwdArgs a) {
     const float f = tokens > 0 && n > 0 ? a.dloss[0] * static_cast<float>(E) / static_cast<float>(n) /
                                               static_cast<float>(tokens)
                                         : 0.0f;
+    if constexpr (many(V)) {
+      if (warp == 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) dp[v] = f * static_cast<float>(c[v]);
+        for (int v = 0; v < V; ++v) dp_of[expert<V>(lane, v)] = f * static_cast<float>(c[v]);
+      }
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) dp[v] = f * static_cast<float>(c[v]);
+      __syncwarp();
+    }
   }
-  __syncwarp();
+  // W of dp, from the lane's v-th expert on
+  const auto dp_at = [&](int v, float (&d)[W]) {
+    if constexpr (many(V)) {
+      const float4 q = *reinterpret_cast<const float4 *>(dp_of + expert<V>(lane, v));
+      d[0] = q.x;
+      d[1] = q.y;
+      d[2] = q.z;
+      d[3] = q.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) d[i] = dp[v + i];
+    }
+  };
   for (; t < a.T; t += warps) {
     float l[V], s[V], c[V];  // c: 1 - s of a sigmoid
-#pragma unroll
-    for (int v = 0; v < V; ++v) l[v] = next.l[v];
-    const int at = next.at;
-    const float dw = next.dw;
     const char *row = static_cast<const char *>(a.logits) + t * a.ld * size_of(kKind);
+    const bool valid = next.valid;
+    if constexpr (many(V)) load_logits<kKind, V>(row, E, lane, a.vec, l);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if constexpr (!many(V)) l[v] = next.l[v];
+      if (!valid) l[v] = -INFINITY;
+    }
+    const int at = valid ? next.at : -1;
+    const float dw = next.dw;
     if (t + warps < a.T) fetch(t + warps);  // in flight while this token is dealt with
 
     bool special = false;
@@ -706,7 +809,12 @@ route_bwd_kernel(const BwdArgs a) {
     }
     float pdp = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) pdp = fmaf(s[v], dp[v], pdp);
+    for (int v = 0; v < V; v += W) {
+      float d[W];
+      dp_at(v, d);
+#pragma unroll
+      for (int i = 0; i < W; ++i) pdp = fmaf(s[v + i], d[i], pdp);
+    }
     const float inv = rcp_ftz(fmaxf(warp_sum(sum), kTiny));
     pdp = warp_sum(pdp) * inv;
 
@@ -734,46 +842,44 @@ route_bwd_kernel(const BwdArgs a) {
       u_of[at] = u;
     }
     __syncwarp();
-    float us[V];
-    if constexpr (V % 4 == 0) {
+    // closed experts have s = 0 and u = 0
+    const float z = pdp + usum;
+    char *out = static_cast<char *>(a.dlogits) + t * a.ld_d * size_of(kKind);
 #pragma unroll
-      for (int v = 0; v < V; v += 4) {
-        const float4 f = *reinterpret_cast<const float4 *>(u_of + lane * V + v);
-        us[v] = f.x;
-        us[v + 1] = f.y;
-        us[v + 2] = f.z;
-        us[v + 3] = f.w;
+    for (int v = 0; v < V; v += W) {
+      const int e = expert<V>(lane, v);
+      float d[W], us[W];
+      dp_at(v, d);
+      if constexpr (W == 4) {
+        const float4 q = *reinterpret_cast<const float4 *>(u_of + e);
+        us[0] = q.x;
+        us[1] = q.y;
+        us[2] = q.z;
+        us[3] = q.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) us[i] = u_of[e + i];
       }
-    } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) us[v] = u_of[lane * V + v];
+      for (int i = 0; i < W; ++i) d[i] = fmaf(s[v + i] * inv, d[i] - z, us[i]) * c[v + i];
+      if (W == 4 && a.vec_d) {
+        if (e < E) {
+          if constexpr (W == 4 && kKind == kFp32)
+            *reinterpret_cast<float4 *>(out + 4 * e) = make_float4(d[0], d[1], d[2], d[3]);
+          else if constexpr (W == 4)
+            *reinterpret_cast<uint2 *>(out + 2 * e) = make_uint2(bf16x2(d[0], d[1]), bf16x2(d[2], d[3]));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          if (e + i < E) {
+            if constexpr (kKind == kFp32) reinterpret_cast<float *>(out)[e + i] = d[i];
+            else reinterpret_cast<uint16_t *>(out)[e + i] = static_cast<uint16_t>(bf16x2(d[i], 0.0f));
+          }
+      }
     }
     __syncwarp();
     if (at >= 0) u_of[at] = 0.0f;
-    // closed experts have s = 0 and u = 0
-    const float z = pdp + usum;
-    float d[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) d[v] = fmaf(s[v] * inv, dp[v] - z, us[v]) * c[v];
-
-    char *out = static_cast<char *>(a.dlogits) + t * a.ld_d * size_of(kKind);
-    const int e0 = lane * V;
-    if (V % 8 == 0 && a.vec_d && e0 + V <= E) {
-#pragma unroll
-      for (int i = 0; i < V / 8; ++i) {
-        float part[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) part[e] = d[8 * i + e];
-        store8<kKind>(out, e0 + 8 * i, part);
-      }
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (e0 + v < E) {
-          if constexpr (kKind == kFp32) reinterpret_cast<float *>(out)[e0 + v] = d[v];
-          else reinterpret_cast<uint16_t *>(out)[e0 + v] = static_cast<uint16_t>(bf16x2(d[v], 0.0f));
-        }
-    }
   }
 }
 
@@ -787,9 +893,9 @@ struct Plan {
   int ctas, per_cta;
 };
 Plan plan(int64_t T, int64_t E) {
-  const int warps = warps_for(E <= 256 ? 8 : E <= 512 ? 16 : 32);
+  const int warps = warps_for(E <= 512 ? 16 : 32);
   Plan p;
-  if (T <= (E <= 256 ? warps : 2 * warps)) {
+  if (T <= warps) {
     p.mode = kOneCta;
     p.ctas = 1;
   } else if (E <= 256 && T <= kCluster * warps) {
@@ -812,7 +918,7 @@ template <int kKind, int V, int kMode>
 fp8q_status launch_choice(const RouteArgs &a, cudaStream_t s) {
   constexpr int kWarps = warps_for(V), kQueues = kWarps * queue_words(V) * 4, kMost = kWarps * 32 * V * 8 + kQueues;
   constexpr auto kern = route_kernel<kKind, V, kMode>;
-  const size_t smem = static_cast<size_t>(kWarps) * a.E * (sizeof(int) + sizeof(float)) + kQueues;
+  const size_t smem = static_cast<size_t>(kWarps) * (a.E + round_up(a.E, 4)) * 4 + kQueues;
   if (smem > 40 * 1024)
     if (fp8q_status st = allow_smem<kern>(kMost)) return st;
   if constexpr (kMode == kOneCluster)
@@ -843,7 +949,7 @@ fp8q_status launch_route(const RouteArgs &a, Mode mode, cudaStream_t s) {
 template <int kKind, int V>
 fp8q_status launch_bwd(const BwdArgs &a, cudaStream_t s) {
   const int warps = 8, need = (a.T + warps - 1) / warps, most = kSms * bwd_ctas_per_sm(V);
-  const size_t smem = static_cast<size_t>(warps) * 32 * V * sizeof(float);
+  const size_t smem = static_cast<size_t>(warps + many(V)) * 32 * V * sizeof(float);
   return launch_dependent(route_bwd_kernel<kKind, V>, dim3(need < most ? need : most), dim3(32 * warps),
                           smem, s, a);
 }
@@ -924,7 +1030,7 @@ extern "C" fp8q_status fp8q_route(const void *logits, int64_t ld, int dtype, con
   a.scale = scale;
   a.sigmoid = score == FP8Q_SCORE_SIGMOID;
   a.normalise = normalise != 0;
-  a.vec = row_vectors(logits, ld, dtype);
+  a.vec = E % 4 == 0 && row_vectors(logits, ld, dtype);
   auto st = static_cast<cudaStream_t>(stream);
   return dtype == kBf16 ? launch_route<kBf16>(a, p.mode, st) : launch_route<kFp32>(a, p.mode, st);
 }
@@ -964,8 +1070,8 @@ extern "C" fp8q_status fp8q_route_bwd(const void *logits, int64_t ld, int dtype,
   a.scale = scale;
   a.sigmoid = score == FP8Q_SCORE_SIGMOID;
   a.normalise = normalise != 0;
-  a.vec = row_vectors(logits, ld, dtype);
-  a.vec_d = row_vectors(dlogits, ld_d, dtype);
+  a.vec = E % 4 == 0 && row_vectors(logits, ld, dtype);
+  a.vec_d = E % 4 == 0 && row_vectors(dlogits, ld_d, dtype);
   auto st = static_cast<cudaStream_t>(stream);
   return dtype == kBf16 ? launch_bwd<kBf16>(a, st) : launch_bwd<kFp32>(a, st);
 }

@@ -131,6 +131,24 @@ def test_ties_take_the_lowest_index(T):
         check(fq.fp8q_route(l.cuda(), 5, score=SIG), l, None, 5, SIG, True, 1.0)
 
 
+@pytest.mark.parametrize("T", [5, 400])
+@pytest.mark.parametrize("E,k", [(8, 8), (20, 3), (100, 8), (256, 1), (256, 32), (400, 16), (700, 31), (1024, 8), (1024, 32)])
+@pytest.mark.parametrize("steps", [1, 4, 300])
+def test_logits_that_differ_in_their_last_bits(T, E, k, steps):
+    # a few values and multiples of a unit in their last place, both signs, equal ones among them:
+    # groups that agree in the upper bits end inside the choice, at its end, behind more than 32
+    g = torch.Generator().manual_seed(E * k + steps)
+    l = torch.randint(-3, 4, (T, E), generator=g).float()
+    l = l * (1 + torch.randint(0, steps, (T, E), generator=g) * 2.0 ** -23)
+    l[:, E // 2] = -0.0
+    l[T // 2] = 1.0
+    l[T // 3, : E - 1] = float("-inf")
+    out = fq.fp8q_route(l.cuda(), k)
+    order = torch.sort(l.double() + 0.0, dim=1, descending=True, stable=True)
+    want = torch.where(order.values > float("-inf"), order.indices, -1)[:, :k].int()
+    assert torch.equal(out.idx.cpu(), want)
+
+
 @pytest.mark.parametrize("T", [6, 300])
 @pytest.mark.parametrize("score", [SOFT, SIG])
 @pytest.mark.parametrize("dtype", [FP, BF])
