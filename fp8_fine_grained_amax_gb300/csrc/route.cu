@@ -569,18 +569,28 @@ __device__ __forceinline__ int sum8(uint4 v, int n) {
   return static_cast<int>(s);
 }
 
-// CTA b turns ranks into rows: expert e's choices of CTA b start at offs[e] plus
-// the counts of the CTAs before it.  As many threads as there is room for share an
-// expert (1 to 32, next to each other) and read its counts eight CTAs at a time.  The
-// last CTA also writes the totals.
+// CTA b turns ranks into rows: expert e's choices of CTA b start at offs[e] plus the
+// counts of the CTAs before it.  The CTAs of a cluster share the experts: each adds up the
+// counts of its part, before the cluster's first CTA and in all, with as many threads per
+// expert as there is room for (1 to 32, next to each other, eight CTAs' counts at a time,
+// kBatch loads in flight in each), and the others read the sums from its shared memory.
+// The last cluster also adds up the probabilities, and its first CTA writes the totals.
+// More than 128 experts take clusters of two (16384 tokens of 256 experts 17.7 us, each
+// CTA by itself 18.3, clusters of four, which do not all run at once, 21.9; of 1024 44.7,
+// 54.8 and 44.7; of 64 13.0, 12.7 and 15.7), and more than 256 need five loads in a thread
+// instead of three (of 256: 17.4 with three, 17.7 with five; of 512: 25.4 and 24.9).
+template <int kRowCluster, int kBatch>
 __global__ void __launch_bounds__(kRowThreads)
 route_rows_kernel(const RouteArgs a) {
+  constexpr int kPart = kMaxExperts / kRowCluster;
   __shared__ int first_row[kMaxExperts], scan[32], tokens_of[32];
-  __shared__ float part[32];
+  __shared__ int total_of[kPart], before_of[kRowCluster][kPart];  // of this CTA's part of the experts
+  __shared__ float prob_of[kPart], loss_of[32];
   __shared__ int rows;
   wait_for_previous_kernel();
   const int E = a.E, k = a.k, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
-  const bool totals = cta == a.ctas - 1;
+  const int rank = cta % kRowCluster, base = cta - rank;
+  const bool last = base + kRowCluster == gridDim.x;
   const int64_t lo = static_cast<int64_t>(cta) * a.per_cta * k;
   const int64_t hi = min(static_cast<int64_t>(a.T) * k, lo + static_cast<int64_t>(a.per_cta) * k);
   // the thread's first choice, in flight while the counts are added up
@@ -589,16 +599,24 @@ route_rows_kernel(const RouteArgs a) {
     next_idx = a.idx[lo + tid];
     next_slot = a.slot[lo + tid];
   }
-  int share = 1;  // threads per expert
-  while (share < 32 && 2 * share * E <= kRowThreads) share *= 2;
-  const int e = tid / share, mine = tid % share;
+  const int part = (E + kRowCluster - 1) / kRowCluster;  // experts of a CTA
+  int share = 1;                                         // threads per expert
+  while (share < 32 && 2 * share * part <= kRowThreads) share *= 2;
+  const int at = tid / share, mine = tid % share, e = rank * part + at;
+  const bool adds = at < part && e < E;
   int total = 0, before = 0, tokens = 0;
   float probs = 0.0f;
-  if (totals)
+  if (last && rank == 0)
     for (int b = tid; b < a.ctas; b += kRowThreads) tokens += a.cta_tokens[b];
-  if (e < E) {
-    constexpr int kBatch = 5;
-    const uint4 *c = reinterpret_cast<const uint4 *>(a.cta_counts + e * round_up(a.ctas, 8));
+  int own[kRowCluster] = {};  // counts of the cluster's CTAs
+  if (adds) {
+    const uint16_t *counts = a.cta_counts + e * round_up(a.ctas, 8);
+    const uint4 *c = reinterpret_cast<const uint4 *>(counts);
+    if (mine == 0) {
+#pragma unroll
+      for (int r = 0; r < kRowCluster; ++r)
+        if (base + r < a.ctas) own[r] = counts[base + r];
+    }
     const int n = round_up(a.ctas, 8) / 8;
     for (int j0 = mine; j0 < n; j0 += kBatch * share) {
       uint4 v[kBatch];
@@ -608,10 +626,10 @@ route_rows_kernel(const RouteArgs a) {
       for (int i = 0; i < kBatch; ++i) {
         const int b0 = 8 * (j0 + i * share);
         total += sum8(v[i], a.ctas - b0);
-        before += sum8(v[i], cta - b0);
+        before += sum8(v[i], base - b0);
       }
     }
-    if (totals) {
+    if (last) {
       const float4 *p = reinterpret_cast<const float4 *>(a.cta_probs + e * round_up(a.ctas, 4));
       const int m = round_up(a.ctas, 4) / 4;
       for (int j0 = mine; j0 < m; j0 += kBatch * share) {
@@ -633,25 +651,45 @@ route_rows_kernel(const RouteArgs a) {
     before += __shfl_xor_sync(~0u, before, o);
     probs += __shfl_xor_sync(~0u, probs, o);
   }
-  const bool leads = e < E && mine == 0;  // for its expert
-  const int first = cta_exclusive_sum(leads ? total : 0, scan);
-  if (leads) first_row[e] = first + before;
-  if (tid == kRowThreads - 1) rows = first + (leads ? total : 0);
-  if (totals) {
-    if (leads) {
-      a.counts[e] = total;
-      a.offs[e] = first;
+  if (adds && mine == 0) {
+    total_of[at] = total;
+    prob_of[at] = probs;
+#pragma unroll
+    for (int r = 0; r < kRowCluster; ++r) {
+      before_of[r][at] = before;
+      before += own[r];
     }
-    const float p = warp_sum(leads ? static_cast<float>(total) * probs : 0.0f);
+  }
+  cluster_sync_all();
+  // thread i has expert i from here on
+  total = before = 0;
+  probs = 0.0f;
+  if (tid < E) {
+    const int owner = tid / part, there = tid % part;
+    total = static_cast<int>(ld_cluster(mapa_shared(smem_u32(total_of + there), owner)));
+    before = static_cast<int>(ld_cluster(mapa_shared(smem_u32(&before_of[rank][there]), owner)));
+    if (last && rank == 0) probs = __uint_as_float(ld_cluster(mapa_shared(smem_u32(prob_of + there), owner)));
+  }
+  const int first = cta_exclusive_sum(total, scan);
+  first_row[tid] = first + before;
+  if (tid == kRowThreads - 1) rows = first + total;
+  if (last && rank == 0) {
+    if (tid < E) {
+      a.counts[tid] = total;
+      a.offs[tid] = first;
+    }
+    const float p = warp_sum(static_cast<float>(total) * probs);
     tokens = warp_sum(tokens);
     if (lane == 0) {
-      part[warp] = p;
+      loss_of[warp] = p;
       tokens_of[warp] = tokens;
     }
   }
   __syncthreads();
-  if (totals && warp == 0) {
-    const float loss = warp_sum(part[lane]);
+  // what this CTA read of the others has arrived: it was stored before the barrier
+  cluster_arrive_relaxed();
+  if (last && rank == 0 && warp == 0) {
+    const float loss = warp_sum(loss_of[lane]);
     tokens = warp_sum(tokens_of[lane]);
     if (lane == 0) {
       a.offs[E] = rows;
@@ -660,18 +698,19 @@ route_rows_kernel(const RouteArgs a) {
     }
   }
   for (int64_t i = lo + tid; i < hi; i += kRowThreads) {
-    const int x = next_idx, rank = next_slot;
+    const int x = next_idx, rank_here = next_slot;
     if (i + kRowThreads < hi) {
       next_idx = a.idx[i + kRowThreads];
       next_slot = a.slot[i + kRowThreads];
     }
     if (x >= 0) {
-      const int r = rank + first_row[x];
+      const int r = rank_here + first_row[x];
       a.slot[i] = r;
       a.order[r] = static_cast<int32_t>(i);
     }
     if (i >= rows) a.order[i] = -1;
   }
+  cluster_wait();  // a CTA's sums stay until all have read them
 }
 
 struct BwdArgs {
@@ -933,7 +972,11 @@ fp8q_status launch_route(const RouteArgs &a, Mode mode, cudaStream_t s) {
     if (mode == kOneCluster) return launch_choice<kKind, V, kOneCluster>(a, s);
   }
   if (fp8q_status st = launch_choice<kKind, V, kGrid>(a, s)) return st;
-  return launch_dependent(route_rows_kernel, dim3(a.ctas), dim3(kRowThreads), 0, s, a);
+  if constexpr (V <= 4)
+    return launch_dependent(route_rows_kernel<1, 3>, dim3(a.ctas), dim3(kRowThreads), 0, s, a);
+  else
+    return launch_dependent_cluster(route_rows_kernel<2, V <= 8 ? 3 : 5>, dim3(round_up(a.ctas, 2)), dim3(kRowThreads),
+                                    0, s, 2, a);
 }
 
 template <int kKind>
