@@ -37,6 +37,7 @@ namespace {
 constexpr int kSms = 152;         // one CTA each
 constexpr int kMaxPerCta = 65535; // tokens of a CTA: its counts are 16 bits
 constexpr int kCluster = 8;
+constexpr int kOneCtaTokens = 32;  // a token per warp, of the most experts two
 constexpr int kFewPerCta = 8;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxChoices = 32;   // one per lane
@@ -733,7 +734,7 @@ struct BwdArgs {
 //   dl  = (u + v) (1 - s) (sigmoid)  or  u - p sum u + v (softmax, sum u = 0 if
 //         normalised).
 // Nothing is divided by a score, so small ones lose nothing.
-constexpr int bwd_ctas_per_sm(int V) { return V <= 16 ? 4 : 2; }
+constexpr int bwd_ctas_per_sm(int V) { return V == 1 ? 6 : V <= 16 ? 4 : 2; }
 
 template <int kKind, int V>
 __global__ void __launch_bounds__(256, bwd_ctas_per_sm(V))
@@ -923,21 +924,21 @@ route_bwd_kernel(const BwdArgs a) {
 }
 
 // How a call's tokens are spread; the same for every device, so that the probabilities'
-// sums are too.  256 experts: 17 tokens take 4.8 us in one CTA and 6.1 in a cluster, 64
-// take 8.0, 6.3 and, in two launches, 9.9, 256 take 8.2 in a cluster and 9.9 in two
-// launches, 512 10.5 and 9.4.  With more than 256 experts the exchange is slower than
-// the second launch (1024 experts, 64 tokens: 22.0 and 16.6 us).
+// sums are too.  256 experts: 17 tokens take 4.5 us in one CTA and 5.4 in a cluster, 64
+// take 7.7, 5.7 and, in two launches, 7.9, 256 take 7.2 in a cluster and 8.2 in two
+// launches, 512 9.6 and 8.5.  512 experts: 64 tokens 10.6, 7.8 and 9.9.  The totals of
+// more take longer to exchange than a second launch (1024 experts: 32 tokens 11.2 in one
+// CTA and 11.9 in two launches, 64 12.4 in a cluster and 12.1, 256 17.7 and 14.2).
 struct Plan {
   Mode mode;
   int ctas, per_cta;
 };
 Plan plan(int64_t T, int64_t E) {
-  const int warps = warps_for(E <= 512 ? 16 : 32);
   Plan p;
-  if (T <= warps) {
+  if (T <= kOneCtaTokens) {
     p.mode = kOneCta;
     p.ctas = 1;
-  } else if (E <= 256 && T <= kCluster * warps) {
+  } else if (E <= 512 && T <= kCluster * kOneCtaTokens) {
     p.mode = kOneCluster;
     p.ctas = kCluster;
   } else {
@@ -968,7 +969,7 @@ fp8q_status launch_choice(const RouteArgs &a, cudaStream_t s) {
 template <int kKind, int V>
 fp8q_status launch_route(const RouteArgs &a, Mode mode, cudaStream_t s) {
   if (mode == kOneCta) return launch_choice<kKind, V, kOneCta>(a, s);
-  if constexpr (V <= 8) {
+  if constexpr (V <= 16) {
     if (mode == kOneCluster) return launch_choice<kKind, V, kOneCluster>(a, s);
   }
   if (fp8q_status st = launch_choice<kKind, V, kGrid>(a, s)) return st;

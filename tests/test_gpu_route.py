@@ -107,7 +107,8 @@ GRID = [(1, 1, 1, FP), (1, 256, 8, FP), (2, 8, 2, BF), (15, 3, 3, FP), (64, 64, 
         (66, 128, 1, BF), (333, 64, 6, BF), (777, 160, 8, FP), (1000, 7, 2, FP), (2431, 16, 1, BF), (2433, 16, 4, FP),
         (5003, 100, 5, BF), (300, 512, 12, FP), (257, 1024, 32, FP), (70, 1000, 16, BF), (20000, 256, 8, FP),
         # one CTA, a cluster and two launches on both sides of where each ends
-        (32, 256, 8, FP), (33, 200, 7, FP), (200, 256, 8, BF), (256, 256, 8, FP), (257, 256, 8, FP), (17, 600, 5, FP)]
+        (32, 256, 8, FP), (33, 200, 7, FP), (200, 256, 8, BF), (256, 256, 8, FP), (257, 256, 8, FP), (17, 600, 5, FP),
+        (33, 512, 8, FP), (255, 400, 9, BF), (256, 512, 32, FP), (257, 512, 3, FP), (32, 1024, 8, FP), (33, 1000, 8, BF)]
 
 
 @pytest.mark.parametrize("T,E,k,dtype", GRID)
