@@ -68,50 +68,64 @@ __device__ __forceinline__ constexpr int expert(int lane, int v) {
   return v / W * 32 * W + lane * W + v % W;
 }
 
-// A lane's logits of a row; -inf behind column E.  `vec`: the row starts on 16 bytes and
-// E is a multiple of four.
+// A lane's logits of a row as they lie in memory, -inf behind column E: what is done with
+// them would make the load wait, so nothing is until their turn.
 template <int kKind, int V>
-__device__ __forceinline__ void load_logits(const void *row, int E, int lane, bool vec, float (&l)[V]) {
-  constexpr int W = width(V), kBytes = W * size_of(kKind);
-  if (vec) {
+struct Row {
+  static constexpr int W = width(V), kWords = kKind == kFp32 ? V : (V + 1) / 2;
+  uint32_t w[kWords];
+
+  // `vec`: the row starts on 16 bytes and E is a multiple of four.
+  __device__ __forceinline__ void load(const void *row, int E, int lane, bool vec) {
+    constexpr uint32_t kClosed = kKind == kFp32 ? 0xFF800000u : 0xFF80FF80u;
 #pragma unroll
-    for (int v = 0; v < V; v += W) {
-      const int e = expert<V>(lane, v);
-      uint32_t w[4] = {};
-      if (e < E) {
+    for (int i = 0; i < kWords; ++i) w[i] = kClosed;
+    if (vec) {
+      constexpr int kBytes = W * size_of(kKind);
+#pragma unroll
+      for (int v = 0; v < V; v += W) {
+        const int e = expert<V>(lane, v);
+        if (e >= E) continue;
         const char *p = static_cast<const char *>(row) + e * size_of(kKind);
         if constexpr (kBytes == 16) {
           const uint4 u = *reinterpret_cast<const uint4 *>(p);
-          w[0] = u.x;
-          w[1] = u.y;
-          w[2] = u.z;
-          w[3] = u.w;
+          w[v] = u.x;
+          w[v + 1] = u.y;
+          w[v + 2] = u.z;
+          w[v + 3] = u.w;
         } else if constexpr (kBytes == 8) {
+          constexpr int at = kKind == kFp32 ? 1 : 2;
           const uint2 u = *reinterpret_cast<const uint2 *>(p);
-          w[0] = u.x;
-          w[1] = u.y;
+          w[v / at] = u.x;
+          w[v / at + 1] = u.y;
         } else if constexpr (kBytes == 4) {
           w[0] = *reinterpret_cast<const uint32_t *>(p);
         } else {
           w[0] = *reinterpret_cast<const uint16_t *>(p);
         }
       }
+    } else {
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const float x = kKind == kFp32 ? __uint_as_float(w[i]) : (i & 1) ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
-        l[v + i] = e < E ? x : -INFINITY;
+      for (int v = 0; v < V; ++v) {
+        const int e = expert<V>(lane, v);
+        if (e >= E) continue;
+        if constexpr (kKind == kFp32) {
+          w[v] = static_cast<const uint32_t *>(row)[e];
+        } else {
+          const uint32_t x = static_cast<const uint16_t *>(row)[e];
+          w[v / 2] = v & 1 ? (w[v / 2] & 0xFFFFu) | x << 16 : (w[v / 2] & 0xFFFF0000u) | x;
+        }
       }
     }
-  } else {
+  }
+  __device__ __forceinline__ void values(float (&l)[V]) const {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = expert<V>(lane, v);
-      if (e >= E) l[v] = -INFINITY;
-      else if constexpr (kKind == kFp32) l[v] = static_cast<const float *>(row)[e];
-      else l[v] = bf16_lo(static_cast<const uint16_t *>(row)[e]);
+      if constexpr (kKind == kFp32) l[v] = __uint_as_float(w[v]);
+      else l[v] = v & 1 ? bf16_hi(w[v / 2]) : bf16_lo(w[v / 2]);
     }
   }
-}
+};
 // A row into the L2: its bytes are at most 32 lines.
 __device__ __forceinline__ void prefetch_row(const char *row, int bytes, int lane) {
   if (lane * 128 < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + lane * 128));
@@ -286,13 +300,14 @@ route_kernel(const RouteArgs a) {
   const int64_t lo = cta_lo + warp * each + min(warp, more), hi = lo + each + (warp < more);
   const char *row = static_cast<const char *>(a.logits) + lo * a.ld * size_of(kKind);
   constexpr int kAhead = many(V) ? 1 : V;
-  float psum[kAhead], next[kAhead];
+  float psum[kAhead];
+  Row<kKind, V> next;
 #pragma unroll
   for (int v = 0; v < kAhead; ++v) psum[v] = 0.0f;
   int routed = 0;
   bool next_valid = true;
   if (lo < hi) {
-    if constexpr (!many(V)) load_logits<kKind, V>(row, E, lane, a.vec, next);
+    if constexpr (!many(V)) next.load(row, E, lane, a.vec);
     if (a.valid) next_valid = a.valid[lo] != 0;
   }
 
@@ -304,15 +319,11 @@ route_kernel(const RouteArgs a) {
     const bool valid = next_valid;
     const char *here = row;
     row += a.ld * size_of(kKind);
-    if constexpr (many(V)) {
-      load_logits<kKind, V>(here, E, lane, a.vec, l);
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) l[v] = next[v];
-    }
+    if constexpr (many(V)) next.load(here, E, lane, a.vec);
+    next.values(l);
     if (t + 1 < hi) {  // in flight while this token is dealt with
       if constexpr (many(V)) prefetch_row(row, E * size_of(kKind), lane);
-      else load_logits<kKind, V>(row, E, lane, a.vec, next);
+      else next.load(row, E, lane, a.vec);
       if (a.valid) next_valid = a.valid[t + 1] != 0;
     }
     int chosen = -1;
@@ -747,7 +758,7 @@ route_bwd_kernel(const BwdArgs a) {
   const int warps = gridDim.x * (blockDim.x >> 5);
   // lane j's choice, and the row's logits
   struct {
-    float l[kAhead];
+    Row<kKind, V> l;
     int at;
     float dw;
     bool valid;
@@ -756,13 +767,12 @@ route_bwd_kernel(const BwdArgs a) {
     next.valid = !a.valid || a.valid[t] != 0;
     const char *row = static_cast<const char *>(a.logits) + t * a.ld * size_of(kKind);
     if constexpr (many(V)) prefetch_row(row, E * size_of(kKind), lane);
-    else load_logits<kKind, V>(row, E, lane, a.vec, next.l);
+    else next.l.load(row, E, lane, a.vec);
     next.at = -1;
     next.dw = 0.0f;
     if (lane < k && a.dweight) {
       next.at = a.idx[t * k + lane];
-      if (next.at >= E) next.at = -1;
-      next.dw = a.dweight[t * k + lane] * a.scale;
+      next.dw = a.dweight[t * k + lane];
     }
   };
   int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp;
@@ -811,14 +821,13 @@ route_bwd_kernel(const BwdArgs a) {
     float l[V], s[V], c[V];  // c: 1 - s of a sigmoid
     const char *row = static_cast<const char *>(a.logits) + t * a.ld * size_of(kKind);
     const bool valid = next.valid;
-    if constexpr (many(V)) load_logits<kKind, V>(row, E, lane, a.vec, l);
+    if constexpr (many(V)) next.l.load(row, E, lane, a.vec);
+    next.l.values(l);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if constexpr (!many(V)) l[v] = next.l[v];
+    for (int v = 0; v < V; ++v)
       if (!valid) l[v] = -INFINITY;
-    }
-    const int at = valid ? next.at : -1;
-    const float dw = next.dw;
+    const int at = valid && next.at < E ? next.at : -1;
+    const float dw = next.dw * a.scale;
     if (t + warps < a.T) fetch(t + warps);  // in flight while this token is dealt with
 
     bool special = false;
@@ -902,12 +911,16 @@ route_bwd_kernel(const BwdArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < W; ++i) d[i] = fmaf(s[v + i] * inv, d[i] - z, us[i]) * c[v + i];
-      if (W == 4 && a.vec_d) {
+      if (W > 1 && a.vec_d) {
         if (e < E) {
           if constexpr (W == 4 && kKind == kFp32)
             *reinterpret_cast<float4 *>(out + 4 * e) = make_float4(d[0], d[1], d[2], d[3]);
           else if constexpr (W == 4)
             *reinterpret_cast<uint2 *>(out + 2 * e) = make_uint2(bf16x2(d[0], d[1]), bf16x2(d[2], d[3]));
+          else if constexpr (W == 2 && kKind == kFp32)
+            *reinterpret_cast<float2 *>(out + 4 * e) = make_float2(d[0], d[1]);
+          else if constexpr (W == 2)
+            *reinterpret_cast<uint32_t *>(out + 2 * e) = bf16x2(d[0], d[1]);
         }
       } else {
 #pragma unroll
