@@ -138,16 +138,15 @@ __device__ __forceinline__ float logit_at(const void *row, int kind, int e) {
 // Warps of a CTA: 64 registers per thread for up to 16 experts per lane, 128 for 32.
 // Many experts leave no room there for the next row, the sums of the probabilities and
 // the words that wait: the row waits in the L2, the others in shared memory.  (16384
-// tokens of 1024 experts, all in registers, eight warps: 73.6 us and backward 63.3, so
-// 55.1 and 28.6; of 512 31.5 and 22.6, so 28.3 and 16.3.  Backward of 256
-// experts 10.1 in registers and 10.7 so.)
+// tokens of 1024 experts, all in registers, eight warps: 73.6 us, so 55.1; of 512 31.5 and
+// 28.3.  Both figures from before the second launch's CTAs shared their sums.)
 __host__ __device__ constexpr bool many(int V) { return V >= 16; }
 __host__ __device__ constexpr int warps_for(int V) { return V <= 16 ? 32 : 16; }
 
 // The lanes' sorted words, of one warp, in shared memory: one column per lane and a zero
-// behind its words.  16384 tokens of 1024 experts, 8 choices: 79.8 us with the words
-// shifted in registers every round, 73.7 so; of 256 18.6 and 18.4, but one token 3.9 and
-// 4.2.
+// behind its words.  Shifted in registers every round, they took 16384 tokens of 1024
+// experts 6 us longer with 8 choices and 28 with 32; of 256 they save 0.2, but one token
+// takes 4.2 us instead of 3.9.
 __host__ __device__ constexpr int queue_words(int V) { return many(V) ? 32 * (V + 1) : 0; }
 
 // Unsigned keys in the order of the logits, the same for both zeros.  -inf is below
@@ -745,10 +744,15 @@ struct BwdArgs {
 //   dl  = (u + v) (1 - s) (sigmoid)  or  u - p sum u + v (softmax, sum u = 0 if
 //         normalised).
 // Nothing is divided by a score, so small ones lose nothing.
-constexpr int bwd_ctas_per_sm(int V) { return V == 1 ? 6 : V <= 16 ? 4 : 2; }
+// CTAs of eight warps that an SM's registers hold.  16384 tokens: 512 experts FP32 13.5 us
+// with three, 16.2 with four, BF16 12.7 and 11.8; 256 8.7 with three and with four, 10.6
+// with five; 1024 24.7 with two, 29.0 with three.
+constexpr int bwd_ctas_per_sm(int kind, int V) {
+  return V == 1 ? 6 : V <= 8 ? 4 : V == 16 ? (kind == kFp32 ? 3 : 4) : 2;
+}
 
 template <int kKind, int V>
-__global__ void __launch_bounds__(256, bwd_ctas_per_sm(V))
+__global__ void __launch_bounds__(256, bwd_ctas_per_sm(kKind, V))
 route_bwd_kernel(const BwdArgs a) {
   extern __shared__ __align__(16) float of_warps[];  // [warps][32 * V], many experts: and dp [32 * V]
   wait_for_previous_kernel();
@@ -1005,7 +1009,7 @@ fp8q_status launch_route(const RouteArgs &a, Mode mode, cudaStream_t s) {
 
 template <int kKind, int V>
 fp8q_status launch_bwd(const BwdArgs &a, cudaStream_t s) {
-  const int warps = 8, need = (a.T + warps - 1) / warps, most = kSms * bwd_ctas_per_sm(V);
+  const int warps = 8, need = (a.T + warps - 1) / warps, most = kSms * bwd_ctas_per_sm(kKind, V);
   const size_t smem = static_cast<size_t>(warps + many(V)) * 32 * V * sizeof(float);
   return launch_dependent(route_bwd_kernel<kKind, V>, dim3(need < most ? need : most), dim3(32 * warps),
                           smem, s, a);
