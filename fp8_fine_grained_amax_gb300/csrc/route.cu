@@ -377,7 +377,7 @@ route_kernel(const RouteArgs a) {
             chosen = choose_exactly<V>(key, k, lane);
           } else {
             chosen = kept >= kOpen ? static_cast<int>(kIndex - (kept & kIndex)) : -1;
-            float x = chosen >= 0 ? logit_at(here, kKind, chosen) : 0.0f;
+            float x = chosen >= 0 ? fminf(logit_at(here, kKind, chosen), kBig) : 0.0f;
             sort_lanes(x, chosen, lane);
             if (lane >= k) chosen = -1;
           }

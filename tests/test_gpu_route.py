@@ -150,6 +150,18 @@ def test_logits_that_differ_in_their_last_bits(T, E, k, steps):
     assert torch.equal(out.idx.cpu(), want)
 
 
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("E", [16, 300, 1024])
+def test_infinity_counts_as_the_largest_value(E, dtype):
+    # equal to it, so the lower index comes first; a weight has six roundings, 1e-6 of 0.2 at most
+    l = torch.zeros(40, E, dtype=dtype)
+    l[:, 3] = l[:, 7] = torch.finfo(FP).max if dtype == FP else float("inf")
+    l[:, 2] = l[:, 5] = l[:, 9] = float("inf")
+    out = fq.fp8q_route(l.cuda(), 6)
+    assert torch.equal(out.idx.cpu(), torch.tensor([[2, 3, 5, 7, 9, 0]], dtype=torch.int32).expand(40, 6))
+    near(out.weight, torch.tensor([[0.2] * 5 + [0.0]], dtype=torch.float64).expand(40, 6), torch.tensor(1e-6), "weight")
+
+
 @pytest.mark.parametrize("T", [6, 300])
 @pytest.mark.parametrize("score", [SOFT, SIG])
 @pytest.mark.parametrize("dtype", [FP, BF])
