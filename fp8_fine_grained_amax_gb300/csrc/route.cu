@@ -485,6 +485,7 @@ route_kernel(const RouteArgs a) {
         }
       }
       if (threadIdx.x == 0) cta_tokens = tokens;
+      __syncwarp();  // whole warps come to a cluster's barriers
       cluster_sync_all();
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
@@ -566,7 +567,10 @@ route_kernel(const RouteArgs a) {
     }
     a.slot[i] = r;
   }
-  if constexpr (clustered) cluster_wait();  // a CTA's totals stay until all have read them
+  if constexpr (clustered) {
+    __syncwarp();
+    cluster_wait();  // a CTA's totals stay until all have read them
+  }
 }
 
 constexpr int kRowThreads = 1024;
@@ -671,6 +675,7 @@ route_rows_kernel(const RouteArgs a) {
       before += own[r];
     }
   }
+  __syncwarp();  // whole warps come to a cluster's barriers
   cluster_sync_all();
   // thread i has expert i from here on
   total = before = 0;
@@ -721,6 +726,7 @@ route_rows_kernel(const RouteArgs a) {
     }
     if (i >= rows) a.order[i] = -1;
   }
+  __syncwarp();
   cluster_wait();  // a CTA's sums stay until all have read them
 }
 
@@ -937,6 +943,7 @@ route_bwd_kernel(const BwdArgs a) {
     }
     __syncwarp();
     if (at >= 0) u_of[at] = 0.0f;
+    __syncwarp();  // before another lane writes the next token's choice of the same expert
   }
 }
 

@@ -365,3 +365,42 @@ def test_repeats_bit_by_bit():
     for _ in range(5):
         again = fq.fp8q_route(l.cuda(), 8, valid=valid.cuda())
         assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+def many_tokens(T, E, k, dtype, seed):
+    """Logits that send most choices of neighbouring tokens to the same few experts, at other places of the choice."""
+    l, valid = make(T, E, dtype, seed, True)
+    l[:, : k + 2] += 6.0
+    return l, valid
+
+
+# more tokens than a launch has warps: each warp takes two to four, in every form
+MANY = [(20000, 16, 4, FP), (20000, 30, 3, BF), (12000, 64, 6, BF), (13000, 33, 5, FP), (12000, 128, 8, FP),
+        (12001, 256, 8, FP), (12000, 200, 6, BF), (11000, 512, 8, FP), (11000, 400, 8, BF), (7000, 1024, 32, FP),
+        (7000, 1000, 16, BF), (6999, 1023, 8, FP)]
+
+
+@pytest.mark.parametrize("T,E,k,dtype", MANY)
+@pytest.mark.parametrize("score,normalise", [(SOFT, True), (SOFT, False), (SIG, True)])
+def test_backward_of_more_tokens_than_warps(T, E, k, dtype, score, normalise):
+    # a token's gradient is its own: the same bits as in calls of 500 tokens, which take one per warp
+    l, valid = many_tokens(T, E, k, dtype, T + E)
+    l, valid = l.cuda(), valid.cuda()
+    kw = dict(score=score, normalise=normalise, scale=1.5)
+    r = fq.fp8q_route(l, k, valid=valid, **kw)
+    dw = torch.randn(T, k, generator=torch.Generator().manual_seed(T)).cuda()
+    dloss = torch.tensor([0.7], device="cuda")
+    got = fq.fp8q_route_bwd(l, r.idx, r.counts, r.tokens, dweight=dw, dloss=dloss, valid=valid, **kw)
+    for lo in range(0, T, 500):
+        at = slice(lo, lo + 500)
+        want = fq.fp8q_route_bwd(l[at], r.idx[at], r.counts, r.tokens, dweight=dw[at], dloss=dloss, valid=valid[at], **kw)
+        assert torch.equal(got[at], want), lo
+
+
+@pytest.mark.parametrize("T,E,k,dtype", [c for c in MANY if c[1] > 128])
+@pytest.mark.parametrize("score,normalise", [(SOFT, True), (SIG, False)])
+def test_forward_of_more_tokens_than_warps(T, E, k, dtype, score, normalise):
+    # several tokens per warp of many experts, and more CTAs than the second launch adds up in one go
+    l, valid = many_tokens(T, E, k, dtype, T + E)
+    r = fq.fp8q_route(l.cuda(), k, score=score, normalise=normalise, scale=2.5, valid=valid.cuda())
+    check(r, l, valid, k, score, normalise, 2.5)
