@@ -836,8 +836,8 @@ route_bwd_kernel(const BwdArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (!valid) l[v] = -INFINITY;
-    const int at = valid && next.at < E ? next.at : -1;
-    const float dw = next.dw * a.scale;
+    const int given = valid && next.at < E ? next.at : -1;
+    const float given_dw = next.dw * a.scale;
     if (t + warps < a.T) fetch(t + warps);  // in flight while this token is dealt with
 
     bool special = false;
@@ -879,8 +879,12 @@ route_bwd_kernel(const BwdArgs a) {
 
     // lane j has choice j's score and gradient; the gradients change lanes through
     // shared memory, all zeros but for these
-    const float x = at >= 0 ? fminf(logit_at(row, kKind, at), kBig) : 0.0f;
-    float u = at < 0 || !(x > -INFINITY) ? 0.0f : a.sigmoid ? sigmoid(x) : exp_above(x, m) * inv;
+    float x = given >= 0 ? logit_at(row, kKind, given) : -INFINITY;
+    // where there is no choice, or of a closed expert, the gradient does not count, whatever it is
+    const int at = x > -INFINITY ? given : -1;
+    x = fminf(x, kBig);
+    const float dw = at >= 0 ? given_dw : 0.0f;
+    float u = at < 0 ? 0.0f : a.sigmoid ? sigmoid(x) : exp_above(x, m) * inv;
     if (a.normalise) {
       u *= rcp_ftz(fmaxf(warp_sum(u), kTiny));
       u *= dw - warp_sum(u * dw);

@@ -404,3 +404,33 @@ def test_forward_of_more_tokens_than_warps(T, E, k, dtype, score, normalise):
     l, valid = many_tokens(T, E, k, dtype, T + E)
     r = fq.fp8q_route(l.cuda(), k, score=score, normalise=normalise, scale=2.5, valid=valid.cuda())
     check(r, l, valid, k, score, normalise, 2.5)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("score,normalise", [(SOFT, True), (SOFT, False), (SIG, True), (SIG, False)])
+@pytest.mark.parametrize("T,E,k,dtype", [(7, 6, 5, FP), (300, 64, 6, BF), (300, 300, 8, FP), (40, 1000, 32, BF)])
+def test_gradients_of_choices_that_are_none_do_not_count(T, E, k, dtype, score, normalise, bad):
+    # tokens with fewer open experts than choices, with none, and padding: whatever stands in dweight there
+    l, _ = make(T, E, dtype, T + E, False)
+    l[::2, k - 2:] = float("-inf")
+    l[1] = float("-inf")
+    valid = torch.ones(T, dtype=torch.bool)
+    valid[3::5] = False
+    l, valid = l.cuda(), valid.cuda()
+    kw = dict(score=score, normalise=normalise, scale=1.5, valid=valid)
+    r = fq.fp8q_route(l, k, **kw)
+    none = r.idx < 0
+    assert none.any() and not none.all()
+    dw = torch.randn(T, k, generator=torch.Generator().manual_seed(T)).cuda()
+    dloss = torch.tensor([0.7], device="cuda")
+    want = fq.fp8q_route_bwd(l, r.idx, r.counts, r.tokens, dweight=dw.masked_fill(none, 0.0), dloss=dloss, **kw)
+    got = fq.fp8q_route_bwd(l, r.idx, r.counts, r.tokens, dweight=dw.masked_fill(none, bad), dloss=dloss, **kw)
+    assert torch.isfinite(want.float()).all() and torch.equal(got, want)
+    assert not got[~valid].any() and not got[1].any()
+    # a choice outside the experts, of a closed one, or of a padding token is none either
+    idx = torch.where(none, E + 3, r.idx)
+    idx[0, k - 1] = E - 1  # closed to token 0
+    idx[3] = 0             # padding
+    dw = dw.masked_fill(none, bad)
+    dw[3] = bad
+    assert torch.equal(fq.fp8q_route_bwd(l, idx, r.counts, r.tokens, dweight=dw, dloss=dloss, **kw), want)
