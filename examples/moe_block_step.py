@@ -60,25 +60,35 @@ class MoEBlock:
         self.qw, self.sw, self.qwT, self.swT = stack(self.copies[0])
         self.qwd, self.swd, self.qwdT, self.swdT = stack(self.copies[1])
 
-    def forward(self, x, res):
+    def forward(self, x, res, valid=None, closed=None):
         """x (BF16, e.g. an attention's result) and the residual stream, [T][D] -> the block's contribution in
-        FP32, the new stream and the balance loss."""
+        FP32, the new stream and the balance loss.  valid (bool [T], optional) is False for padding, closed (bool
+        [T][E], optional) True where a token may not take an expert: what takes no expert contributes nothing."""
         n = self.n = fq.fp8q_rmsnorm(x, self.norm, residual=res, with_y=True, with_rstd=True)
         self.logits = n.y.float() @ self.router.t()
-        r = self.r = fq.fp8q_route(self.logits, self.k)
-        self.rows = r.order // self.k  # the token of each sorted row
+        if closed is not None:
+            self.logits = self.logits.masked_fill(closed, float("-inf"))
+        self.valid = valid
+        r = self.r = fq.fp8q_route(self.logits, self.k, valid=valid)
+        self.rows = r.order // self.k  # the token of each sorted row (any token behind the last choice)
+        # a choice that is none (slot -1) has no row: rows behind the last choice are not written by the products,
+        # so what is gathered there is replaced, not multiplied by a weight of zero
+        self.none = (r.slot < 0)[..., None]
         g = fq.fp8q_grouped_gemm_swiglu(n.q[self.rows], n.s[:, self.rows].contiguous(), self.qw, self.sw, r.offs,
                                         with_h=True, with_gu=True, with_codes=True)
         self.h, self.gu = g.h, g.gu
-        self.y = fq.fp8q_grouped_gemm(g.q, g.s, self.qwd, self.swd, r.offs)[r.slot].float()  # [T][k][D]
+        y = fq.fp8q_grouped_gemm(g.q, g.s, self.qwd, self.swd, r.offs)
+        self.y = y[r.slot].float().masked_fill(self.none, 0.0)  # [T][k][D]
         return (self.y * r.weight[..., None]).sum(1), n.r, r.loss
 
     def backward(self, dout):
         """dout (FP32 [T][D]): the gradient of the contribution, and of the stream, which the block's result
         adds up.  Leaves the weights' gradients and returns that of x (and of res)."""
         n, r, T = self.n, self.r, dout.shape[0]
-        dy = torch.empty(T * self.k, self.D, dtype=torch.bfloat16, device="cuda")
+        # one row more than choices: -1 is that one
+        dy = torch.empty(T * self.k + 1, self.D, dtype=torch.bfloat16, device="cuda")
         dy[r.slot.reshape(-1)] = (dout[:, None] * r.weight[..., None]).bfloat16().reshape(-1, self.D)
+        dy = dy[:-1]
         q, s = fq.fp8q_quant_act(dy)
         dh = fq.fp8q_grouped_gemm(q, s, self.qwdT, self.swdT, r.offs)
         d = fq.fp8q_swiglu_bwd(dh, self.gu, with_d=True, with_rows=True, with_cols=False, with_h=False)
@@ -91,9 +101,9 @@ class MoEBlock:
             self.dwd[e] = dy[lo:hi].t() @ self.h[lo:hi]
         dweight = (self.y * dout[:, None]).sum(-1)
         dlogits = fq.fp8q_route_bwd(self.logits, r.idx, r.counts, r.tokens, dweight=dweight,
-                                    dloss=torch.full((1,), self.balance, device="cuda"))
+                                    dloss=torch.full((1,), self.balance, device="cuda"), valid=self.valid)
         self.drouter = dlogits.t() @ n.y.float()
-        dnorm = dx[r.slot].float().sum(1) + dlogits @ self.router
+        dnorm = dx[r.slot].float().masked_fill(self.none, 0.0).sum(1) + dlogits @ self.router
         g = fq.fp8q_rmsnorm_bwd(dnorm, n.r, n.rstd, self.norm, dres=dout, out_dtype=fq.FP8Q_OUT_FP32)
         self.dnorm = g.dw
         return g.dx

@@ -208,3 +208,69 @@ def test_two_threads_at_once():
     [t.start() for t in threads]
     [t.join() for t in threads]
     assert not wrong
+
+
+def plain_masked(b, x, res, idx, may):
+    """`plain` for choices of -1 and experts that are closed (`may` False) to a token."""
+    leaves = [t.double().requires_grad_() for t in (x.double() + res.double(), b.norm, b.router, b.w, b.wd)]
+    h, norm, router, w, wd = leaves
+    y = h * (h.square().mean(1, keepdim=True) + 1e-6).rsqrt() * norm
+    alive, has = may.any(1), idx >= 0
+    p = torch.softmax(torch.where(may, y @ router.t(), -1e4), 1) * alive[:, None]
+    weight = torch.where(has, p.gather(1, idx.clamp_min(0)), 0.0)
+    weight = weight / torch.where(alive, weight.sum(1), 1.0)[:, None]
+    out = torch.zeros_like(y)
+    for e in range(b.E):
+        t, j = (idx == e).nonzero(as_tuple=True)
+        gate, up = (y[t] @ w[e].t()).chunk(2, 1)
+        out = out.index_add(0, t, (torch.nn.functional.silu(gate) * up) @ wd[e].t() * weight[t, j, None])
+    counts = torch.bincount(idx[has], minlength=b.E).double()
+    loss = b.E * (counts / counts.sum() * p.sum(0)).sum() / alive.sum()
+    return out, loss, leaves
+
+
+def test_block_with_padding_and_closed_experts(example):
+    """Tokens without a choice and with fewer than k: no rows of theirs are written, whatever is in that memory.
+    Bounds as in test_gradients_of_the_whole_block."""
+    T, D, E, k = 300, 256, 6, 3
+    b = example.MoEBlock(D, 384, E, k, 15)
+    x, res, dout = inputs(T, D, 17)
+    dout = dout.float() / T
+    g = torch.Generator(device="cuda").manual_seed(18)
+    valid = torch.rand(T, generator=g, device="cuda") > 0.2
+    closed = torch.rand(T, E, generator=g, device="cuda") < 0.6
+    closed[::7] = True
+
+    def spoil():  # free memory full of NaN: what the calls take next
+        held = [torch.full((T * k * D,), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(16)]
+        torch.cuda.synchronize()
+        del held
+
+    spoil()
+    out, stream, loss = b.forward(x, res, valid, closed)
+    spoil()
+    dx = b.backward(dout)
+    idx = b.r.idx.long()
+    none = idx < 0
+    assert none.all(1).any() and (none.any(1) & ~none.all(1)).any()
+    assert not out[none.all(1)].any() and torch.equal(none, b.r.slot < 0)
+    may = ~closed & valid[:, None]
+    want, want_loss, leaves = plain_masked(b, x, res, idx, may)
+    far = lambda a, c: float((a.double() - c.detach()).norm() / c.detach().norm())  # noqa: E731
+    assert far(out, want) < 0.08 and abs(float(loss) - float(want_loss.detach())) < 1e-2
+    assert far(stream, leaves[0].detach()) < 2.0 ** -8
+    grads = torch.autograd.grad((want * dout.double()).sum() + b.balance * want_loss, leaves)
+    got = (dx - dout, b.dnorm, b.drouter, b.dw, b.dwd)
+    for name, a, c in zip(("x", "norm", "router", "w", "wd"), got, grads):
+        assert far(a, c) < 0.15, name
+    b.update(1e-3)
+    assert all(torch.isfinite(t).all() for t in (b.norm, b.router, b.w, b.wd))
+
+
+def test_block_without_any_choice(example):
+    b = example.MoEBlock(256, 128, 4, 2, 16)
+    x, res, dout = inputs(40, 256, 19)
+    out, _, loss = b.forward(x, res, torch.zeros(40, dtype=torch.bool, device="cuda"))
+    dx = b.backward(dout.float())
+    assert not out.any() and loss.item() == 0 and torch.equal(dx, dout.float())
+    assert not any(t.any() for t in (b.dnorm, b.drouter, b.dw, b.dwd))
