@@ -226,6 +226,11 @@ constexpr float kLog2e = 1.44269504f;
 __device__ __forceinline__ float exp_above(float l, float m) { return ex2_ftz((l - m) * kLog2e); }
 __device__ __forceinline__ float exp_minus(float l) { return ex2_ftz(-kLog2e * l); }
 __device__ __forceinline__ float sigmoid(float l) { return rcp_ftz(1.0f + exp_minus(l)); }
+// x's share of a sum of which it is a part; exactly 1 where it is all of it.
+__device__ __forceinline__ float share_of(float x, float sum) {
+  sum = fmaxf(sum, kTiny);
+  return x == sum ? 1.0f : x * rcp_ftz(sum);
+}
 
 // Logits that are no numbers are closed, infinite ones the largest value.  Rare: the
 // callers look for one in the row first.
@@ -416,7 +421,7 @@ route_kernel(const RouteArgs a) {
       }
 
       if (chosen >= 0) w = a.sigmoid ? sigmoid(x) : exp_above(x, m) * inv;
-      if (a.normalise) w *= rcp_ftz(fmaxf(warp_sum(w), kTiny));
+      if (a.normalise) w = share_of(w, warp_sum(w));
     }
     if (lane < k) {
       const int64_t at = t * k + lane;
@@ -886,7 +891,7 @@ route_bwd_kernel(const BwdArgs a) {
     const float dw = at >= 0 ? given_dw : 0.0f;
     float u = at < 0 ? 0.0f : a.sigmoid ? sigmoid(x) : exp_above(x, m) * inv;
     if (a.normalise) {
-      u *= rcp_ftz(fmaxf(warp_sum(u), kTiny));
+      u = share_of(u, warp_sum(u));
       u *= dw - warp_sum(u * dw);
     } else {
       u *= dw;

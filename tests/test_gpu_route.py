@@ -434,3 +434,17 @@ def test_gradients_of_choices_that_are_none_do_not_count(T, E, k, dtype, score, 
     dw = dw.masked_fill(none, bad)
     dw[3] = bad
     assert torch.equal(fq.fp8q_route_bwd(l, idx, r.counts, r.tokens, dweight=dw, dloss=dloss, **kw), want)
+
+
+@pytest.mark.parametrize("score", [SOFT, SIG])
+@pytest.mark.parametrize("T,E,k", [(500, 64, 1), (3000, 256, 1), (400, 600, 4), (100, 24, 1)])
+def test_one_normalised_choice_is_a_constant(T, E, k, score):
+    # one choice, or one open expert: its weight is the scale, and its gradient nothing
+    l, _ = make(T, E, FP, 3 * T + E, False)
+    if k > 1:
+        l[torch.arange(E) != torch.arange(T)[:, None] % E] = float("-inf")
+    r = fq.fp8q_route(l.cuda(), k, score=score, scale=2.5)
+    assert (r.weight[:, 0] == 2.5).all() and not r.weight[:, 1:].any()
+    dw = torch.randn(T, k, generator=torch.Generator().manual_seed(T)).cuda()
+    d = fq.fp8q_route_bwd(l.cuda(), r.idx, r.counts, r.tokens, dweight=dw, score=score, scale=2.5)
+    assert not d.any()
