@@ -219,13 +219,20 @@ __device__ __forceinline__ void sort_lanes(float &x, int &e, int lane) {
   }
 }
 
-// exp2 and the reciprocal are right to 2 units and 1 unit in the last place, and
-// flush what is below 2^-126 to 0; the difference and its product with log2(e) are
-// rounded once each, 2 |l - m| 2^-24 relative in the result (|l| in a sigmoid).
+// Scores of all experts, for the probabilities: exp2 and the reciprocal are right to 2
+// units and 1 unit in the last place, and flush what is below 2^-126 to 0; the difference
+// and its product with log2(e) are rounded once each, 2 |l - m| 2^-24 relative in the
+// result (2 |l| in a sigmoid).
 constexpr float kLog2e = 1.44269504f;
 __device__ __forceinline__ float exp_above(float l, float m) { return ex2_ftz((l - m) * kLog2e); }
 __device__ __forceinline__ float exp_minus(float l) { return ex2_ftz(-kLog2e * l); }
 __device__ __forceinline__ float sigmoid(float l) { return rcp_ftz(1.0f + exp_minus(l)); }
+// Scores of the choices, one per lane and token, for the weights: their error does not grow
+// with the argument (but for the rounding of l - m).  16384 tokens of 256 experts 17.65 us
+// with the fast form here too, 17.75 so; backward 8.55 and 8.65; 262144 of 128 in BF16
+// 102.0 and 103.8, 68.0 and 69.0.
+__device__ __forceinline__ float chosen_above(float l, float m) { return expf(l - m); }
+__device__ __forceinline__ float chosen_sigmoid(float l) { return rcp_ftz(1.0f + expf(-l)); }
 // x's share of a sum of which it is a part; exactly 1 where it is all of it.
 __device__ __forceinline__ float share_of(float x, float sum) {
   sum = fmaxf(sum, kTiny);
@@ -420,7 +427,7 @@ route_kernel(const RouteArgs a) {
         for (int v = 0; v < V; ++v) psum[v] = fmaf(s[v], inv, psum[v]);
       }
 
-      if (chosen >= 0) w = a.sigmoid ? sigmoid(x) : exp_above(x, m) * inv;
+      if (chosen >= 0) w = a.sigmoid ? chosen_sigmoid(x) : chosen_above(x, m) * inv;
       if (a.normalise) w = share_of(w, warp_sum(w));
     }
     if (lane < k) {
@@ -889,7 +896,7 @@ route_bwd_kernel(const BwdArgs a) {
     const int at = x > -INFINITY ? given : -1;
     x = fminf(x, kBig);
     const float dw = at >= 0 ? given_dw : 0.0f;
-    float u = at < 0 ? 0.0f : a.sigmoid ? sigmoid(x) : exp_above(x, m) * inv;
+    float u = at < 0 ? 0.0f : a.sigmoid ? chosen_sigmoid(x) : chosen_above(x, m) * inv;
     if (a.normalise) {
       u = share_of(u, warp_sum(u));
       u *= dw - warp_sum(u * dw);

@@ -448,3 +448,26 @@ def test_one_normalised_choice_is_a_constant(T, E, k, score):
     dw = torch.randn(T, k, generator=torch.Generator().manual_seed(T)).cuda()
     d = fq.fp8q_route_bwd(l.cuda(), r.idx, r.counts, r.tokens, dweight=dw, score=score, scale=2.5)
     assert not d.any()
+
+
+@pytest.mark.parametrize("T,E", [(30, 100), (600, 300)])
+@pytest.mark.parametrize("centre", [-4, -12, -40, -80])
+def test_weights_of_small_sigmoids_keep_their_digits(T, E, centre):
+    """exp to 1 unit in the last place (2 u), 1 + exp (u), its reciprocal to a unit (2 u): 5 u whatever the logit;
+    normalised 5 u more for the sum's terms, 5 for its tree, 2 and 1 for reciprocal and product: 18 u.  The gradient
+    has the factor 1 - s, 5 u of the same kind, and four products: 14 u alone; normalised the weight's 18 u, the
+    mean's 18 + 6 u of its terms, a difference, two products and 1 - s: 50 u of the terms' size."""
+    k = 6
+    l = centre + 0.5 * torch.randn(T, E, generator=torch.Generator().manual_seed(T + centre))
+    dw = torch.randn(T, k, generator=torch.Generator().manual_seed(T))
+    for normalise, tol, grad_tol in ((False, 5, 14), (True, 18, 50)):
+        r = fq.fp8q_route(l.cuda(), k, score=SIG, normalise=normalise)
+        at = r.idx.cpu().long()
+        s = torch.sigmoid(l.double().gather(1, at))
+        w = s / s.sum(1, keepdim=True) if normalise else s
+        near(r.weight, w, tol * U * w, "weight")
+        d = fq.fp8q_route_bwd(l.cuda(), r.idx, r.counts, r.tokens, dweight=dw.cuda(), score=SIG, normalise=normalise)
+        g = dw.double()
+        mean = (w * g).sum(1, keepdim=True) if normalise else 0.0
+        size = g.abs() + ((w * g.abs()).sum(1, keepdim=True) if normalise else 0.0)
+        near(d.cpu().gather(1, at), w * (g - mean) * (1 - s), grad_tol * U * w * size, "gradient")
