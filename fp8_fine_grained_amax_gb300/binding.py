@@ -534,17 +534,20 @@ def fp8q_rmsnorm_bwd(dy, x, rstd, w, *, dres=None, with_dx=True, with_dw=True, o
     return tuple.__new__(RmsNormGrads, out)
 
 
-def fp8q_adamw(params, grads, m, v, *, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, grad_scale=None,
+def fp8q_adamw(params, grads, m, v, *, step, lr, betas=None, eps=1e-8, weight_decay=0.0, grad_scale=None,
                m_scales=None, v_scales=None, copies=None, stream=None):
     """One AdamW step, in place, over lists of contiguous tensors: params and grads FP32 or BF16, moments m and v
     FP32, BF16, or uint8 codes of m and sqrt(v) with f32 scales [ceil(n/128)] in m_scales and v_scales (all zeros
     before the first step); copies receive the new parameters in BF16.  step (an int from 1 on, or an int64 tensor)
     and lr (a float or an f32 tensor) may be device tensors of one element, which a captured call then follows;
-    grad_scale (an f32 tensor of one element) multiplies the gradients."""
+    grad_scale (an f32 tensor of one element) multiplies the gradients.  betas: (0.9, 0.999) where not given with
+    FP32 moments, (0.9, 0.95) with the others, which a beta2 of 0.99 and more moves by less than half their last
+    place (include/fp8q.h)."""
+    b1, b2 = (None, None) if betas is None else (betas[0], betas[1])
     step_dev = step if isinstance(step, torch.Tensor) else None
     lr_dev = lr if isinstance(lr, torch.Tensor) else None
     st = (_torch_calls or _calls()).adamw(
-        params, grads, m, v, m_scales, v_scales, copies, 0.0 if lr_dev is not None else lr, betas[0], betas[1], eps,
+        params, grads, m, v, m_scales, v_scales, copies, 0.0 if lr_dev is not None else lr, b1, b2, eps,
         weight_decay, 1 if step_dev is not None else step, lr_dev, step_dev, grad_scale, _handle(stream))
     if st:
         raise FP8QError(st, "fp8q_adamw")

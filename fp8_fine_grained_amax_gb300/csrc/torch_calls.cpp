@@ -658,7 +658,7 @@ bool entry(const List &l, Py_ssize_t i, const char *name, int64_t count, at::Sca
 }
 
 // (params, grads, m, v, m_scales, v_scales, copies, lr, beta1, beta2, eps, weight_decay, step,
-//  lr tensor, step tensor, grad_scale, stream)
+//  lr tensor, step tensor, grad_scale, stream); betas of None: what the moments' type can follow
 PyObject *adamw_impl(PyObject *const *v, Py_ssize_t n) {
   if (n != 17) return wrong_count("adamw");
   List params, grads, ms, vs, mscales, vscales, copies;
@@ -681,7 +681,9 @@ PyObject *adamw_impl(PyObject *const *v, Py_ssize_t n) {
     return nullptr;
   }
   double num[5];
-  for (int i = 0; i < 5; ++i) num[i] = PyFloat_AsDouble(v[7 + i]);
+  const bool own_betas = v[8] != Py_None && v[9] != Py_None;
+  for (int i = 0; i < 5; ++i)
+    if (own_betas || (i != 1 && i != 2)) num[i] = PyFloat_AsDouble(v[7 + i]);
   const long long step = PyLong_AsLongLong(v[12]);
   if (PyErr_Occurred()) return nullptr;
   if (count == 0) return PyLong_FromLong(FP8Q_OK);
@@ -694,6 +696,10 @@ PyObject *adamw_impl(PyObject *const *v, Py_ssize_t n) {
   if (codes != has_scales) {
     fail(codes ? "uint8 moments need m_scales and v_scales" : "only uint8 moments have scales");
     return nullptr;
+  }
+  if (!own_betas) {
+    num[1] = 0.9;
+    num[2] = state == FP8Q_STATE_FP32 ? 0.999 : 0.95;
   }
   const at::Device dev = p0->device();
   if (!dev.is_cuda()) {
