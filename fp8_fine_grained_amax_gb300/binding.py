@@ -5,7 +5,9 @@ kernels of libfp8q.so.  The gated feed-forward, Newton-Schulz, norm, AdamW and
 router calls marshal in a compiled module (csrc/torch_calls.cpp), the others
 through ctypes.  Tensors are torch CUDA tensors (torch supplies device
 memory and the current stream); outputs that are not passed in are allocated
-with torch.  ``stream`` names another stream than the current one: the call, and
+with torch (small results of one norm or router call share an allocation of up to
+2 MB, results of up to 4 KB one of up to 64 KB: a result that is kept for long, or
+saved, is better cloned).  ``stream`` names another stream than the current one: the call, and
 the memory that it takes for results and scratch, are then that stream's, as
 under ``torch.cuda.stream``.  E4M3 tensors are torch.uint8 (raw codes; ``.view(torch.float8_e4m3fn)``
 gives the FP8 dtype).  A failing call raises FP8QError; there is no fallback.

@@ -155,8 +155,10 @@ struct NoGil {
 };
 
 // Results of a call: the caller's tensor, checked, a new one, or None.  With
-// `together` small new ones are parts of one allocation, 256 bytes apart at least: it
-// takes longer to ask the allocator for each than to run a small call.
+// `together` new ones are parts of an allocation, 256 bytes apart at least: it takes
+// longer to ask the allocator for each than to run a small call.  A part keeps the whole
+// alive, so what is little (a loss, a few rows' statistics) shares with no more than
+// kFew bytes, however many of it a program keeps.
 class Results {
  public:
   explicit Results(bool together = false) : together_(together) {}
@@ -200,13 +202,13 @@ class Results {
   }
   // Make the new ones (needs no GIL).
   void make(const Place &place) {
-    if (together_ && make_together(place)) return;
-    if (scratch_) {
+    if (together_) make_together(place);
+    if (scratch_ && !*scratch_) {
       scratch_made_ = place.scratch(scratch_bytes_);
       *scratch_ = scratch_made_.data_ptr();
     }
     for (int i = 0; i < n_; ++i)
-      if (Mat *m = all_[i].wanted) {
+      if (Mat *m = all_[i].wanted; m && !all_[i].made.defined()) {
         One &r = all_[i];
         r.made = r.vector ? place.result({r.rows}, r.dtype) : place.result({r.rows, m->ld}, r.dtype);
         m->p = r.made.data_ptr();
@@ -233,30 +235,48 @@ class Results {
     bool vector = false;
     at::Tensor made;
   };
-  static constexpr int64_t kSmall = 2 << 20;  // bytes of all results together
-  bool make_together(const Place &place) {
+  static constexpr int64_t kLittle = 4 << 10, kFew = 64 << 10, kMost = 2 << 20;  // bytes
+  int64_t room(const One &r) const {
+    const int64_t n = r.vector ? r.rows : r.rows * r.wanted->ld;
+    return (n * static_cast<int64_t>(c10::elementSize(r.dtype)) + 255) / 256 * 256;
+  }
+  void make_together(const Place &place) {
+    int64_t all = scratch_bytes_;
+    for (int i = 0; i < n_; ++i)
+      if (all_[i].wanted) all += room(all_[i]);
+    if (all <= kFew) {
+      make_block(place, -1, kFew, kFew, true);
+    } else {
+      make_block(place, -1, kLittle, kFew, false);
+      make_block(place, kLittle, kMost, kMost, true);
+    }
+  }
+  // Those of more than `over` and at most `upto` bytes, and the scratch, in one allocation, if
+  // there are two at least and `most` bytes hold them.
+  void make_block(const Place &place, int64_t over, int64_t upto, int64_t most, bool with_scratch) {
     int64_t at[8], bytes = 0;
     int count = 0;
     for (int i = 0; i < n_; ++i) {
-      const One &r = all_[i];
-      if (!r.wanted) continue;
+      at[i] = -1;
+      if (!all_[i].wanted) continue;
+      const int64_t size = room(all_[i]);
+      if (size <= over || size > upto) continue;
       at[i] = bytes;
-      const int64_t n = r.vector ? r.rows : r.rows * r.wanted->ld;
-      if (n > kSmall) return false;
-      bytes += (n * static_cast<int64_t>(c10::elementSize(r.dtype)) + 255) / 256 * 256;
+      bytes += size;
       ++count;
     }
+    with_scratch = with_scratch && scratch_;
     const int64_t scratch_at = bytes;
-    if (scratch_) {
+    if (with_scratch) {
       bytes += scratch_bytes_;
       ++count;
     }
-    if (count < 2 || bytes > kSmall) return false;
+    if (count < 2 || bytes > most) return;
     const at::Tensor block = place.result({bytes}, at::kByte);
     char *base = static_cast<char *>(block.data_ptr());
     for (int i = 0; i < n_; ++i) {
+      if (at[i] < 0) continue;
       One &r = all_[i];
-      if (!r.wanted) continue;
       r.made = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(block.storage()), block.key_set(),
                                                         c10::scalarTypeToTypeMeta(r.dtype));
       c10::TensorImpl *impl = r.made.unsafeGetTensorImpl();
@@ -265,8 +285,10 @@ class Results {
       else impl->set_sizes_contiguous({r.rows, r.wanted->ld});
       r.wanted->p = base ? base + at[i] : nullptr;
     }
-    if (scratch_) *scratch_ = base + scratch_at;
-    return true;
+    if (with_scratch) {
+      scratch_made_ = block;
+      *scratch_ = base + scratch_at;
+    }
   }
   One all_[8];
   void **scratch_ = nullptr;

@@ -274,3 +274,34 @@ def test_block_without_any_choice(example):
     dx = b.backward(dout.float())
     assert not out.any() and loss.item() == 0 and torch.equal(dx, dout.float())
     assert not any(t.any() for t in (b.dnorm, b.drouter, b.dw, b.dwd))
+
+
+def test_what_a_result_keeps_alive():
+    """Results of a call share allocations; what is little, and kept, holds no more than 64 KB."""
+    held = lambda t: t.untyped_storage().nbytes()  # noqa: E731
+    for T, E, k in ((1, 64, 4), (2000, 64, 4), (4096, 256, 8), (40000, 256, 8)):
+        r = fq.fp8q_route(torch.randn(T, E, device="cuda"), k)
+        assert max(map(held, (r.loss, r.tokens, r.counts, r.offs))) <= 64 << 10
+        assert all(held(t) <= max(t.nbytes, 2 << 20) for t in r)
+        check = fq.fp8q_route_bwd(torch.randn(T, E, device="cuda"), r.idx, r.counts, r.tokens, dloss=r.loss)
+        assert held(check) == check.nbytes
+    for T, C in ((1, 7168), (40, 7168), (333, 896), (1000, 7168)):
+        x = torch.randn(T, C, device="cuda").bfloat16()
+        w = torch.ones(C, device="cuda")
+        n = fq.fp8q_rmsnorm(x, w, residual=x, with_y=True, with_rstd=True)
+        assert held(n.rstd) <= 64 << 10
+        g = fq.fp8q_rmsnorm_bwd(x, n.r, n.rstd, w)
+        assert all(held(t) <= max(t.nbytes, 2 << 20) for t in (*n, *g))
+        # parts of one allocation do not overlap, and start where wide loads may
+        parts = sorted((t.data_ptr(), t.nbytes) for t in (*n, *g))
+        assert all(p + size <= q for (p, size), (q, _) in zip(parts, parts[1:])) and all(p % 256 == 0 for p, _ in parts)
+
+
+def test_a_logged_loss_holds_no_more_than_itself_and_little_else():
+    l = torch.randn(4000, 64, device="cuda")
+    fq.fp8q_route(l, 8)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    losses = [fq.fp8q_route(l, 8).loss for _ in range(100)]
+    assert torch.cuda.memory_allocated() - before <= 100 * (64 << 10)
+    assert len({float(x) for x in losses}) == 1
