@@ -16,6 +16,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <vector>
@@ -352,7 +353,7 @@ fp8q_status adamw(const fp8q_adamw_tensor *tensors, int64_t count, int p_dtype, 
   a.omb1 = static_cast<float>(1.0 - beta1);
   a.b2 = static_cast<float>(beta2);
   a.omb2 = static_cast<float>(1.0 - beta2);
-  a.eps = static_cast<float>(eps);
+  a.eps = eps > 0.0 ? std::max(static_cast<float>(eps), FLT_MIN) : 0.0f;
   if (!step_dev) {
     a.ic1 = static_cast<float>(1.0 / (1.0 - std::pow(beta1, static_cast<double>(step))));
     a.isc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, static_cast<double>(step))));
@@ -405,9 +406,9 @@ extern "C" fp8q_status fp8q_adamw(const fp8q_adamw_tensor *tensors, int64_t coun
   if ((p_dtype != kBf16 && p_dtype != kFp32) || (g_dtype != kBf16 && g_dtype != kFp32) ||
       state_kind < kStateBf16 || state_kind > kStateE4m3)
     return FP8Q_ERR_INVALID;
+  const auto is_value = [](double v) { return std::fabs(v) <= static_cast<double>(FLT_MAX); };
   if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) ||
-      !std::isfinite(eps) || !std::isfinite(lr) || !std::isfinite(weight_decay) ||
-      (!step_dev && step < 1))
+      !is_value(eps) || !is_value(lr) || !is_value(weight_decay) || (!step_dev && step < 1))
     return FP8Q_ERR_INVALID;
   if (count < 0) return FP8Q_ERR_SHAPE;
   if (count == 0) return FP8Q_OK;

@@ -485,8 +485,9 @@ fp8q_status fp8q_rmsnorm_bwd(const void *dy, int64_t ld_dy, int dy_dtype, const 
  *   lr, step   by value, or from device memory where lr_dev / step_dev are not
  *              NULL (a captured call then follows them); step counts from 1.
  *   grad_scale optional (NULL: 1) FP32 in device memory, e.g. a clipping factor.
- *   0 <= beta1, beta2 < 1, eps >= 0; lr, weight_decay finite; n >= 0, the
- *   tensors of a call below 2^42 values together.
+ *   0 <= beta1, beta2 < 1, eps >= 0 (a positive one below 2^-126 counts as that; with
+ *   0 a value whose gradients were all 0 becomes NaN); eps, lr, weight_decay at most
+ *   the largest FP32 value; n >= 0, the tensors of a call below 2^42 values together.
  * Alignment: every address at its element's; tensors whose addresses are all
  * 16-byte aligned take wide loads.
  */

@@ -359,3 +359,13 @@ def test_betas_where_none_are_given():
             b.step(step=step, lr=1e-2, betas=betas)
         for x, y in zip(a.p + a.m + a.v, b.p + b.m + b.v):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("state", ["fp32", "bf16", "e4m3"])
+@pytest.mark.parametrize("eps", [1e-30, 1e-40, 1e-60])
+def test_zero_gradients_with_the_smallest_eps(state, eps):
+    st = State([300], "fp32", "fp32", state, seed=23)
+    st.g[0].zero_()
+    p = st.p[0].clone()
+    st.step(step=1, **{**HYPER, "eps": eps})
+    near(st.p[0], p.double().cpu() * (1 - 1e-3), 4 * U * p.double().abs().cpu(), "decay alone")

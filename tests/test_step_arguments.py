@@ -181,3 +181,9 @@ def test_binding_refuses_wrong_tensors(lib):
     with pytest.raises(TypeError):
         fq.fp8q_adamw([3], [x], [x], [x], step=1, lr=1e-3)
     assert fq.fp8q_adamw([], [], [], [], step=1, lr=1e-3) is None
+
+
+@pytest.mark.parametrize("change", [dict(lr=1e39), dict(lr=-1e300), dict(wd=3.5e38), dict(eps=1e39)])
+def test_adamw_numbers_past_fp32_are_refused(lib, B, change):
+    # they would be infinite in the kernel
+    assert adamw(lib, entries({}, {}), **change) == B.FP8Q_ERR_INVALID
