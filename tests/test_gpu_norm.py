@@ -258,3 +258,31 @@ def test_rows_past_32_bit_offsets():
     want, tol, dw, tolw = reference_bwd(h, h, out.rstd.cpu(), w, h)
     near(g.dx, want, tol + 2.0 ** -8 * (want.abs() + tol), "dx")
     near(g.dw, dw, tolw, "dw")
+
+
+# more rows than a launch has CTAs (or warps) for: each takes two to four, so the ring's places are used again
+@pytest.mark.parametrize("T,C,kx,kres", [
+    (6000, 520, BF, BF), (6000, 640, FP, FP), (3000, 1152, BF, BF), (3001, 1280, FP, BF), (1500, 4088, BF, FP),
+    (1500, 3968, BF, None), (500, 4096, FP, FP), (400, 8320, BF, BF), (310, 16384, BF, None), (400, 16512, BF, BF),
+    (310, 24576, FP, None), (200, 32768, BF, FP)])
+def test_forward_of_more_rows_than_a_launch_takes(T, C, kx, kres):
+    x, w = rand(T + C, T, C, dtype=kx), 1 + rand(1, C, std=0.3)
+    x = (x.float() * (1 + torch.arange(T) % 7)[:, None]).to(kx)  # rows that are not mistaken for one another
+    res = None if kres is None else rand(T + C + 1, T, C, dtype=kres, std=3.0)
+    codes = C % 128 == 0
+    out = fq.fp8q_rmsnorm(x.cuda(), w.cuda(), residual=None if res is None else res.cuda(), with_y=True, with_rstd=True,
+                          with_codes=codes)
+    check_forward(out, x, w, res, 1e-6, fq.FP8Q_SCALE_FP32)
+    # statistics alone: rows that end before their results
+    only = fq.fp8q_rmsnorm(x.cuda(), w.cuda(), residual=None if res is None else res.cuda(), with_r=False, with_codes=False,
+                           with_rstd=True)
+    assert torch.equal(only.rstd, out.rstd)
+
+
+@pytest.mark.parametrize("T,C,kdy,kx,kd,with_dres", [
+    (9000, 256, BF, BF, BF, True), (9001, 136, FP, FP, BF, False), (8000, 8, BF, FP, FP, True), (6000, 512, BF, FP, FP, True),
+    (6001, 264, FP, FP, BF, True), (3000, 1024, FP, FP, FP, True), (3000, 1152, BF, BF, BF, True), (3001, 1032, FP, FP, BF, True),
+    (1500, 2048, BF, FP, FP, True), (400, 8704, BF, BF, BF, True), (400, 9216, FP, FP, BF, False), (310, 16384, BF, BF, BF, True),
+    (400, 10240, FP, FP, FP, True), (310, 16512, BF, FP, FP, True), (310, 4096, FP, BF, BF, True)])
+def test_backward_of_more_rows_than_a_launch_takes(T, C, kdy, kx, kd, with_dres):
+    test_backward(T, C, kdy, kx, kd, with_dres)
