@@ -703,7 +703,7 @@ PyObject *adamw_impl(PyObject *const *v, Py_ssize_t n) {
     return nullptr;
   }
   double num[5];
-  const bool own_betas = v[8] != Py_None && v[9] != Py_None;
+  const bool own_betas = v[8] != Py_None || v[9] != Py_None;
   for (int i = 0; i < 5; ++i)
     if (own_betas || (i != 1 && i != 2)) num[i] = PyFloat_AsDouble(v[7 + i]);
   const long long step = PyLong_AsLongLong(v[12]);

@@ -187,3 +187,13 @@ def test_binding_refuses_wrong_tensors(lib):
 def test_adamw_numbers_past_fp32_are_refused(lib, B, change):
     # they would be infinite in the kernel
     assert adamw(lib, entries({}, {}), **change) == B.FP8Q_ERR_INVALID
+
+
+def test_one_beta_alone_is_refused(lib):
+    import torch
+
+    import fp8_fine_grained_amax_gb300 as fq
+    x = torch.zeros(4)
+    for betas in ((None, 0.9), (0.9, None)):
+        with pytest.raises(TypeError):
+            fq.fp8q_adamw([x], [x], [x], [x], step=1, lr=1e-3, betas=betas)
