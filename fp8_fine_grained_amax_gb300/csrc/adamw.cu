@@ -160,13 +160,9 @@ __device__ __forceinline__ void decode8(uint2 c, float s, Pairs &v) {
   }
 }
 __device__ __forceinline__ float absmax8(const Pairs &p) {
-  float m = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack_f32x2(p[i]);
-    m = max3_abs(m, f.x, f.y);
-  }
-  return m;
+  float v[8];
+  unpack(p, v);
+  return fp8q::absmax8(v);
 }
 __device__ __forceinline__ uint2 codes8(const Pairs &p) { return make_uint2(codes4(p[0], p[1]), codes4(p[2], p[3])); }
 

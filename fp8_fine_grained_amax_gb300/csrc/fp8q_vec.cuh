@@ -1,5 +1,6 @@
 // fp8q_vec.cuh -- eight consecutive BF16 or FP32 values of a row or a list, as
-// one thread moves them: 16-byte loads and stores and the conversions between.
+// one thread moves them: 16-byte loads and stores and the conversions between; and a
+// warp's sums.
 #pragma once
 
 #include <cstdint>
@@ -12,6 +13,22 @@ namespace fp8q {
 enum Kind { kBf16 = FP8Q_OUT_BF16, kFp32 = FP8Q_OUT_FP32, kNone = 2 };
 
 __host__ __device__ constexpr int size_of(int kind) { return kind == kBf16 ? 2 : 4; }
+constexpr bool kind_ok(int kind) { return kind == kBf16 || kind == kFp32; }
+
+// The same sum in all lanes.
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  return v;
+}
+__device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(~0u, v); }
+
+__device__ __forceinline__ float absmax8(const float (&v)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) m = max3_abs(m, v[e], v[e + 1]);
+  return m;
+}
 
 // Read once by one thread: not kept in L1.  (Not the read-only path: a result may
 // be its own input, as when the residual stream is updated in place.)

@@ -28,12 +28,6 @@ constexpr int kRowWarps = 8;            // rows per CTA in the warp forms
 constexpr int kSms = 152;
 constexpr int kRingBytes = 216 * 1024;  // of an SM's shared memory, for rings
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  return v;
-}
-
 // Sum over the row's threads, the same in all of them: a warp, or the CTA's
 // warps through shared memory (`part` may be used again after another barrier).
 template <bool kWarpRow>
@@ -116,12 +110,6 @@ struct NormArgs {
   bool w_fp32, pow2;
 };
 
-__device__ __forceinline__ float absmax8(const float (&h)[8]) {
-  float m = 0.0f;
-#pragma unroll
-  for (int e = 0; e < 8; e += 2) m = max3_abs(m, h[e], h[e + 1]);
-  return m;
-}
 __device__ __forceinline__ void store_codes(const NormArgs &a, int64_t row, int vec, float inv,
                                             float (&h)[8]) {
 #pragma unroll
@@ -598,8 +586,8 @@ rmsnorm_dw_kernel(const float *part, int n, int C, float *dw, bool accumulate) {
 }
 
 // How rows of C columns are taken, and by how many CTAs: as many as fit 152 SMs at
-// once.  It depends on the types (dres or none) and on T and C alone, not on the
-// device, so that the sums' order does too.
+// once.  The CTAs depend on T and C alone, the stages on the types' bytes too, nothing on
+// the device or on whether there is a dres, so that the sums' order does not either.
 struct BwdPlan {
   int V, threads, stages, ctas;  // stages 0: the long form
 };
@@ -641,8 +629,6 @@ fp8q_status launch_bwd(const BwdArgs &a, const BwdPlan &p, cudaStream_t s) {
   if (p.stages) return launch_ring<rmsnorm_bwd_kernel<kDy, kX, kDx, 2, false>>(p.ctas, p.threads, ring, s, a);
   return launch_ring<rmsnorm_bwd_long_kernel<kDy, kX, kDx>>(p.ctas, 1024, static_cast<int>(sizeof(float)) * C, s, a);
 }
-
-bool kind_ok(int kind) { return kind == kBf16 || kind == kFp32; }
 
 // Whether rows of `kind` at p with pitch ld start on 16-byte boundaries.
 bool rows_aligned(const void *p, int64_t ld, int kind) {

@@ -247,13 +247,6 @@ __device__ __forceinline__ void make_finite(float (&l)[V]) {
   for (int v = 0; v < V; ++v) l[v] = l[v] > -INFINITY ? fminf(l[v], kBig) : -INFINITY;
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  return v;
-}
-__device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(~0u, v); }
-
 // E * sum_e (counts_e / choices) * (probs_e / tokens) from the sum of their products.
 __device__ __forceinline__ float balance(float sum, int E, int choices, int tokens) {
   return tokens > 0 ? static_cast<float>(E) * (sum / static_cast<float>(choices)) / static_cast<float>(tokens)
@@ -1048,7 +1041,6 @@ fp8q_status launch_bwd(const BwdArgs &a, cudaStream_t s) {
   return launch_bwd<kKind, 32>(a, s);
 }
 
-bool kind_ok(int kind) { return kind == kBf16 || kind == kFp32; }
 bool row_vectors(const void *p, int64_t ld, int kind) {
   return aligned16(p) && ld * size_of(kind) % 16 == 0;
 }
