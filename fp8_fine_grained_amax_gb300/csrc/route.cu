@@ -957,9 +957,9 @@ route_bwd_kernel(const BwdArgs a) {
 }
 
 // How a call's tokens are spread; the same for every device, so that the probabilities'
-// sums are too.  256 experts: 17 tokens take 4.5 us in one CTA and 5.4 in a cluster, 64
-// take 7.7, 5.7 and, in two launches, 7.9, 256 take 7.2 in a cluster and 8.2 in two
-// launches, 512 9.6 and 8.5.  512 experts: 64 tokens 10.6, 7.8 and 9.9.  The totals of
+// sums are too.  256 experts: 17 tokens take 4.7 us in one CTA and 5.6 in a cluster, 64
+// take 7.9, 5.8 and, in two launches, 8.0, 256 take 7.4 in a cluster and 8.4 in two
+// launches, 512 9.9 and 8.5.  512 experts: 64 tokens 10.8, 7.9 and 10.0.  The totals of
 // more take longer to exchange than a second launch (1024 experts: 32 tokens 11.2 in one
 // CTA and 11.9 in two launches, 64 12.4 in a cluster and 12.1, 256 17.7 and 14.2).
 struct Plan {

@@ -527,7 +527,10 @@ fp8q_status fp8q_adamw(const fp8q_adamw_tensor *tensors, int64_t count, int p_dt
  *   loss   FP32 [1]: the balance loss, E * sum_e f_e P_e with f_e expert e's share
  *          of all choices and P_e the mean over those tokens of s_e / sum s; 1
  *          where all experts are used alike, 0 without tokens.
- * Sums of scores below 2^-126 count as 2^-126.
+ * Sums of scores below 2^-126 count as 2^-126.  With u = 2^-24, weights of sigmoid scores
+ * are right to 18 u whatever the logit, of softmax scores to 70 u and the rounding of
+ * logit - maximum; the probabilities s / sum s of the loss, and their gradient, to 70 u
+ * and 4 |logit| u (sigmoid) or 2 |logit - maximum| u (softmax).
  *   1 <= k <= min(E, 32), E <= 1024, 0 <= T <= 2^26, T * k < 2^31.
  *   workspace  device scratch of fp8q_route_workspace_bytes(T, E) bytes (0 for
  *              sizes outside the limits), 16-byte aligned, owned by the caller;
@@ -550,7 +553,8 @@ fp8q_status fp8q_route(const void *logits, int64_t ld, int dtype, const uint8_t 
  *   idx, counts, tokens  its results.
  *   dweight  optional (NULL: 0) FP32 [T][k];  dloss optional (NULL: 0) FP32 [1].
  *   dlogits  [T][ld_d] of the logits' type: 0 at closed experts and padding.
- * An idx outside [0, E) is no choice.
+ * An idx outside [0, E), of a closed expert or of a padding token is no choice: its
+ * dweight does not count, whatever it holds (NaN, memory never written).
  */
 fp8q_status fp8q_route_bwd(const void *logits, int64_t ld, int dtype, const uint8_t *valid,
                            int score, int normalise, float scale, const int32_t *idx,
